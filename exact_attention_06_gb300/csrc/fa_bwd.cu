@@ -268,9 +268,16 @@ __device__ __forceinline__ void ew_pairs_dkdv(const uint32_t (&sv)[32], const ui
   }
 }
 
+// A key row behind its sequence (whatever its K and V hold): no gradient.
+__device__ __forceinline__ void clear_pairs(uint32_t (&pp)[16], uint32_t (&dp)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) pp[i] = dp[i] = 0;
+}
+
 // Elementwise step of the dQ kernel on 32 key columns of one query row: dS = P (dP - D) with
-// P = 2^(S c - lse2), rounded to bf16 pairs.  MASK zeroes keys past the row's last key.
-template <bool MASK>
+// P = 2^(S c - lse2), rounded to bf16 pairs.  MASK zeroes keys past the row's last key; with CLEAR
+// their dS is cleared after the product, so that padding behind them may hold anything.
+template <bool MASK, bool CLEAR = false>
 __device__ __forceinline__ void ew_pairs_dq(const uint32_t (&sv)[32], const uint32_t (&pv)[32], uint64_t c2,
                                             uint64_t nl2, uint64_t nd2, int key0, int lim, uint32_t (&dp)[16]) {
 #pragma unroll
@@ -285,8 +292,32 @@ __device__ __forceinline__ void ew_pairs_dq(const uint32_t (&sv)[32], const uint
     float s0, s1;
     f2_unpack(f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(pv[e]), __uint_as_float(pv[e + 1])), nd2)), s0,
               s1);
+    if (MASK && CLEAR) {
+      if (key0 + e > lim) s0 = 0.f;
+      if (key0 + e + 1 > lim) s1 = 0.f;
+    }
     dp[e / 2] = pack_bf16(s0, s1);
   }
+}
+
+// Cross attention, by value: see BwdLaunch.  n_keys: keys of the k, v tensors; tiles: tiles of the
+// scanned side per block (blockIdx.z takes tiles z * tiles ..); part_stride: elements from one
+// partial sum to the next (0: the gradient itself is written).
+struct CrossArgs {
+  const int* kv_lens;
+  int kv_heads, n_keys, tiles;
+  long long part_stride;
+  __device__ __forceinline__ int keys(int bh) const {
+    return kv_lens ? min(max(kv_lens[bh / kv_heads], 0), n_keys) : n_keys;
+  }
+};
+
+// Rows row0 .. row0 + rows - 1 of a gradient [.., D] that no pair reaches: zeros.
+template <int D>
+__device__ __forceinline__ void zero_rows(void* out, size_t row0, int rows, bool fp32) {
+  const int row_bytes = D * (fp32 ? 4 : 2);
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + row0 * row_bytes);
+  for (int i = threadIdx.x; i < rows * row_bytes / 16; i += blockDim.x) dst[i] = make_uint4(0, 0, 0, 0);
 }
 
 // --------------------------------------------------------------------- dK, dV: one CTA per key tile
@@ -311,14 +342,15 @@ struct DkdvCfg : BwdCfg<D> {
 };
 static_assert(DkdvCfg<128>::SMEM <= 232448, "dK/dV kernel shared memory");
 
-template <int D, bool CAUSAL>
+template <int D, bool CAUSAL, bool CROSS = false>
 __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                     const float* __restrict__ lse, const float* __restrict__ delta, void* __restrict__ dk,
                     void* __restrict__ dv, int N, float sl2, float scale, int grad_fp32,
                     unsigned long long budget, const __grid_constant__ CUtensorMap tdk,
-                    const __grid_constant__ CUtensorMap tdv, int ng) {
+                    const __grid_constant__ CUtensorMap tdv, int ng, const CrossArgs x) {
+  static_assert(!CROSS || !CAUSAL, "cross attention is not causal");
   using C = DkdvCfg<D>;
   using W = BwdWarps<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -335,8 +367,24 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
   int bh, kt;  // key tile; small kt has the most causal work and is scheduled first (within a head group)
   grouped_block(ng, bh, kt);
   const int n_tiles = (N + kTile - 1) / kTile;
-  const int i0 = CAUSAL ? kt : 0;  // first query tile that sees this key tile
-  const int n_i = n_tiles - i0;
+  const int i0 = CROSS ? static_cast<int>(blockIdx.z) * x.tiles : CAUSAL ? kt : 0;  // first query tile of this block
+  const int n_i = CROSS ? min(x.tiles, n_tiles - i0) : n_tiles - i0;
+  const int n_keys = CROSS ? x.n_keys : N;
+  int lim = n_keys;  // CROSS: keys of this sequence
+  if constexpr (CROSS) {
+    if (x.part_stride) {  // this range of queries' partial sums
+      dk = static_cast<float*>(dk) + blockIdx.z * x.part_stride;
+      dv = static_cast<float*>(dv) + blockIdx.z * x.part_stride;
+    }
+    lim = x.keys(bh);
+    if (kt * kTile >= lim) {  // padding only
+      const size_t row0 = static_cast<size_t>(bh) * n_keys + kt * kTile;
+      const int rows = min(kTile, n_keys - kt * kTile);
+      zero_rows<D>(dk, row0, rows, grad_fp32);
+      zero_rows<D>(dv, row0, rows, grad_fp32);
+      return;
+    }
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(BAR(C::B_KV), 1);
@@ -532,6 +580,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           uint32_t pp[16], dp[16];
           if (diag) ew_pairs_dkdv<true>(sv, pv, nv, c2, 64 * q + 32 * h, qt * kTile, key, pp, dp);
           else ew_pairs_dkdv<false>(sv, pv, nv, c2, 64 * q + 32 * h, qt * kTile, key, pp, dp);
+          if (CROSS && key >= lim) clear_pairs(pp, dp);
           tmem_st2_x16<32>(tA + 64 * q, pp);  // P^T packed: columns 64q + 32h .. + 15
           tmem_st2_x16<32>(tB + 64 * q, dp);  // dS^T packed
           tmem_wait_st();
@@ -560,6 +609,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           uint32_t pp[16], dp[16];
           if (diag) ew_pairs_dkdv<true>(sv, pv, nv, c2, 32 * c, qt * kTile, key, pp, dp);
           else ew_pairs_dkdv<false>(sv, pv, nv, c2, 32 * c, qt * kTile, key, pp, dp);
+          if (CROSS && key >= lim) clear_pairs(pp, dp);
           tmem_st1_x16(tA + 16 * c, pp);  // P^T packed
           tmem_st1_x16(tB + 16 * c, dp);  // dS^T packed
           tmem_wait_st();
@@ -571,14 +621,14 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
     if (ok) ok = bwait_all(BAR(C::B_GF), 0, abort_flag, budget);  // gradients final
     if (ok) {
       tc_fence_after();
-      const size_t row_off = static_cast<size_t>(bh) * N + key;
+      const size_t row_off = static_cast<size_t>(bh) * n_keys + key;
       if (grad_fp32) {
         if constexpr (W::ONE) {
-          store_grad_row128(dv, row_off, key < N, tmem + lane_addr + kColG1, 1.f);
-          store_grad_row128(dk, row_off, key < N, tmem + lane_addr + C::COL_G2, scale);
+          store_grad_row128(dv, row_off, key < n_keys, tmem + lane_addr + kColG1, 1.f);
+          store_grad_row128(dk, row_off, key < n_keys, tmem + lane_addr + C::COL_G2, scale);
         } else {
-          store_grad_half_row<D>(dv, row_off, h, key < N, true, tmem + lane_addr + kColG1, 1.f);
-          store_grad_half_row<D>(dk, row_off, h, key < N, true, tmem + lane_addr + C::COL_G2, scale);
+          store_grad_half_row<D>(dv, row_off, h, key < n_keys, true, tmem + lane_addr + kColG1, 1.f);
+          store_grad_half_row<D>(dk, row_off, h, key < n_keys, true, tmem + lane_addr + C::COL_G2, scale);
         }
       } else {
         // bf16 dV and dK through shared memory: the V and K tiles have their shape and are no
@@ -622,20 +672,21 @@ struct DqCfg : BwdCfg<D> {
   static constexpr uint32_t STAGE = 2 * B::TB;
   static constexpr uint32_t OFF_BAR = OFF_RING + B::ST * STAGE;
   static constexpr int B_QD = 0, B_FULL = 1, B_EMPTY = B_FULL + B::ST, B_SF = B_EMPTY + B::ST, B_PF = B_SF + 1,
-                       B_DRAIN = B_PF + 4, B_OW = B_DRAIN + 1, NBAR = B_OW + 1;  // B_PF + c: chunk c of the
+                       B_DRAIN = B_PF + 4, B_OW = B_DRAIN + 1, B_KC = B_OW + 1, NBAR = B_KC + 1;  // B_PF + c: chunk c of the
                                                                                // elementwise step
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR;
   static constexpr uint32_t SMEM = OFF_MISC + 16u + 1024u;
 };
 static_assert(DqCfg<128>::SMEM <= 232448, "dQ kernel shared memory");
 
-template <int D, bool CAUSAL>
+template <int D, bool CAUSAL, bool CROSS = false>
 __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                   const float* __restrict__ lse, const float* __restrict__ delta, void* __restrict__ dq, int N,
                   float sl2, float scale, int grad_fp32, unsigned long long budget,
-                  const __grid_constant__ CUtensorMap tdq, int ng) {
+                  const __grid_constant__ CUtensorMap tdq, int ng, const CrossArgs x) {
+  static_assert(!CROSS || !CAUSAL, "cross attention is not causal");
   using C = DqCfg<D>;
   using W = BwdWarps<D>;  // thread = query row here
   extern __shared__ uint8_t smem_raw[];
@@ -652,7 +703,21 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
   grouped_block(ng, bh, qt);
   const int n_tiles = (N + kTile - 1) / kTile;
   qt = n_tiles - 1 - qt;  // most causal work first (within a head group)
-  const int n_j = CAUSAL ? qt + 1 : n_tiles;
+  int n_j = CAUSAL ? qt + 1 : n_tiles;
+  int j0 = 0, n_keys = N;  // CROSS: this block's first key tile, the keys of its sequence
+  bool k_tail = false;     // CROSS: rows of K behind the sequence share its last tile
+  if constexpr (CROSS) {
+    j0 = static_cast<int>(blockIdx.z) * x.tiles;
+    n_keys = x.keys(bh);
+    const int end = (n_keys + kTile - 1) / kTile;
+    n_j = min(x.tiles, end - j0);
+    k_tail = n_keys < x.n_keys && n_keys % kTile != 0 && j0 + n_j == end;
+    if (x.part_stride) dq = static_cast<float*>(dq) + blockIdx.z * x.part_stride;
+    if (n_j <= 0) {  // no key in this range
+      zero_rows<D>(dq, static_cast<size_t>(bh) * N + qt * kTile, min(kTile, N - qt * kTile), grad_fp32);
+      return;
+    }
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(BAR(C::B_QD), 1);
@@ -664,6 +729,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
     for (int c = 0; c < W::CHUNKS; ++c) mbar_init(BAR(C::B_PF + c), W::EW * 32);
     mbar_init(BAR(C::B_DRAIN), 1);
     mbar_init(BAR(C::B_OW), W::EW * 32);  // bf16 gradients staged
+    if constexpr (CROSS) mbar_init(BAR(C::B_KC), 32);  // K's last tile cleared behind the sequence
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -677,6 +743,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
   if (warp == W::TMA) {
+    int issued = 0;
     if (lane == 0) {
       tma_prefetch_desc(&tq);
       tma_prefetch_desc(&tk);
@@ -687,18 +754,34 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
         tma_load_3d(sQ + h * kBox, &tq, BAR(C::B_QD), h * 64, qt * kTile, bh);
         tma_load_3d(sDO + h * kBox, &tdo, BAR(C::B_QD), h * 64, qt * kTile, bh);
       }
-      int issued = 0;
       for (int j = 0; j < n_j; ++j) {
         const int s = j % C::ST;
         if (j >= C::ST && !bwait(BAR(C::B_EMPTY + s), ((j / C::ST) - 1) & 1, abort_flag, budget)) break;
         mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * C::TB);
         const uint32_t st = sRing + s * C::STAGE;
         for (int h = 0; h < C::NH; ++h) {
-          tma_load_3d(st + h * kBox, &tk, BAR(C::B_FULL + s), h * 64, j * kTile, bh);
-          tma_load_3d(st + C::TB + h * kBox, &tv, BAR(C::B_FULL + s), h * 64, j * kTile, bh);
+          tma_load_3d(st + h * kBox, &tk, BAR(C::B_FULL + s), h * 64, (j0 + j) * kTile, bh);
+          tma_load_3d(st + C::TB + h * kBox, &tv, BAR(C::B_FULL + s), h * 64, (j0 + j) * kTile, bh);
         }
         issued = j + 1;
       }
+    }
+    if constexpr (CROSS) {
+      // dQ = dS K multiplies the last tile's K rows behind the sequence by dS = 0: clear what the
+      // caller's padding holds there (0 times an infinity or NaN).
+      issued = __shfl_sync(0xffffffffu, issued, 0);
+      if (k_tail && issued == n_j) {
+        const int last = n_j - 1;
+        if (bwait_all(BAR(C::B_FULL + last % C::ST), (last / C::ST) & 1, abort_flag, budget)) {
+          const uint32_t tile = sRing + (last % C::ST) * C::STAGE;
+          for (int i = (n_keys - (j0 + last) * kTile) * 8 + lane; i < kTile * 8; i += 32)
+            for (int h = 0; h < C::NH; ++h) sts128(tile + h * kBox + i * 16, 0, 0, 0, 0);
+          fence_proxy_async_smem();
+          mbar_arrive(BAR(C::B_KC));
+        }
+      }
+    }
+    if (lane == 0) {
       bdrain(BAR(C::B_QD), 0, budget);
       for (int j = max(0, issued - C::ST); j < issued; ++j) bdrain(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, budget);
     }
@@ -719,7 +802,11 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
         const uint32_t st = (j % C::ST) * C::STAGE;
         issue_product<D>(tmem + kColB, dDO, sdesc_add(dR, st + C::TB), idesc_p);  // dP = dO V^T
       };
-      bool ok = bwait(BAR(C::B_QD), 0, abort_flag, budget) && bwait(BAR(C::B_FULL), 0, abort_flag, budget);
+      auto full = [&](int j) {  // K_j, V_j loaded (and cleared behind the sequence)
+        return bwait(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, abort_flag, budget) &&
+               (!CROSS || !k_tail || j + 1 < n_j || bwait(BAR(C::B_KC), 0, abort_flag, budget));
+      };
+      bool ok = bwait(BAR(C::B_QD), 0, abort_flag, budget) && full(0);
       if (ok) {
         tc_fence_after();
         issue_s(0);
@@ -737,7 +824,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           issue_grad_part<D>(tmem + kColG1, tmem + kColB, sdesc_add(dRmn, (j % C::ST) * C::STAGE), idesc_g, j > 0,
                              0);
         if (j + 1 < n_j) {
-          if (!bwait(BAR(C::B_FULL + (j + 1) % C::ST), ((j + 1) / C::ST) & 1, abort_flag, budget)) break;
+          if (!full(j + 1)) break;
           tc_fence_after();
           issue_s(j + 1);
         }
@@ -772,7 +859,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
     const bool in = row < N;
     const float lse2 = in ? lse[static_cast<size_t>(bh) * N + row] * kLog2e : INFINITY;
     const float dd = in ? delta[static_cast<size_t>(bh) * N + row] : 0.f;
-    const int lim = CAUSAL ? min(row, N - 1) : N - 1;  // last key this row attends
+    const int lim = CAUSAL ? min(row, N - 1) : n_keys - 1;  // last key this row attends
     const uint64_t c2 = f2_pack(sl2, sl2), nl2 = f2_pack(-lse2, -lse2), nd2 = f2_pack(-dd, -dd);
     bool ok = true;
     for (int j = 0; ok && j < n_j; ++j) {
@@ -788,8 +875,8 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           tmem_ld_x32(tmem + lane_addr + ((j & 1) ? kColS1 : kColA) + 32 * c, sv);
           tmem_ld_x32(tB + 32 * c, pv);
           uint32_t dp[16];
-          const int key0 = j * kTile + 32 * c;
-          if (key0 + 31 > lim) ew_pairs_dq<true>(sv, pv, c2, nl2, nd2, key0, lim, dp);
+          const int key0 = (j0 + j) * kTile + 32 * c;
+          if (key0 + 31 > lim) ew_pairs_dq<true, CROSS>(sv, pv, c2, nl2, nd2, key0, lim, dp);
           else ew_pairs_dq<false>(sv, pv, c2, nl2, nd2, key0, lim, dp);
           tmem_st1_x16(tB + 16 * c, dp);
           tmem_wait_st();
@@ -803,9 +890,9 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           tmem_ld2_x32<64>(tmem + lane_addr + ((j & 1) ? kColS1 : kColA) + 32 * c, sv);
           tmem_ld2_x32<64>(tB + 32 * c, pv);
           uint32_t dp[16];
-          const int key0 = j * kTile + 64 * h + 32 * c;
+          const int key0 = (j0 + j) * kTile + 64 * h + 32 * c;
           // only the diagonal and the ragged last key tile reach past this row's last key
-          if (key0 + 31 > lim) ew_pairs_dq<true>(sv, pv, c2, nl2, nd2, key0, lim, dp);
+          if (key0 + 31 > lim) ew_pairs_dq<true, CROSS>(sv, pv, c2, nl2, nd2, key0, lim, dp);
           else ew_pairs_dq<false>(sv, pv, c2, nl2, nd2, key0, lim, dp);
           tmem_st2_x16<64>(tB + 16 * c, dp);  // dS packed into dP's columns 64h + 16c ..
           tmem_wait_st();
@@ -844,13 +931,18 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
   }
 }
 
-template <int D, bool CAUSAL>
-cudaError_t launch_bwd_t(const BwdLaunch& a, cudaStream_t stream) {
+template <int D>
+cudaError_t launch_delta(const BwdLaunch& a, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.BH) * a.N;
   const long long threads = rows * (D / 8);
   bwd_delta_kernel<D><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.dout), a.delta, rows);
-  cudaError_t e = cudaGetLastError();
+  return cudaGetLastError();
+}
+
+template <int D, bool CAUSAL>
+cudaError_t launch_bwd_t(const BwdLaunch& a, cudaStream_t stream) {
+  cudaError_t e = launch_delta<D>(a, stream);
   if (e != cudaSuccess) return e;
   const int n_tiles = (a.N + kTile - 1) / kTile;
   const int ng = head_groups(a.BH, n_tiles, CAUSAL, a.sms);
@@ -859,17 +951,81 @@ cudaError_t launch_bwd_t(const BwdLaunch& a, cudaStream_t stream) {
   if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::SMEM)) != cudaSuccess)
     return e;
   k1<<<grid, BwdWarps<D>::THREADS, DkdvCfg<D>::SMEM, stream>>>(a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, a.dk, a.dv, a.N,
-                                                   a.scale_log2, a.scale, a.grad_fp32, a.budget, a.tdk, a.tdv, ng);
+                                                   a.scale_log2, a.scale, a.grad_fp32, a.budget, a.tdk, a.tdv, ng,
+                                                   CrossArgs{});
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   auto k2 = bwd_dq_kernel<D, CAUSAL>;
   if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::SMEM)) != cudaSuccess)
     return e;
   k2<<<grid, BwdWarps<D>::THREADS, DqCfg<D>::SMEM, stream>>>(a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, a.dq, a.N, a.scale_log2,
-                                                 a.scale, a.grad_fp32, a.budget, a.tdq, ng);
+                                                 a.scale, a.grad_fp32, a.budget, a.tdq, ng, CrossArgs{});
   return cudaGetLastError();
 }
 
+// out = sum of S partial sums of n elements each, in their order; 4 elements a thread.
+__global__ void __launch_bounds__(256) bwd_sum_kernel(const float* __restrict__ part, void* __restrict__ out,
+                                                      long long n, int S, int fp32) {
+  const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  float4 acc = *reinterpret_cast<const float4*>(part + i);
+  for (int s = 1; s < S; ++s) {
+    const float4 y = *reinterpret_cast<const float4*>(part + s * n + i);
+    acc.x += y.x;
+    acc.y += y.y;
+    acc.z += y.z;
+    acc.w += y.w;
+  }
+  if (fp32)
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + i) = acc;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + i) =
+        make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+}
+
+cudaError_t launch_sum(const float* part, void* out, long long n, int S, int fp32, cudaStream_t stream) {
+  bwd_sum_kernel<<<static_cast<unsigned>((n / 4 + 255) / 256), 256, 0, stream>>>(part, out, n, S, fp32);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_cross_bwd_t(const BwdLaunch& a, cudaStream_t stream) {
+  cudaError_t e = launch_delta<D>(a, stream);
+  if (e != cudaSuccess) return e;
+  const long long kv_elems = static_cast<long long>(a.BH) * a.Nk * D, q_elems = static_cast<long long>(a.BH) * a.N * D;
+  const int k_tiles = (a.Nk + kTile - 1) / kTile, q_tiles = (a.N + kTile - 1) / kTile;
+  auto k1 = bwd_dkdv_kernel<D, false, true>;
+  if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::SMEM)) != cudaSuccess)
+    return e;
+  const bool kv_part = a.kv_splits > 1, q_part = a.q_splits > 1;
+  const dim3 g1(static_cast<unsigned>(a.BH), static_cast<unsigned>(k_tiles), static_cast<unsigned>(a.kv_splits));
+  float* dv_part = a.kv_part + a.kv_splits * kv_elems;
+  k1<<<g1, BwdWarps<D>::THREADS, DkdvCfg<D>::SMEM, stream>>>(
+      a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, kv_part ? a.kv_part : a.dk, kv_part ? dv_part : a.dv, a.N, a.scale_log2,
+      a.scale, kv_part || a.grad_fp32, a.budget, a.tdk, a.tdv, head_groups(a.BH, k_tiles, false, a.sms),
+      CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.q_tiles, kv_part ? kv_elems : 0});
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (kv_part) {
+    if ((e = launch_sum(a.kv_part, a.dk, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess) return e;
+    if ((e = launch_sum(dv_part, a.dv, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess) return e;
+  }
+  auto k2 = bwd_dq_kernel<D, false, true>;
+  if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::SMEM)) != cudaSuccess)
+    return e;
+  const dim3 g2(static_cast<unsigned>(a.BH), static_cast<unsigned>(q_tiles), static_cast<unsigned>(a.q_splits));
+  k2<<<g2, BwdWarps<D>::THREADS, DqCfg<D>::SMEM, stream>>>(
+      a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, q_part ? a.q_part : a.dq, a.N, a.scale_log2, a.scale,
+      q_part || a.grad_fp32, a.budget, a.tdq, head_groups(a.BH, q_tiles, false, a.sms),
+      CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.k_tiles, q_part ? q_elems : 0});
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (q_part) return launch_sum(a.q_part, a.dq, q_elems, a.q_splits, a.grad_fp32, stream);
+  return cudaSuccess;
+}
+
 }  // namespace
+
+cudaError_t launch_cross_bwd(const BwdLaunch& a, cudaStream_t stream) {
+  return a.d == 64 ? launch_cross_bwd_t<64>(a, stream) : launch_cross_bwd_t<128>(a, stream);
+}
 
 cudaError_t launch_bwd(const BwdLaunch& a, cudaStream_t stream) {
   if (a.d == 64) return a.causal ? launch_bwd_t<64, true>(a, stream) : launch_bwd_t<64, false>(a, stream);

@@ -92,7 +92,7 @@ struct FwdCfg {
   static constexpr uint32_t KVB = NH * kBox;        // bytes of one K (or V) tile
   static constexpr int B_Q = 0, B_QE = B_Q + 1, B_KF = B_QE + 1, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST,
                        B_SF = B_VE + VST, B_PF = B_SF + 2, B_SC = B_PF + 2, B_OF = B_SC + 2, B_DRAIN = B_OF + 2,
-                       B_OSF = B_DRAIN + 2, B_OW = B_OSF + 2, NBAR = B_OW + 2;
+                       B_OSF = B_DRAIN + 2, B_OW = B_OSF + 2, B_VC = B_OW + 2, NBAR = B_VC + 1;
   // d = 64 leaves 128 TMEM columns free: P~_t gets its own columns there, so S_t(j+1) can be
   // computed while the softmax of tile j still runs ("separate P~").  At d = 128 P~ aliases S,
   // for bf16 (two keys a column) and E4M3 (four keys a column) alike.
@@ -404,7 +404,9 @@ __device__ __forceinline__ void store_lse(float* lse, size_t row_off, int h, boo
   if (h == 0 && valid) lse[row_off] = (l > 0.f) ? (m2 + log2f(l)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool CAUSAL, bool FP8>
+// CROSS (fa_cross_fwd): the rows are those of all the query heads that share key head bh, the keys
+// the first kv_lens[bh / kv_heads] of Nk, and blockIdx.z one of aux.S ranges of kchunk keys.
+template <int D, bool CAUSAL, bool FP8, bool CROSS = false>
 __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                const __grid_constant__ CUtensorMap tv, void* __restrict__ o, float* __restrict__ lse, int N,
@@ -414,7 +416,10 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
   const float* __restrict__ sq = aux.sq;
   const float* __restrict__ sk = aux.sk;
   const float* __restrict__ sv = aux.sv;
-  const int Nk = aux.Nk, koff = aux.koff;  // this launch's keys: global indices koff .. koff + Nk - 1
+  static_assert(!CROSS || (!CAUSAL && !FP8), "cross attention is not causal, and bf16");
+  int Nk = aux.Nk;                // this launch's (CROSS: this CTA's) keys
+  const int koff = aux.koff;      // global index of key 0
+  int kload0 = aux.kload0;        // its row in the k, v tensors
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -433,6 +438,18 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
   int bh, pair;
   grouped_block(aux.ng, bh, pair);
   pair = static_cast<int>(gridDim.y) - 1 - pair;
+  const int shard = CROSS ? static_cast<int>(blockIdx.z) : aux.shard;  // partial slot
+  bool v_tail = false;  // CROSS: rows of V behind the sequence share its last tile
+  if constexpr (CROSS) {
+    int len = Nk;
+    if (aux.kv_lens) {  // (written, perhaps, by the previous kernel in the stream)
+      grid_dep_wait();
+      len = min(max(aux.kv_lens[bh / aux.kv_heads], 0), Nk);
+    }
+    kload0 = shard * aux.kchunk;
+    v_tail = len < Nk && len - kload0 <= aux.kchunk && len % kBc != 0;
+    Nk = min(max(len - kload0, 0), aux.kchunk);
+  }
   const int n_tiles = (Nk + kBc - 1) / kBc;
   // KV steps of each query tile: all key tiles, or (causal) those holding a key at or before
   // its last row; 0 if the tile is past N.
@@ -452,11 +469,20 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
     for (int i = threadIdx.x; i < kRowsPerCta; i += blockDim.x) {
       const int row = pair * kRowsPerCta + i;
       if (row < N) {
-        const size_t slot = (static_cast<size_t>(bh) * N + row) * aux.S + aux.shard;
+        const size_t slot = (static_cast<size_t>(bh) * N + row) * aux.S + shard;
         aux.m_part[slot] = -INFINITY;
         aux.l_part[slot] = 0.f;
       }
     }
+    return;
+  }
+  if (CROSS && n_max == 0) {  // a sequence without keys: O = 0, lse = -inf
+    const int rows = min(kRowsPerCta, N - pair * kRowsPerCta);
+    const size_t row0 = static_cast<size_t>(bh) * N + pair * kRowsPerCta;
+    const int vecs = rows * D * (o_fp32 ? 4 : 2) / 16;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(o) + row0 * D * (o_fp32 ? 4 : 2));
+    for (int i = threadIdx.x; i < vecs; i += blockDim.x) dst[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < rows; i += blockDim.x) lse[row0 + i] = -INFINITY;
     return;
   }
 
@@ -482,6 +508,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
     mbar_init(BAR(C::B_DRAIN + 1), 1);
     mbar_init(BAR(C::B_OW), C::SMW * 32);  // O of tile t staged (bf16 O)
     mbar_init(BAR(C::B_OW + 1), C::SMW * 32);
+    if constexpr (CROSS) mbar_init(BAR(C::B_VC), 32);  // V's last tile cleared behind the sequence
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -508,6 +535,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
 
   if (warp == C::WARP_TMA) {
     // ------------------------------------------------------------ producer
+    int k_issued = 0, v_issued = 0;
     if (lane == 0) {
       tma_prefetch_desc(&tq);
       tma_prefetch_desc(&tk);
@@ -516,7 +544,6 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
       for (int t = 0; t < 2; ++t)
         for (int h = 0; h < C::NH; ++h)
           tma_load_3d(sQ + t * C::QB + h * kBox, &tq, BAR(C::B_Q), h * C::BOX_X, pair * kRowsPerCta + t * kBr, bh);
-      int k_issued = 0, v_issued = 0;
       for (int j = 0; j < n_max; ++j) {
         const int ks = j % C::KST;
         if (j >= C::KST &&
@@ -524,7 +551,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
           break;
         mbar_arrive_expect_tx(BAR(C::B_KF + ks), C::KVB);
         for (int h = 0; h < C::NH; ++h)
-          tma_load_3d(sK + ks * C::KVB + h * kBox, &tk, BAR(C::B_KF + ks), h * C::BOX_X, aux.kload0 + j * kBc, bh);
+          tma_load_3d(sK + ks * C::KVB + h * kBox, &tk, BAR(C::B_KF + ks), h * C::BOX_X, kload0 + j * kBc, bh);
         k_issued = j + 1;
         const int vs = j % C::VST;
         if (j >= C::VST &&
@@ -532,9 +559,27 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
           break;
         mbar_arrive_expect_tx(BAR(C::B_VF + vs), C::KVB);
         for (int h = 0; h < C::NH; ++h)
-          tma_load_3d(sV + vs * C::KVB + h * kBox, &tv, BAR(C::B_VF + vs), h * C::BOX_X, aux.kload0 + j * kBc, bh);
+          tma_load_3d(sV + vs * C::KVB + h * kBox, &tv, BAR(C::B_VF + vs), h * C::BOX_X, kload0 + j * kBc, bh);
         v_issued = j + 1;
       }
+    }
+    if constexpr (CROSS) {
+      // The last tile's V rows behind the sequence hold whatever the caller's padding does, and
+      // their P~ = 0 times an infinity or NaN there would reach U: clear them.  (K's need nothing:
+      // their scores are replaced by -inf.)
+      v_issued = __shfl_sync(0xffffffffu, v_issued, 0);
+      if (v_tail && v_issued == n_max) {
+        const int last = n_max - 1;
+        if (wait_all(BAR(C::B_VF + last % C::VST), (last / C::VST) & 1, abort_flag, budget)) {
+          const uint32_t tile = sV + (last % C::VST) * C::KVB;
+          for (int i = (Nk - last * kBc) * 8 + lane; i < kBc * 8; i += 32)
+            for (int h = 0; h < C::NH; ++h) sts128(tile + h * kBox + i * 16, 0, 0, 0, 0);
+          fence_proxy_async_smem();
+          mbar_arrive(BAR(C::B_VC));
+        }
+      }
+    }
+    if (lane == 0) {
       // Every copy this CTA started must land before its shared memory is released.
       drain_wait(BAR(C::B_Q), 0, budget);
       for (int j = max(0, k_issued - C::KST); j < k_issued; ++j)
@@ -599,6 +644,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
             tc_commit(BAR(C::B_KE + (j + 1) % C::KST));
           }
           ok = wait(BAR(C::B_PF + t), j & 1) && wait(BAR(C::B_VF + j % C::VST), (j / C::VST) & 1);
+          if (CROSS && ok && v_tail && j == n - 1) ok = wait(BAR(C::B_VC), 0);
           if (!ok) break;
           tc_fence_after();
           issue_pv(j);
@@ -692,6 +738,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
         // issue back to back: a wait between them lets the tensor pipe drain.
         ok = mbar_wait(BAR(C::B_VF + (j - 1) % C::VST), ((j - 1) / C::VST) & 1, abort_flag, budget,
                        &g_fwd_status) &&
+             (!CROSS || !v_tail || j < n_max || mbar_wait(BAR(C::B_VC), 0, abort_flag, budget, &g_fwd_status)) &&
              (j >= n_max ||
               mbar_wait(BAR(C::B_KF + j % C::KST), (j / C::KST) & 1, abort_flag, budget, &g_fwd_status));
         if (!ok) break;
@@ -839,9 +886,9 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
       const float l_row = C::ONE ? l : l + __shfl_xor_sync(0xffffffffu, l, 16);
       if (aux.u_part) {
         if constexpr (C::ONE)
-          store_full_partial(aux, (static_cast<size_t>(bh) * N + row) * aux.S + aux.shard, row < N, t_o, l_row, m2);
+          store_full_partial(aux, (static_cast<size_t>(bh) * N + row) * aux.S + shard, row < N, t_o, l_row, m2);
         else
-          store_half_partial<D>(aux, (static_cast<size_t>(bh) * N + row) * aux.S + aux.shard, h, row < N, t_o, l_row,
+          store_half_partial<D>(aux, (static_cast<size_t>(bh) * N + row) * aux.S + shard, h, row < N, t_o, l_row,
                                 m2, true);
       } else if (!o_fp32) {
         // bf16 O through shared memory, in buffers this tile no longer reads: Q_t (its S MMAs are
@@ -872,7 +919,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
       }
     } else if (aux.u_part && n == 0) {
       // no key of this shard is admissible for the tile: an empty partial, U never touched
-      store_half_partial<D>(aux, (static_cast<size_t>(bh) * N + row) * aux.S + aux.shard, h, row < N, t_o, 0.f,
+      store_half_partial<D>(aux, (static_cast<size_t>(bh) * N + row) * aux.S + shard, h, row < N, t_o, 0.f,
                             -INFINITY, false);
     }
     tmem_wait_st();
@@ -1285,6 +1332,18 @@ cudaError_t launch_kernel(Kern kern, dim3 grid, int threads, uint32_t smem, cuda
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Cross attention: one CTA per block of 256 rows of a key head and range of kchunk keys.
+template <int D>
+cudaError_t launch_cross_t(const FwdLaunch& a, cudaStream_t stream) {
+  using C = FwdCfg<D>;
+  const int n_pairs = (a.N + kRowsPerCta - 1) / kRowsPerCta;
+  FwdAux aux = a.aux;
+  aux.ng = head_groups(a.BH, n_pairs, false, a.sms);
+  const dim3 grid(static_cast<unsigned>(a.BH), static_cast<unsigned>(n_pairs), static_cast<unsigned>(aux.S));
+  return launch_kernel(fwd_kernel<D, false, false, true>, grid, C::THREADS, C::SMEM, stream, a.tq, a.tk, a.tv, a.o,
+                       a.lse, a.N, a.scale_log2, a.o_fp32, a.budget, aux, a.to);
+}
+
 template <int D, bool CAUSAL, bool FP8 = false>
 cudaError_t launch_t(const FwdLaunch& a, cudaStream_t stream) {
   using C = FwdCfg<D, FP8>;
@@ -1314,6 +1373,7 @@ cudaError_t launch_t(const FwdLaunch& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_fwd(const FwdLaunch& a, cudaStream_t stream) {
+  if (a.cross) return a.d == 64 ? launch_cross_t<64>(a, stream) : launch_cross_t<128>(a, stream);
   if (a.fp8) return a.causal ? launch_t<128, true, true>(a, stream) : launch_t<128, false, true>(a, stream);
   if (a.d == 64) return a.causal ? launch_t<64, true>(a, stream) : launch_t<64, false>(a, stream);
   return a.causal ? launch_t<128, true>(a, stream) : launch_t<128, false>(a, stream);

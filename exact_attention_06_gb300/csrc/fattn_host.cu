@@ -243,6 +243,108 @@ fa_status_t check_paged_args(int B, int H, int d, int page_size, int max_pages, 
   return FA_OK;
 }
 
+// Cross attention.  The G = Hq / Hkv query heads of a key head are adjacent in q, so their rows are
+// G * Nq rows of one [B * Hkv, G * Nq, d] tensor against the key head's [Nk, d]: shared heads need
+// nothing more, and dK, dV sum over the group by themselves.
+struct CrossShape {
+  long long bh = 0;  // B * Hkv
+  int rows = 0;      // G * Nq
+};
+
+fa_status_t check_cross_args(int B, int Hq, int Hkv, int Nq, int Nk, int d, CrossShape* c) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Nk < 1)
+    return fail(FA_ERR_INVALID_ARG, "B, Hq, Hkv, Nq and Nk must be >= 1 (got %d, %d, %d, %d, %d)", B, Hq, Hkv, Nq, Nk);
+  if (Hq % Hkv != 0) return fail(FA_ERR_INVALID_ARG, "Hq=%d must be a multiple of Hkv=%d", Hq, Hkv);
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dimension d=%d is not supported (64 or 128)", d);
+  c->bh = static_cast<long long>(B) * Hkv;
+  const long long rows = static_cast<long long>(Hq / Hkv) * Nq;
+  if (c->bh > INT_MAX) return fail(FA_ERR_UNSUPPORTED, "B*Hkv=%lld exceeds the grid limit", c->bh);
+  if ((rows + 127) / 128 > 65535)
+    return fail(FA_ERR_UNSUPPORTED, "Hq/Hkv*Nq=%lld exceeds the 65535 query-tile grid limit", rows);
+  if ((static_cast<long long>(Nk) + 127) / 128 > 65535)
+    return fail(FA_ERR_UNSUPPORTED, "Nk=%d exceeds the 65535 key-tile grid limit", Nk);
+  c->rows = static_cast<int>(rows);
+  return FA_OK;
+}
+
+// How often to cut a scan of `tiles` tiles when `units` blocks (one per SM at a time) each make it:
+// more, shorter blocks fill the last round of SMs, at the price of fp32 partial results and a
+// kernel that joins them.  Costs in tile steps (about 1 us): a block costs its tiles plus ~3 of
+// set-up and epilogue, joining ~3 and its traffic, 8 MB a step.  A cut has to save 5 %.
+int cut_scan(long long units, int tiles, int sms, double part_bytes) {
+  constexpr double kFixed = 3.0, kJoin = 3.0, kStepBytes = 8e6;
+  auto rounds = [&](int s) { return static_cast<double>((units * s + sms - 1) / sms); };
+  const double whole = rounds(1) * (tiles + kFixed);
+  double best_t = 0.95 * whole;
+  int best = 1;
+  for (int s = 2; s <= tiles && s <= 256; ++s) {
+    const int each = (tiles + s - 1) / s;
+    if ((tiles + each - 1) / each != s) continue;  // would leave a block without tiles
+    const double t = rounds(s) * (each + kFixed) + kJoin + 2.0 * s * part_bytes / kStepBytes;
+    if (t < best_t) {
+      best_t = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+struct CrossPlan {
+  int splits = 1, kchunk = 0;
+  size_t u_bytes = 0, m_bytes = 0;
+  size_t total() const { return splits > 1 ? u_bytes + 2 * m_bytes : 0; }
+};
+
+CrossPlan plan_cross(const CrossShape& c, int Nk, int d, int sms) {
+  CrossPlan p;
+  const int tiles = (Nk + 127) / 128;
+  const long long rows = c.bh * c.rows;
+  if (rows <= INT_MAX)  // (the combine kernel's row count)
+    p.splits = cut_scan(c.bh * ((c.rows + 255) / 256), tiles, sms, static_cast<double>(rows) * (d + 2) * 4);
+  p.kchunk = (tiles + p.splits - 1) / p.splits * 128;
+  p.u_bytes = round256(static_cast<size_t>(rows) * p.splits * d * sizeof(float));
+  p.m_bytes = round256(static_cast<size_t>(rows) * p.splits * sizeof(float));
+  return p;
+}
+
+struct CrossBwdPlan {
+  int kv_splits = 1, q_tiles = 0;  // dK, dV: ranges of query tiles
+  int q_splits = 1, k_tiles = 0;   // dQ: ranges of key tiles
+  size_t delta_bytes = 0, kv_bytes = 0, q_bytes = 0;
+  size_t total() const { return delta_bytes + kv_bytes + q_bytes; }
+};
+
+CrossBwdPlan plan_cross_bwd(const CrossShape& c, int Nk, int d, int sms) {
+  CrossBwdPlan p;
+  const int qt = (c.rows + 127) / 128, kt = (Nk + 127) / 128;
+  const double kv = 2.0 * c.bh * Nk * d * sizeof(float), q = 1.0 * c.bh * c.rows * d * sizeof(float);
+  p.kv_splits = cut_scan(c.bh * kt, qt, sms, kv);
+  p.q_splits = cut_scan(c.bh * qt, kt, sms, q);
+  p.q_tiles = (qt + p.kv_splits - 1) / p.kv_splits;
+  p.k_tiles = (kt + p.q_splits - 1) / p.q_splits;
+  p.delta_bytes = round256(static_cast<size_t>(c.bh) * c.rows * sizeof(float));
+  if (p.kv_splits > 1) p.kv_bytes = round256(2ull * c.bh * Nk * d * sizeof(float) * p.kv_splits);
+  if (p.q_splits > 1) p.q_bytes = round256(1ull * c.bh * c.rows * d * sizeof(float) * p.q_splits);
+  return p;
+}
+
+fa_status_t check_rope_args(const fa_rope_axes_plan_t* plan, const int* pos, int B, int Hq, int Hk, int N, int inverse) {
+  if (!plan || !pos) return fail(FA_ERR_INVALID_ARG, "null plan or pos");
+  if ((plan->d != 64 && plan->d != 128) || plan->n_axes < 1 || plan->n_axes > FA_ROPE_MAX_AXES)
+    return fail(FA_ERR_INVALID_ARG, "plan was not made by fa_rope_axes_plan");
+  for (int i = 0; i < plan->d / 2; ++i)
+    if (plan->axis[i] >= plan->n_axes) return fail(FA_ERR_INVALID_ARG, "plan was not made by fa_rope_axes_plan");
+  if (B < 1 || Hq < 1 || Hk < 0 || N < 1)
+    return fail(FA_ERR_INVALID_ARG, "B, Hq and N must be >= 1, Hk >= 0 (got %d, %d, %d, %d)", B, Hq, N, Hk);
+  if (inverse != 0 && inverse != 1) return fail(FA_ERR_INVALID_ARG, "inverse must be 0 or 1");
+  if (!aligned(pos, 4)) return fail(FA_ERR_INVALID_ARG, "pos must be 4-byte aligned");
+  if (static_cast<long long>(Hq) + 2LL * Hk > 65535)
+    return fail(FA_ERR_UNSUPPORTED, "Hq=%d and Hk=%d exceed the 65535 head grid limit", Hq, Hk);
+  if (static_cast<long long>(B) * N > INT_MAX)
+    return fail(FA_ERR_UNSUPPORTED, "B*N=%lld exceeds the row limit", static_cast<long long>(B) * N);
+  return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -764,6 +866,258 @@ fa_status_t fa_bwd_ex(const void* q, const void* k, const void* v, const void* o
   cudaGetLastError();
   cudaError_t e = fattn::launch_bwd(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fa_bwd launch");
+  return FA_OK;
+}
+
+size_t fa_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
+  const int saved = g_last_error[0];
+  CrossShape c;
+  int sms = 0;
+  fa_status_t st = check_cross_args(B, Hq, Hkv, Nq, Nk, d, &c);
+  if (st == FA_OK) st = check_device(&sms);
+  if (!saved) g_last_error[0] = '\0';
+  return st == FA_OK ? plan_cross(c, Nk, d, sms).total() : 0;
+}
+
+fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int* kv_lens, void* o, float* lse, int B,
+                         int Hq, int Hkv, int Nq, int Nk, int d, float scale, void* workspace, size_t ws_bytes,
+                         void* stream, const fa_cross_opts* opts) {
+  g_last_error[0] = '\0';
+  if (!q || !k || !v || !o || !lse) return fail(FA_ERR_INVALID_ARG, "null tensor pointer");
+  const int o_fp32 = opts ? opts->o_fp32 : 0;
+  if (o_fp32 != 0 && o_fp32 != 1) return fail(FA_ERR_INVALID_ARG, "opts->o_fp32 must be 0 or 1");
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16))
+    return fail(FA_ERR_INVALID_ARG, "q, k, v and o must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(kv_lens, 4)) return fail(FA_ERR_INVALID_ARG, "lse and kv_lens must be 4-byte aligned");
+  if (workspace && !aligned(workspace, 256)) return fail(FA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  CrossShape c;
+  fa_status_t st = check_cross_args(B, Hq, Hkv, Nq, Nk, d, &c);
+  if (st != FA_OK) return st;
+  int sms = 0;
+  if ((st = check_device(&sms)) != FA_OK) return st;
+  CrossPlan plan = plan_cross(c, Nk, d, sms);
+  if (!workspace) {  // one launch, the keys uncut
+    plan.splits = 1;
+    plan.kchunk = (Nk + 127) / 128 * 128;
+  } else if (ws_bytes < plan.total()) {
+    return fail(FA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes fa_cross_workspace_bytes gives",
+                ws_bytes, plan.total());
+  }
+  fattn::FwdLaunch a{};
+  if ((st = make_map(&a.tq, q, d, c.rows, c.bh, 128)) != FA_OK) return st;
+  if ((st = make_map(&a.tk, k, d, Nk, c.bh, 128)) != FA_OK) return st;
+  if ((st = make_map(&a.tv, v, d, Nk, c.bh, 128)) != FA_OK) return st;
+  if (!o_fp32 && (st = make_map(&a.to, o, d, c.rows, c.bh, 128)) != FA_OK) return st;
+  a.o = o;
+  a.lse = lse;
+  a.N = c.rows;
+  a.BH = static_cast<int>(c.bh);
+  a.d = d;
+  a.o_fp32 = o_fp32;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.budget = (opts && opts->wait_budget_cycles) ? opts->wait_budget_cycles : kDefaultBudget;
+  a.sms = sms;
+  a.cross = 1;
+  a.aux.Nk = Nk;
+  a.aux.kv_lens = kv_lens;
+  a.aux.kv_heads = Hkv;
+  a.aux.kchunk = plan.kchunk;
+  a.aux.S = plan.splits;
+  if (plan.splits > 1) {
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    a.aux.u_part = reinterpret_cast<float*>(w);
+    a.aux.m_part = reinterpret_cast<float*>(w + plan.u_bytes);
+    a.aux.l_part = reinterpret_cast<float*>(w + plan.u_bytes + plan.m_bytes);
+  }
+  cudaGetLastError();
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = fattn::launch_fwd(a, s);
+  if (e != cudaSuccess) return cuda_fail(e, "fa_cross_fwd launch");
+  if (plan.splits > 1) {
+    e = fattn::launch_combine(a.aux.u_part, a.aux.m_part, a.aux.l_part, o, lse, static_cast<int>(c.bh * c.rows),
+                              plan.splits, d, o_fp32, s);
+    if (e != cudaSuccess) return cuda_fail(e, "fa_cross_fwd combine launch");
+  }
+  return FA_OK;
+}
+
+size_t fa_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
+  const int saved = g_last_error[0];
+  CrossShape c;
+  int sms = 0;
+  fa_status_t st = check_cross_args(B, Hq, Hkv, Nq, Nk, d, &c);
+  if (st == FA_OK) st = check_device(&sms);
+  if (!saved) g_last_error[0] = '\0';
+  return st == FA_OK ? plan_cross_bwd(c, Nk, d, sms).total() : 0;
+}
+
+fa_status_t fa_cross_bwd(const void* q, const void* k, const void* v, const int* kv_lens, const void* o,
+                         const void* dout, const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
+                         int Nq, int Nk, int d, float scale, int grad_fp32, void* workspace, size_t ws_bytes,
+                         void* stream, const fa_bwd_opts* opts) {
+  g_last_error[0] = '\0';
+  if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv) return fail(FA_ERR_INVALID_ARG, "null tensor pointer");
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (grad_fp32 != 0 && grad_fp32 != 1) return fail(FA_ERR_INVALID_ARG, "grad_fp32 must be 0 or 1");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(dout, 16) ||
+      !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16))
+    return fail(FA_ERR_INVALID_ARG, "q, k, v, o, dout, dq, dk and dv must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(kv_lens, 4)) return fail(FA_ERR_INVALID_ARG, "lse and kv_lens must be 4-byte aligned");
+  CrossShape c;
+  fa_status_t st = check_cross_args(B, Hq, Hkv, Nq, Nk, d, &c);
+  if (st != FA_OK) return st;
+  if (!workspace) return fail(FA_ERR_WORKSPACE, "fa_cross_bwd needs a workspace (fa_cross_bwd_workspace_bytes)");
+  if (!aligned(workspace, 256)) return fail(FA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  int sms = 0;
+  if ((st = check_device(&sms)) != FA_OK) return st;
+  const CrossBwdPlan plan = plan_cross_bwd(c, Nk, d, sms);
+  if (ws_bytes < plan.total())
+    return fail(FA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes, plan.total());
+  fattn::BwdLaunch a{};
+  a.sms = sms;
+  if ((st = make_map(&a.tq, q, d, c.rows, c.bh, 128)) != FA_OK) return st;
+  if ((st = make_map(&a.tk, k, d, Nk, c.bh, 128)) != FA_OK) return st;
+  if ((st = make_map(&a.tv, v, d, Nk, c.bh, 128)) != FA_OK) return st;
+  if ((st = make_map(&a.tdo, dout, d, c.rows, c.bh, 128)) != FA_OK) return st;
+  if (!grad_fp32) {
+    if ((st = make_map(&a.tdq, dq, d, c.rows, c.bh, 128)) != FA_OK) return st;
+    if ((st = make_map(&a.tdk, dk, d, Nk, c.bh, 128)) != FA_OK) return st;
+    if ((st = make_map(&a.tdv, dv, d, Nk, c.bh, 128)) != FA_OK) return st;
+  }
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.o = o;
+  a.dout = dout;
+  a.lse = lse;
+  a.delta = reinterpret_cast<float*>(w);
+  a.kv_part = reinterpret_cast<float*>(w + plan.delta_bytes);
+  a.q_part = reinterpret_cast<float*>(w + plan.delta_bytes + plan.kv_bytes);
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.N = c.rows;
+  a.BH = static_cast<int>(c.bh);
+  a.d = d;
+  a.grad_fp32 = grad_fp32;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.budget = (opts && opts->wait_budget_cycles) ? opts->wait_budget_cycles : kDefaultBudget;
+  a.cross = 1;
+  a.Nk = Nk;
+  a.kv_lens = kv_lens;
+  a.kv_heads = Hkv;
+  a.q_tiles = plan.q_tiles;
+  a.kv_splits = plan.kv_splits;
+  a.k_tiles = plan.k_tiles;
+  a.q_splits = plan.q_splits;
+  cudaGetLastError();
+  cudaError_t e = fattn::launch_cross_bwd(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_cross_bwd launch");
+  return FA_OK;
+}
+
+fa_status_t fa_rope_axes_plan(fa_rope_axes_plan_t* plan, int d, int n_axes, const int* sections, double base,
+                              int interleaved, int per_axis, int cyclic) {
+  g_last_error[0] = '\0';
+  if (!plan || !sections) return fail(FA_ERR_INVALID_ARG, "null plan or sections");
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dimension d=%d is not supported (64 or 128)", d);
+  if (n_axes < 1 || n_axes > FA_ROPE_MAX_AXES)
+    return fail(FA_ERR_INVALID_ARG, "n_axes=%d must be in [1, %d]", n_axes, FA_ROPE_MAX_AXES);
+  if (!std::isfinite(base) || !(base >= 1.0)) return fail(FA_ERR_INVALID_ARG, "base must be finite and >= 1");
+  if ((interleaved | per_axis | cyclic) & ~1)
+    return fail(FA_ERR_INVALID_ARG, "interleaved, per_axis and cyclic must be 0 or 1");
+  long long sum = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (sections[a] < 1) return fail(FA_ERR_INVALID_ARG, "sections[%d]=%d must be >= 1", a, sections[a]);
+    sum += sections[a];
+  }
+  const int n = d / 2;
+  if (sum != n) return fail(FA_ERR_INVALID_ARG, "sections sum to %lld pairs, expected d/2 = %d", sum, n);
+  *plan = fa_rope_axes_plan_t{};
+  plan->d = d;
+  plan->n_axes = n_axes;
+  plan->interleaved = interleaved;
+  int used[FA_ROPE_MAX_AXES] = {};
+  for (int i = 0, a = 0; i < n; ++i) {
+    while (used[a] == sections[a]) a = (a + 1) % n_axes;  // (pairs are left, so some axis has one)
+    plan->axis[i] = static_cast<unsigned char>(a);
+    const double exponent = per_axis ? static_cast<double>(used[a]) / sections[a] : static_cast<double>(i) / n;
+    ++used[a];
+    // rate / (2 pi) <= 0.16 turns a position, to the nearest 2^-64 turn
+    const double turns = std::pow(base, -exponent) * 0.15915494309189533577;
+    plan->turns[i] = static_cast<unsigned long long>(std::rint(std::ldexp(turns, 64)));
+    if (cyclic) a = (a + 1) % n_axes;
+  }
+  return FA_OK;
+}
+
+fa_status_t fa_rope_axes(const void* q, const void* k, const int* pos, void* q_out, void* k_out, int B, int Hq, int Hk,
+                         int N, const fa_rope_axes_plan_t* plan, int inverse, void* stream) {
+  g_last_error[0] = '\0';
+  if (!q || !q_out) return fail(FA_ERR_INVALID_ARG, "null tensor pointer");
+  fa_status_t st = check_rope_args(plan, pos, B, Hq, Hk, N, inverse);
+  if (st != FA_OK) return st;
+  if (Hk > 0 && (!k || !k_out)) return fail(FA_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned(q, 16) || !aligned(q_out, 16) || (Hk > 0 && (!aligned(k, 16) || !aligned(k_out, 16))))
+    return fail(FA_ERR_INVALID_ARG, "q, k, q_out and k_out must be 16-byte aligned");
+  fattn::RopeLaunch a{};
+  if ((st = check_device(&a.sms)) != FA_OK) return st;
+  a.plan = *plan;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.pos = pos;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.N = N;
+  a.sign = inverse ? -1.f : 1.f;
+  cudaGetLastError();
+  cudaError_t e = fattn::launch_rope(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_rope_axes launch");
+  return FA_OK;
+}
+
+fa_status_t fa_rope_axes_paged(const void* q, const void* k, const void* v, const int* pos, void* q_out, void* k_pages,
+                               void* v_pages, const int* block_table, const int* seq_lens, const int* new_lens, int B,
+                               int Hq, int Hk, int N, int page_size, int max_pages, int num_pages,
+                               const fa_rope_axes_plan_t* plan, void* stream) {
+  g_last_error[0] = '\0';
+  if (!q || !k || !v || !q_out || !k_pages || !v_pages || !block_table || !seq_lens)
+    return fail(FA_ERR_INVALID_ARG, "null tensor pointer");
+  fa_status_t st = check_rope_args(plan, pos, B, Hq, Hk, N, 0);
+  if (st != FA_OK) return st;
+  if ((st = check_paged_args(B, Hk, plan->d, page_size, max_pages, num_pages, 1)) != FA_OK) return st;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_pages, 16) ||
+      !aligned(v_pages, 16))
+    return fail(FA_ERR_INVALID_ARG, "q, k, v, q_out, k_pages and v_pages must be 16-byte aligned");
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(new_lens, 4))
+    return fail(FA_ERR_INVALID_ARG, "block_table, seq_lens and new_lens must be 4-byte aligned");
+  fattn::RopeLaunch a{};
+  if ((st = check_device(&a.sms)) != FA_OK) return st;
+  a.plan = *plan;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_out = static_cast<__nv_bfloat16*>(k_pages);
+  a.v_out = static_cast<__nv_bfloat16*>(v_pages);
+  a.pos = pos;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.N = N;
+  a.sign = 1.f;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  cudaGetLastError();
+  cudaError_t e = fattn::launch_rope(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_rope_axes_paged launch");
   return FA_OK;
 }
 

@@ -2,9 +2,12 @@
 // units.  Not installed; callers use include/fattn.h.
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
+
+#include "fattn.h"
 
 namespace fattn {
 
@@ -44,6 +47,12 @@ struct FwdAux {
   int qsplit;
   // Persistent CTAs (non-causal bf16 d = 64): the number of work items; set by launch_fwd.
   int n_items;
+  // Cross attention (fa_cross_fwd): rows of a key head are its query heads' rows, one after
+  // another; Nk above is the tensors' key count, the sequence of key head bh has kv_lens[bh /
+  // kv_heads] of them (null: all).  blockIdx.z takes the keys z * kchunk .. + kchunk - 1 and, with
+  // u_part, partial slot z of S.
+  const int* kv_lens;
+  int kv_heads;
   // One-block-per-CTA kernel: the heads are dispatched in ng groups (each group's blocks
   // longest first) so that the blocks of a head run close together in time; set by launch_fwd.
   int ng;
@@ -76,6 +85,7 @@ struct FwdLaunch {
   unsigned long long budget;
   int fp8;            // 1: q, k, v are E4M3 with per-128-row block scales in aux (d = 128)
   int sms;            // SMs of the device: the persistent grid size (0: one CTA per work item)
+  int cross;          // 1: cross attention (aux.kv_lens, aux.kv_heads, aux.kchunk, aux.S splits)
   FwdAux aux;
 };
 cudaError_t launch_fwd(const FwdLaunch& a, cudaStream_t stream);
@@ -132,12 +142,49 @@ struct BwdLaunch {
   float scale_log2;
   unsigned long long budget;
   int sms;  // SMs of the device (block order of the dK/dV and dQ kernels)
+  // Cross attention (fa_cross_bwd): N query rows (of all the query heads of a key head) against
+  // Nk keys, kv_lens[bh / kv_heads] of them real (null: all).  The dK/dV kernel's blocks take
+  // q_tiles query tiles each (kv_splits blocks per key tile), the dQ kernel's k_tiles key tiles
+  // (q_splits blocks per query tile); with more than one, they leave fp32 partial sums
+  // [splits][rows, d] in kv_part (dK's, then dV's) and q_part, which a last kernel adds up.
+  int cross;
+  int Nk;
+  const int* kv_lens;
+  int kv_heads;
+  int q_tiles, kv_splits;
+  int k_tiles, q_splits;
+  float* kv_part;
+  float* q_part;
 };
 cudaError_t launch_bwd(const BwdLaunch& a, cudaStream_t stream);
+cudaError_t launch_cross_bwd(const BwdLaunch& a, cudaStream_t stream);
 unsigned int bwd_read_and_clear_status();
 
 // E4M3 block quantization: x [BH, N, d] bf16 -> codes [BH, N, d] bytes, scales [BH, ceil(N/128)].
 cudaError_t launch_quant_e4m3(const void* x, void* codes, float* scales, int BH, int N, int d, cudaStream_t stream);
+
+// Rotary positions: q [B, Hq, N, d] and k [B, Hk, N, d] turned into q_out, k_out; with a block
+// table k_out and v_out are the pools [num_pages, Hk, page_size, d] and token n of sequence b is key
+// seq_lens[b] + n (tokens from new_lens[b] on are skipped).
+struct RopeLaunch {
+  fa_rope_axes_plan_t plan;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+  const int* pos;  // [n_axes, B, N]
+  int B, Hq, Hk, N;
+  float sign;      // -1: the inverse rotation
+  int heads;       // heads per block; set by launch_rope
+  int sms;
+  const int* block_table;  // [B, max_pages], or null
+  const int* seq_lens;
+  const int* new_lens;
+  int page_size, max_pages, num_pages;
+};
+cudaError_t launch_rope(const RopeLaunch& a, cudaStream_t stream);
 
 // Fixed device scratch used by fa_decode_splitkv_noalloc in place of a
 // caller-provided workspace.  Size limit of that entry point.

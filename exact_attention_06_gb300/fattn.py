@@ -29,9 +29,12 @@ EXPORTED = ("fa_fwd", "fa_fwd_ex", "fa_fwd_workspace_bytes", "fa_fwd_partial", "
             "fa_quantize_e4m3", "fa_fwd_fp8",
             "fa_bwd_workspace_bytes", "fa_bwd", "fa_bwd_ex", "fa_decode_workspace_bytes", "fa_decode_splitkv",
             "fa_decode_splitkv_ex", "fa_decode_splitkv_noalloc", "fa_decode_paged_workspace_bytes",
-            "fa_decode_paged", "fa_decode_paged_ex", "fa_combine", "fa_combine_ex", "fa_get_status",
+            "fa_decode_paged", "fa_decode_paged_ex", "fa_combine", "fa_combine_ex",
+            "fa_cross_workspace_bytes", "fa_cross_fwd", "fa_cross_bwd_workspace_bytes", "fa_cross_bwd",
+            "fa_rope_axes_plan", "fa_rope_axes", "fa_rope_axes_paged", "fa_get_status",
             "fa_status_string", "fa_last_error")
 FA_NOALLOC_SCRATCH_BYTES = 8 << 20
+FA_ROPE_MAX_AXES = 4
 
 
 class FattnError(RuntimeError):
@@ -51,6 +54,16 @@ class FaDecodeOpts(ctypes.Structure):
 
 class FaBwdOpts(ctypes.Structure):
     _fields_ = [("wait_budget_cycles", ctypes.c_ulonglong)]
+
+
+class FaCrossOpts(ctypes.Structure):
+    _fields_ = [("o_fp32", ctypes.c_int), ("wait_budget_cycles", ctypes.c_ulonglong)]
+
+
+class FaRopeAxesPlan(ctypes.Structure):
+    """fa_rope_axes_plan_t: the axis and rate of each pair of dimensions (host memory)."""
+    _fields_ = [("d", ctypes.c_int), ("n_axes", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("axis", ctypes.c_ubyte * 64), ("turns", ctypes.c_ulonglong * 64)]
 
 
 _lib = None
@@ -90,6 +103,17 @@ def lib() -> ctypes.CDLL:
                                          ctypes.POINTER(FaDecodeOpts)]
         L.fa_combine.argtypes = [vp, vp, vp, vp, vp, i, i, i, vp]
         L.fa_combine_ex.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, vp]
+        L.fa_cross_workspace_bytes.argtypes = [i, i, i, i, i, i]
+        L.fa_cross_workspace_bytes.restype = sz
+        L.fa_cross_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, vp, sz, vp, ctypes.POINTER(FaCrossOpts)]
+        L.fa_cross_bwd_workspace_bytes.argtypes = [i, i, i, i, i, i]
+        L.fa_cross_bwd_workspace_bytes.restype = sz
+        L.fa_cross_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, vp, sz, vp,
+                                   ctypes.POINTER(FaBwdOpts)]
+        plan = ctypes.POINTER(FaRopeAxesPlan)
+        L.fa_rope_axes_plan.argtypes = [plan, i, i, ctypes.POINTER(i), ctypes.c_double, i, i, i]
+        L.fa_rope_axes.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, plan, i, vp]
+        L.fa_rope_axes_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, plan, vp]
         L.fa_get_status.argtypes = [vp]
         L.fa_status_string.argtypes = [i]
         L.fa_status_string.restype = ctypes.c_char_p
@@ -98,7 +122,8 @@ def lib() -> ctypes.CDLL:
         for name in ("fa_fwd", "fa_fwd_ex", "fa_fwd_partial", "fa_fwd_partial_ex", "fa_quantize_e4m3", "fa_fwd_fp8",
                      "fa_bwd", "fa_bwd_ex",
                      "fa_decode_splitkv", "fa_decode_splitkv_ex", "fa_decode_splitkv_noalloc", "fa_decode_paged",
-                     "fa_decode_paged_ex", "fa_combine", "fa_combine_ex", "fa_get_status"):
+                     "fa_decode_paged_ex", "fa_combine", "fa_combine_ex", "fa_cross_fwd", "fa_cross_bwd",
+                     "fa_rope_axes_plan", "fa_rope_axes", "fa_rope_axes_paged", "fa_get_status"):
             getattr(L, name).restype = i
         _lib = L
     return _lib
@@ -367,6 +392,177 @@ def fa_combine(u_part, m_part, l_part, o, lse, stream=None):
     st = lib().fa_combine_ex(_ptr(u_part), _ptr(m_part), _ptr(l_part), _ptr(o), _ptr(lse), R, S, d,
                              int(o.dtype == torch.float32), _stream(stream))
     _check(st, "fa_combine_ex")
+
+
+def _need_current_device(func: str, *tensors):
+    """The kernels run on the current device: refuse tensors of another one."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise FattnError(FA_ERR_INVALID_ARG, func, f"a tensor is on cuda:{t.get_device()}, the current device is "
+                                                       f"cuda:{dev}")
+
+
+def _workspace_on(stream, nbytes: int, device):
+    """Scratch that lives as long as the stream's work needs it: allocated on that stream, so that its
+    memory goes to no other stream's tensor while the kernels may still use it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def fa_cross_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
+    """Scratch bytes with which fa_cross_fwd cuts the keys into ranges on the current device (0: no cut)."""
+    return int(lib().fa_cross_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
+
+
+def _need_4d(func: str, **tensors):
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} must be a 4-dimensional torch.Tensor")
+
+
+def fa_cross_fwd(q, k, v, o, lse, scale: float, kv_lens=None, workspace=None, stream=None,
+                 wait_budget_cycles: int = 0):
+    """Cross attention: q [B, Hq, Nq, d] against k, v [B, Hkv, Nk, d] (query head h reads key head
+    h // (Hq // Hkv)), of which sequence b has the first kv_lens[b] (int32 [B]; None: all); o like q, bf16 or
+    fp32 (from its dtype); lse [B, Hq, Nq] fp32.  Nq = 1 is a decode step.  ``workspace``: a uint8 CUDA
+    tensor of fa_cross_workspace_bytes() bytes; allocated here when None."""
+    _need_4d("fa_cross_fwd", q=q, k=k)
+    B, Hq, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    _need("fa_cross_fwd", "q", q, _BF16)
+    _need("fa_cross_fwd", "k", k, _BF16, (B, Hkv, Nk, d))
+    _need("fa_cross_fwd", "v", v, _BF16, (B, Hkv, Nk, d))
+    _need("fa_cross_fwd", "o", o, _OUT, (B, Hq, Nq, d))
+    _need("fa_cross_fwd", "lse", lse, _F32, (B, Hq, Nq))
+    if kv_lens is not None:
+        _need("fa_cross_fwd", "kv_lens", kv_lens, _I32, (B,))
+    if workspace is None:
+        nbytes = fa_cross_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
+        workspace = _workspace_on(stream, nbytes, q.device) if nbytes else None
+    else:
+        nbytes = workspace.numel()
+        _need("fa_cross_fwd", "workspace", workspace, _U8)
+    _need_current_device("fa_cross_fwd", q, k, v, o, lse, kv_lens, workspace)
+    opts = FaCrossOpts(int(o.dtype == torch.float32), int(wait_budget_cycles))
+    st = lib().fa_cross_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, d,
+                            float(scale), _ptr(workspace), nbytes, _stream(stream), ctypes.byref(opts))
+    _check(st, "fa_cross_fwd")
+
+
+def fa_cross_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
+    return int(lib().fa_cross_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
+
+
+def fa_cross_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale: float, kv_lens=None, workspace=None, stream=None,
+                 wait_budget_cycles: int = 0):
+    """Gradients of fa_cross_fwd (which produced the bf16 o, and lse, with the same kv_lens and scale): dq like q,
+    dk and dv like k, bf16 or fp32 (from dq's dtype).  ``workspace``: a uint8 CUDA tensor of
+    fa_cross_bwd_workspace_bytes() bytes; allocated here when None."""
+    _need_4d("fa_cross_bwd", q=q, k=k)
+    B, Hq, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    for name, t in (("q", q), ("o", o), ("dout", dout)):
+        _need("fa_cross_bwd", name, t, _BF16, (B, Hq, Nq, d))
+    for name, t in (("k", k), ("v", v)):
+        _need("fa_cross_bwd", name, t, _BF16, (B, Hkv, Nk, d))
+    _need("fa_cross_bwd", "lse", lse, _F32, (B, Hq, Nq))
+    _need("fa_cross_bwd", "dq", dq, _OUT, (B, Hq, Nq, d))
+    for name, t in (("dk", dk), ("dv", dv)):
+        _need("fa_cross_bwd", name, t, (dq.dtype,), (B, Hkv, Nk, d))
+    if kv_lens is not None:
+        _need("fa_cross_bwd", "kv_lens", kv_lens, _I32, (B,))
+    if workspace is None:
+        nbytes = fa_cross_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
+        workspace = _workspace_on(stream, nbytes, q.device)
+    else:
+        nbytes = workspace.numel()
+        _need("fa_cross_bwd", "workspace", workspace, _U8)
+    _need_current_device("fa_cross_bwd", q, k, v, o, dout, lse, dq, dk, dv, kv_lens, workspace)
+    opts = FaBwdOpts(int(wait_budget_cycles))
+    st = lib().fa_cross_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
+                            _ptr(dk), _ptr(dv), B, Hq, Hkv, Nq, Nk, d, float(scale),
+                            int(dq.dtype == torch.float32), _ptr(workspace), nbytes, _stream(stream),
+                            ctypes.byref(opts))
+    _check(st, "fa_cross_bwd")
+
+
+def fa_rope_axes_plan(d: int, sections, base: float = 10000.0, interleaved: bool = False, per_axis: bool = False,
+                      cyclic: bool = False) -> FaRopeAxesPlan:
+    """The plan of a rotation: ``sections`` are the pairs of each axis (d / 2 in all).  Host only; kept and
+    passed to every fa_rope_axes and fa_rope_axes_paged call of a model."""
+    sections = [int(x) for x in sections]
+    plan = FaRopeAxesPlan()
+    st = lib().fa_rope_axes_plan(ctypes.byref(plan), d, len(sections), (ctypes.c_int * len(sections))(*sections),
+                                 float(base), int(bool(interleaved)), int(bool(per_axis)), int(bool(cyclic)))
+    _check(st, "fa_rope_axes_plan")
+    return plan
+
+
+def _need_plan(func: str, plan, d: int):
+    if not isinstance(plan, FaRopeAxesPlan) or plan.d != d:
+        raise FattnError(FA_ERR_INVALID_ARG, func, f"plan must be fa_rope_axes_plan's for d={d}")
+
+
+def fa_rope_axes(q, k, pos, plan, q_out=None, k_out=None, inverse: bool = False, stream=None):
+    """Turn q [B, Hq, N, d] into q_out and k [B, Hk, N, d] (or None) into k_out by the positions pos
+    [axes, B, N] int32; in place where an output is None or its input.  inverse=True turns back: the
+    gradients of q and k from those of q_out and k_out."""
+    _need_4d("fa_rope_axes", q=q)
+    B, Hq, N, d = q.shape
+    _need("fa_rope_axes", "q", q, _BF16)
+    q_out = q if q_out is None else q_out
+    _need("fa_rope_axes", "q_out", q_out, _BF16, (B, Hq, N, d))
+    Hk = 0
+    if k is not None:
+        _need_4d("fa_rope_axes", k=k)
+        Hk = k.shape[1]
+        _need("fa_rope_axes", "k", k, _BF16, (B, Hk, N, d))
+        k_out = k if k_out is None else k_out
+        _need("fa_rope_axes", "k_out", k_out, _BF16, (B, Hk, N, d))
+    elif k_out is not None:
+        raise FattnError(FA_ERR_INVALID_ARG, "fa_rope_axes", "k_out without k")
+    _need_plan("fa_rope_axes", plan, d)
+    _need("fa_rope_axes", "pos", pos, _I32, (plan.n_axes, B, N))
+    _need_current_device("fa_rope_axes", q, k, pos, q_out, k_out)
+    st = lib().fa_rope_axes(_ptr(q), _ptr(k), _ptr(pos), _ptr(q_out), _ptr(k_out), B, Hq, Hk, N, ctypes.byref(plan),
+                            int(bool(inverse)), _stream(stream))
+    _check(st, "fa_rope_axes")
+
+
+def fa_rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table, seq_lens, new_lens=None,
+                       stream=None):
+    """New tokens of a decode step or prompt chunk: q [B, Hq, N, d] turned into q_out, k [B, Hk, N, d] turned and
+    v copied into the pools k_pages, v_pages [P, Hk, page_size, d] of fa_decode_paged, as keys seq_lens[b] ..
+    of sequence b (int32 [B], the lengths before this call); tokens from new_lens[b] on are padding."""
+    _need_4d("fa_rope_axes_paged", q=q, k=k, k_pages=k_pages)
+    B, Hq, N, d = q.shape
+    Hk = k.shape[1]
+    P, _, page_size, _ = k_pages.shape
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise FattnError(FA_ERR_INVALID_ARG, "fa_rope_axes_paged", "block_table must be a 2-dimensional torch.Tensor")
+    max_pages = block_table.shape[1]
+    _need("fa_rope_axes_paged", "q", q, _BF16)
+    _need("fa_rope_axes_paged", "q_out", q_out, _BF16, (B, Hq, N, d))
+    _need("fa_rope_axes_paged", "k", k, _BF16, (B, Hk, N, d))
+    _need("fa_rope_axes_paged", "v", v, _BF16, (B, Hk, N, d))
+    _need("fa_rope_axes_paged", "k_pages", k_pages, _BF16, (P, Hk, page_size, d))
+    _need("fa_rope_axes_paged", "v_pages", v_pages, _BF16, (P, Hk, page_size, d))
+    _need("fa_rope_axes_paged", "block_table", block_table, _I32, (B, max_pages))
+    _need("fa_rope_axes_paged", "seq_lens", seq_lens, _I32, (B,))
+    if new_lens is not None:
+        _need("fa_rope_axes_paged", "new_lens", new_lens, _I32, (B,))
+    _need_plan("fa_rope_axes_paged", plan, d)
+    _need("fa_rope_axes_paged", "pos", pos, _I32, (plan.n_axes, B, N))
+    _need_current_device("fa_rope_axes_paged", q, k, v, pos, q_out, k_pages, v_pages, block_table, seq_lens, new_lens)
+    st = lib().fa_rope_axes_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(pos), _ptr(q_out), _ptr(k_pages), _ptr(v_pages),
+                                  _ptr(block_table), _ptr(seq_lens), _ptr(new_lens), B, Hq, Hk, N, page_size,
+                                  max_pages, P, ctypes.byref(plan), _stream(stream))
+    _check(st, "fa_rope_axes_paged")
 
 
 def fa_get_status(stream=None) -> int:

@@ -397,6 +397,111 @@ fa_status_t fa_bwd_ex(const void* q, const void* k, const void* v, const void* o
                       void* stream, const fa_bwd_opts* opts);
 
 /*
+ * Cross attention: queries of a decoder against an encoder's states, whose count differs from the
+ * queries' and from sequence to sequence (the scaled-dot-product interface takes k and v of another
+ * length than q: xuesongtap §6).  Not causal.  Query heads may share key heads: query head h reads
+ * key head h / (Hq / Hkv).  With Nq = 1 it is the single-token form: the same call, its keys cut
+ * into ranges whose partials the combine kernel joins.
+ *
+ *   q         [B, Hq, Nq, d] bf16, 16-byte aligned.
+ *   k, v      [B, Hkv, Nk, d] bf16, 16-byte aligned.  Hq a multiple of Hkv.
+ *   kv_lens   [B] int32, 4-byte aligned, or NULL: sequence b attends its keys 0 .. kv_lens[b] - 1
+ *             (values are clamped to [0, Nk]; NULL: all Nk).  What k and v hold behind them may be
+ *             anything, infinities and NaN included, and has no influence.  A sequence of length 0
+ *             gets O = 0 and lse = -inf, and gradients of 0.
+ *   o         [B, Hq, Nq, d] bf16, or fp32 with opts->o_fp32 (written), 16-byte aligned.
+ *   lse       [B, Hq, Nq] fp32 (written), natural log of the scaled scores, as for fa_fwd.
+ *   d in {64, 128}; scale finite and > 0; every size >= 1.
+ */
+typedef struct {
+  int o_fp32;                            /* 0: O is bf16 (round to nearest even); 1: O is fp32 */
+  unsigned long long wait_budget_cycles; /* per-wait budget in SM cycles, as in fa_fwd_opts (0 = default) */
+} fa_cross_opts;
+
+/* Scratch bytes with which fa_cross_fwd cuts the keys into ranges on the current device, so that
+ * few query rows still fill the SMs; 0 when it would not cut them (or for invalid sizes, or
+ * without a device). */
+size_t fa_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
+
+/* fa_cross_fwd -- workspace: caller-owned device scratch of fa_cross_workspace_bytes() bytes,
+ * 256-byte aligned (FA_ERR_WORKSPACE if smaller), or NULL: one kernel, the keys uncut.  O and lse
+ * are the same function of the inputs either way, up to rounding order.  opts may be NULL. */
+fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int* kv_lens, void* o, float* lse,
+                         int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, void* workspace,
+                         size_t ws_bytes, void* stream, const fa_cross_opts* opts);
+
+/* Scratch bytes of fa_cross_bwd on the current device: rowsum(O * dO) per query row, and fp32
+ * partial gradients where it cuts a long scan into ranges (few key tiles under many queries, or
+ * the reverse).  0 for invalid sizes or without a device. */
+size_t fa_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
+
+/* fa_cross_bwd -- the gradients, by the formulas of fa_bwd: dq like q, dk and dv like k and v (bf16,
+ * or fp32 when grad_fp32 = 1).  dk and dv sum over the query heads that share the key head; rows of
+ * keys behind kv_lens[b] are written as 0.  o (bf16) and lse are fa_cross_fwd's for the same q, k, v,
+ * kv_lens and scale.  No atomics: the gradients are bitwise repeatable.  opts may be NULL. */
+fa_status_t fa_cross_bwd(const void* q, const void* k, const void* v, const int* kv_lens, const void* o,
+                         const void* dout, const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
+                         int Nq, int Nk, int d, float scale, int grad_fp32, void* workspace, size_t ws_bytes,
+                         void* stream, const fa_bwd_opts* opts);
+
+/*
+ * Rotary positions with several axes, for q and k before attention: pair i of a row's d
+ * dimensions belongs to one axis (time, height, width, ...) and is turned by the angle
+ * pos[axis_i] * rate_i: (a, b) -> (a cos - b sin, a sin + b cos).
+ */
+#define FA_ROPE_MAX_AXES 4
+typedef struct {  /* made by fa_rope_axes_plan; host memory, copied by each call */
+  int d, n_axes, interleaved;
+  unsigned char axis[64];       /* of each pair */
+  unsigned long long turns[64]; /* rate / (2 pi) of each pair, in 2^-64 turns per position */
+} fa_rope_axes_plan_t;
+
+/*
+ * fa_rope_axes_plan -- fill *plan (host only; no device is touched).
+ *   d            64 or 128.
+ *   sections     [n_axes] pairs of each axis, each >= 1, d/2 in all; 1 <= n_axes <= FA_ROPE_MAX_AXES
+ *                (one axis is the ordinary rotary embedding).
+ *   base         finite, >= 1.
+ *   interleaved  0: pair i is dimensions i and i + d/2; 1: dimensions 2i and 2i + 1.
+ *   per_axis     0: rate_i = base^(-i / (d/2)) over all pairs; 1: each axis starts anew,
+ *                base^(-j / sections[a]) for its j-th pair.
+ *   cyclic       0: the axes' pairs lie one section after another; 1: they are dealt out in turn
+ *                (t h w t h w ..) to the axes that have pairs left.
+ */
+fa_status_t fa_rope_axes_plan(fa_rope_axes_plan_t* plan, int d, int n_axes, const int* sections, double base,
+                              int interleaved, int per_axis, int cyclic);
+
+/*
+ * fa_rope_axes -- turn q [B, Hq, N, d] into q_out and k [B, Hk, N, d] into k_out (bf16, 16-byte
+ * aligned), in one kernel.  An output may be its own input (in place); otherwise they do not overlap.
+ *   pos      [n_axes, B, N] int32, 4-byte aligned: any values; angles are exact to 2^-24 of a half
+ *            turn for every position up to 2^24 (2^-18 for any 32-bit one).
+ *   Hk       0: q alone (k and k_out are not used).
+ *   inverse  1: turn back.  The rotation's inverse is its transpose, so this is the backward pass:
+ *            the gradients of q and k from those of q_out and k_out.
+ * cos, sin and products in fp32, one rounding to bf16 (nearest even).
+ */
+fa_status_t fa_rope_axes(const void* q, const void* k, const int* pos, void* q_out, void* k_out, int B, int Hq,
+                         int Hk, int N, const fa_rope_axes_plan_t* plan, int inverse, void* stream);
+
+/*
+ * fa_rope_axes_paged -- the serving form: N new tokens of each sequence (1 in a decode step, more in
+ * a chunk of a prompt).  q [B, Hq, N, d] is turned into q_out; k [B, Hk, N, d] is turned and v (the
+ * same shape) copied into the paged cache of fa_decode_paged: pools [num_pages, Hk, page_size, d] with
+ * block_table [B, max_pages].
+ *   seq_lens   [B] int32: keys that sequence b had before; its token t becomes key seq_lens[b] + t.
+ *   new_lens   [B] int32 or NULL: tokens of sequence b in this call; those from new_lens[b] on are
+ *              padding, for which nothing is written (not to q_out either).
+ *   A token whose key has no page (a negative length, a key past max_pages * page_size, an id
+ *   outside [0, num_pages)) is not written to the pools.  page_size as for fa_decode_paged; Hk >= 1.
+ *   The pools are written only at the new tokens' rows; two tokens of one call must not share a row.
+ */
+fa_status_t fa_rope_axes_paged(const void* q, const void* k, const void* v, const int* pos, void* q_out,
+                               void* k_pages, void* v_pages, const int* block_table, const int* seq_lens,
+                               const int* new_lens, int B, int Hq, int Hk, int N, int page_size, int max_pages,
+                               int num_pages, const fa_rope_axes_plan_t* plan, void* stream);
+
+/*
  * fa_get_status -- synchronise `stream`, then read and clear the current
  * device's kernel status word.  Returns FA_ERR_TIMEOUT if any kernel of this
  * library ran out of its wait budget since the last call, FA_ERR_CUDA if the
