@@ -156,7 +156,8 @@ def _check(status: int, func: str):
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    """A tensor's device pointer for a c_void_p argument (an int converts faster than a c_void_p object)."""
+    return t.data_ptr() if t is not None else None
 
 
 _BF16 = (torch.bfloat16,)
@@ -181,10 +182,16 @@ def _need(func: str, name: str, t, dtypes, shape=None):
         raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} must be a CUDA tensor")
 
 
+# The current stream's handle without building a torch Stream object (3 us of a 4 us call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def fa_fwd_workspace_bytes(B: int, H: int, N: int, d: int, causal: bool = False) -> int:
@@ -394,13 +401,18 @@ def fa_combine(u_part, m_part, l_part, o, lse, stream=None):
     _check(st, "fa_combine_ex")
 
 
-def _need_current_device(func: str, *tensors):
-    """The kernels run on the current device: refuse tensors of another one."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise FattnError(FA_ERR_INVALID_ARG, func, f"a tensor is on cuda:{t.get_device()}, the current device is "
-                                                       f"cuda:{dev}")
+def _need_here(func: str, tensors):
+    """Check (name, tensor, dtypes, shape) entries as _need does, and that each tensor is on the current
+    device, where the kernels run.  (One pass of cheap comparisons: a decode step's calls take a few
+    microseconds, and their checks count.)"""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    for name, t, dtypes, shape in tensors:
+        if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+                and t.get_device() == dev):
+            _need(func, name, t, dtypes, shape)
+            if t.get_device() != torch.cuda.current_device():
+                raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} is on cuda:{t.get_device()}, the current device "
+                                                           f"is cuda:{torch.cuda.current_device()}")
 
 
 def _workspace_on(stream, nbytes: int, device):
@@ -431,27 +443,29 @@ def fa_cross_fwd(q, k, v, o, lse, scale: float, kv_lens=None, workspace=None, st
     h // (Hq // Hkv)), of which sequence b has the first kv_lens[b] (int32 [B]; None: all); o like q, bf16 or
     fp32 (from its dtype); lse [B, Hq, Nq] fp32.  Nq = 1 is a decode step.  ``workspace``: a uint8 CUDA
     tensor of fa_cross_workspace_bytes() bytes; allocated here when None."""
-    _need_4d("fa_cross_fwd", q=q, k=k)
-    B, Hq, Nq, d = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    _need("fa_cross_fwd", "q", q, _BF16)
-    _need("fa_cross_fwd", "k", k, _BF16, (B, Hkv, Nk, d))
-    _need("fa_cross_fwd", "v", v, _BF16, (B, Hkv, Nk, d))
-    _need("fa_cross_fwd", "o", o, _OUT, (B, Hq, Nq, d))
-    _need("fa_cross_fwd", "lse", lse, _F32, (B, Hq, Nq))
+    func = "fa_cross_fwd"
+    _need_4d(func, q=q, k=k)
+    B, Hq, Nq, d = qs = q.shape
+    _, Hkv, Nk, _ = k.shape
+    ks = (B, Hkv, Nk, d)
+    checks = [("q", q, _BF16, qs), ("k", k, _BF16, ks), ("v", v, _BF16, ks), ("o", o, _OUT, qs),
+              ("lse", lse, _F32, (B, Hq, Nq))]
     if kv_lens is not None:
-        _need("fa_cross_fwd", "kv_lens", kv_lens, _I32, (B,))
+        checks.append(("kv_lens", kv_lens, _I32, (B,)))
+    if workspace is not None:
+        checks.append(("workspace", workspace, _U8, (workspace.numel(),)))
+    _need_here(func, checks)
+    L = lib()
     if workspace is None:
-        nbytes = fa_cross_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
-        workspace = _workspace_on(stream, nbytes, q.device) if nbytes else None
+        nbytes = L.fa_cross_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
+        if nbytes:
+            workspace = _workspace_on(stream, nbytes, q.device)
     else:
         nbytes = workspace.numel()
-        _need("fa_cross_fwd", "workspace", workspace, _U8)
-    _need_current_device("fa_cross_fwd", q, k, v, o, lse, kv_lens, workspace)
-    opts = FaCrossOpts(int(o.dtype == torch.float32), int(wait_budget_cycles))
-    st = lib().fa_cross_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, d,
-                            float(scale), _ptr(workspace), nbytes, _stream(stream), ctypes.byref(opts))
-    _check(st, "fa_cross_fwd")
+    o_fp32 = o.dtype == torch.float32
+    opts = ctypes.byref(FaCrossOpts(o_fp32, wait_budget_cycles)) if o_fp32 or wait_budget_cycles else None
+    _check(L.fa_cross_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, d, float(scale),
+                          _ptr(workspace), nbytes, _stream(stream), opts), func)
 
 
 def fa_cross_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
@@ -463,32 +477,26 @@ def fa_cross_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale: float, kv_lens=None, 
     """Gradients of fa_cross_fwd (which produced the bf16 o, and lse, with the same kv_lens and scale): dq like q,
     dk and dv like k, bf16 or fp32 (from dq's dtype).  ``workspace``: a uint8 CUDA tensor of
     fa_cross_bwd_workspace_bytes() bytes; allocated here when None."""
-    _need_4d("fa_cross_bwd", q=q, k=k)
-    B, Hq, Nq, d = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    for name, t in (("q", q), ("o", o), ("dout", dout)):
-        _need("fa_cross_bwd", name, t, _BF16, (B, Hq, Nq, d))
-    for name, t in (("k", k), ("v", v)):
-        _need("fa_cross_bwd", name, t, _BF16, (B, Hkv, Nk, d))
-    _need("fa_cross_bwd", "lse", lse, _F32, (B, Hq, Nq))
-    _need("fa_cross_bwd", "dq", dq, _OUT, (B, Hq, Nq, d))
-    for name, t in (("dk", dk), ("dv", dv)):
-        _need("fa_cross_bwd", name, t, (dq.dtype,), (B, Hkv, Nk, d))
+    func = "fa_cross_bwd"
+    _need_4d(func, q=q, k=k, dq=dq)
+    B, Hq, Nq, d = qs = q.shape
+    _, Hkv, Nk, _ = k.shape
+    ks, grad = (B, Hkv, Nk, d), (dq.dtype,) if dq.dtype in _OUT else _OUT
+    checks = [("q", q, _BF16, qs), ("o", o, _BF16, qs), ("dout", dout, _BF16, qs), ("k", k, _BF16, ks),
+              ("v", v, _BF16, ks), ("lse", lse, _F32, (B, Hq, Nq)), ("dq", dq, grad, qs), ("dk", dk, grad, ks),
+              ("dv", dv, grad, ks)]
     if kv_lens is not None:
-        _need("fa_cross_bwd", "kv_lens", kv_lens, _I32, (B,))
+        checks.append(("kv_lens", kv_lens, _I32, (B,)))
+    if workspace is not None:
+        checks.append(("workspace", workspace, _U8, (workspace.numel(),)))
+    _need_here(func, checks)
+    L = lib()
     if workspace is None:
-        nbytes = fa_cross_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
-        workspace = _workspace_on(stream, nbytes, q.device)
-    else:
-        nbytes = workspace.numel()
-        _need("fa_cross_bwd", "workspace", workspace, _U8)
-    _need_current_device("fa_cross_bwd", q, k, v, o, dout, lse, dq, dk, dv, kv_lens, workspace)
-    opts = FaBwdOpts(int(wait_budget_cycles))
-    st = lib().fa_cross_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
-                            _ptr(dk), _ptr(dv), B, Hq, Hkv, Nq, Nk, d, float(scale),
-                            int(dq.dtype == torch.float32), _ptr(workspace), nbytes, _stream(stream),
-                            ctypes.byref(opts))
-    _check(st, "fa_cross_bwd")
+        workspace = _workspace_on(stream, L.fa_cross_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, d), q.device)
+    opts = ctypes.byref(FaBwdOpts(wait_budget_cycles)) if wait_budget_cycles else None
+    _check(L.fa_cross_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
+                          _ptr(dk), _ptr(dv), B, Hq, Hkv, Nq, Nk, d, float(scale), dq.dtype == torch.float32,
+                          _ptr(workspace), workspace.numel(), _stream(stream), opts), func)
 
 
 def fa_rope_axes_plan(d: int, sections, base: float = 10000.0, interleaved: bool = False, per_axis: bool = False,
@@ -512,26 +520,25 @@ def fa_rope_axes(q, k, pos, plan, q_out=None, k_out=None, inverse: bool = False,
     """Turn q [B, Hq, N, d] into q_out and k [B, Hk, N, d] (or None) into k_out by the positions pos
     [axes, B, N] int32; in place where an output is None or its input.  inverse=True turns back: the
     gradients of q and k from those of q_out and k_out."""
-    _need_4d("fa_rope_axes", q=q)
-    B, Hq, N, d = q.shape
-    _need("fa_rope_axes", "q", q, _BF16)
+    func = "fa_rope_axes"
+    _need_4d(func, q=q)
+    B, Hq, N, d = qs = q.shape
     q_out = q if q_out is None else q_out
-    _need("fa_rope_axes", "q_out", q_out, _BF16, (B, Hq, N, d))
+    checks = [("q", q, _BF16, qs), ("q_out", q_out, _BF16, qs)]
     Hk = 0
     if k is not None:
-        _need_4d("fa_rope_axes", k=k)
+        _need_4d(func, k=k)
         Hk = k.shape[1]
-        _need("fa_rope_axes", "k", k, _BF16, (B, Hk, N, d))
         k_out = k if k_out is None else k_out
-        _need("fa_rope_axes", "k_out", k_out, _BF16, (B, Hk, N, d))
+        ks = (B, Hk, N, d)
+        checks += [("k", k, _BF16, ks), ("k_out", k_out, _BF16, ks)]
     elif k_out is not None:
-        raise FattnError(FA_ERR_INVALID_ARG, "fa_rope_axes", "k_out without k")
-    _need_plan("fa_rope_axes", plan, d)
-    _need("fa_rope_axes", "pos", pos, _I32, (plan.n_axes, B, N))
-    _need_current_device("fa_rope_axes", q, k, pos, q_out, k_out)
-    st = lib().fa_rope_axes(_ptr(q), _ptr(k), _ptr(pos), _ptr(q_out), _ptr(k_out), B, Hq, Hk, N, ctypes.byref(plan),
-                            int(bool(inverse)), _stream(stream))
-    _check(st, "fa_rope_axes")
+        raise FattnError(FA_ERR_INVALID_ARG, func, "k_out without k")
+    _need_plan(func, plan, d)
+    checks.append(("pos", pos, _I32, (plan.n_axes, B, N)))
+    _need_here(func, checks)
+    _check(lib().fa_rope_axes(_ptr(q), _ptr(k), _ptr(pos), _ptr(q_out), _ptr(k_out), B, Hq, Hk, N, plan,
+                              bool(inverse), _stream(stream)), func)
 
 
 def fa_rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table, seq_lens, new_lens=None,
@@ -539,30 +546,26 @@ def fa_rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table,
     """New tokens of a decode step or prompt chunk: q [B, Hq, N, d] turned into q_out, k [B, Hk, N, d] turned and
     v copied into the pools k_pages, v_pages [P, Hk, page_size, d] of fa_decode_paged, as keys seq_lens[b] ..
     of sequence b (int32 [B], the lengths before this call); tokens from new_lens[b] on are padding."""
-    _need_4d("fa_rope_axes_paged", q=q, k=k, k_pages=k_pages)
-    B, Hq, N, d = q.shape
+    func = "fa_rope_axes_paged"
+    _need_4d(func, q=q, k=k, k_pages=k_pages)
+    B, Hq, N, d = qs = q.shape
     Hk = k.shape[1]
     P, _, page_size, _ = k_pages.shape
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise FattnError(FA_ERR_INVALID_ARG, "fa_rope_axes_paged", "block_table must be a 2-dimensional torch.Tensor")
+        raise FattnError(FA_ERR_INVALID_ARG, func, "block_table must be a 2-dimensional torch.Tensor")
     max_pages = block_table.shape[1]
-    _need("fa_rope_axes_paged", "q", q, _BF16)
-    _need("fa_rope_axes_paged", "q_out", q_out, _BF16, (B, Hq, N, d))
-    _need("fa_rope_axes_paged", "k", k, _BF16, (B, Hk, N, d))
-    _need("fa_rope_axes_paged", "v", v, _BF16, (B, Hk, N, d))
-    _need("fa_rope_axes_paged", "k_pages", k_pages, _BF16, (P, Hk, page_size, d))
-    _need("fa_rope_axes_paged", "v_pages", v_pages, _BF16, (P, Hk, page_size, d))
-    _need("fa_rope_axes_paged", "block_table", block_table, _I32, (B, max_pages))
-    _need("fa_rope_axes_paged", "seq_lens", seq_lens, _I32, (B,))
+    _need_plan(func, plan, d)
+    ks, pool = (B, Hk, N, d), (P, Hk, page_size, d)
+    checks = [("q", q, _BF16, qs), ("q_out", q_out, _BF16, qs), ("k", k, _BF16, ks), ("v", v, _BF16, ks),
+              ("k_pages", k_pages, _BF16, pool), ("v_pages", v_pages, _BF16, pool),
+              ("block_table", block_table, _I32, (B, max_pages)), ("seq_lens", seq_lens, _I32, (B,)),
+              ("pos", pos, _I32, (plan.n_axes, B, N))]
     if new_lens is not None:
-        _need("fa_rope_axes_paged", "new_lens", new_lens, _I32, (B,))
-    _need_plan("fa_rope_axes_paged", plan, d)
-    _need("fa_rope_axes_paged", "pos", pos, _I32, (plan.n_axes, B, N))
-    _need_current_device("fa_rope_axes_paged", q, k, v, pos, q_out, k_pages, v_pages, block_table, seq_lens, new_lens)
-    st = lib().fa_rope_axes_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(pos), _ptr(q_out), _ptr(k_pages), _ptr(v_pages),
-                                  _ptr(block_table), _ptr(seq_lens), _ptr(new_lens), B, Hq, Hk, N, page_size,
-                                  max_pages, P, ctypes.byref(plan), _stream(stream))
-    _check(st, "fa_rope_axes_paged")
+        checks.append(("new_lens", new_lens, _I32, (B,)))
+    _need_here(func, checks)
+    _check(lib().fa_rope_axes_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(pos), _ptr(q_out), _ptr(k_pages), _ptr(v_pages),
+                                    _ptr(block_table), _ptr(seq_lens), _ptr(new_lens), B, Hq, Hk, N, page_size,
+                                    max_pages, P, plan, _stream(stream)), func)
 
 
 def fa_get_status(stream=None) -> int:
