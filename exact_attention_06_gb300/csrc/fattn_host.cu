@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdarg>
@@ -290,17 +291,55 @@ int cut_scan(long long units, int tiles, int sms, double part_bytes) {
 }
 
 struct CrossPlan {
+  int few = 0;  // 1: the few-row kernel; its splits are a cluster unless `parts`
+  int parts = 0;
   int splits = 1, kchunk = 0;
   size_t u_bytes = 0, m_bytes = 0;
-  size_t total() const { return splits > 1 ? u_bytes + 2 * m_bytes : 0; }
+  size_t total() const { return parts ? u_bytes + 2 * m_bytes : 0; }
 };
 
-CrossPlan plan_cross(const CrossShape& c, int Nk, int d, int sms) {
+// The few-row kernel's blocks per key head.  Costs in the time a 64-key stage takes an SM at its share of
+// HBM: the whole call cannot be faster than all stages shared out, one block takes at least 0.73 a
+// stage (its chain of copies and products), set-up and join cost 3 a round of resident blocks, partials and the combine
+// kernel 3 more.  Clusters (up to 8 blocks) need neither partials nor a second kernel; of theirs the
+// largest within 5 % of the best is taken, since shorter blocks even out sequences of different lengths.
+// Measured (GB300, d = 128): 64 key heads x 577 keys, S = 1 / 2 / 4 / 5: 8.2 / 6.2 / 6.2 / 10.0 us;
+// 64 x 18k-32k keys, S = 2 / 4 / 8 / 19: 143 / 124 / 120 / 128 us; 8 x 16384, S = 8 / 16 / 32: 20.3 / 15.6 /
+// 17.7 us; 512 x 1500 at d = 64, S = 1 / 4 / 8: 41 / 43 / 60 us.
+void plan_few(CrossPlan* p, const CrossShape& c, int Nk, int d, int sms, bool allow_parts) {
+  constexpr double kBlock = 0.73, kFixed = 3.0, kJoin = 3.0;
+  const int stages = (Nk + fattn::kRowsStageKeys - 1) / fattn::kRowsStageKeys;
+  const long long slots = static_cast<long long>(sms) * fattn::cross_rows_per_sm(d, c.rows);
+  const double all = static_cast<double>(c.bh) * stages / sms;
+  auto cost = [&](int s) {
+    const double rounds = static_cast<double>((c.bh * s + slots - 1) / slots);
+    return std::fmax(all, kBlock * rounds * ((stages + s - 1) / s)) + kFixed * rounds;
+  };
+  const int most = std::min(stages, 8);
+  double best = cost(1);
+  for (int s = 2; s <= most; ++s) best = std::fmin(best, cost(s));
+  p->splits = 1;
+  for (int s = 2; s <= most; ++s)
+    if (cost(s) <= 1.05 * best && c.bh * s <= INT_MAX) p->splits = s;
+  for (int s = 9; allow_parts && s <= 256 && s <= stages && c.bh * s <= INT_MAX; ++s)
+    if (cost(s) + kJoin < best) {
+      best = cost(s) + kJoin;
+      p->splits = s;
+    }
+  p->few = 1;
+  p->parts = p->splits > 8;
+}
+
+CrossPlan plan_cross(const CrossShape& c, int Nk, int d, int sms, bool workspace) {
   CrossPlan p;
   const int tiles = (Nk + 127) / 128;
   const long long rows = c.bh * c.rows;
-  if (rows <= INT_MAX)  // (the combine kernel's row count)
+  const bool can_join = workspace && rows <= INT_MAX;  // (the combine kernel's row count)
+  if (c.rows <= fattn::kCrossRowsMax)
+    plan_few(&p, c, Nk, d, sms, can_join);
+  else if (can_join)
     p.splits = cut_scan(c.bh * ((c.rows + 255) / 256), tiles, sms, static_cast<double>(rows) * (d + 2) * 4);
+  if (!p.few) p.parts = p.splits > 1;
   p.kchunk = (tiles + p.splits - 1) / p.splits * 128;
   p.u_bytes = round256(static_cast<size_t>(rows) * p.splits * d * sizeof(float));
   p.m_bytes = round256(static_cast<size_t>(rows) * p.splits * sizeof(float));
@@ -876,7 +915,7 @@ size_t fa_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   fa_status_t st = check_cross_args(B, Hq, Hkv, Nq, Nk, d, &c);
   if (st == FA_OK) st = check_device(&sms);
   if (!saved) g_last_error[0] = '\0';
-  return st == FA_OK ? plan_cross(c, Nk, d, sms).total() : 0;
+  return st == FA_OK ? plan_cross(c, Nk, d, sms, true).total() : 0;
 }
 
 fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int* kv_lens, void* o, float* lse, int B,
@@ -896,13 +935,34 @@ fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int*
   if (st != FA_OK) return st;
   int sms = 0;
   if ((st = check_device(&sms)) != FA_OK) return st;
-  CrossPlan plan = plan_cross(c, Nk, d, sms);
-  if (!workspace) {  // one launch, the keys uncut
-    plan.splits = 1;
-    plan.kchunk = (Nk + 127) / 128 * 128;
-  } else if (ws_bytes < plan.total()) {
+  const CrossPlan plan = plan_cross(c, Nk, d, sms, workspace != nullptr);
+  if (workspace && ws_bytes < plan.total())
     return fail(FA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes fa_cross_workspace_bytes gives",
                 ws_bytes, plan.total());
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  float* u_part = plan.parts ? reinterpret_cast<float*>(w) : nullptr;
+  float* m_part = plan.parts ? reinterpret_cast<float*>(w + plan.u_bytes) : nullptr;
+  float* l_part = plan.parts ? reinterpret_cast<float*>(w + plan.u_bytes + plan.m_bytes) : nullptr;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  const unsigned long long budget = (opts && opts->wait_budget_cycles) ? opts->wait_budget_cycles : kDefaultBudget;
+  auto join = [&]() -> fa_status_t {
+    if (!plan.parts) return FA_OK;
+    const cudaError_t e = fattn::launch_combine(u_part, m_part, l_part, o, lse, static_cast<int>(c.bh * c.rows),
+                                                plan.splits, d, o_fp32, s);
+    return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_cross_fwd combine launch");
+  };
+  if (plan.few) {
+    fattn::CrossRowsLaunch f{};
+    if ((st = make_map(&f.tk, k, d, Nk, c.bh, fattn::kRowsStageKeys)) != FA_OK) return st;
+    if ((st = make_map(&f.tv, v, d, Nk, c.bh, fattn::kRowsStageKeys)) != FA_OK) return st;
+    f.BH = static_cast<int>(c.bh);
+    f.d = d;
+    f.args = {q, o, lse, u_part, m_part, l_part, kv_lens, Hkv, c.rows, Nk, plan.splits, o_fp32, scale_log2, budget};
+    cudaGetLastError();
+    const cudaError_t e = fattn::launch_cross_rows(f, s);
+    if (e != cudaSuccess) return cuda_fail(e, "fa_cross_fwd launch");
+    return join();
   }
   fattn::FwdLaunch a{};
   if ((st = make_map(&a.tq, q, d, c.rows, c.bh, 128)) != FA_OK) return st;
@@ -915,8 +975,8 @@ fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int*
   a.BH = static_cast<int>(c.bh);
   a.d = d;
   a.o_fp32 = o_fp32;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.budget = (opts && opts->wait_budget_cycles) ? opts->wait_budget_cycles : kDefaultBudget;
+  a.scale_log2 = scale_log2;
+  a.budget = budget;
   a.sms = sms;
   a.cross = 1;
   a.aux.Nk = Nk;
@@ -924,22 +984,13 @@ fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int*
   a.aux.kv_heads = Hkv;
   a.aux.kchunk = plan.kchunk;
   a.aux.S = plan.splits;
-  if (plan.splits > 1) {
-    uint8_t* w = static_cast<uint8_t*>(workspace);
-    a.aux.u_part = reinterpret_cast<float*>(w);
-    a.aux.m_part = reinterpret_cast<float*>(w + plan.u_bytes);
-    a.aux.l_part = reinterpret_cast<float*>(w + plan.u_bytes + plan.m_bytes);
-  }
+  a.aux.u_part = u_part;
+  a.aux.m_part = m_part;
+  a.aux.l_part = l_part;
   cudaGetLastError();
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = fattn::launch_fwd(a, s);
   if (e != cudaSuccess) return cuda_fail(e, "fa_cross_fwd launch");
-  if (plan.splits > 1) {
-    e = fattn::launch_combine(a.aux.u_part, a.aux.m_part, a.aux.l_part, o, lse, static_cast<int>(c.bh * c.rows),
-                              plan.splits, d, o_fp32, s);
-    if (e != cudaSuccess) return cuda_fail(e, "fa_cross_fwd combine launch");
-  }
-  return FA_OK;
+  return join();
 }
 
 size_t fa_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
@@ -1126,7 +1177,7 @@ fa_status_t fa_get_status(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fa_get_status synchronize");
   const unsigned int bits = fattn::fwd_read_and_clear_status() | fattn::decode_read_and_clear_status() |
-                            fattn::bwd_read_and_clear_status();
+                            fattn::bwd_read_and_clear_status() | fattn::cross_rows_read_and_clear_status();
   if (bits & fattn::kStatusTimeout) return fail(FA_ERR_TIMEOUT, "a kernel wait exceeded its budget");
   return FA_OK;
 }

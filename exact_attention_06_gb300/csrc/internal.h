@@ -121,6 +121,32 @@ cudaError_t launch_combine(const float* u_part, const float* m_part, const float
                            int R, int S, int d, int o_fp32, cudaStream_t stream);
 unsigned int decode_read_and_clear_status();
 
+// Cross attention of few rows: R <= kCrossRowsMax query rows of each of BH key heads against the first
+// kv_lens[bh / kv_heads] (null: Nk) of its keys, shared out over S blocks.  u_part == null: the S <= 8
+// blocks of a key head are a cluster and write o and lse; else partial slots [BH * R, S].
+constexpr int kRowsStageKeys = 64;
+constexpr int kCrossRowsMax = 32;
+constexpr int cross_rows_per_sm(int d, int rows) { return d == 128 && rows > 16 ? 1 : 2; }
+struct CrossRowsArgs {
+  const void* q;
+  void* o;
+  float* lse;
+  float* u_part;
+  float* m_part;
+  float* l_part;
+  const int* kv_lens;
+  int kv_heads, R, Nk, S, o_fp32;
+  float sl2;  // scale * log2(e)
+  unsigned long long budget;
+};
+struct CrossRowsLaunch {
+  CUtensorMap tk, tv;  // 64-key boxes
+  CrossRowsArgs args;
+  int BH, d;
+};
+cudaError_t launch_cross_rows(const CrossRowsLaunch& a, cudaStream_t stream);
+unsigned int cross_rows_read_and_clear_status();
+
 // Backward launch description: q, k, v, dO as 3-D tensors {d, N, B*H} with
 // 64 x 128 boxes and 128-byte swizzle; delta is the caller's [B*H, N] fp32 scratch.
 struct BwdLaunch {

@@ -464,8 +464,8 @@ def fa_cross_fwd(q, k, v, o, lse, scale: float, kv_lens=None, workspace=None, st
         nbytes = workspace.numel()
     o_fp32 = o.dtype == torch.float32
     opts = ctypes.byref(FaCrossOpts(o_fp32, wait_budget_cycles)) if o_fp32 or wait_budget_cycles else None
-    _check(L.fa_cross_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, d, float(scale),
-                          _ptr(workspace), nbytes, _stream(stream), opts), func)
+    _check(L.fa_cross_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, d,
+                          float(scale), _ptr(workspace), nbytes, _stream(stream), opts), func)
 
 
 def fa_cross_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
