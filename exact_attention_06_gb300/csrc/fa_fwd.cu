@@ -130,7 +130,7 @@ struct PersistCfg : FwdCfg<64> {
   static constexpr int THREADS = (WARP_TMA + 1) * 32;
   static constexpr int B_Q = 0, B_QE = B_Q + 1, B_KF = B_QE + 1, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST,
                        B_SF = B_VE + VST, B_PF = B_SF + 2, B_SC = B_PF + 2, B_OF = B_SC + 2, B_DRAIN = B_OF + 2,
-                       B_OSF = B_DRAIN + N_ISSUERS, B_OW = B_OSF + 2, NBAR = B_OW + 2;
+                       B_OSF = B_DRAIN + N_ISSUERS, B_OW = B_OSF + 2, B_VC = B_OW + 2, NBAR = B_VC + VST;
   static constexpr uint32_t OFF_BAR = OFF_V + VST * KVB;
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR;
   static constexpr uint32_t OFF_O = (OFF_MISC + 16u + 1023u) & ~1023u;
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
   const float* __restrict__ sq = aux.sq;
   const float* __restrict__ sk = aux.sk;
   const float* __restrict__ sv = aux.sv;
-  static_assert(!CROSS || (!CAUSAL && !FP8), "cross attention is not causal, and bf16");
+  static_assert(!CROSS || (D == 128 && !CAUSAL && !FP8), "cross attention at d = 64 runs the persistent kernel");
   int Nk = aux.Nk;                // this launch's (CROSS: this CTA's) keys
   const int koff = aux.koff;      // global index of key 0
   int kload0 = aux.kload0;        // its row in the k, v tensors
@@ -644,7 +644,6 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
             tc_commit(BAR(C::B_KE + (j + 1) % C::KST));
           }
           ok = wait(BAR(C::B_PF + t), j & 1) && wait(BAR(C::B_VF + j % C::VST), (j / C::VST) & 1);
-          if (CROSS && ok && v_tail && j == n - 1) ok = wait(BAR(C::B_VC), 0);
           if (!ok) break;
           tc_fence_after();
           issue_pv(j);
@@ -947,11 +946,14 @@ __global__ void __launch_bounds__(FwdCfg<D, FP8>::THREADS, 1)
 // each tile's PV products by a thread of its own.
 struct FwdItem {
   int bh, pair, koff, kload, Nk, n0, n1;
+  int tile;     // the one query tile of a query-split item (-1: both)
+  bool v_tail;  // CROSS: rows of V behind the sequence share the item's last tile
   bool to_part;
   long long srow0;  // partial slot of flat row r (= b*h*N + n): (r - srow0) * smul + sadd
   int smul, sadd;
 };
 
+template <bool CROSS>
 __device__ __forceinline__ FwdItem item_at(int w, const FwdAux& aux, int N) {
   FwdItem I;
   I.koff = aux.koff;
@@ -978,15 +980,26 @@ __device__ __forceinline__ FwdItem item_at(int w, const FwdAux& aux, int N) {
     I.srow0 = aux.prow0;
     I.smul = aux.ksplit;
   }
+  if (CROSS && aux.S > 1) {  // the key ranges of a block are items of their own
+    u = w / aux.S;
+    I.sadd = w % aux.S;
+    I.kload = I.sadd * aux.kchunk;
+  }
   I.bh = u / n_pairs;
   I.pair = u % n_pairs;
+  if constexpr (CROSS) {
+    const int len = aux.kv_lens ? min(max(aux.kv_lens[I.bh / aux.kv_heads], 0), aux.Nk) : aux.Nk;
+    I.Nk = min(max(len - I.kload, 0), aux.kchunk);
+    I.v_tail = len < aux.Nk && len % kBc != 0 && len > I.kload && len - I.kload <= aux.kchunk;
+  }
   const int n_tiles = (I.Nk + kBc - 1) / kBc;
+  I.tile = tile;
   I.n0 = tile == 1 ? 0 : n_tiles;  // tile 0 of a block is inside N; a query-split item runs one of the two
   I.n1 = (tile != 0 && I.pair * kRowsPerCta + kBr < N) ? n_tiles : 0;
   return I;
 }
 
-template <int D>
+template <int D, bool CROSS = false>
 __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
     fwd_persist_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, void* __restrict__ o, float* __restrict__ lse,
@@ -1032,6 +1045,8 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
       mbar_init(BAR(C::B_OSF + t), 1);                 // O staging of tile t free again
       mbar_init(BAR(C::B_OW + t), kSoftmaxWarps * 32);  // O staging of tile t written
     }
+    if constexpr (CROSS)
+      for (int s = 0; s < C::VST; ++s) mbar_init(BAR(C::B_VC + s), kSoftmaxWarps * 32);  // V stage cleared
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -1056,7 +1071,7 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
       int k_issued = 0, v_issued = 0, q_issued = 0, kc = 0;
       bool ok = true;
       for (int w = w0, it = 0; ok && w < n_items; w += w_step, ++it) {
-        const FwdItem I = item_at(w, aux, N);
+        const FwdItem I = item_at<CROSS>(w, aux, N);
         const int n_max = max(I.n0, I.n1);
         // The previous item's Q is free once both tiles' last S MMAs have completed.
         if (it > 0 && !mbar_wait(BAR(C::B_QE), (it - 1) & 1, abort_flag, budget, &g_fwd_status)) break;
@@ -1140,9 +1155,10 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
         return mbar_wait(bar, parity, abort_flag, budget, &g_fwd_status);
       };
       int g0 = 0, g1 = 0, kc = 0;  // each tile's steps and the CTA's key tiles over the items so far
+      uint32_t tails = 0;          // CROSS: bit s: the phase of stage s's B_VC
       bool ok = true, issued = false;
       for (int w = w0, it = 0; ok && w < n_items; w += w_step, ++it) {
-        const FwdItem I = item_at(w, aux, N);
+        const FwdItem I = item_at<CROSS>(w, aux, N);
         const int n_max = max(I.n0, I.n1);
         if (s_issuer) {
           // This item's Q; a tile with no rows in the item releases its share of Q at once and
@@ -1182,6 +1198,7 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
               continue;
             }
             ok = wait(BAR(C::B_PF + t), (g + j) & 1);
+            if (CROSS && ok && I.v_tail && j + 1 == n_max) ok = wait(BAR(C::B_VC + gv % C::VST), (tails >> (gv % C::VST)) & 1);
             if (!ok) break;
             tc_fence_after();
             issue_pv(t, gv, j == 0);
@@ -1193,6 +1210,7 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
         g0 += I.n0;
         g1 += I.n1;
         kc += n_max;
+        if (CROSS && I.v_tail) tails ^= 1u << ((kc - 1) % C::VST);
       }
       if (issued) {  // all MMAs complete before TMEM is released
         tc_commit(BAR(C::B_DRAIN + role));
@@ -1217,9 +1235,10 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
     const uint32_t o_stage = base + C::OFF_O + static_cast<uint32_t>(t) * (kBr * 128u);
     int g = 0;   // this tile's steps over the items so far: the phases of its SF and OF barriers
     int gi = 0;  // this tile's O tiles staged so far: the phases of its OSF and OW barriers
+    int kc = 0;  // CROSS: the CTA's key tiles so far (ring stages)
     bool ok = true;
     for (int w = w0; ok && w < n_items; w += w_step) {
-      const FwdItem I = item_at(w, aux, N);
+      const FwdItem I = item_at<CROSS>(w, aux, N);
       const int n = t ? I.n1 : I.n0;
       // The staging is free once the previous store has read it (long done by now); one phase
       // per item whose O is staged.
@@ -1263,20 +1282,48 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
         f2_unpack(rs_a, s0, s1);
         f2_unpack(rs_b, s2, s3);
         l = fmaf(alpha, l, (s0 + s1) + (s2 + s3));
+        if constexpr (CROSS) {
+          // The last tile's V rows behind the sequence hold whatever the caller's padding does, and
+          // their P~ = 0 times an infinity or NaN there would reach U: one tile's threads clear them.
+          if (j + 1 == n && (t == 0 || I.n0 == 0) && I.v_tail) {
+            const int gv = kc + j;
+            ok = wait_all(BAR(C::B_VF + gv % C::VST), (gv / C::VST) & 1, abort_flag, budget);
+            if (!ok) break;
+            const uint32_t tile = sV + (gv % C::VST) * C::KVB;
+            for (int i = (I.Nk - j * kBc) * 8 + (threadIdx.x % (kSoftmaxWarps * 32)); i < kBc * 8; i += kSoftmaxWarps * 32)
+              sts128(tile + i * 16, 0, 0, 0, 0);
+            fence_proxy_async_smem();
+            mbar_arrive(BAR(C::B_VC + gv % C::VST));
+          }
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(BAR(C::B_PF + t));
         m2 = m_new;
       }
       if (!ok) break;
-      if (n == 0) continue;  // the tile is past N: nothing to write
+      if constexpr (CROSS) {
+        kc += max(I.n0, I.n1);
+        if (I.Nk == 0 && row < N && (I.tile < 0 || I.tile == t)) {  // no keys: O = 0, lse = -inf, or an empty partial
+          const size_t frow = static_cast<size_t>(I.bh) * N + row;
+          if (I.to_part) {
+            store_half_partial<D>(aux, (frow - I.srow0) * I.smul + I.sadd, h, true, t_o, 0.f, -INFINITY, false);
+          } else {
+            const int bytes = (o_fp32 ? 4 : 2) * (D / 2);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(o) + (frow * 2 + h) * bytes);
+            for (int i = 0; i < bytes / 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+            if (h == 0) lse[frow] = -INFINITY;
+          }
+        }
+      }
+      if (n == 0) continue;  // the tile is past N, or has no keys: nothing (more) to write
       ok = wait_all(BAR(C::B_OF + t), (g + n - 1) & 1, abort_flag, budget);  // U_t final
       if (!ok) break;
       g += n;
       tc_fence_after();
       const float l_row = l + __shfl_xor_sync(0xffffffffu, l, 16);
       // (the item is decoded again here rather than kept live through the steps)
-      const FwdItem E = item_at(w, aux, N);
+      const FwdItem E = item_at<CROSS>(w, aux, N);
       const long long frow = static_cast<long long>(E.bh) * N + row;
       if (E.to_part) {
         store_half_partial<D>(aux, static_cast<size_t>(frow - E.srow0) * E.smul + E.sadd, h, row < N, t_o, l_row, m2,
@@ -1332,15 +1379,24 @@ cudaError_t launch_kernel(Kern kern, dim3 grid, int threads, uint32_t smem, cuda
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Cross attention: one CTA per block of 256 rows of a key head and range of kchunk keys.
-template <int D>
-cudaError_t launch_cross_t(const FwdLaunch& a, cudaStream_t stream) {
-  using C = FwdCfg<D>;
+// Cross attention: at d = 128 one CTA per block of 256 rows of a key head and range of kchunk keys; at
+// d = 64 the persistent kernel over these items.
+cudaError_t launch_cross(const FwdLaunch& a, cudaStream_t stream) {
   const int n_pairs = (a.N + kRowsPerCta - 1) / kRowsPerCta;
   FwdAux aux = a.aux;
+  if (a.d == 64) {
+    const long long units = static_cast<long long>(a.BH) * n_pairs;
+    const long long items = aux.qsplit ? aux.n_full + (units - aux.n_full) * 2 : units * aux.S;
+    if (items > INT_MAX) return cudaErrorInvalidValue;
+    aux.n_items = static_cast<int>(items);
+    const dim3 grid(static_cast<unsigned>(std::min<long long>(items, a.sms)));
+    return launch_kernel(fwd_persist_kernel<64, true>, grid, PersistCfg::THREADS, PersistCfg::SMEM, stream, a.tq, a.tk,
+                         a.tv, a.o, a.lse, a.N, a.scale_log2, a.o_fp32, a.budget, aux, a.to);
+  }
+  using C = FwdCfg<128>;
   aux.ng = head_groups(a.BH, n_pairs, false, a.sms);
   const dim3 grid(static_cast<unsigned>(a.BH), static_cast<unsigned>(n_pairs), static_cast<unsigned>(aux.S));
-  return launch_kernel(fwd_kernel<D, false, false, true>, grid, C::THREADS, C::SMEM, stream, a.tq, a.tk, a.tv, a.o,
+  return launch_kernel(fwd_kernel<128, false, false, true>, grid, C::THREADS, C::SMEM, stream, a.tq, a.tk, a.tv, a.o,
                        a.lse, a.N, a.scale_log2, a.o_fp32, a.budget, aux, a.to);
 }
 
@@ -1373,7 +1429,7 @@ cudaError_t launch_t(const FwdLaunch& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_fwd(const FwdLaunch& a, cudaStream_t stream) {
-  if (a.cross) return a.d == 64 ? launch_cross_t<64>(a, stream) : launch_cross_t<128>(a, stream);
+  if (a.cross) return launch_cross(a, stream);
   if (a.fp8) return a.causal ? launch_t<128, true, true>(a, stream) : launch_t<128, false, true>(a, stream);
   if (a.d == 64) return a.causal ? launch_t<64, true>(a, stream) : launch_t<64, false>(a, stream);
   return a.causal ? launch_t<128, true>(a, stream) : launch_t<128, false>(a, stream);

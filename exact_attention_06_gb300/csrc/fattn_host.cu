@@ -984,6 +984,14 @@ fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int*
   a.aux.kv_heads = Hkv;
   a.aux.kchunk = plan.kchunk;
   a.aux.S = plan.splits;
+  if (d == 64 && plan.splits == 1) {
+    // The persistent kernel's last round, when at most half full, as single query tiles (as fa_fwd_ex).
+    const long long units = c.bh * ((c.rows + 255) / 256), rem = units % sms;
+    if (rem > 0 && 2 * rem <= sms && units + rem <= INT_MAX) {
+      a.aux.qsplit = 1;
+      a.aux.n_full = static_cast<int>(units - rem);
+    }
+  }
   a.aux.u_part = u_part;
   a.aux.m_part = m_part;
   a.aux.l_part = l_part;

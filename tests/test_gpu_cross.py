@@ -134,6 +134,26 @@ def test_backward(B, Hq, Hkv, Nq, Nk, lens, d):
             assert (got["dk"][b, :, n:] == 0).all() and (got["dv"][b, :, n:] == 0).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,Nk", [(64, 8, 8, 40, 100), (100, 6, 3, 70, 130), (30, 8, 8, 300, 257)])
+def test_many_blocks_of_few_keys(B, Hq, Hkv, Nq, Nk, d):
+    """More blocks than SMs, each with a tile or two of keys and padding (or nothing) behind them."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(-1, Nk + 2, (B,), generator=g).tolist()
+    q, k, v, do, kl = _inputs(B, Hq, Hkv, Nq, Nk, d, lens)
+    scale = d ** -0.5
+    o, lse = _fwd(q, k, v, kl, scale)
+    _check_fwd(o, lse, q, k, v, scale, lens)
+    ref, _, otol, _, eps = _bounds(q, k, v, scale, lens)
+    want, bound = oc.cross_backward(q, k, v, do, scale, lens, rel=U + 4 * eps + 2.0 ** -10,
+                                    o_err=otol + U * (np.abs(ref) + otol))
+    got = {n: torch.full(x.shape, float("nan"), device=DEV) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+    fattn.fa_cross_bwd(q, k, v, o, do, lse, *got.values(), scale, kv_lens=kl)
+    assert fattn.fa_get_status() == fattn.FA_OK
+    for n, x in got.items():
+        _inside(x, want[n], bound[n] * (1 + 2.0 ** -6) + 1e-30, n)
+
+
 def test_a_peaked_softmax():
     """Keys x8 (scores far apart): the running maximum moves, most probabilities vanish."""
     B, H, Nq, Nk, d, lens = 1, 2, 200, 700, 128, [650]
