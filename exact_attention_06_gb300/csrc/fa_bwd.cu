@@ -140,24 +140,26 @@ __device__ __forceinline__ void store_grad_half_row(void* out, size_t row_off, i
   }
 }
 
-// d = 128, one thread per row: a 128-column fp32 tile row in TMEM * scale -> global (fp32), or as
-// bf16 into the staged tile (box0: columns 0..63, box1: 64..127, 128-byte swizzle).
-__device__ __forceinline__ void store_grad_row128(void* out, size_t row_off, bool valid, uint32_t taddr, float scale) {
+// One thread per row: a D-column fp32 tile row in TMEM * scale -> global (fp32), or as bf16 into the
+// staged tile (box0: columns 0..63, box1: 64..127, 128-byte swizzle).
+template <int D>
+__device__ __forceinline__ void store_grad_row(void* out, size_t row_off, bool valid, uint32_t taddr, float scale) {
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
+  for (int half = 0; half < D / 64; ++half) {
     uint32_t ur[64];
     tmem_ld_x64(taddr + 64u * half, ur);
     if (!valid) continue;
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + row_off * 128 + 64 * half);
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + row_off * D + 64 * half);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       dst[i] = make_float4(__uint_as_float(ur[4 * i]) * scale, __uint_as_float(ur[4 * i + 1]) * scale,
                            __uint_as_float(ur[4 * i + 2]) * scale, __uint_as_float(ur[4 * i + 3]) * scale);
   }
 }
-__device__ __forceinline__ void stage_row128_bf16(uint32_t box0, uint32_t box1, int r, uint32_t taddr, float scale) {
+template <int D>
+__device__ __forceinline__ void stage_row_bf16(uint32_t box0, uint32_t box1, int r, uint32_t taddr, float scale) {
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
+  for (int half = 0; half < D / 64; ++half) {
     uint32_t ur[64];
     tmem_ld_x64(taddr + 64u * half, ur);
     const uint32_t srow = (half ? box1 : box0) + static_cast<uint32_t>(r) * 128u;
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
                     void* __restrict__ dv, int N, float sl2, float scale, int grad_fp32,
                     unsigned long long budget, const __grid_constant__ CUtensorMap tdk,
                     const __grid_constant__ CUtensorMap tdv, int ng, const CrossArgs x) {
-  static_assert(!CROSS || !CAUSAL, "cross attention is not causal");
+  static_assert(!CROSS || (D == 128 && !CAUSAL), "cross attention at d = 64 has its own kernels");
   using C = DkdvCfg<D>;
   using W = BwdWarps<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -580,7 +582,6 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           uint32_t pp[16], dp[16];
           if (diag) ew_pairs_dkdv<true>(sv, pv, nv, c2, 64 * q + 32 * h, qt * kTile, key, pp, dp);
           else ew_pairs_dkdv<false>(sv, pv, nv, c2, 64 * q + 32 * h, qt * kTile, key, pp, dp);
-          if (CROSS && key >= lim) clear_pairs(pp, dp);
           tmem_st2_x16<32>(tA + 64 * q, pp);  // P^T packed: columns 64q + 32h .. + 15
           tmem_st2_x16<32>(tB + 64 * q, dp);  // dS^T packed
           tmem_wait_st();
@@ -624,8 +625,8 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
       const size_t row_off = static_cast<size_t>(bh) * n_keys + key;
       if (grad_fp32) {
         if constexpr (W::ONE) {
-          store_grad_row128(dv, row_off, key < n_keys, tmem + lane_addr + kColG1, 1.f);
-          store_grad_row128(dk, row_off, key < n_keys, tmem + lane_addr + C::COL_G2, scale);
+          store_grad_row<D>(dv, row_off, key < n_keys, tmem + lane_addr + kColG1, 1.f);
+          store_grad_row<D>(dk, row_off, key < n_keys, tmem + lane_addr + C::COL_G2, scale);
         } else {
           store_grad_half_row<D>(dv, row_off, h, key < n_keys, true, tmem + lane_addr + kColG1, 1.f);
           store_grad_half_row<D>(dk, row_off, h, key < n_keys, true, tmem + lane_addr + C::COL_G2, scale);
@@ -634,8 +635,8 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
         // bf16 dV and dK through shared memory: the V and K tiles have their shape and are no
         // longer read (every product MMA is complete); one thread stores them with TMA.
         if constexpr (W::ONE) {
-          stage_row128_bf16(sV, sV + kBox, r, tmem + lane_addr + kColG1, 1.f);
-          stage_row128_bf16(sK, sK + kBox, r, tmem + lane_addr + C::COL_G2, scale);
+          stage_row_bf16<D>(sV, sV + kBox, r, tmem + lane_addr + kColG1, 1.f);
+          stage_row_bf16<D>(sK, sK + kBox, r, tmem + lane_addr + C::COL_G2, scale);
         } else {
           stage_half_row_bf16<D>(sV, sV + kBox, r, h, tmem + lane_addr + kColG1, 1.f);
           stage_half_row_bf16<D>(sK, sK + kBox, r, h, tmem + lane_addr + C::COL_G2, scale);
@@ -686,7 +687,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
                   const float* __restrict__ lse, const float* __restrict__ delta, void* __restrict__ dq, int N,
                   float sl2, float scale, int grad_fp32, unsigned long long budget,
                   const __grid_constant__ CUtensorMap tdq, int ng, const CrossArgs x) {
-  static_assert(!CROSS || !CAUSAL, "cross attention is not causal");
+  static_assert(!CROSS || (D == 128 && !CAUSAL), "cross attention at d = 64 has its own kernels");
   using C = DqCfg<D>;
   using W = BwdWarps<D>;  // thread = query row here
   extern __shared__ uint8_t smem_raw[];
@@ -892,7 +893,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           uint32_t dp[16];
           const int key0 = (j0 + j) * kTile + 64 * h + 32 * c;
           // only the diagonal and the ragged last key tile reach past this row's last key
-          if (key0 + 31 > lim) ew_pairs_dq<true, CROSS>(sv, pv, c2, nl2, nd2, key0, lim, dp);
+          if (key0 + 31 > lim) ew_pairs_dq<true>(sv, pv, c2, nl2, nd2, key0, lim, dp);
           else ew_pairs_dq<false>(sv, pv, c2, nl2, nd2, key0, lim, dp);
           tmem_st2_x16<64>(tB + 16 * c, dp);  // dS packed into dP's columns 64h + 16c ..
           tmem_wait_st();
@@ -905,11 +906,11 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
     if (ok) {
       tc_fence_after();
       if (grad_fp32) {
-        if constexpr (W::ONE) store_grad_row128(dq, static_cast<size_t>(bh) * N + row, in, tmem + lane_addr + kColG1, scale);
+        if constexpr (W::ONE) store_grad_row<D>(dq, static_cast<size_t>(bh) * N + row, in, tmem + lane_addr + kColG1, scale);
         else store_grad_half_row<D>(dq, static_cast<size_t>(bh) * N + row, h, in, true, tmem + lane_addr + kColG1, scale);
       } else {
         // bf16 dQ through shared memory: the Q tile has its shape and is no longer read
-        if constexpr (W::ONE) stage_row128_bf16(sQ, sQ + kBox, r, tmem + lane_addr + kColG1, scale);
+        if constexpr (W::ONE) stage_row_bf16<D>(sQ, sQ + kBox, r, tmem + lane_addr + kColG1, scale);
         else stage_half_row_bf16<D>(sQ, sQ + kBox, r, h, tmem + lane_addr + kColG1, scale);
         mbar_arrive(BAR(C::B_OW));
         if (warp == 0 && lane == 0 && bwait(BAR(C::B_OW), 0, abort_flag, budget)) {
@@ -928,6 +929,418 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
   if (warp == W::MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// --------------------------------------------------------------------- cross attention, d = 64: two blocks per SM
+// At d = 64 the MMAs are short (N = 64) and one block, whose steps are a chain of products, elementwise
+// work and gradients, leaves the tensor core idle for half of it.  These kernels take the scanned side in
+// halves of 64 rows, so that S and dP need 64 TMEM columns each and a block 256 of the 512: two blocks
+// share an SM and one's products run under the other's elementwise step.  Four elementwise warps, one
+// thread per row (192 threads, 168 registers twice over), two chunks of 32 columns a half; two-stage ring.
+constexpr int kHalf = kTile / 2;
+constexpr int kW64Mma = 4, kW64Tma = 5, kThreads64 = 192;
+constexpr uint32_t kTmemCols64 = 256;
+constexpr uint32_t kBox64 = kBox;  // a 128-row x 64-column bf16 tile is one box
+
+struct Cross64Cfg {
+  static constexpr int ST = 2;
+  static constexpr uint32_t OFF_A = 0, OFF_B = kBox64;  // the block's own tiles: K, V or Q, dO
+  static constexpr uint32_t OFF_RING = 2 * kBox64;      // stage: Q_i, dO_i or K_j, V_j
+  static constexpr uint32_t STAGE = 2 * kBox64;
+  static constexpr uint32_t OFF_VEC = OFF_RING + ST * STAGE;  // dK/dV: -lse2, -D of the stage's rows (see DkdvCfg)
+  static constexpr uint32_t VEC = 2 * kTile * 4;
+  static constexpr uint32_t OFF_BAR = OFF_VEC + ST * VEC;
+  static constexpr int B_OWN = 0, B_FULL = 1, B_EMPTY = B_FULL + ST, B_SF = B_EMPTY + ST, B_PF = B_SF + 1,
+                       B_GF = B_PF + 2, B_DRAIN = B_GF + 1, B_OW = B_DRAIN + 1, B_KC = B_OW + 1, NBAR = B_KC + 1;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR;
+  static constexpr uint32_t SMEM = OFF_MISC + 16u + 1024u;
+  static_assert(2 * (SMEM + 1024) <= 233472, "two blocks per SM");
+};
+
+// Products of a 128-row tile A with rows 64 q .. of a streamed tile: 128 x 64, K = 64.
+__device__ __forceinline__ void issue_half_product(uint32_t d_tmem, uint64_t da, uint64_t db, int q) {
+  constexpr uint32_t idesc = idesc_bf16_f32(kTile, kHalf, 0);
+  issue_product<64>(d_tmem, da, sdesc_add(db, static_cast<uint32_t>(q) * kHalf * 128u), idesc);
+}
+// G (+)= X Y for chunk c (32 of the half's 64 rows): X packed at columns 16 c .., Y rows 64 q + 32 c ..
+__device__ __forceinline__ void issue_half_chunk(uint32_t g_tmem, uint32_t x_tmem, uint64_t dy, int q, int c,
+                                                 bool accumulate) {
+  issue_grad_chunk(g_tmem, x_tmem, sdesc_add(dy, static_cast<uint32_t>(q) * kHalf * 128u),
+                   idesc_bf16_f32(kTile, 64, 1), accumulate, c);
+}
+
+// TMEM: S^T at 0 (P^T packed into it), dP^T at 64 (dS^T packed into it), dV at 128, dK at 192.
+__global__ void __launch_bounds__(kThreads64, 2)
+    cross_dkdv64_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                        const float* __restrict__ lse, const float* __restrict__ delta, void* __restrict__ dk,
+                        void* __restrict__ dv, int N, float sl2, float scale, int grad_fp32, unsigned long long budget,
+                        const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv, int ng,
+                        const CrossArgs x) {
+  using C = Cross64Cfg;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t sK = base + C::OFF_A, sV = base + C::OFF_B, sRing = base + C::OFF_RING, sBar = base + C::OFF_BAR;
+  float* vec = reinterpret_cast<float*>(gbase + C::OFF_VEC);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 4);
+#define BAR(i) (sBar + 8u * static_cast<uint32_t>(i))
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int bh, kt;
+  grouped_block(ng, bh, kt);
+  const int row0 = static_cast<int>(blockIdx.z) * x.tiles * kTile;  // this block's query rows
+  const int n_h = (min(x.tiles * kTile, N - row0) + kHalf - 1) / kHalf, n_i = (n_h + 1) / 2;
+  if (x.part_stride) {
+    dk = static_cast<float*>(dk) + blockIdx.z * x.part_stride;
+    dv = static_cast<float*>(dv) + blockIdx.z * x.part_stride;
+  }
+  const int lim = x.keys(bh);
+  if (kt * kTile >= lim) {  // padding only
+    const size_t k0 = static_cast<size_t>(bh) * x.n_keys + kt * kTile;
+    const int rows = min(kTile, x.n_keys - kt * kTile);
+    zero_rows<64>(dk, k0, rows, grad_fp32);
+    zero_rows<64>(dv, k0, rows, grad_fp32);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(BAR(C::B_OWN), 1);
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(BAR(C::B_FULL + s), 1 + 32);  // TMA bytes + the producer warp's lse/D stores
+      mbar_init(BAR(C::B_EMPTY + s), 1);
+    }
+    mbar_init(BAR(C::B_SF), 1);
+    for (int c = 0; c < 2; ++c) mbar_init(BAR(C::B_PF + c), 128);
+    mbar_init(BAR(C::B_GF), 1);
+    mbar_init(BAR(C::B_DRAIN), 1);
+    mbar_init(BAR(C::B_OW), 128);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kW64Mma) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols64);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  constexpr uint32_t kS = 0, kP = 64, kV = 128, kK = 192;
+
+  if (warp == kW64Tma) {
+    // ------------------------------------------------------------ producer (whole warp)
+    if (lane == 0) {
+      tma_prefetch_desc(&tq);
+      tma_prefetch_desc(&tdo);
+      mbar_arrive_expect_tx(BAR(C::B_OWN), 2 * kBox64);
+      tma_load_3d(sK, &tk, BAR(C::B_OWN), 0, kt * kTile, bh);
+      tma_load_3d(sV, &tv, BAR(C::B_OWN), 0, kt * kTile, bh);
+    }
+    int issued = 0;
+    for (int i = 0; i < n_i; ++i) {
+      const int s = i % C::ST;
+      if (i >= C::ST && !bwait_all(BAR(C::B_EMPTY + s), ((i / C::ST) - 1) & 1, abort_flag, budget)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * kBox64);
+        tma_load_3d(sRing + s * C::STAGE, &tq, BAR(C::B_FULL + s), 0, row0 + i * kTile, bh);
+        tma_load_3d(sRing + s * C::STAGE + kBox64, &tdo, BAR(C::B_FULL + s), 0, row0 + i * kTile, bh);
+      }
+      float* vs = vec + s * (2 * kTile);
+#pragma unroll
+      for (int c = 0; c < kTile / 32; ++c) {  // rows past N get -lse = -inf, so P = 0
+        const int col = 32 * c + lane, r = row0 + i * kTile + col;
+        const bool in = r < N;
+        vs[4 * (col >> 1) + (col & 1)] = in ? -lse[static_cast<size_t>(bh) * N + r] * kLog2e : -INFINITY;
+        vs[4 * (col >> 1) + 2 + (col & 1)] = in ? -delta[static_cast<size_t>(bh) * N + r] : 0.f;
+      }
+      mbar_arrive(BAR(C::B_FULL + s));
+      issued = i + 1;
+    }
+    if (lane == 0) {
+      bdrain(BAR(C::B_OWN), 0, budget);
+      for (int i = max(0, issued - C::ST); i < issued; ++i) bdrain(BAR(C::B_FULL + i % C::ST), (i / C::ST) & 1, budget);
+    }
+  } else if (warp == kW64Mma) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint64_t dK = sdesc_sw128(sK, 16, 1024), dV = sdesc_sw128(sV, 16, 1024);
+      const uint64_t dR = sdesc_sw128(sRing, 16, 1024), dRmn = sdesc_sw128(sRing, kBox64, 1024);
+      auto products = [&](int hh) {
+        const uint32_t st = ((hh >> 1) % C::ST) * C::STAGE;
+        issue_half_product(tmem + kS, dK, sdesc_add(dR, st), hh & 1);            // S^T = K Q^T
+        issue_half_product(tmem + kP, dV, sdesc_add(dR, st + kBox64), hh & 1);   // dP^T = V dO^T
+        tc_commit(BAR(C::B_SF));
+      };
+      bool ok = bwait(BAR(C::B_OWN), 0, abort_flag, budget) && bwait(BAR(C::B_FULL), 0, abort_flag, budget);
+      if (ok) {
+        tc_fence_after();
+        products(0);
+      }
+      for (int hh = 0; ok && hh < n_h; ++hh) {
+        const uint32_t st = ((hh >> 1) % C::ST) * C::STAGE;
+        for (int c = 0; ok && c < 2; ++c) {
+          ok = bwait(BAR(C::B_PF + c), hh & 1, abort_flag, budget);
+          if (!ok) break;
+          tc_fence_after();
+          issue_half_chunk(tmem + kV, tmem + kS, sdesc_add(dRmn, st + kBox64), hh & 1, c, hh > 0 || c > 0);  // dV += P^T dO
+          issue_half_chunk(tmem + kK, tmem + kP, sdesc_add(dRmn, st), hh & 1, c, hh > 0 || c > 0);           // dK += dS^T Q
+        }
+        if (!ok) break;
+        if (hh & 1) tc_commit(BAR(C::B_EMPTY + (hh >> 1) % C::ST));  // Q_i, dO_i fully read
+        if (hh + 1 < n_h) {
+          // (into the columns that the gradient MMAs above read: they were issued first, and MMAs
+          // complete in issue order)
+          const int i = (hh + 1) >> 1;
+          if ((hh & 1) && !bwait(BAR(C::B_FULL + i % C::ST), (i / C::ST) & 1, abort_flag, budget)) break;
+          tc_fence_after();
+          products(hh + 1);
+        }
+      }
+      tc_commit(BAR(C::B_GF));
+      tc_commit(BAR(C::B_DRAIN));
+      bdrain(BAR(C::B_DRAIN), 0, budget);
+    }
+  } else {
+    // ------------------------------------------------------------ elementwise warps: thread = key row
+    const int r = 32 * warp + lane, key = kt * kTile + r;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const uint64_t c2 = f2_pack(sl2, sl2);
+    bool ok = true;
+    for (int hh = 0; ok && hh < n_h; ++hh) {
+      const int i = hh >> 1, s = i % C::ST;
+      ok = ((hh & 1) || bwait_all(BAR(C::B_FULL + s), (i / C::ST) & 1, abort_flag, budget)) &&
+           bwait_all(BAR(C::B_SF), hh & 1, abort_flag, budget);
+      if (!ok) break;
+      tc_fence_after();
+      const float4* nv = reinterpret_cast<const float4*>(vec + s * (2 * kTile));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t sv[32], pv[32];
+        tmem_ld_x32(lanes + kS + 32 * c, sv);
+        tmem_ld_x32(lanes + kP + 32 * c, pv);
+        uint32_t pp[16], dp[16];
+        ew_pairs_dkdv<false>(sv, pv, nv, c2, kHalf * (hh & 1) + 32 * c, 0, 0, pp, dp);
+        if (key >= lim) clear_pairs(pp, dp);
+        tmem_st1_x16(lanes + kS + 16 * c, pp);
+        tmem_st1_x16(lanes + kP + 16 * c, dp);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(BAR(C::B_PF + c));
+      }
+    }
+    if (ok) ok = bwait_all(BAR(C::B_GF), 0, abort_flag, budget);
+    if (ok) {
+      tc_fence_after();
+      const size_t row_off = static_cast<size_t>(bh) * x.n_keys + key;
+      if (grad_fp32) {
+        store_grad_row<64>(dv, row_off, key < x.n_keys, lanes + kV, 1.f);
+        store_grad_row<64>(dk, row_off, key < x.n_keys, lanes + kK, scale);
+      } else {  // through shared memory: the V and K tiles have their shape and are no longer read
+        stage_row_bf16<64>(sV, sV, r, lanes + kV, 1.f);
+        stage_row_bf16<64>(sK, sK, r, lanes + kK, scale);
+        mbar_arrive(BAR(C::B_OW));
+        if (warp == 0 && lane == 0 && bwait(BAR(C::B_OW), 0, abort_flag, budget)) {
+          tma_store_3d(&tdv, sV, 0, kt * kTile, bh);
+          tma_store_3d(&tdk, sK, 0, kt * kTile, bh);
+          bulk_commit();
+          bulk_wait_all();  // complete before the CTA exits
+        }
+      }
+    }
+    tmem_wait_st();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kW64Mma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols64);
+  }
+}
+
+// TMEM: S of even halves at 0, of odd ones at 64, dP at 128 (dS packed into it), dQ at 192.
+__global__ void __launch_bounds__(kThreads64, 2)
+    cross_dq64_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                      const float* __restrict__ lse, const float* __restrict__ delta, void* __restrict__ dq, int N,
+                      float sl2, float scale, int grad_fp32, unsigned long long budget,
+                      const __grid_constant__ CUtensorMap tdq, int ng, const CrossArgs x) {
+  using C = Cross64Cfg;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t sQ = base + C::OFF_A, sDO = base + C::OFF_B, sRing = base + C::OFF_RING, sBar = base + C::OFF_BAR;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int bh, qt;
+  grouped_block(ng, bh, qt);
+  const int key0 = static_cast<int>(blockIdx.z) * x.tiles * kTile;  // this block's keys
+  const int n_keys = x.keys(bh);
+  const int mine = min(x.tiles * kTile, n_keys - key0);
+  if (x.part_stride) dq = static_cast<float*>(dq) + blockIdx.z * x.part_stride;
+  if (mine <= 0) {  // no key in this range
+    zero_rows<64>(dq, static_cast<size_t>(bh) * N + qt * kTile, min(kTile, N - qt * kTile), grad_fp32);
+    return;
+  }
+  const int n_h = (mine + kHalf - 1) / kHalf, n_j = (n_h + 1) / 2;
+  const bool k_tail = mine % kTile != 0 && n_keys < x.n_keys;  // rows behind the sequence in K's last tile
+  if (threadIdx.x == 0) {
+    mbar_init(BAR(C::B_OWN), 1);
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(BAR(C::B_FULL + s), 1);
+      mbar_init(BAR(C::B_EMPTY + s), 1);
+    }
+    mbar_init(BAR(C::B_SF), 1);
+    for (int c = 0; c < 2; ++c) mbar_init(BAR(C::B_PF + c), 128);
+    mbar_init(BAR(C::B_DRAIN), 1);
+    mbar_init(BAR(C::B_OW), 128);
+    mbar_init(BAR(C::B_KC), 32);  // K's last tile cleared behind the sequence
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kW64Mma) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols64);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  constexpr uint32_t kP = 128, kG = 192;
+
+  if (warp == kW64Tma) {
+    int issued = 0;
+    if (lane == 0) {
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+      mbar_arrive_expect_tx(BAR(C::B_OWN), 2 * kBox64);
+      tma_load_3d(sQ, &tq, BAR(C::B_OWN), 0, qt * kTile, bh);
+      tma_load_3d(sDO, &tdo, BAR(C::B_OWN), 0, qt * kTile, bh);
+      for (int j = 0; j < n_j; ++j) {
+        const int s = j % C::ST;
+        if (j >= C::ST && !bwait(BAR(C::B_EMPTY + s), ((j / C::ST) - 1) & 1, abort_flag, budget)) break;
+        mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * kBox64);
+        tma_load_3d(sRing + s * C::STAGE, &tk, BAR(C::B_FULL + s), 0, key0 + j * kTile, bh);
+        tma_load_3d(sRing + s * C::STAGE + kBox64, &tv, BAR(C::B_FULL + s), 0, key0 + j * kTile, bh);
+        issued = j + 1;
+      }
+    }
+    // dQ = dS K multiplies the last tile's K rows behind the sequence by dS = 0: clear what the
+    // caller's padding holds there (0 times an infinity or NaN).
+    issued = __shfl_sync(0xffffffffu, issued, 0);
+    if (k_tail && issued == n_j) {
+      const int last = n_j - 1;
+      if (bwait_all(BAR(C::B_FULL + last % C::ST), (last / C::ST) & 1, abort_flag, budget)) {
+        const uint32_t tile = sRing + (last % C::ST) * C::STAGE;
+        for (int i = (mine - last * kTile) * 8 + lane; i < kTile * 8; i += 32) sts128(tile + i * 16, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+        mbar_arrive(BAR(C::B_KC));
+      }
+    }
+    if (lane == 0) {
+      bdrain(BAR(C::B_OWN), 0, budget);
+      for (int j = max(0, issued - C::ST); j < issued; ++j) bdrain(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, budget);
+    }
+  } else if (warp == kW64Mma) {
+    if (lane == 0) {
+      const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dDO = sdesc_sw128(sDO, 16, 1024);
+      const uint64_t dR = sdesc_sw128(sRing, 16, 1024), dRmn = sdesc_sw128(sRing, kBox64, 1024);
+      auto issue_s = [&](int hh) {  // S = Q K^T
+        issue_half_product(tmem + ((hh & 1) ? 64u : 0u), dQ, sdesc_add(dR, ((hh >> 1) % C::ST) * C::STAGE), hh & 1);
+      };
+      auto issue_dp = [&](int hh) {  // dP = dO V^T
+        issue_half_product(tmem + kP, dDO, sdesc_add(dR, ((hh >> 1) % C::ST) * C::STAGE + kBox64), hh & 1);
+      };
+      auto issue_g = [&](int hh, int c) {  // dQ += dS K
+        issue_half_chunk(tmem + kG, tmem + kP, sdesc_add(dRmn, ((hh >> 1) % C::ST) * C::STAGE), hh & 1, c,
+                         hh > 0 || c > 0);
+      };
+      auto full = [&](int j) {  // K_j, V_j loaded (and cleared behind the sequence)
+        return bwait(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, abort_flag, budget) &&
+               (!k_tail || j + 1 < n_j || bwait(BAR(C::B_KC), 0, abort_flag, budget));
+      };
+      bool ok = bwait(BAR(C::B_OWN), 0, abort_flag, budget) && full(0);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0);
+        issue_dp(0);
+        tc_commit(BAR(C::B_SF));
+      }
+      for (int hh = 0; ok && hh < n_h; ++hh) {
+        // the first chunk's dQ MMAs, then S of the next half (under the second chunk's elementwise
+        // work), then the second chunk's and the next dP, whose columns they free
+        if (!bwait(BAR(C::B_PF), hh & 1, abort_flag, budget)) break;
+        tc_fence_after();
+        issue_g(hh, 0);
+        if (hh + 1 < n_h) {
+          if ((hh & 1) && !full((hh + 1) >> 1)) break;
+          tc_fence_after();
+          issue_s(hh + 1);
+        }
+        if (!bwait(BAR(C::B_PF + 1), hh & 1, abort_flag, budget)) break;
+        tc_fence_after();
+        issue_g(hh, 1);
+        if (hh & 1) tc_commit(BAR(C::B_EMPTY + (hh >> 1) % C::ST));
+        if (hh + 1 < n_h) issue_dp(hh + 1);
+        tc_commit(BAR(C::B_SF));
+      }
+      tc_commit(BAR(C::B_DRAIN));
+      bdrain(BAR(C::B_DRAIN), 0, budget);
+    }
+  } else {
+    // ------------------------------------------------------------ elementwise warps: thread = query row
+    const int r = 32 * warp + lane, row = qt * kTile + r;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const bool in = row < N;
+    const float lse2 = in ? lse[static_cast<size_t>(bh) * N + row] * kLog2e : INFINITY;
+    const float dd = in ? delta[static_cast<size_t>(bh) * N + row] : 0.f;
+    const uint64_t c2 = f2_pack(sl2, sl2), nl2 = f2_pack(-lse2, -lse2), nd2 = f2_pack(-dd, -dd);
+    bool ok = true;
+    for (int hh = 0; ok && hh < n_h; ++hh) {
+      ok = bwait_all(BAR(C::B_SF), hh & 1, abort_flag, budget);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t sv[32], pv[32];
+        tmem_ld_x32(lanes + ((hh & 1) ? 64u : 0u) + 32 * c, sv);
+        tmem_ld_x32(lanes + kP + 32 * c, pv);
+        uint32_t dp[16];
+        const int k0 = hh * kHalf + 32 * c;
+        if (k0 + 32 > mine) ew_pairs_dq<true, true>(sv, pv, c2, nl2, nd2, k0, mine - 1, dp);
+        else ew_pairs_dq<false>(sv, pv, c2, nl2, nd2, k0, mine - 1, dp);
+        tmem_st1_x16(lanes + kP + 16 * c, dp);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(BAR(C::B_PF + c));
+      }
+    }
+    if (ok) ok = bwait_all(BAR(C::B_SF), n_h & 1, abort_flag, budget);  // dQ final
+    if (ok) {
+      tc_fence_after();
+      if (grad_fp32) {
+        store_grad_row<64>(dq, static_cast<size_t>(bh) * N + row, in, lanes + kG, scale);
+      } else {  // through shared memory: the Q tile has its shape and is no longer read
+        stage_row_bf16<64>(sQ, sQ, r, lanes + kG, scale);
+        mbar_arrive(BAR(C::B_OW));
+        if (warp == 0 && lane == 0 && bwait(BAR(C::B_OW), 0, abort_flag, budget)) {
+          tma_store_3d(&tdq, sQ, 0, qt * kTile, bh);
+          bulk_commit();
+          bulk_wait_all();  // complete before the CTA exits
+        }
+      }
+    }
+    tmem_wait_st();
+  }
+#undef BAR
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kW64Mma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols64);
   }
 }
 
@@ -993,13 +1406,15 @@ cudaError_t launch_cross_bwd_t(const BwdLaunch& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const long long kv_elems = static_cast<long long>(a.BH) * a.Nk * D, q_elems = static_cast<long long>(a.BH) * a.N * D;
   const int k_tiles = (a.Nk + kTile - 1) / kTile, q_tiles = (a.N + kTile - 1) / kTile;
-  auto k1 = bwd_dkdv_kernel<D, false, true>;
-  if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::SMEM)) != cudaSuccess)
-    return e;
+  constexpr int threads = D == 64 ? kThreads64 : BwdWarps<128>::THREADS;
+  constexpr uint32_t smem1 = D == 64 ? Cross64Cfg::SMEM : DkdvCfg<128>::SMEM;
+  constexpr uint32_t smem2 = D == 64 ? Cross64Cfg::SMEM : DqCfg<128>::SMEM;
+  auto k1 = D == 64 ? cross_dkdv64_kernel : bwd_dkdv_kernel<128, false, true>;
+  if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1)) != cudaSuccess) return e;
   const bool kv_part = a.kv_splits > 1, q_part = a.q_splits > 1;
   const dim3 g1(static_cast<unsigned>(a.BH), static_cast<unsigned>(k_tiles), static_cast<unsigned>(a.kv_splits));
   float* dv_part = a.kv_part + a.kv_splits * kv_elems;
-  k1<<<g1, BwdWarps<D>::THREADS, DkdvCfg<D>::SMEM, stream>>>(
+  k1<<<g1, threads, smem1, stream>>>(
       a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, kv_part ? a.kv_part : a.dk, kv_part ? dv_part : a.dv, a.N, a.scale_log2,
       a.scale, kv_part || a.grad_fp32, a.budget, a.tdk, a.tdv, head_groups(a.BH, k_tiles, false, a.sms),
       CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.q_tiles, kv_part ? kv_elems : 0});
@@ -1008,11 +1423,10 @@ cudaError_t launch_cross_bwd_t(const BwdLaunch& a, cudaStream_t stream) {
     if ((e = launch_sum(a.kv_part, a.dk, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess) return e;
     if ((e = launch_sum(dv_part, a.dv, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess) return e;
   }
-  auto k2 = bwd_dq_kernel<D, false, true>;
-  if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::SMEM)) != cudaSuccess)
-    return e;
+  auto k2 = D == 64 ? cross_dq64_kernel : bwd_dq_kernel<128, false, true>;
+  if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, smem2)) != cudaSuccess) return e;
   const dim3 g2(static_cast<unsigned>(a.BH), static_cast<unsigned>(q_tiles), static_cast<unsigned>(a.q_splits));
-  k2<<<g2, BwdWarps<D>::THREADS, DqCfg<D>::SMEM, stream>>>(
+  k2<<<g2, threads, smem2, stream>>>(
       a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, q_part ? a.q_part : a.dq, a.N, a.scale_log2, a.scale,
       q_part || a.grad_fp32, a.budget, a.tdq, head_groups(a.BH, q_tiles, false, a.sms),
       CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.k_tiles, q_part ? q_elems : 0});

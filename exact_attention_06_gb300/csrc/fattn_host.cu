@@ -268,13 +268,13 @@ fa_status_t check_cross_args(int B, int Hq, int Hkv, int Nq, int Nk, int d, Cros
   return FA_OK;
 }
 
-// How often to cut a scan of `tiles` tiles when `units` blocks (one per SM at a time) each make it:
+// How often to cut a scan of `tiles` tiles when `units` blocks (`slots` at a time) each make it:
 // more, shorter blocks fill the last round of SMs, at the price of fp32 partial results and a
 // kernel that joins them.  Costs in tile steps (about 1 us): a block costs its tiles plus ~3 of
 // set-up and epilogue, joining ~3 and its traffic, 8 MB a step.  A cut has to save 5 %.
-int cut_scan(long long units, int tiles, int sms, double part_bytes) {
+int cut_scan(long long units, int tiles, int slots, double part_bytes) {
   constexpr double kFixed = 3.0, kJoin = 3.0, kStepBytes = 8e6;
-  auto rounds = [&](int s) { return static_cast<double>((units * s + sms - 1) / sms); };
+  auto rounds = [&](int s) { return static_cast<double>((units * s + slots - 1) / slots); };
   const double whole = rounds(1) * (tiles + kFixed);
   double best_t = 0.95 * whole;
   int best = 1;
@@ -357,8 +357,9 @@ CrossBwdPlan plan_cross_bwd(const CrossShape& c, int Nk, int d, int sms) {
   CrossBwdPlan p;
   const int qt = (c.rows + 127) / 128, kt = (Nk + 127) / 128;
   const double kv = 2.0 * c.bh * Nk * d * sizeof(float), q = 1.0 * c.bh * c.rows * d * sizeof(float);
-  p.kv_splits = cut_scan(c.bh * kt, qt, sms, kv);
-  p.q_splits = cut_scan(c.bh * qt, kt, sms, q);
+  const int slots = d == 64 ? 2 * sms : sms;  // (the d = 64 kernels run two blocks per SM)
+  p.kv_splits = cut_scan(c.bh * kt, qt, slots, kv);
+  p.q_splits = cut_scan(c.bh * qt, kt, slots, q);
   p.q_tiles = (qt + p.kv_splits - 1) / p.kv_splits;
   p.k_tiles = (kt + p.q_splits - 1) / p.q_splits;
   p.delta_bytes = round256(static_cast<size_t>(c.bh) * c.rows * sizeof(float));
