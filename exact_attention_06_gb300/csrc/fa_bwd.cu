@@ -932,30 +932,33 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
   }
 }
 
-// --------------------------------------------------------------------- cross attention, d = 64: two blocks per SM
-// At d = 64 the MMAs are short (N = 64) and one block, whose steps are a chain of products, elementwise
-// work and gradients, leaves the tensor core idle for half of it.  These kernels take the scanned side in
-// halves of 64 rows, so that S and dP need 64 TMEM columns each and a block 256 of the 512: two blocks
-// share an SM and one's products run under the other's elementwise step.  Four elementwise warps, one
-// thread per row (192 threads, 168 registers twice over), two chunks of 32 columns a half; two-stage ring.
+// --------------------------------------------------------------------- cross attention, d = 64: three steps in flight
+// At d = 64 the MMAs are short (N = 64) and a step is a chain -- products, their way through TMEM,
+// exponentials, P and dS back, gradients -- several times as long as its work, so the tensor core waits on
+// latency.  These kernels take the scanned side in halves of 64 rows and keep three of them in flight: S and
+// dP of a half are 64 TMEM columns each, three pairs take 384 and leave 128 for the accumulators, and each pair
+// has four elementwise warps of its own (one thread per row, two chunks of 32 columns).
 constexpr int kHalf = kTile / 2;
-constexpr int kW64Mma = 4, kW64Tma = 5, kThreads64 = 192;
-constexpr uint32_t kTmemCols64 = 256;
-constexpr uint32_t kBox64 = kBox;  // a 128-row x 64-column bf16 tile is one box
+constexpr int kFlight = 3;                       // halves in flight: half hh uses pair hh % 3
+constexpr int kEw64 = 4 * kFlight;               // elementwise warps
+constexpr int kIssuers = 3;                      // MMA-issuing threads, a warp each
+constexpr int kMma64 = kEw64, kTma64 = kEw64 + kIssuers, kThreads64 = (kTma64 + 1) * 32;
+constexpr uint32_t kPair64 = 128, kAcc64 = 384;  // TMEM: pair g: S at 128 g, dP at 128 g + 64; accumulators from 384
 
 struct Cross64Cfg {
-  static constexpr int ST = 2;
-  static constexpr uint32_t OFF_A = 0, OFF_B = kBox64;  // the block's own tiles: K, V or Q, dO
-  static constexpr uint32_t OFF_RING = 2 * kBox64;      // stage: Q_i, dO_i or K_j, V_j
-  static constexpr uint32_t STAGE = 2 * kBox64;
+  static constexpr int ST = 4;
+  static constexpr uint32_t TB = kBox;              // a 128-row x 64-column bf16 tile is one box
+  static constexpr uint32_t OFF_A = 0, OFF_B = TB;  // the block's own tiles: K, V or Q, dO
+  static constexpr uint32_t OFF_RING = 2 * TB;      // stage: Q_i, dO_i or K_j, V_j
+  static constexpr uint32_t STAGE = 2 * TB;
   static constexpr uint32_t OFF_VEC = OFF_RING + ST * STAGE;  // dK/dV: -lse2, -D of the stage's rows (see DkdvCfg)
   static constexpr uint32_t VEC = 2 * kTile * 4;
   static constexpr uint32_t OFF_BAR = OFF_VEC + ST * VEC;
-  static constexpr int B_OWN = 0, B_FULL = 1, B_EMPTY = B_FULL + ST, B_SF = B_EMPTY + ST, B_PF = B_SF + 1,
-                       B_GF = B_PF + 2, B_DRAIN = B_GF + 1, B_OW = B_DRAIN + 1, B_KC = B_OW + 1, NBAR = B_KC + 1;
+  static constexpr int B_OWN = 0, B_FULL = 1, B_EMPTY = B_FULL + ST, B_SF = B_EMPTY + ST, B_PF = B_SF + kFlight,
+                       B_GD = B_PF + 2 * kFlight, B_GF = B_GD + kFlight, B_DRAIN = B_GF + 1, B_OW = B_DRAIN + kIssuers, B_KC = B_OW + 2, NBAR = B_KC + 1;
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR;
   static constexpr uint32_t SMEM = OFF_MISC + 16u + 1024u;
-  static_assert(2 * (SMEM + 1024) <= 233472, "two blocks per SM");
+  static_assert(SMEM <= 232448, "shared memory");
 };
 
 // Products of a 128-row tile A with rows 64 q .. of a streamed tile: 128 x 64, K = 64.
@@ -970,8 +973,8 @@ __device__ __forceinline__ void issue_half_chunk(uint32_t g_tmem, uint32_t x_tme
                    idesc_bf16_f32(kTile, 64, 1), accumulate, c);
 }
 
-// TMEM: S^T at 0 (P^T packed into it), dP^T at 64 (dS^T packed into it), dV at 128, dK at 192.
-__global__ void __launch_bounds__(kThreads64, 2)
+// One CTA per key tile and range of query tiles.  P^T and dS^T are packed into their S^T and dP^T.
+__global__ void __launch_bounds__(kThreads64, 1)
     cross_dkdv64_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                         const float* __restrict__ lse, const float* __restrict__ delta, void* __restrict__ dk,
@@ -1009,32 +1012,36 @@ __global__ void __launch_bounds__(kThreads64, 2)
     mbar_init(BAR(C::B_OWN), 1);
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(BAR(C::B_FULL + s), 1 + 32);  // TMA bytes + the producer warp's lse/D stores
-      mbar_init(BAR(C::B_EMPTY + s), 1);
+      mbar_init(BAR(C::B_EMPTY + s), 2);  // dV and dK have read the stage
     }
-    mbar_init(BAR(C::B_SF), 1);
-    for (int c = 0; c < 2; ++c) mbar_init(BAR(C::B_PF + c), 128);
-    mbar_init(BAR(C::B_GF), 1);
-    mbar_init(BAR(C::B_DRAIN), 1);
+    for (int g = 0; g < kFlight; ++g) {
+      mbar_init(BAR(C::B_SF + g), 1);
+      mbar_init(BAR(C::B_GD + g), 2);  // the pair's gradient MMAs are complete
+    }
+    for (int c = 0; c < 2 * kFlight; ++c) mbar_init(BAR(C::B_PF + c), 128);
+    mbar_init(BAR(C::B_GF), 2);
+    for (int i = 0; i < kIssuers; ++i) mbar_init(BAR(C::B_DRAIN + i), 1);
     mbar_init(BAR(C::B_OW), 128);
+    mbar_init(BAR(C::B_OW + 1), 128);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kW64Mma) {
-    tmem_alloc(smem_u32(tmem_slot), kTmemCols64);
+  if (warp == kMma64) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  constexpr uint32_t kS = 0, kP = 64, kV = 128, kK = 192;
+  constexpr uint32_t kV = kAcc64, kK = kAcc64 + 64;
 
-  if (warp == kW64Tma) {
+  if (warp == kTma64) {
     // ------------------------------------------------------------ producer (whole warp)
     if (lane == 0) {
       tma_prefetch_desc(&tq);
       tma_prefetch_desc(&tdo);
-      mbar_arrive_expect_tx(BAR(C::B_OWN), 2 * kBox64);
+      mbar_arrive_expect_tx(BAR(C::B_OWN), 2 * kBox);
       tma_load_3d(sK, &tk, BAR(C::B_OWN), 0, kt * kTile, bh);
       tma_load_3d(sV, &tv, BAR(C::B_OWN), 0, kt * kTile, bh);
     }
@@ -1043,9 +1050,9 @@ __global__ void __launch_bounds__(kThreads64, 2)
       const int s = i % C::ST;
       if (i >= C::ST && !bwait_all(BAR(C::B_EMPTY + s), ((i / C::ST) - 1) & 1, abort_flag, budget)) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * kBox64);
+        mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * kBox);
         tma_load_3d(sRing + s * C::STAGE, &tq, BAR(C::B_FULL + s), 0, row0 + i * kTile, bh);
-        tma_load_3d(sRing + s * C::STAGE + kBox64, &tdo, BAR(C::B_FULL + s), 0, row0 + i * kTile, bh);
+        tma_load_3d(sRing + s * C::STAGE + kBox, &tdo, BAR(C::B_FULL + s), 0, row0 + i * kTile, bh);
       }
       float* vs = vec + s * (2 * kTile);
 #pragma unroll
@@ -1062,72 +1069,75 @@ __global__ void __launch_bounds__(kThreads64, 2)
       bdrain(BAR(C::B_OWN), 0, budget);
       for (int i = max(0, issued - C::ST); i < issued; ++i) bdrain(BAR(C::B_FULL + i % C::ST), (i / C::ST) & 1, budget);
     }
-  } else if (warp == kW64Mma) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp >= kMma64) {
+    // ------------------------------------------------------------ MMA issuers: the products, dV, dK
     if (lane == 0) {
-      const uint64_t dK = sdesc_sw128(sK, 16, 1024), dV = sdesc_sw128(sV, 16, 1024);
-      const uint64_t dR = sdesc_sw128(sRing, 16, 1024), dRmn = sdesc_sw128(sRing, kBox64, 1024);
-      auto products = [&](int hh) {
-        const uint32_t st = ((hh >> 1) % C::ST) * C::STAGE;
-        issue_half_product(tmem + kS, dK, sdesc_add(dR, st), hh & 1);            // S^T = K Q^T
-        issue_half_product(tmem + kP, dV, sdesc_add(dR, st + kBox64), hh & 1);   // dP^T = V dO^T
-        tc_commit(BAR(C::B_SF));
-      };
-      bool ok = bwait(BAR(C::B_OWN), 0, abort_flag, budget) && bwait(BAR(C::B_FULL), 0, abort_flag, budget);
-      if (ok) {
-        tc_fence_after();
-        products(0);
-      }
-      for (int hh = 0; ok && hh < n_h; ++hh) {
-        const uint32_t st = ((hh >> 1) % C::ST) * C::STAGE;
-        for (int c = 0; ok && c < 2; ++c) {
-          ok = bwait(BAR(C::B_PF + c), hh & 1, abort_flag, budget);
+      const int role = warp - kMma64;
+      bool ok = true;
+      if (role == 0) {
+        const uint64_t dK = sdesc_sw128(sK, 16, 1024), dV = sdesc_sw128(sV, 16, 1024), dR = sdesc_sw128(sRing, 16, 1024);
+        ok = bwait(BAR(C::B_OWN), 0, abort_flag, budget);
+        for (int hh = 0; ok && hh < n_h; ++hh) {
+          const int i = hh >> 1, g = hh % kFlight;
+          // the stage loaded, and the pair's last gradients done with its columns
+          ok = bwait(BAR(C::B_FULL + i % C::ST), (i / C::ST) & 1, abort_flag, budget) &&
+               (hh < kFlight || bwait(BAR(C::B_GD + g), ((hh / kFlight) - 1) & 1, abort_flag, budget));
           if (!ok) break;
           tc_fence_after();
-          issue_half_chunk(tmem + kV, tmem + kS, sdesc_add(dRmn, st + kBox64), hh & 1, c, hh > 0 || c > 0);  // dV += P^T dO
-          issue_half_chunk(tmem + kK, tmem + kP, sdesc_add(dRmn, st), hh & 1, c, hh > 0 || c > 0);           // dK += dS^T Q
+          const uint32_t st = (i % C::ST) * C::STAGE, d = tmem + kPair64 * g;
+          issue_half_product(d, dK, sdesc_add(dR, st), hh & 1);                 // S^T = K Q^T
+          issue_half_product(d + 64, dV, sdesc_add(dR, st + kBox), hh & 1);     // dP^T = V dO^T
+          tc_commit(BAR(C::B_SF + g));
         }
-        if (!ok) break;
-        if (hh & 1) tc_commit(BAR(C::B_EMPTY + (hh >> 1) % C::ST));  // Q_i, dO_i fully read
-        if (hh + 1 < n_h) {
-          // (into the columns that the gradient MMAs above read: they were issued first, and MMAs
-          // complete in issue order)
-          const int i = (hh + 1) >> 1;
-          if ((hh & 1) && !bwait(BAR(C::B_FULL + i % C::ST), (i / C::ST) & 1, abort_flag, budget)) break;
-          tc_fence_after();
-          products(hh + 1);
+      } else {
+        // dV += P^T dO (role 1), dK += dS^T Q (role 2)
+        const uint64_t dY = sdesc_add(sdesc_sw128(sRing, kBox, 1024), role == 1 ? kBox : 0u);
+        const uint32_t acc = tmem + (role == 1 ? kV : kK), x0 = tmem + (role == 1 ? 0u : 64u);
+        for (int hh = 0; ok && hh < n_h; ++hh) {
+          const int g = hh % kFlight;
+          const uint64_t dy = sdesc_add(dY, ((hh >> 1) % C::ST) * C::STAGE);
+          for (int c = 0; ok && c < 2; ++c) {
+            ok = bwait(BAR(C::B_PF + 2 * g + c), (hh / kFlight) & 1, abort_flag, budget);
+            if (!ok) break;
+            tc_fence_after();
+            issue_half_chunk(acc, x0 + kPair64 * g, dy, hh & 1, c, hh > 0 || c > 0);
+          }
+          if (!ok) break;
+          tc_commit(BAR(C::B_GD + g));
+          if (hh & 1) tc_commit(BAR(C::B_EMPTY + (hh >> 1) % C::ST));
         }
+        tc_commit(BAR(C::B_GF));
       }
-      tc_commit(BAR(C::B_GF));
-      tc_commit(BAR(C::B_DRAIN));
-      bdrain(BAR(C::B_DRAIN), 0, budget);
+      tc_commit(BAR(C::B_DRAIN + role));
+      bdrain(BAR(C::B_DRAIN + role), 0, budget);
     }
   } else {
     // ------------------------------------------------------------ elementwise warps: thread = key row
-    const int r = 32 * warp + lane, key = kt * kTile + r;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const int g = warp >> 2, r = 32 * (warp & 3) + lane, key = kt * kTile + r;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t tS = lanes + kPair64 * g, tP = tS + 64;
     const uint64_t c2 = f2_pack(sl2, sl2);
     bool ok = true;
-    for (int hh = 0; ok && hh < n_h; ++hh) {
+    for (int hh = g; ok && hh < n_h; hh += kFlight) {
       const int i = hh >> 1, s = i % C::ST;
-      ok = ((hh & 1) || bwait_all(BAR(C::B_FULL + s), (i / C::ST) & 1, abort_flag, budget)) &&
-           bwait_all(BAR(C::B_SF), hh & 1, abort_flag, budget);
+      ok = bwait_all(BAR(C::B_FULL + s), (i / C::ST) & 1, abort_flag, budget) &&
+           bwait_all(BAR(C::B_SF + g), (hh / kFlight) & 1, abort_flag, budget);
       if (!ok) break;
       tc_fence_after();
       const float4* nv = reinterpret_cast<const float4*>(vec + s * (2 * kTile));
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t sv[32], pv[32];
-        tmem_ld_x32(lanes + kS + 32 * c, sv);
-        tmem_ld_x32(lanes + kP + 32 * c, pv);
+        tmem_ld_x32(tS + 32 * c, sv);
+        tmem_ld_x32(tP + 32 * c, pv);
         uint32_t pp[16], dp[16];
         ew_pairs_dkdv<false>(sv, pv, nv, c2, kHalf * (hh & 1) + 32 * c, 0, 0, pp, dp);
         if (key >= lim) clear_pairs(pp, dp);
-        tmem_st1_x16(lanes + kS + 16 * c, pp);
-        tmem_st1_x16(lanes + kP + 16 * c, dp);
+        tmem_st1_x16(tS + 16 * c, pp);
+        tmem_st1_x16(tP + 16 * c, dp);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(BAR(C::B_PF + c));
+        mbar_arrive(BAR(C::B_PF + 2 * g + c));
       }
     }
     if (ok) ok = bwait_all(BAR(C::B_GF), 0, abort_flag, budget);
@@ -1135,15 +1145,14 @@ __global__ void __launch_bounds__(kThreads64, 2)
       tc_fence_after();
       const size_t row_off = static_cast<size_t>(bh) * x.n_keys + key;
       if (grad_fp32) {
-        store_grad_row<64>(dv, row_off, key < x.n_keys, lanes + kV, 1.f);
-        store_grad_row<64>(dk, row_off, key < x.n_keys, lanes + kK, scale);
-      } else {  // through shared memory: the V and K tiles have their shape and are no longer read
-        stage_row_bf16<64>(sV, sV, r, lanes + kV, 1.f);
-        stage_row_bf16<64>(sK, sK, r, lanes + kK, scale);
-        mbar_arrive(BAR(C::B_OW));
-        if (warp == 0 && lane == 0 && bwait(BAR(C::B_OW), 0, abort_flag, budget)) {
-          tma_store_3d(&tdv, sV, 0, kt * kTile, bh);
-          tma_store_3d(&tdk, sK, 0, kt * kTile, bh);
+        if (g == 0) store_grad_row<64>(dv, row_off, key < x.n_keys, lanes + kV, 1.f);
+        if (g == 1) store_grad_row<64>(dk, row_off, key < x.n_keys, lanes + kK, scale);
+      } else if (g < 2) {  // through shared memory: the V and K tiles have their shape and are no longer read
+        const uint32_t tile = g == 0 ? sV : sK;
+        stage_row_bf16<64>(tile, tile, r, lanes + (g == 0 ? kV : kK), g == 0 ? 1.f : scale);
+        mbar_arrive(BAR(C::B_OW + g));
+        if ((warp & 3) == 0 && lane == 0 && bwait(BAR(C::B_OW + g), 0, abort_flag, budget)) {
+          tma_store_3d(g == 0 ? &tdv : &tdk, tile, 0, kt * kTile, bh);
           bulk_commit();
           bulk_wait_all();  // complete before the CTA exits
         }
@@ -1153,14 +1162,14 @@ __global__ void __launch_bounds__(kThreads64, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kW64Mma) {
+  if (warp == kMma64) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols64);
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-// TMEM: S of even halves at 0, of odd ones at 64, dP at 128 (dS packed into it), dQ at 192.
-__global__ void __launch_bounds__(kThreads64, 2)
+// One CTA per query tile and range of key tiles.  dS is packed into its dP.
+__global__ void __launch_bounds__(kThreads64, 1)
     cross_dq64_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                       const float* __restrict__ lse, const float* __restrict__ delta, void* __restrict__ dq, int N,
@@ -1193,38 +1202,41 @@ __global__ void __launch_bounds__(kThreads64, 2)
       mbar_init(BAR(C::B_FULL + s), 1);
       mbar_init(BAR(C::B_EMPTY + s), 1);
     }
-    mbar_init(BAR(C::B_SF), 1);
-    for (int c = 0; c < 2; ++c) mbar_init(BAR(C::B_PF + c), 128);
-    mbar_init(BAR(C::B_DRAIN), 1);
+    for (int g = 0; g < kFlight; ++g) {
+      mbar_init(BAR(C::B_SF + g), 2);  // S and dP
+      mbar_init(BAR(C::B_GD + g), 1);  // the pair's dQ MMAs are complete
+    }
+    for (int c = 0; c < 2 * kFlight; ++c) mbar_init(BAR(C::B_PF + c), 128);
+    mbar_init(BAR(C::B_GF), 1);
+    for (int i = 0; i < kIssuers; ++i) mbar_init(BAR(C::B_DRAIN + i), 1);
     mbar_init(BAR(C::B_OW), 128);
     mbar_init(BAR(C::B_KC), 32);  // K's last tile cleared behind the sequence
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kW64Mma) {
-    tmem_alloc(smem_u32(tmem_slot), kTmemCols64);
+  if (warp == kMma64) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  constexpr uint32_t kP = 128, kG = 192;
 
-  if (warp == kW64Tma) {
+  if (warp == kTma64) {
     int issued = 0;
     if (lane == 0) {
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
-      mbar_arrive_expect_tx(BAR(C::B_OWN), 2 * kBox64);
+      mbar_arrive_expect_tx(BAR(C::B_OWN), 2 * kBox);
       tma_load_3d(sQ, &tq, BAR(C::B_OWN), 0, qt * kTile, bh);
       tma_load_3d(sDO, &tdo, BAR(C::B_OWN), 0, qt * kTile, bh);
       for (int j = 0; j < n_j; ++j) {
         const int s = j % C::ST;
         if (j >= C::ST && !bwait(BAR(C::B_EMPTY + s), ((j / C::ST) - 1) & 1, abort_flag, budget)) break;
-        mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * kBox64);
+        mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * kBox);
         tma_load_3d(sRing + s * C::STAGE, &tk, BAR(C::B_FULL + s), 0, key0 + j * kTile, bh);
-        tma_load_3d(sRing + s * C::STAGE + kBox64, &tv, BAR(C::B_FULL + s), 0, key0 + j * kTile, bh);
+        tma_load_3d(sRing + s * C::STAGE + kBox, &tv, BAR(C::B_FULL + s), 0, key0 + j * kTile, bh);
         issued = j + 1;
       }
     }
@@ -1244,87 +1256,82 @@ __global__ void __launch_bounds__(kThreads64, 2)
       bdrain(BAR(C::B_OWN), 0, budget);
       for (int j = max(0, issued - C::ST); j < issued; ++j) bdrain(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, budget);
     }
-  } else if (warp == kW64Mma) {
+  } else if (warp >= kMma64) {
+    // ------------------------------------------------------------ MMA issuers: S, dP, dQ
     if (lane == 0) {
-      const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dDO = sdesc_sw128(sDO, 16, 1024);
-      const uint64_t dR = sdesc_sw128(sRing, 16, 1024), dRmn = sdesc_sw128(sRing, kBox64, 1024);
-      auto issue_s = [&](int hh) {  // S = Q K^T
-        issue_half_product(tmem + ((hh & 1) ? 64u : 0u), dQ, sdesc_add(dR, ((hh >> 1) % C::ST) * C::STAGE), hh & 1);
-      };
-      auto issue_dp = [&](int hh) {  // dP = dO V^T
-        issue_half_product(tmem + kP, dDO, sdesc_add(dR, ((hh >> 1) % C::ST) * C::STAGE + kBox64), hh & 1);
-      };
-      auto issue_g = [&](int hh, int c) {  // dQ += dS K
-        issue_half_chunk(tmem + kG, tmem + kP, sdesc_add(dRmn, ((hh >> 1) % C::ST) * C::STAGE), hh & 1, c,
-                         hh > 0 || c > 0);
-      };
-      auto full = [&](int j) {  // K_j, V_j loaded (and cleared behind the sequence)
-        return bwait(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, abort_flag, budget) &&
-               (!k_tail || j + 1 < n_j || bwait(BAR(C::B_KC), 0, abort_flag, budget));
-      };
-      bool ok = bwait(BAR(C::B_OWN), 0, abort_flag, budget) && full(0);
-      if (ok) {
-        tc_fence_after();
-        issue_s(0);
-        issue_dp(0);
-        tc_commit(BAR(C::B_SF));
-      }
-      for (int hh = 0; ok && hh < n_h; ++hh) {
-        // the first chunk's dQ MMAs, then S of the next half (under the second chunk's elementwise
-        // work), then the second chunk's and the next dP, whose columns they free
-        if (!bwait(BAR(C::B_PF), hh & 1, abort_flag, budget)) break;
-        tc_fence_after();
-        issue_g(hh, 0);
-        if (hh + 1 < n_h) {
-          if ((hh & 1) && !full((hh + 1) >> 1)) break;
+      const int role = warp - kMma64;
+      bool ok = true;
+      if (role < 2) {  // S = Q K^T, dP = dO V^T
+        const uint64_t dA = sdesc_sw128(role == 0 ? sQ : sDO, 16, 1024);
+        const uint64_t dR = sdesc_add(sdesc_sw128(sRing, 16, 1024), role == 0 ? 0u : kBox);
+        ok = bwait(BAR(C::B_OWN), 0, abort_flag, budget);
+        for (int hh = 0; ok && hh < n_h; ++hh) {
+          const int j = hh >> 1, g = hh % kFlight;
+          // the stage loaded (and cleared behind the sequence), and the pair's last dQ MMAs done with its columns
+          ok = bwait(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, abort_flag, budget) &&
+               (!k_tail || j + 1 < n_j || bwait(BAR(C::B_KC), 0, abort_flag, budget)) &&
+               (hh < kFlight || bwait(BAR(C::B_GD + g), ((hh / kFlight) - 1) & 1, abort_flag, budget));
+          if (!ok) break;
           tc_fence_after();
-          issue_s(hh + 1);
+          issue_half_product(tmem + kPair64 * g + 64 * role, dA, sdesc_add(dR, (j % C::ST) * C::STAGE), hh & 1);
+          tc_commit(BAR(C::B_SF + g));
         }
-        if (!bwait(BAR(C::B_PF + 1), hh & 1, abort_flag, budget)) break;
-        tc_fence_after();
-        issue_g(hh, 1);
-        if (hh & 1) tc_commit(BAR(C::B_EMPTY + (hh >> 1) % C::ST));
-        if (hh + 1 < n_h) issue_dp(hh + 1);
-        tc_commit(BAR(C::B_SF));
+      } else {  // dQ += dS K
+        const uint64_t dRmn = sdesc_sw128(sRing, kBox, 1024);
+        for (int hh = 0; ok && hh < n_h; ++hh) {
+          const int g = hh % kFlight;
+          for (int c = 0; ok && c < 2; ++c) {
+            ok = bwait(BAR(C::B_PF + 2 * g + c), (hh / kFlight) & 1, abort_flag, budget);
+            if (!ok) break;
+            tc_fence_after();
+            issue_half_chunk(tmem + kAcc64, tmem + kPair64 * g + 64, sdesc_add(dRmn, ((hh >> 1) % C::ST) * C::STAGE),
+                             hh & 1, c, hh > 0 || c > 0);
+          }
+          if (!ok) break;
+          tc_commit(BAR(C::B_GD + g));
+          if (hh & 1) tc_commit(BAR(C::B_EMPTY + (hh >> 1) % C::ST));
+        }
+        tc_commit(BAR(C::B_GF));
       }
-      tc_commit(BAR(C::B_DRAIN));
-      bdrain(BAR(C::B_DRAIN), 0, budget);
+      tc_commit(BAR(C::B_DRAIN + role));
+      bdrain(BAR(C::B_DRAIN + role), 0, budget);
     }
   } else {
     // ------------------------------------------------------------ elementwise warps: thread = query row
-    const int r = 32 * warp + lane, row = qt * kTile + r;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const int g = warp >> 2, r = 32 * (warp & 3) + lane, row = qt * kTile + r;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t tS = lanes + kPair64 * g, tP = tS + 64;
     const bool in = row < N;
     const float lse2 = in ? lse[static_cast<size_t>(bh) * N + row] * kLog2e : INFINITY;
     const float dd = in ? delta[static_cast<size_t>(bh) * N + row] : 0.f;
     const uint64_t c2 = f2_pack(sl2, sl2), nl2 = f2_pack(-lse2, -lse2), nd2 = f2_pack(-dd, -dd);
     bool ok = true;
-    for (int hh = 0; ok && hh < n_h; ++hh) {
-      ok = bwait_all(BAR(C::B_SF), hh & 1, abort_flag, budget);
+    for (int hh = g; ok && hh < n_h; hh += kFlight) {
+      ok = bwait_all(BAR(C::B_SF + g), (hh / kFlight) & 1, abort_flag, budget);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t sv[32], pv[32];
-        tmem_ld_x32(lanes + ((hh & 1) ? 64u : 0u) + 32 * c, sv);
-        tmem_ld_x32(lanes + kP + 32 * c, pv);
+        tmem_ld_x32(tS + 32 * c, sv);
+        tmem_ld_x32(tP + 32 * c, pv);
         uint32_t dp[16];
         const int k0 = hh * kHalf + 32 * c;
         if (k0 + 32 > mine) ew_pairs_dq<true, true>(sv, pv, c2, nl2, nd2, k0, mine - 1, dp);
         else ew_pairs_dq<false>(sv, pv, c2, nl2, nd2, k0, mine - 1, dp);
-        tmem_st1_x16(lanes + kP + 16 * c, dp);
+        tmem_st1_x16(tP + 16 * c, dp);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(BAR(C::B_PF + c));
+        mbar_arrive(BAR(C::B_PF + 2 * g + c));
       }
     }
-    if (ok) ok = bwait_all(BAR(C::B_SF), n_h & 1, abort_flag, budget);  // dQ final
-    if (ok) {
+    if (ok) ok = bwait_all(BAR(C::B_GF), 0, abort_flag, budget);
+    if (ok && g == 0) {
       tc_fence_after();
       if (grad_fp32) {
-        store_grad_row<64>(dq, static_cast<size_t>(bh) * N + row, in, lanes + kG, scale);
+        store_grad_row<64>(dq, static_cast<size_t>(bh) * N + row, in, lanes + kAcc64, scale);
       } else {  // through shared memory: the Q tile has its shape and is no longer read
-        stage_row_bf16<64>(sQ, sQ, r, lanes + kG, scale);
+        stage_row_bf16<64>(sQ, sQ, r, lanes + kAcc64, scale);
         mbar_arrive(BAR(C::B_OW));
         if (warp == 0 && lane == 0 && bwait(BAR(C::B_OW), 0, abort_flag, budget)) {
           tma_store_3d(&tdq, sQ, 0, qt * kTile, bh);
@@ -1338,9 +1345,9 @@ __global__ void __launch_bounds__(kThreads64, 2)
 #undef BAR
   tc_fence_before();
   __syncthreads();
-  if (warp == kW64Mma) {
+  if (warp == kMma64) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols64);
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 

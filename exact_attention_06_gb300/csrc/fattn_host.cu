@@ -357,9 +357,8 @@ CrossBwdPlan plan_cross_bwd(const CrossShape& c, int Nk, int d, int sms) {
   CrossBwdPlan p;
   const int qt = (c.rows + 127) / 128, kt = (Nk + 127) / 128;
   const double kv = 2.0 * c.bh * Nk * d * sizeof(float), q = 1.0 * c.bh * c.rows * d * sizeof(float);
-  const int slots = d == 64 ? 2 * sms : sms;  // (the d = 64 kernels run two blocks per SM)
-  p.kv_splits = cut_scan(c.bh * kt, qt, slots, kv);
-  p.q_splits = cut_scan(c.bh * qt, kt, slots, q);
+  p.kv_splits = cut_scan(c.bh * kt, qt, sms, kv);
+  p.q_splits = cut_scan(c.bh * qt, kt, sms, q);
   p.q_tiles = (qt + p.kv_splits - 1) / p.kv_splits;
   p.k_tiles = (kt + p.q_splits - 1) / p.q_splits;
   p.delta_bytes = round256(static_cast<size_t>(c.bh) * c.rows * sizeof(float));
