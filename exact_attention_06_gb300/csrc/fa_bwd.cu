@@ -23,20 +23,12 @@
 // columns the gradient MMAs read.
 #include <cuda_bf16.h>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "bwd_common.cuh"
 #include "stage_io.cuh"
-#include "tmem_io.cuh"
 
 namespace fattn {
-
-__device__ unsigned int g_bwd_status = 0;
-
 namespace {
 
-constexpr int kTile = 128;                // rows per tile on either side
-constexpr uint32_t kBox = 128u * 128u;    // bytes of a 128-row x 64-column bf16 box
-constexpr uint32_t kTmemCols = 512;
 // Elementwise warps of the dK/dV and dQ kernels: at d = 128 one thread per (key or query) row (4
 // warps, .32x32b TMEM access, the row's 128 columns in four chunks of 32); at d = 64 8 warps, two
 // threads a row (.16x32bx2, two chunks; the dK/dV kernel takes each query tile in two halves).
@@ -49,32 +41,6 @@ struct BwdWarps {
 };
 constexpr uint32_t kColA = 0, kColB = 128, kColG1 = 256;  // products at 0 / 128, gradients from 256
 constexpr uint32_t kColS1 = 384;  // dQ kernel: second S buffer (S(j) at kColA for even j, here for odd j)
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                      unsigned long long budget) {
-  return mbar_wait(bar, parity, abort_flag, budget, &g_bwd_status);
-}
-__device__ __forceinline__ bool bwait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          unsigned long long budget) {
-  return __all_sync(0xffffffffu, bwait(bar, parity, abort_flag, budget));
-}
-__device__ __forceinline__ void bdrain(uint32_t bar, uint32_t parity, unsigned long long budget) {
-  if (budget < kDrainBudget) budget = kDrainBudget;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (static_cast<unsigned long long>(clock64() - t0) > budget) {
-      atomicOr(&g_bwd_status, kStatusTimeout);
-      return;
-    }
-  }
-}
-
-__device__ __forceinline__ void tmem_st1_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n"
-               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-                  "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
-}
 
 // --------------------------------------------------------------------- D = rowsum(O * dO)
 template <int D>
@@ -140,52 +106,6 @@ __device__ __forceinline__ void store_grad_half_row(void* out, size_t row_off, i
   }
 }
 
-// One thread per row: a D-column fp32 tile row in TMEM * scale -> global (fp32), or as bf16 into the
-// staged tile (box0: columns 0..63, box1: 64..127, 128-byte swizzle).
-template <int D>
-__device__ __forceinline__ void store_grad_row(void* out, size_t row_off, bool valid, uint32_t taddr, float scale) {
-#pragma unroll
-  for (int half = 0; half < D / 64; ++half) {
-    uint32_t ur[64];
-    tmem_ld_x64(taddr + 64u * half, ur);
-    if (!valid) continue;
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + row_off * D + 64 * half);
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      dst[i] = make_float4(__uint_as_float(ur[4 * i]) * scale, __uint_as_float(ur[4 * i + 1]) * scale,
-                           __uint_as_float(ur[4 * i + 2]) * scale, __uint_as_float(ur[4 * i + 3]) * scale);
-  }
-}
-template <int D>
-__device__ __forceinline__ void stage_row_bf16(uint32_t box0, uint32_t box1, int r, uint32_t taddr, float scale) {
-#pragma unroll
-  for (int half = 0; half < D / 64; ++half) {
-    uint32_t ur[64];
-    tmem_ld_x64(taddr + 64u * half, ur);
-    const uint32_t srow = (half ? box1 : box0) + static_cast<uint32_t>(r) * 128u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t* u = ur + 8 * i;
-      sts128(srow + ((static_cast<uint32_t>(i) ^ static_cast<uint32_t>(r & 7)) << 4),
-             pack_bf16(__uint_as_float(u[0]) * scale, __uint_as_float(u[1]) * scale),
-             pack_bf16(__uint_as_float(u[2]) * scale, __uint_as_float(u[3]) * scale),
-             pack_bf16(__uint_as_float(u[4]) * scale, __uint_as_float(u[5]) * scale),
-             pack_bf16(__uint_as_float(u[6]) * scale, __uint_as_float(u[7]) * scale));
-    }
-  }
-  fence_proxy_async_smem();
-}
-
-// S = A B^T into TMEM: A and B are resident/streamed 128 x d K-major tiles.
-template <int D>
-__device__ __forceinline__ void issue_product(uint32_t d_tmem, uint64_t da, uint64_t db, uint32_t idesc) {
-#pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = static_cast<uint32_t>(kk >> 2) * kBox + static_cast<uint32_t>(kk & 3) * 32u;
-    if (kk == 0) mma_ss_c<0>(d_tmem, sdesc_add(da, off), sdesc_add(db, off), idesc);
-    else mma_ss_c<1>(d_tmem, sdesc_add(da, off), sdesc_add(db, off), idesc);
-  }
-}
 // Packed bf16 operands in TMEM keep each half of the 128-wide K dimension in its own half of
 // the 128 columns it was computed in: elements 0..63 at packed columns 0..31, elements 64..127 at
 // 64..95.  The elementwise threads that produce a half then only overwrite columns they have
@@ -243,85 +163,6 @@ __device__ __forceinline__ void issue_grad_half(uint32_t d_tmem, uint32_t a_tmem
   }
 }
 
-// Elementwise step of the dK/dV kernel on 32 query columns of one key row (column pairs packed
-// as f32x2): P^T = 2^(S^T c - lse2), dS^T = P^T (dP^T - D), both rounded to bf16 pairs.  MASK
-// (the diagonal tile only) zeroes P^T where the query precedes the key.
-template <bool MASK>
-__device__ __forceinline__ void ew_pairs_dkdv(const uint32_t (&sv)[32], const uint32_t (&pv)[32], const float4* nv,
-                                              uint64_t c2, int col0, int qrow0, int key, uint32_t (&pp)[16],
-                                              uint32_t (&dp)[16]) {
-#pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    const int col = col0 + e;  // query row within the tile
-    const float4 x = nv[col >> 1];
-    float x0, x1;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, f2_pack(x.x, x.y)), x0, x1);
-    float p0 = ex2(x0), p1 = ex2(x1);
-    if (MASK) {
-      if (qrow0 + col < key) p0 = 0.f;
-      if (qrow0 + col + 1 < key) p1 = 0.f;
-    }
-    const uint64_t p2 = f2_pack(p0, p1);
-    float s0, s1;
-    f2_unpack(f2_mul(p2, f2_add(f2_pack(__uint_as_float(pv[e]), __uint_as_float(pv[e + 1])), f2_pack(x.z, x.w))),
-              s0, s1);
-    pp[e / 2] = pack_bf16(p0, p1);
-    dp[e / 2] = pack_bf16(s0, s1);
-  }
-}
-
-// A key row behind its sequence (whatever its K and V hold): no gradient.
-__device__ __forceinline__ void clear_pairs(uint32_t (&pp)[16], uint32_t (&dp)[16]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) pp[i] = dp[i] = 0;
-}
-
-// Elementwise step of the dQ kernel on 32 key columns of one query row: dS = P (dP - D) with
-// P = 2^(S c - lse2), rounded to bf16 pairs.  MASK zeroes keys past the row's last key; with CLEAR
-// their dS is cleared after the product, so that padding behind them may hold anything.
-template <bool MASK, bool CLEAR = false>
-__device__ __forceinline__ void ew_pairs_dq(const uint32_t (&sv)[32], const uint32_t (&pv)[32], uint64_t c2,
-                                            uint64_t nl2, uint64_t nd2, int key0, int lim, uint32_t (&dp)[16]) {
-#pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    float x0, x1;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nl2), x0, x1);
-    float p0 = ex2(x0), p1 = ex2(x1);
-    if (MASK) {
-      if (key0 + e > lim) p0 = 0.f;
-      if (key0 + e + 1 > lim) p1 = 0.f;
-    }
-    float s0, s1;
-    f2_unpack(f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(pv[e]), __uint_as_float(pv[e + 1])), nd2)), s0,
-              s1);
-    if (MASK && CLEAR) {
-      if (key0 + e > lim) s0 = 0.f;
-      if (key0 + e + 1 > lim) s1 = 0.f;
-    }
-    dp[e / 2] = pack_bf16(s0, s1);
-  }
-}
-
-// Cross attention, by value: see BwdLaunch.  n_keys: keys of the k, v tensors; tiles: tiles of the
-// scanned side per block (blockIdx.z takes tiles z * tiles ..); part_stride: elements from one
-// partial sum to the next (0: the gradient itself is written).
-struct CrossArgs {
-  const int* kv_lens;
-  int kv_heads, n_keys, tiles;
-  long long part_stride;
-  __device__ __forceinline__ int keys(int bh) const {
-    return kv_lens ? min(max(kv_lens[bh / kv_heads], 0), n_keys) : n_keys;
-  }
-};
-
-// Rows row0 .. row0 + rows - 1 of a gradient [.., D] that no pair reaches: zeros.
-template <int D>
-__device__ __forceinline__ void zero_rows(void* out, size_t row0, int rows, bool fp32) {
-  const int row_bytes = D * (fp32 ? 4 : 2);
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + row0 * row_bytes);
-  for (int i = threadIdx.x; i < rows * row_bytes / 16; i += blockDim.x) dst[i] = make_uint4(0, 0, 0, 0);
-}
-
 // --------------------------------------------------------------------- dK, dV: one CTA per key tile
 // TMEM: S^T at 0 (P^T packed into it), dP^T at 128 (dS^T packed into it), dV at 256, dK at 256 + d.
 template <int D>
@@ -344,15 +185,14 @@ struct DkdvCfg : BwdCfg<D> {
 };
 static_assert(DkdvCfg<128>::SMEM <= 232448, "dK/dV kernel shared memory");
 
-template <int D, bool CAUSAL, bool CROSS = false>
+template <int D, bool CAUSAL>
 __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                     const float* __restrict__ lse, const float* __restrict__ delta, void* __restrict__ dk,
                     void* __restrict__ dv, int N, float sl2, float scale, int grad_fp32,
                     unsigned long long budget, const __grid_constant__ CUtensorMap tdk,
-                    const __grid_constant__ CUtensorMap tdv, int ng, const CrossArgs x) {
-  static_assert(!CROSS || (D == 128 && !CAUSAL), "cross attention at d = 64 has its own kernels");
+                    const __grid_constant__ CUtensorMap tdv, int ng) {
   using C = DkdvCfg<D>;
   using W = BwdWarps<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -369,24 +209,8 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
   int bh, kt;  // key tile; small kt has the most causal work and is scheduled first (within a head group)
   grouped_block(ng, bh, kt);
   const int n_tiles = (N + kTile - 1) / kTile;
-  const int i0 = CROSS ? static_cast<int>(blockIdx.z) * x.tiles : CAUSAL ? kt : 0;  // first query tile of this block
-  const int n_i = CROSS ? min(x.tiles, n_tiles - i0) : n_tiles - i0;
-  const int n_keys = CROSS ? x.n_keys : N;
-  int lim = n_keys;  // CROSS: keys of this sequence
-  if constexpr (CROSS) {
-    if (x.part_stride) {  // this range of queries' partial sums
-      dk = static_cast<float*>(dk) + blockIdx.z * x.part_stride;
-      dv = static_cast<float*>(dv) + blockIdx.z * x.part_stride;
-    }
-    lim = x.keys(bh);
-    if (kt * kTile >= lim) {  // padding only
-      const size_t row0 = static_cast<size_t>(bh) * n_keys + kt * kTile;
-      const int rows = min(kTile, n_keys - kt * kTile);
-      zero_rows<D>(dk, row0, rows, grad_fp32);
-      zero_rows<D>(dv, row0, rows, grad_fp32);
-      return;
-    }
-  }
+  const int i0 = CAUSAL ? kt : 0;  // first query tile that sees this key tile
+  const int n_i = n_tiles - i0;
 
   if (threadIdx.x == 0) {
     mbar_init(BAR(C::B_KV), 1);
@@ -610,7 +434,6 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           uint32_t pp[16], dp[16];
           if (diag) ew_pairs_dkdv<true>(sv, pv, nv, c2, 32 * c, qt * kTile, key, pp, dp);
           else ew_pairs_dkdv<false>(sv, pv, nv, c2, 32 * c, qt * kTile, key, pp, dp);
-          if (CROSS && key >= lim) clear_pairs(pp, dp);
           tmem_st1_x16(tA + 16 * c, pp);  // P^T packed
           tmem_st1_x16(tB + 16 * c, dp);  // dS^T packed
           tmem_wait_st();
@@ -622,14 +445,14 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
     if (ok) ok = bwait_all(BAR(C::B_GF), 0, abort_flag, budget);  // gradients final
     if (ok) {
       tc_fence_after();
-      const size_t row_off = static_cast<size_t>(bh) * n_keys + key;
+      const size_t row_off = static_cast<size_t>(bh) * N + key;
       if (grad_fp32) {
         if constexpr (W::ONE) {
-          store_grad_row<D>(dv, row_off, key < n_keys, tmem + lane_addr + kColG1, 1.f);
-          store_grad_row<D>(dk, row_off, key < n_keys, tmem + lane_addr + C::COL_G2, scale);
+          store_grad_row<D>(dv, row_off, key < N, tmem + lane_addr + kColG1, 1.f);
+          store_grad_row<D>(dk, row_off, key < N, tmem + lane_addr + C::COL_G2, scale);
         } else {
-          store_grad_half_row<D>(dv, row_off, h, key < n_keys, true, tmem + lane_addr + kColG1, 1.f);
-          store_grad_half_row<D>(dk, row_off, h, key < n_keys, true, tmem + lane_addr + C::COL_G2, scale);
+          store_grad_half_row<D>(dv, row_off, h, key < N, true, tmem + lane_addr + kColG1, 1.f);
+          store_grad_half_row<D>(dk, row_off, h, key < N, true, tmem + lane_addr + C::COL_G2, scale);
         }
       } else {
         // bf16 dV and dK through shared memory: the V and K tiles have their shape and are no
@@ -673,21 +496,20 @@ struct DqCfg : BwdCfg<D> {
   static constexpr uint32_t STAGE = 2 * B::TB;
   static constexpr uint32_t OFF_BAR = OFF_RING + B::ST * STAGE;
   static constexpr int B_QD = 0, B_FULL = 1, B_EMPTY = B_FULL + B::ST, B_SF = B_EMPTY + B::ST, B_PF = B_SF + 1,
-                       B_DRAIN = B_PF + 4, B_OW = B_DRAIN + 1, B_KC = B_OW + 1, NBAR = B_KC + 1;  // B_PF + c: chunk c of the
+                       B_DRAIN = B_PF + 4, B_OW = B_DRAIN + 1, NBAR = B_OW + 1;  // B_PF + c: chunk c of the
                                                                                // elementwise step
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR;
   static constexpr uint32_t SMEM = OFF_MISC + 16u + 1024u;
 };
 static_assert(DqCfg<128>::SMEM <= 232448, "dQ kernel shared memory");
 
-template <int D, bool CAUSAL, bool CROSS = false>
+template <int D, bool CAUSAL>
 __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                   const float* __restrict__ lse, const float* __restrict__ delta, void* __restrict__ dq, int N,
                   float sl2, float scale, int grad_fp32, unsigned long long budget,
-                  const __grid_constant__ CUtensorMap tdq, int ng, const CrossArgs x) {
-  static_assert(!CROSS || (D == 128 && !CAUSAL), "cross attention at d = 64 has its own kernels");
+                  const __grid_constant__ CUtensorMap tdq, int ng) {
   using C = DqCfg<D>;
   using W = BwdWarps<D>;  // thread = query row here
   extern __shared__ uint8_t smem_raw[];
@@ -704,21 +526,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
   grouped_block(ng, bh, qt);
   const int n_tiles = (N + kTile - 1) / kTile;
   qt = n_tiles - 1 - qt;  // most causal work first (within a head group)
-  int n_j = CAUSAL ? qt + 1 : n_tiles;
-  int j0 = 0, n_keys = N;  // CROSS: this block's first key tile, the keys of its sequence
-  bool k_tail = false;     // CROSS: rows of K behind the sequence share its last tile
-  if constexpr (CROSS) {
-    j0 = static_cast<int>(blockIdx.z) * x.tiles;
-    n_keys = x.keys(bh);
-    const int end = (n_keys + kTile - 1) / kTile;
-    n_j = min(x.tiles, end - j0);
-    k_tail = n_keys < x.n_keys && n_keys % kTile != 0 && j0 + n_j == end;
-    if (x.part_stride) dq = static_cast<float*>(dq) + blockIdx.z * x.part_stride;
-    if (n_j <= 0) {  // no key in this range
-      zero_rows<D>(dq, static_cast<size_t>(bh) * N + qt * kTile, min(kTile, N - qt * kTile), grad_fp32);
-      return;
-    }
-  }
+  const int n_j = CAUSAL ? qt + 1 : n_tiles;
 
   if (threadIdx.x == 0) {
     mbar_init(BAR(C::B_QD), 1);
@@ -730,7 +538,6 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
     for (int c = 0; c < W::CHUNKS; ++c) mbar_init(BAR(C::B_PF + c), W::EW * 32);
     mbar_init(BAR(C::B_DRAIN), 1);
     mbar_init(BAR(C::B_OW), W::EW * 32);  // bf16 gradients staged
-    if constexpr (CROSS) mbar_init(BAR(C::B_KC), 32);  // K's last tile cleared behind the sequence
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -744,7 +551,6 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
   if (warp == W::TMA) {
-    int issued = 0;
     if (lane == 0) {
       tma_prefetch_desc(&tq);
       tma_prefetch_desc(&tk);
@@ -755,34 +561,18 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
         tma_load_3d(sQ + h * kBox, &tq, BAR(C::B_QD), h * 64, qt * kTile, bh);
         tma_load_3d(sDO + h * kBox, &tdo, BAR(C::B_QD), h * 64, qt * kTile, bh);
       }
+      int issued = 0;
       for (int j = 0; j < n_j; ++j) {
         const int s = j % C::ST;
         if (j >= C::ST && !bwait(BAR(C::B_EMPTY + s), ((j / C::ST) - 1) & 1, abort_flag, budget)) break;
         mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * C::TB);
         const uint32_t st = sRing + s * C::STAGE;
         for (int h = 0; h < C::NH; ++h) {
-          tma_load_3d(st + h * kBox, &tk, BAR(C::B_FULL + s), h * 64, (j0 + j) * kTile, bh);
-          tma_load_3d(st + C::TB + h * kBox, &tv, BAR(C::B_FULL + s), h * 64, (j0 + j) * kTile, bh);
+          tma_load_3d(st + h * kBox, &tk, BAR(C::B_FULL + s), h * 64, j * kTile, bh);
+          tma_load_3d(st + C::TB + h * kBox, &tv, BAR(C::B_FULL + s), h * 64, j * kTile, bh);
         }
         issued = j + 1;
       }
-    }
-    if constexpr (CROSS) {
-      // dQ = dS K multiplies the last tile's K rows behind the sequence by dS = 0: clear what the
-      // caller's padding holds there (0 times an infinity or NaN).
-      issued = __shfl_sync(0xffffffffu, issued, 0);
-      if (k_tail && issued == n_j) {
-        const int last = n_j - 1;
-        if (bwait_all(BAR(C::B_FULL + last % C::ST), (last / C::ST) & 1, abort_flag, budget)) {
-          const uint32_t tile = sRing + (last % C::ST) * C::STAGE;
-          for (int i = (n_keys - (j0 + last) * kTile) * 8 + lane; i < kTile * 8; i += 32)
-            for (int h = 0; h < C::NH; ++h) sts128(tile + h * kBox + i * 16, 0, 0, 0, 0);
-          fence_proxy_async_smem();
-          mbar_arrive(BAR(C::B_KC));
-        }
-      }
-    }
-    if (lane == 0) {
       bdrain(BAR(C::B_QD), 0, budget);
       for (int j = max(0, issued - C::ST); j < issued; ++j) bdrain(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, budget);
     }
@@ -803,11 +593,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
         const uint32_t st = (j % C::ST) * C::STAGE;
         issue_product<D>(tmem + kColB, dDO, sdesc_add(dR, st + C::TB), idesc_p);  // dP = dO V^T
       };
-      auto full = [&](int j) {  // K_j, V_j loaded (and cleared behind the sequence)
-        return bwait(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, abort_flag, budget) &&
-               (!CROSS || !k_tail || j + 1 < n_j || bwait(BAR(C::B_KC), 0, abort_flag, budget));
-      };
-      bool ok = bwait(BAR(C::B_QD), 0, abort_flag, budget) && full(0);
+      bool ok = bwait(BAR(C::B_QD), 0, abort_flag, budget) && bwait(BAR(C::B_FULL), 0, abort_flag, budget);
       if (ok) {
         tc_fence_after();
         issue_s(0);
@@ -825,7 +611,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           issue_grad_part<D>(tmem + kColG1, tmem + kColB, sdesc_add(dRmn, (j % C::ST) * C::STAGE), idesc_g, j > 0,
                              0);
         if (j + 1 < n_j) {
-          if (!full(j + 1)) break;
+          if (!bwait(BAR(C::B_FULL + (j + 1) % C::ST), ((j + 1) / C::ST) & 1, abort_flag, budget)) break;
           tc_fence_after();
           issue_s(j + 1);
         }
@@ -860,7 +646,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
     const bool in = row < N;
     const float lse2 = in ? lse[static_cast<size_t>(bh) * N + row] * kLog2e : INFINITY;
     const float dd = in ? delta[static_cast<size_t>(bh) * N + row] : 0.f;
-    const int lim = CAUSAL ? min(row, N - 1) : n_keys - 1;  // last key this row attends
+    const int lim = CAUSAL ? min(row, N - 1) : N - 1;  // last key this row attends
     const uint64_t c2 = f2_pack(sl2, sl2), nl2 = f2_pack(-lse2, -lse2), nd2 = f2_pack(-dd, -dd);
     bool ok = true;
     for (int j = 0; ok && j < n_j; ++j) {
@@ -876,8 +662,8 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           tmem_ld_x32(tmem + lane_addr + ((j & 1) ? kColS1 : kColA) + 32 * c, sv);
           tmem_ld_x32(tB + 32 * c, pv);
           uint32_t dp[16];
-          const int key0 = (j0 + j) * kTile + 32 * c;
-          if (key0 + 31 > lim) ew_pairs_dq<true, CROSS>(sv, pv, c2, nl2, nd2, key0, lim, dp);
+          const int key0 = j * kTile + 32 * c;
+          if (key0 + 31 > lim) ew_pairs_dq<true>(sv, pv, c2, nl2, nd2, key0, lim, dp);
           else ew_pairs_dq<false>(sv, pv, c2, nl2, nd2, key0, lim, dp);
           tmem_st1_x16(tB + 16 * c, dp);
           tmem_wait_st();
@@ -891,7 +677,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           tmem_ld2_x32<64>(tmem + lane_addr + ((j & 1) ? kColS1 : kColA) + 32 * c, sv);
           tmem_ld2_x32<64>(tB + 32 * c, pv);
           uint32_t dp[16];
-          const int key0 = (j0 + j) * kTile + 64 * h + 32 * c;
+          const int key0 = j * kTile + 64 * h + 32 * c;
           // only the diagonal and the ragged last key tile reach past this row's last key
           if (key0 + 31 > lim) ew_pairs_dq<true>(sv, pv, c2, nl2, nd2, key0, lim, dp);
           else ew_pairs_dq<false>(sv, pv, c2, nl2, nd2, key0, lim, dp);
@@ -932,437 +718,17 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
   }
 }
 
-// --------------------------------------------------------------------- cross attention, d = 64: three steps in flight
-// At d = 64 the MMAs are short (N = 64) and a step is a chain -- products, their way through TMEM,
-// exponentials, P and dS back, gradients -- several times as long as its work, so the tensor core waits on
-// latency.  These kernels take the scanned side in halves of 64 rows and keep three of them in flight: S and
-// dP of a half are 64 TMEM columns each, three pairs take 384 and leave 128 for the accumulators, and each pair
-// has four elementwise warps of its own (one thread per row, two chunks of 32 columns).
-constexpr int kHalf = kTile / 2;
-constexpr int kFlight = 3;                       // halves in flight: half hh uses pair hh % 3
-constexpr int kEw64 = 4 * kFlight;               // elementwise warps
-constexpr int kIssuers = 3;                      // MMA-issuing threads, a warp each
-constexpr int kMma64 = kEw64, kTma64 = kEw64 + kIssuers, kThreads64 = (kTma64 + 1) * 32;
-constexpr uint32_t kPair64 = 128, kAcc64 = 384;  // TMEM: pair g: S at 128 g, dP at 128 g + 64; accumulators from 384
-
-struct Cross64Cfg {
-  static constexpr int ST = 4;
-  static constexpr uint32_t TB = kBox;              // a 128-row x 64-column bf16 tile is one box
-  static constexpr uint32_t OFF_A = 0, OFF_B = TB;  // the block's own tiles: K, V or Q, dO
-  static constexpr uint32_t OFF_RING = 2 * TB;      // stage: Q_i, dO_i or K_j, V_j
-  static constexpr uint32_t STAGE = 2 * TB;
-  static constexpr uint32_t OFF_VEC = OFF_RING + ST * STAGE;  // dK/dV: -lse2, -D of the stage's rows (see DkdvCfg)
-  static constexpr uint32_t VEC = 2 * kTile * 4;
-  static constexpr uint32_t OFF_BAR = OFF_VEC + ST * VEC;
-  static constexpr int B_OWN = 0, B_FULL = 1, B_EMPTY = B_FULL + ST, B_SF = B_EMPTY + ST, B_PF = B_SF + kFlight,
-                       B_GD = B_PF + 2 * kFlight, B_GF = B_GD + kFlight, B_DRAIN = B_GF + 1, B_OW = B_DRAIN + kIssuers, B_KC = B_OW + 2, NBAR = B_KC + 1;
-  static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR;
-  static constexpr uint32_t SMEM = OFF_MISC + 16u + 1024u;
-  static_assert(SMEM <= 232448, "shared memory");
-};
-
-// Products of a 128-row tile A with rows 64 q .. of a streamed tile: 128 x 64, K = 64.
-__device__ __forceinline__ void issue_half_product(uint32_t d_tmem, uint64_t da, uint64_t db, int q) {
-  constexpr uint32_t idesc = idesc_bf16_f32(kTile, kHalf, 0);
-  issue_product<64>(d_tmem, da, sdesc_add(db, static_cast<uint32_t>(q) * kHalf * 128u), idesc);
-}
-// G (+)= X Y for chunk c (32 of the half's 64 rows): X packed at columns 16 c .., Y rows 64 q + 32 c ..
-__device__ __forceinline__ void issue_half_chunk(uint32_t g_tmem, uint32_t x_tmem, uint64_t dy, int q, int c,
-                                                 bool accumulate) {
-  issue_grad_chunk(g_tmem, x_tmem, sdesc_add(dy, static_cast<uint32_t>(q) * kHalf * 128u),
-                   idesc_bf16_f32(kTile, 64, 1), accumulate, c);
-}
-
-// One CTA per key tile and range of query tiles.  P^T and dS^T are packed into their S^T and dP^T.
-__global__ void __launch_bounds__(kThreads64, 1)
-    cross_dkdv64_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
-                        const float* __restrict__ lse, const float* __restrict__ delta, void* __restrict__ dk,
-                        void* __restrict__ dv, int N, float sl2, float scale, int grad_fp32, unsigned long long budget,
-                        const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv, int ng,
-                        const CrossArgs x) {
-  using C = Cross64Cfg;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t sK = base + C::OFF_A, sV = base + C::OFF_B, sRing = base + C::OFF_RING, sBar = base + C::OFF_BAR;
-  float* vec = reinterpret_cast<float*>(gbase + C::OFF_VEC);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 4);
-#define BAR(i) (sBar + 8u * static_cast<uint32_t>(i))
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int bh, kt;
-  grouped_block(ng, bh, kt);
-  const int row0 = static_cast<int>(blockIdx.z) * x.tiles * kTile;  // this block's query rows
-  const int n_h = (min(x.tiles * kTile, N - row0) + kHalf - 1) / kHalf, n_i = (n_h + 1) / 2;
-  if (x.part_stride) {
-    dk = static_cast<float*>(dk) + blockIdx.z * x.part_stride;
-    dv = static_cast<float*>(dv) + blockIdx.z * x.part_stride;
-  }
-  const int lim = x.keys(bh);
-  if (kt * kTile >= lim) {  // padding only
-    const size_t k0 = static_cast<size_t>(bh) * x.n_keys + kt * kTile;
-    const int rows = min(kTile, x.n_keys - kt * kTile);
-    zero_rows<64>(dk, k0, rows, grad_fp32);
-    zero_rows<64>(dv, k0, rows, grad_fp32);
-    return;
-  }
-  if (threadIdx.x == 0) {
-    mbar_init(BAR(C::B_OWN), 1);
-    for (int s = 0; s < C::ST; ++s) {
-      mbar_init(BAR(C::B_FULL + s), 1 + 32);  // TMA bytes + the producer warp's lse/D stores
-      mbar_init(BAR(C::B_EMPTY + s), 2);  // dV and dK have read the stage
-    }
-    for (int g = 0; g < kFlight; ++g) {
-      mbar_init(BAR(C::B_SF + g), 1);
-      mbar_init(BAR(C::B_GD + g), 2);  // the pair's gradient MMAs are complete
-    }
-    for (int c = 0; c < 2 * kFlight; ++c) mbar_init(BAR(C::B_PF + c), 128);
-    mbar_init(BAR(C::B_GF), 2);
-    for (int i = 0; i < kIssuers; ++i) mbar_init(BAR(C::B_DRAIN + i), 1);
-    mbar_init(BAR(C::B_OW), 128);
-    mbar_init(BAR(C::B_OW + 1), 128);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == kMma64) {
-    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  constexpr uint32_t kV = kAcc64, kK = kAcc64 + 64;
-
-  if (warp == kTma64) {
-    // ------------------------------------------------------------ producer (whole warp)
-    if (lane == 0) {
-      tma_prefetch_desc(&tq);
-      tma_prefetch_desc(&tdo);
-      mbar_arrive_expect_tx(BAR(C::B_OWN), 2 * kBox);
-      tma_load_3d(sK, &tk, BAR(C::B_OWN), 0, kt * kTile, bh);
-      tma_load_3d(sV, &tv, BAR(C::B_OWN), 0, kt * kTile, bh);
-    }
-    int issued = 0;
-    for (int i = 0; i < n_i; ++i) {
-      const int s = i % C::ST;
-      if (i >= C::ST && !bwait_all(BAR(C::B_EMPTY + s), ((i / C::ST) - 1) & 1, abort_flag, budget)) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * kBox);
-        tma_load_3d(sRing + s * C::STAGE, &tq, BAR(C::B_FULL + s), 0, row0 + i * kTile, bh);
-        tma_load_3d(sRing + s * C::STAGE + kBox, &tdo, BAR(C::B_FULL + s), 0, row0 + i * kTile, bh);
-      }
-      float* vs = vec + s * (2 * kTile);
-#pragma unroll
-      for (int c = 0; c < kTile / 32; ++c) {  // rows past N get -lse = -inf, so P = 0
-        const int col = 32 * c + lane, r = row0 + i * kTile + col;
-        const bool in = r < N;
-        vs[4 * (col >> 1) + (col & 1)] = in ? -lse[static_cast<size_t>(bh) * N + r] * kLog2e : -INFINITY;
-        vs[4 * (col >> 1) + 2 + (col & 1)] = in ? -delta[static_cast<size_t>(bh) * N + r] : 0.f;
-      }
-      mbar_arrive(BAR(C::B_FULL + s));
-      issued = i + 1;
-    }
-    if (lane == 0) {
-      bdrain(BAR(C::B_OWN), 0, budget);
-      for (int i = max(0, issued - C::ST); i < issued; ++i) bdrain(BAR(C::B_FULL + i % C::ST), (i / C::ST) & 1, budget);
-    }
-  } else if (warp >= kMma64) {
-    // ------------------------------------------------------------ MMA issuers: the products, dV, dK
-    if (lane == 0) {
-      const int role = warp - kMma64;
-      bool ok = true;
-      if (role == 0) {
-        const uint64_t dK = sdesc_sw128(sK, 16, 1024), dV = sdesc_sw128(sV, 16, 1024), dR = sdesc_sw128(sRing, 16, 1024);
-        ok = bwait(BAR(C::B_OWN), 0, abort_flag, budget);
-        for (int hh = 0; ok && hh < n_h; ++hh) {
-          const int i = hh >> 1, g = hh % kFlight;
-          // the stage loaded, and the pair's last gradients done with its columns
-          ok = bwait(BAR(C::B_FULL + i % C::ST), (i / C::ST) & 1, abort_flag, budget) &&
-               (hh < kFlight || bwait(BAR(C::B_GD + g), ((hh / kFlight) - 1) & 1, abort_flag, budget));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t st = (i % C::ST) * C::STAGE, d = tmem + kPair64 * g;
-          issue_half_product(d, dK, sdesc_add(dR, st), hh & 1);                 // S^T = K Q^T
-          issue_half_product(d + 64, dV, sdesc_add(dR, st + kBox), hh & 1);     // dP^T = V dO^T
-          tc_commit(BAR(C::B_SF + g));
-        }
-      } else {
-        // dV += P^T dO (role 1), dK += dS^T Q (role 2)
-        const uint64_t dY = sdesc_add(sdesc_sw128(sRing, kBox, 1024), role == 1 ? kBox : 0u);
-        const uint32_t acc = tmem + (role == 1 ? kV : kK), x0 = tmem + (role == 1 ? 0u : 64u);
-        for (int hh = 0; ok && hh < n_h; ++hh) {
-          const int g = hh % kFlight;
-          const uint64_t dy = sdesc_add(dY, ((hh >> 1) % C::ST) * C::STAGE);
-          for (int c = 0; ok && c < 2; ++c) {
-            ok = bwait(BAR(C::B_PF + 2 * g + c), (hh / kFlight) & 1, abort_flag, budget);
-            if (!ok) break;
-            tc_fence_after();
-            issue_half_chunk(acc, x0 + kPair64 * g, dy, hh & 1, c, hh > 0 || c > 0);
-          }
-          if (!ok) break;
-          tc_commit(BAR(C::B_GD + g));
-          if (hh & 1) tc_commit(BAR(C::B_EMPTY + (hh >> 1) % C::ST));
-        }
-        tc_commit(BAR(C::B_GF));
-      }
-      tc_commit(BAR(C::B_DRAIN + role));
-      bdrain(BAR(C::B_DRAIN + role), 0, budget);
-    }
-  } else {
-    // ------------------------------------------------------------ elementwise warps: thread = key row
-    const int g = warp >> 2, r = 32 * (warp & 3) + lane, key = kt * kTile + r;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const uint32_t tS = lanes + kPair64 * g, tP = tS + 64;
-    const uint64_t c2 = f2_pack(sl2, sl2);
-    bool ok = true;
-    for (int hh = g; ok && hh < n_h; hh += kFlight) {
-      const int i = hh >> 1, s = i % C::ST;
-      ok = bwait_all(BAR(C::B_FULL + s), (i / C::ST) & 1, abort_flag, budget) &&
-           bwait_all(BAR(C::B_SF + g), (hh / kFlight) & 1, abort_flag, budget);
-      if (!ok) break;
-      tc_fence_after();
-      const float4* nv = reinterpret_cast<const float4*>(vec + s * (2 * kTile));
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t sv[32], pv[32];
-        tmem_ld_x32(tS + 32 * c, sv);
-        tmem_ld_x32(tP + 32 * c, pv);
-        uint32_t pp[16], dp[16];
-        ew_pairs_dkdv<false>(sv, pv, nv, c2, kHalf * (hh & 1) + 32 * c, 0, 0, pp, dp);
-        if (key >= lim) clear_pairs(pp, dp);
-        tmem_st1_x16(tS + 16 * c, pp);
-        tmem_st1_x16(tP + 16 * c, dp);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(BAR(C::B_PF + 2 * g + c));
-      }
-    }
-    if (ok) ok = bwait_all(BAR(C::B_GF), 0, abort_flag, budget);
-    if (ok) {
-      tc_fence_after();
-      const size_t row_off = static_cast<size_t>(bh) * x.n_keys + key;
-      if (grad_fp32) {
-        if (g == 0) store_grad_row<64>(dv, row_off, key < x.n_keys, lanes + kV, 1.f);
-        if (g == 1) store_grad_row<64>(dk, row_off, key < x.n_keys, lanes + kK, scale);
-      } else if (g < 2) {  // through shared memory: the V and K tiles have their shape and are no longer read
-        const uint32_t tile = g == 0 ? sV : sK;
-        stage_row_bf16<64>(tile, tile, r, lanes + (g == 0 ? kV : kK), g == 0 ? 1.f : scale);
-        mbar_arrive(BAR(C::B_OW + g));
-        if ((warp & 3) == 0 && lane == 0 && bwait(BAR(C::B_OW + g), 0, abort_flag, budget)) {
-          tma_store_3d(g == 0 ? &tdv : &tdk, tile, 0, kt * kTile, bh);
-          bulk_commit();
-          bulk_wait_all();  // complete before the CTA exits
-        }
-      }
-    }
-    tmem_wait_st();
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == kMma64) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
-}
-
-// One CTA per query tile and range of key tiles.  dS is packed into its dP.
-__global__ void __launch_bounds__(kThreads64, 1)
-    cross_dq64_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
-                      const float* __restrict__ lse, const float* __restrict__ delta, void* __restrict__ dq, int N,
-                      float sl2, float scale, int grad_fp32, unsigned long long budget,
-                      const __grid_constant__ CUtensorMap tdq, int ng, const CrossArgs x) {
-  using C = Cross64Cfg;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t sQ = base + C::OFF_A, sDO = base + C::OFF_B, sRing = base + C::OFF_RING, sBar = base + C::OFF_BAR;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int bh, qt;
-  grouped_block(ng, bh, qt);
-  const int key0 = static_cast<int>(blockIdx.z) * x.tiles * kTile;  // this block's keys
-  const int n_keys = x.keys(bh);
-  const int mine = min(x.tiles * kTile, n_keys - key0);
-  if (x.part_stride) dq = static_cast<float*>(dq) + blockIdx.z * x.part_stride;
-  if (mine <= 0) {  // no key in this range
-    zero_rows<64>(dq, static_cast<size_t>(bh) * N + qt * kTile, min(kTile, N - qt * kTile), grad_fp32);
-    return;
-  }
-  const int n_h = (mine + kHalf - 1) / kHalf, n_j = (n_h + 1) / 2;
-  const bool k_tail = mine % kTile != 0 && n_keys < x.n_keys;  // rows behind the sequence in K's last tile
-  if (threadIdx.x == 0) {
-    mbar_init(BAR(C::B_OWN), 1);
-    for (int s = 0; s < C::ST; ++s) {
-      mbar_init(BAR(C::B_FULL + s), 1);
-      mbar_init(BAR(C::B_EMPTY + s), 1);
-    }
-    for (int g = 0; g < kFlight; ++g) {
-      mbar_init(BAR(C::B_SF + g), 2);  // S and dP
-      mbar_init(BAR(C::B_GD + g), 1);  // the pair's dQ MMAs are complete
-    }
-    for (int c = 0; c < 2 * kFlight; ++c) mbar_init(BAR(C::B_PF + c), 128);
-    mbar_init(BAR(C::B_GF), 1);
-    for (int i = 0; i < kIssuers; ++i) mbar_init(BAR(C::B_DRAIN + i), 1);
-    mbar_init(BAR(C::B_OW), 128);
-    mbar_init(BAR(C::B_KC), 32);  // K's last tile cleared behind the sequence
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == kMma64) {
-    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-
-  if (warp == kTma64) {
-    int issued = 0;
-    if (lane == 0) {
-      tma_prefetch_desc(&tk);
-      tma_prefetch_desc(&tv);
-      mbar_arrive_expect_tx(BAR(C::B_OWN), 2 * kBox);
-      tma_load_3d(sQ, &tq, BAR(C::B_OWN), 0, qt * kTile, bh);
-      tma_load_3d(sDO, &tdo, BAR(C::B_OWN), 0, qt * kTile, bh);
-      for (int j = 0; j < n_j; ++j) {
-        const int s = j % C::ST;
-        if (j >= C::ST && !bwait(BAR(C::B_EMPTY + s), ((j / C::ST) - 1) & 1, abort_flag, budget)) break;
-        mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * kBox);
-        tma_load_3d(sRing + s * C::STAGE, &tk, BAR(C::B_FULL + s), 0, key0 + j * kTile, bh);
-        tma_load_3d(sRing + s * C::STAGE + kBox, &tv, BAR(C::B_FULL + s), 0, key0 + j * kTile, bh);
-        issued = j + 1;
-      }
-    }
-    // dQ = dS K multiplies the last tile's K rows behind the sequence by dS = 0: clear what the
-    // caller's padding holds there (0 times an infinity or NaN).
-    issued = __shfl_sync(0xffffffffu, issued, 0);
-    if (k_tail && issued == n_j) {
-      const int last = n_j - 1;
-      if (bwait_all(BAR(C::B_FULL + last % C::ST), (last / C::ST) & 1, abort_flag, budget)) {
-        const uint32_t tile = sRing + (last % C::ST) * C::STAGE;
-        for (int i = (mine - last * kTile) * 8 + lane; i < kTile * 8; i += 32) sts128(tile + i * 16, 0, 0, 0, 0);
-        fence_proxy_async_smem();
-        mbar_arrive(BAR(C::B_KC));
-      }
-    }
-    if (lane == 0) {
-      bdrain(BAR(C::B_OWN), 0, budget);
-      for (int j = max(0, issued - C::ST); j < issued; ++j) bdrain(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, budget);
-    }
-  } else if (warp >= kMma64) {
-    // ------------------------------------------------------------ MMA issuers: S, dP, dQ
-    if (lane == 0) {
-      const int role = warp - kMma64;
-      bool ok = true;
-      if (role < 2) {  // S = Q K^T, dP = dO V^T
-        const uint64_t dA = sdesc_sw128(role == 0 ? sQ : sDO, 16, 1024);
-        const uint64_t dR = sdesc_add(sdesc_sw128(sRing, 16, 1024), role == 0 ? 0u : kBox);
-        ok = bwait(BAR(C::B_OWN), 0, abort_flag, budget);
-        for (int hh = 0; ok && hh < n_h; ++hh) {
-          const int j = hh >> 1, g = hh % kFlight;
-          // the stage loaded (and cleared behind the sequence), and the pair's last dQ MMAs done with its columns
-          ok = bwait(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, abort_flag, budget) &&
-               (!k_tail || j + 1 < n_j || bwait(BAR(C::B_KC), 0, abort_flag, budget)) &&
-               (hh < kFlight || bwait(BAR(C::B_GD + g), ((hh / kFlight) - 1) & 1, abort_flag, budget));
-          if (!ok) break;
-          tc_fence_after();
-          issue_half_product(tmem + kPair64 * g + 64 * role, dA, sdesc_add(dR, (j % C::ST) * C::STAGE), hh & 1);
-          tc_commit(BAR(C::B_SF + g));
-        }
-      } else {  // dQ += dS K
-        const uint64_t dRmn = sdesc_sw128(sRing, kBox, 1024);
-        for (int hh = 0; ok && hh < n_h; ++hh) {
-          const int g = hh % kFlight;
-          for (int c = 0; ok && c < 2; ++c) {
-            ok = bwait(BAR(C::B_PF + 2 * g + c), (hh / kFlight) & 1, abort_flag, budget);
-            if (!ok) break;
-            tc_fence_after();
-            issue_half_chunk(tmem + kAcc64, tmem + kPair64 * g + 64, sdesc_add(dRmn, ((hh >> 1) % C::ST) * C::STAGE),
-                             hh & 1, c, hh > 0 || c > 0);
-          }
-          if (!ok) break;
-          tc_commit(BAR(C::B_GD + g));
-          if (hh & 1) tc_commit(BAR(C::B_EMPTY + (hh >> 1) % C::ST));
-        }
-        tc_commit(BAR(C::B_GF));
-      }
-      tc_commit(BAR(C::B_DRAIN + role));
-      bdrain(BAR(C::B_DRAIN + role), 0, budget);
-    }
-  } else {
-    // ------------------------------------------------------------ elementwise warps: thread = query row
-    const int g = warp >> 2, r = 32 * (warp & 3) + lane, row = qt * kTile + r;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const uint32_t tS = lanes + kPair64 * g, tP = tS + 64;
-    const bool in = row < N;
-    const float lse2 = in ? lse[static_cast<size_t>(bh) * N + row] * kLog2e : INFINITY;
-    const float dd = in ? delta[static_cast<size_t>(bh) * N + row] : 0.f;
-    const uint64_t c2 = f2_pack(sl2, sl2), nl2 = f2_pack(-lse2, -lse2), nd2 = f2_pack(-dd, -dd);
-    bool ok = true;
-    for (int hh = g; ok && hh < n_h; hh += kFlight) {
-      ok = bwait_all(BAR(C::B_SF + g), (hh / kFlight) & 1, abort_flag, budget);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t sv[32], pv[32];
-        tmem_ld_x32(tS + 32 * c, sv);
-        tmem_ld_x32(tP + 32 * c, pv);
-        uint32_t dp[16];
-        const int k0 = hh * kHalf + 32 * c;
-        if (k0 + 32 > mine) ew_pairs_dq<true, true>(sv, pv, c2, nl2, nd2, k0, mine - 1, dp);
-        else ew_pairs_dq<false>(sv, pv, c2, nl2, nd2, k0, mine - 1, dp);
-        tmem_st1_x16(tP + 16 * c, dp);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(BAR(C::B_PF + 2 * g + c));
-      }
-    }
-    if (ok) ok = bwait_all(BAR(C::B_GF), 0, abort_flag, budget);
-    if (ok && g == 0) {
-      tc_fence_after();
-      if (grad_fp32) {
-        store_grad_row<64>(dq, static_cast<size_t>(bh) * N + row, in, lanes + kAcc64, scale);
-      } else {  // through shared memory: the Q tile has its shape and is no longer read
-        stage_row_bf16<64>(sQ, sQ, r, lanes + kAcc64, scale);
-        mbar_arrive(BAR(C::B_OW));
-        if (warp == 0 && lane == 0 && bwait(BAR(C::B_OW), 0, abort_flag, budget)) {
-          tma_store_3d(&tdq, sQ, 0, qt * kTile, bh);
-          bulk_commit();
-          bulk_wait_all();  // complete before the CTA exits
-        }
-      }
-    }
-    tmem_wait_st();
-  }
-#undef BAR
-  tc_fence_before();
-  __syncthreads();
-  if (warp == kMma64) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
-}
-
 template <int D>
-cudaError_t launch_delta(const BwdLaunch& a, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(a.BH) * a.N;
+cudaError_t launch_delta_t(const void* o, const void* dout, float* delta, long long rows, cudaStream_t stream) {
   const long long threads = rows * (D / 8);
   bwd_delta_kernel<D><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(
-      static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.dout), a.delta, rows);
+      static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), delta, rows);
   return cudaGetLastError();
 }
 
 template <int D, bool CAUSAL>
 cudaError_t launch_bwd_t(const BwdLaunch& a, cudaStream_t stream) {
-  cudaError_t e = launch_delta<D>(a, stream);
+  cudaError_t e = launch_delta_t<D>(a.o, a.dout, a.delta, static_cast<long long>(a.BH) * a.N, stream);
   if (e != cudaSuccess) return e;
   const int n_tiles = (a.N + kTile - 1) / kTile;
   const int ng = head_groups(a.BH, n_tiles, CAUSAL, a.sms);
@@ -1371,81 +737,20 @@ cudaError_t launch_bwd_t(const BwdLaunch& a, cudaStream_t stream) {
   if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::SMEM)) != cudaSuccess)
     return e;
   k1<<<grid, BwdWarps<D>::THREADS, DkdvCfg<D>::SMEM, stream>>>(a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, a.dk, a.dv, a.N,
-                                                   a.scale_log2, a.scale, a.grad_fp32, a.budget, a.tdk, a.tdv, ng,
-                                                   CrossArgs{});
+                                                   a.scale_log2, a.scale, a.grad_fp32, a.budget, a.tdk, a.tdv, ng);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   auto k2 = bwd_dq_kernel<D, CAUSAL>;
   if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::SMEM)) != cudaSuccess)
     return e;
   k2<<<grid, BwdWarps<D>::THREADS, DqCfg<D>::SMEM, stream>>>(a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, a.dq, a.N, a.scale_log2,
-                                                 a.scale, a.grad_fp32, a.budget, a.tdq, ng, CrossArgs{});
+                                                 a.scale, a.grad_fp32, a.budget, a.tdq, ng);
   return cudaGetLastError();
-}
-
-// out = sum of S partial sums of n elements each, in their order; 4 elements a thread.
-__global__ void __launch_bounds__(256) bwd_sum_kernel(const float* __restrict__ part, void* __restrict__ out,
-                                                      long long n, int S, int fp32) {
-  const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
-  float4 acc = *reinterpret_cast<const float4*>(part + i);
-  for (int s = 1; s < S; ++s) {
-    const float4 y = *reinterpret_cast<const float4*>(part + s * n + i);
-    acc.x += y.x;
-    acc.y += y.y;
-    acc.z += y.z;
-    acc.w += y.w;
-  }
-  if (fp32)
-    *reinterpret_cast<float4*>(static_cast<float*>(out) + i) = acc;
-  else
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + i) =
-        make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
-}
-
-cudaError_t launch_sum(const float* part, void* out, long long n, int S, int fp32, cudaStream_t stream) {
-  bwd_sum_kernel<<<static_cast<unsigned>((n / 4 + 255) / 256), 256, 0, stream>>>(part, out, n, S, fp32);
-  return cudaGetLastError();
-}
-
-template <int D>
-cudaError_t launch_cross_bwd_t(const BwdLaunch& a, cudaStream_t stream) {
-  cudaError_t e = launch_delta<D>(a, stream);
-  if (e != cudaSuccess) return e;
-  const long long kv_elems = static_cast<long long>(a.BH) * a.Nk * D, q_elems = static_cast<long long>(a.BH) * a.N * D;
-  const int k_tiles = (a.Nk + kTile - 1) / kTile, q_tiles = (a.N + kTile - 1) / kTile;
-  constexpr int threads = D == 64 ? kThreads64 : BwdWarps<128>::THREADS;
-  constexpr uint32_t smem1 = D == 64 ? Cross64Cfg::SMEM : DkdvCfg<128>::SMEM;
-  constexpr uint32_t smem2 = D == 64 ? Cross64Cfg::SMEM : DqCfg<128>::SMEM;
-  auto k1 = D == 64 ? cross_dkdv64_kernel : bwd_dkdv_kernel<128, false, true>;
-  if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1)) != cudaSuccess) return e;
-  const bool kv_part = a.kv_splits > 1, q_part = a.q_splits > 1;
-  const dim3 g1(static_cast<unsigned>(a.BH), static_cast<unsigned>(k_tiles), static_cast<unsigned>(a.kv_splits));
-  float* dv_part = a.kv_part + a.kv_splits * kv_elems;
-  k1<<<g1, threads, smem1, stream>>>(
-      a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, kv_part ? a.kv_part : a.dk, kv_part ? dv_part : a.dv, a.N, a.scale_log2,
-      a.scale, kv_part || a.grad_fp32, a.budget, a.tdk, a.tdv, head_groups(a.BH, k_tiles, false, a.sms),
-      CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.q_tiles, kv_part ? kv_elems : 0});
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (kv_part) {
-    if ((e = launch_sum(a.kv_part, a.dk, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess) return e;
-    if ((e = launch_sum(dv_part, a.dv, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess) return e;
-  }
-  auto k2 = D == 64 ? cross_dq64_kernel : bwd_dq_kernel<128, false, true>;
-  if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, smem2)) != cudaSuccess) return e;
-  const dim3 g2(static_cast<unsigned>(a.BH), static_cast<unsigned>(q_tiles), static_cast<unsigned>(a.q_splits));
-  k2<<<g2, threads, smem2, stream>>>(
-      a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, q_part ? a.q_part : a.dq, a.N, a.scale_log2, a.scale,
-      q_part || a.grad_fp32, a.budget, a.tdq, head_groups(a.BH, q_tiles, false, a.sms),
-      CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.k_tiles, q_part ? q_elems : 0});
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (q_part) return launch_sum(a.q_part, a.dq, q_elems, a.q_splits, a.grad_fp32, stream);
-  return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_cross_bwd(const BwdLaunch& a, cudaStream_t stream) {
-  return a.d == 64 ? launch_cross_bwd_t<64>(a, stream) : launch_cross_bwd_t<128>(a, stream);
+cudaError_t launch_delta(const void* o, const void* dout, float* delta, long long rows, int d, cudaStream_t stream) {
+  return d == 64 ? launch_delta_t<64>(o, dout, delta, rows, stream) : launch_delta_t<128>(o, dout, delta, rows, stream);
 }
 
 cudaError_t launch_bwd(const BwdLaunch& a, cudaStream_t stream) {

@@ -1061,7 +1061,6 @@ fa_status_t fa_cross_bwd(const void* q, const void* k, const void* v, const int*
   a.scale = scale;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.budget = (opts && opts->wait_budget_cycles) ? opts->wait_budget_cycles : kDefaultBudget;
-  a.cross = 1;
   a.Nk = Nk;
   a.kv_lens = kv_lens;
   a.kv_heads = Hkv;
@@ -1185,7 +1184,8 @@ fa_status_t fa_get_status(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fa_get_status synchronize");
   const unsigned int bits = fattn::fwd_read_and_clear_status() | fattn::decode_read_and_clear_status() |
-                            fattn::bwd_read_and_clear_status() | fattn::cross_rows_read_and_clear_status();
+                            fattn::bwd_read_and_clear_status() | fattn::cross_bwd_read_and_clear_status() |
+                            fattn::cross_rows_read_and_clear_status();
   if (bits & fattn::kStatusTimeout) return fail(FA_ERR_TIMEOUT, "a kernel wait exceeded its budget");
   return FA_OK;
 }

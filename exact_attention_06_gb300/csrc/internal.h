@@ -173,7 +173,6 @@ struct BwdLaunch {
   // q_tiles query tiles each (kv_splits blocks per key tile), the dQ kernel's k_tiles key tiles
   // (q_splits blocks per query tile); with more than one, they leave fp32 partial sums
   // [splits][rows, d] in kv_part (dK's, then dV's) and q_part, which a last kernel adds up.
-  int cross;
   int Nk;
   const int* kv_lens;
   int kv_heads;
@@ -184,6 +183,9 @@ struct BwdLaunch {
 };
 cudaError_t launch_bwd(const BwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_cross_bwd(const BwdLaunch& a, cudaStream_t stream);
+unsigned int cross_bwd_read_and_clear_status();
+// delta[r] = rowsum(o_r * dout_r) of `rows` bf16 rows of d
+cudaError_t launch_delta(const void* o, const void* dout, float* delta, long long rows, int d, cudaStream_t stream);
 unsigned int bwd_read_and_clear_status();
 
 // E4M3 block quantization: x [BH, N, d] bf16 -> codes [BH, N, d] bytes, scales [BH, ceil(N/128)].
