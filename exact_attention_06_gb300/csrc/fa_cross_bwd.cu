@@ -77,6 +77,12 @@ __device__ __forceinline__ void clear_pairs(uint32_t (&pp)[16], uint32_t (&dp)[1
   for (int i = 0; i < 16; ++i) pp[i] = dp[i] = 0;
 }
 
+// The dQ kernel needs nothing of the dK/dV kernel that it is launched programmatically after (and overlaps), but what
+// follows in the stream may: its last block ends only when that grid is complete.
+__device__ __forceinline__ void wait_as_last_block() {
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) grid_dep_wait();
+}
+
 // Products of a 128-row tile A with rows 64 q .. of a streamed tile: 128 x 64, K = d.
 template <int D>
 __device__ __forceinline__ void issue_half_product(uint32_t d_tmem, uint64_t da, uint64_t db, int q) {
@@ -118,6 +124,7 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 4);
 #define BAR(i) (sBar + 8u * static_cast<uint32_t>(i))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_launch();  // the dQ kernel may take SMs as this grid's last round leaves them idle
   int bh, kt;
   grouped_block(ng, bh, kt);
   const int row0 = static_cast<int>(blockIdx.z) * x.tiles * kTile;  // this block's query rows
@@ -325,6 +332,7 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
   if (x.part_stride) dq = static_cast<float*>(dq) + blockIdx.z * x.part_stride;
   if (mine <= 0) {  // no key in this range
     zero_rows<D>(dq, static_cast<size_t>(bh) * N + qt * kTile, min(kTile, N - qt * kTile), grad_fp32);
+    wait_as_last_block();
     return;
   }
   const int n_h = (mine + kHalf - 1) / kHalf, n_j = (n_h + 1) / 2;
@@ -488,13 +496,19 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  wait_as_last_block();
 }
 
-// out = sum of S partial sums of n elements each, in their order; 4 elements a thread.
-__global__ void __launch_bounds__(256) bwd_sum_kernel(const float* __restrict__ part, void* __restrict__ out,
-                                                      long long n, int S, int fp32) {
+// out = sum of S partial sums of n elements each, in their order; 4 elements a thread.  blockIdx.y = 1: out2 from
+// the S after those.
+__global__ void __launch_bounds__(256) cross_sum_kernel(const float* __restrict__ part, void* __restrict__ out,
+                                                        void* __restrict__ out2, long long n, int S, int fp32) {
   const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (i >= n) return;
+  if (blockIdx.y) {
+    part += S * n;
+    out = out2;
+  }
   float4 acc = *reinterpret_cast<const float4*>(part + i);
   for (int s = 1; s < S; ++s) {
     const float4 y = *reinterpret_cast<const float4*>(part + s * n + i);
@@ -510,8 +524,9 @@ __global__ void __launch_bounds__(256) bwd_sum_kernel(const float* __restrict__ 
         make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
 }
 
-cudaError_t launch_sum(const float* part, void* out, long long n, int S, int fp32, cudaStream_t stream) {
-  bwd_sum_kernel<<<static_cast<unsigned>((n / 4 + 255) / 256), 256, 0, stream>>>(part, out, n, S, fp32);
+cudaError_t launch_sum(const float* part, void* out, void* out2, long long n, int S, int fp32, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((n / 4 + 255) / 256), out2 ? 2 : 1);
+  cross_sum_kernel<<<grid, 256, 0, stream>>>(part, out, out2, n, S, fp32);
   return cudaGetLastError();
 }
 
@@ -533,19 +548,28 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
       a.scale, kv_part || a.grad_fp32, a.budget, a.tdk, a.tdv, head_groups(a.BH, k_tiles, false, a.sms),
       CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.q_tiles, kv_part ? kv_elems : 0});
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (kv_part) {
-    if ((e = launch_sum(a.kv_part, a.dk, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess) return e;
-    if ((e = launch_sum(dv_part, a.dv, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess) return e;
-  }
   auto k2 = cross_dq_kernel<D>;
   if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::SMEM)) != cudaSuccess) return e;
   const dim3 g2(static_cast<unsigned>(a.BH), static_cast<unsigned>(q_tiles), static_cast<unsigned>(a.q_splits));
-  k2<<<g2, Q::THREADS, Q::SMEM, stream>>>(
-      a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, q_part ? a.q_part : a.dq, a.N, a.scale_log2, a.scale,
-      q_part || a.grad_fp32, a.budget, a.tdq, head_groups(a.BH, q_tiles, false, a.sms),
-      CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.k_tiles, q_part ? q_elems : 0});
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (q_part) return launch_sum(a.q_part, a.dq, q_elems, a.q_splits, a.grad_fp32, stream);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = g2;
+  cfg.blockDim = dim3(Q::THREADS);
+  cfg.dynamicSmemBytes = Q::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, k2, a.tq, a.tk, a.tv, a.tdo, a.lse, static_cast<const float*>(a.delta),
+                              q_part ? static_cast<void*>(a.q_part) : a.dq, a.N, a.scale_log2, a.scale,
+                              static_cast<int>(q_part || a.grad_fp32), a.budget, a.tdq,
+                              head_groups(a.BH, q_tiles, false, a.sms),
+                              CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.k_tiles, q_part ? q_elems : 0})) != cudaSuccess)
+    return e;
+  if (kv_part && (e = launch_sum(a.kv_part, a.dk, a.dv, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess)
+    return e;
+  if (q_part) return launch_sum(a.q_part, a.dq, nullptr, q_elems, a.q_splits, a.grad_fp32, stream);
   return cudaSuccess;
 }
 
