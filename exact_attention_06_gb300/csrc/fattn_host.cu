@@ -268,20 +268,26 @@ fa_status_t check_cross_args(int B, int Hq, int Hkv, int Nq, int Nk, int d, Cros
   return FA_OK;
 }
 
-// How often to cut a scan of `tiles` tiles when `units` blocks (`slots` at a time) each make it:
-// more, shorter blocks fill the last round of SMs, at the price of fp32 partial results and a
-// kernel that joins them.  Costs in tile steps (about 1 us): a block costs its tiles plus ~3 of
-// set-up and epilogue, joining ~3 and its traffic, 8 MB a step.  A cut has to save 5 %.
-int cut_scan(long long units, int tiles, int slots, double part_bytes) {
+// How often to cut a scan of `tiles` tiles when `units` blocks (one per SM at a time) each make it:
+// more, shorter blocks fill the SMs, at the price of fp32 partial results and a kernel that joins
+// them.  Costs in tile steps (about 1 us): a block costs its tiles plus ~3 of set-up and epilogue,
+// joining ~3 and its traffic, 8 MB a step.  A cut has to save 5 %.  `filler`: steps of work (over all
+// SMs) of a kernel that runs on the SMs which this one's last round leaves idle; with it only the longest
+// SM and the sum of the work count.
+int cut_scan(long long units, int tiles, int sms, double part_bytes, double filler = 0.0) {
   constexpr double kFixed = 3.0, kJoin = 3.0, kStepBytes = 8e6;
-  auto rounds = [&](int s) { return static_cast<double>((units * s + slots - 1) / slots); };
-  const double whole = rounds(1) * (tiles + kFixed);
+  auto time = [&](int s, int each) {
+    const double rounds = static_cast<double>((units * s + sms - 1) / sms);
+    return std::fmax(rounds * (each + kFixed),
+                     (static_cast<double>(units) * s * (each + kFixed) + filler) / sms);
+  };
+  const double whole = time(1, tiles);
   double best_t = 0.95 * whole;
   int best = 1;
   for (int s = 2; s <= tiles && s <= 256; ++s) {
     const int each = (tiles + s - 1) / s;
     if ((tiles + each - 1) / each != s) continue;  // would leave a block without tiles
-    const double t = rounds(s) * (each + kFixed) + kJoin + 2.0 * s * part_bytes / kStepBytes;
+    const double t = time(s, each) + kJoin + 2.0 * s * part_bytes / kStepBytes;
     if (t < best_t) {
       best_t = t;
       best = s;
@@ -357,8 +363,12 @@ CrossBwdPlan plan_cross_bwd(const CrossShape& c, int Nk, int d, int sms) {
   CrossBwdPlan p;
   const int qt = (c.rows + 127) / 128, kt = (Nk + 127) / 128;
   const double kv = 2.0 * c.bh * Nk * d * sizeof(float), q = 1.0 * c.bh * c.rows * d * sizeof(float);
-  p.kv_splits = cut_scan(c.bh * kt, qt, sms, kv);
+  // The dQ kernel fills the dK/dV kernel's last round; a step of it costs about 0.75 of the latter's.  Measured
+  // (GB300, ranges of queries per key tile 1 / 2 / 3 / 4, both kernels and the join): B4 H16/4 2048 x 1500 at
+  // d = 64: 193 / 204 / 215 / 222 us; B2 H16/4 1000 x 577: 40 / 33 / 36 / 35 us; B1 H8/2 4096 x 300, 1 / 8 / 16 / 32:
+  // 134 / 28 / 26 / 32 us.
   p.q_splits = cut_scan(c.bh * qt, kt, sms, q);
+  p.kv_splits = cut_scan(c.bh * kt, qt, sms, kv, 0.75 * c.bh * qt * (kt + 3));
   p.q_tiles = (qt + p.kv_splits - 1) / p.kv_splits;
   p.k_tiles = (kt + p.q_splits - 1) / p.q_splits;
   p.delta_bytes = round256(static_cast<size_t>(c.bh) * c.rows * sizeof(float));
