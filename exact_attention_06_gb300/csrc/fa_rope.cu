@@ -23,7 +23,7 @@
 namespace fattn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPairs = 8;   // pairs per thread: two 16-byte vectors of a row
 constexpr int kUnroll = 4;  // heads whose loads are in flight together
 
@@ -198,8 +198,12 @@ cudaError_t launch_t(RopeLaunch a, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.B) * a.N;
   const long long bx = (rows + RopeCfg<D>::ROWS - 1) / RopeCfg<D>::ROWS;
   const int heads = a.Hq + a.Hk * (a.block_table ? 2 : 1);
-  // Heads per thread: 8 spread the angles' cost; fewer when that leaves the SMs without blocks.
-  a.heads = 8;
+  // Heads per thread: the angles cost about as much as turning three heads, so few heads make the kernel bound by
+  // them, many leave the SMs without blocks.  Measured (GB300), 1 / 2 / 4 / 8 / 16 heads: B2 H16+16 N8192 d128 92 / 57 /
+  // 42.3 / 42.5 / 43.6 us (6.4 TB/s), B4 H16+16 N2048 d64 23.6 / 15.6 / 13.2 / 14.3 / 13.5, a paged chunk of 4 x 517
+  // tokens of 16 + 32 heads 11.7 / 7.7 / 6.2 / 6.0 / 7.6, one token of 8 sequences 3.3 / 3.3 / 3.4 / 4.3 / 6.2.  (256
+  // threads a block: 42.5 at best, 13.4 and 6.2.)
+  a.heads = 4;
   while (a.heads > 1 && bx * ((heads + a.heads - 1) / a.heads) < 4LL * a.sms) a.heads /= 2;
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>((heads + a.heads - 1) / a.heads));
   if (a.block_table)
