@@ -9,6 +9,7 @@ All computation happens in the library's kernels; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -403,8 +404,8 @@ def fa_combine(u_part, m_part, l_part, o, lse, stream=None):
 
 def _need_here(func: str, tensors):
     """Check (name, tensor, dtypes, shape) entries as _need does, and that each tensor is on the current
-    device, where the kernels run.  (One pass of cheap comparisons: a decode step's calls take a few
-    microseconds, and their checks count.)"""
+    device, where the kernels run; its ordinal.  (One pass of cheap comparisons: a decode step's calls take a
+    few microseconds, and their checks count.)"""
     dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
     for name, t, dtypes, shape in tensors:
         if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
@@ -413,6 +414,19 @@ def _need_here(func: str, tensors):
             if t.get_device() != torch.cuda.current_device():
                 raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} is on cuda:{t.get_device()}, the current device "
                                                            f"is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _shape4(func: str, name: str, t):
+    try:
+        a, b, c, d = shape = t.shape
+    except (AttributeError, TypeError, ValueError):
+        raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} must be a 4-dimensional torch.Tensor") from None
+    return shape
+
+
+def _stream_on(dev: int, stream):
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _workspace_on(stream, nbytes: int, device):
@@ -431,10 +445,10 @@ def fa_cross_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int
     return int(lib().fa_cross_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
 
 
-def _need_4d(func: str, **tensors):
-    for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} must be a 4-dimensional torch.Tensor")
+@functools.lru_cache(maxsize=1024)
+def _cross_workspace(dev: int, *sizes) -> int:
+    """fa_cross_workspace_bytes on device ``dev`` (the current one), which depends on nothing else."""
+    return lib().fa_cross_workspace_bytes(*sizes)
 
 
 def fa_cross_fwd(q, k, v, o, lse, scale: float, kv_lens=None, workspace=None, stream=None,
@@ -444,9 +458,8 @@ def fa_cross_fwd(q, k, v, o, lse, scale: float, kv_lens=None, workspace=None, st
     fp32 (from its dtype); lse [B, Hq, Nq] fp32.  Nq = 1 is a decode step.  ``workspace``: a uint8 CUDA
     tensor of fa_cross_workspace_bytes() bytes; allocated here when None."""
     func = "fa_cross_fwd"
-    _need_4d(func, q=q, k=k)
-    B, Hq, Nq, d = qs = q.shape
-    _, Hkv, Nk, _ = k.shape
+    B, Hq, Nq, d = qs = _shape4(func, "q", q)
+    _, Hkv, Nk, _ = _shape4(func, "k", k)
     ks = (B, Hkv, Nk, d)
     checks = [("q", q, _BF16, qs), ("k", k, _BF16, ks), ("v", v, _BF16, ks), ("o", o, _OUT, qs),
               ("lse", lse, _F32, (B, Hq, Nq))]
@@ -454,18 +467,18 @@ def fa_cross_fwd(q, k, v, o, lse, scale: float, kv_lens=None, workspace=None, st
         checks.append(("kv_lens", kv_lens, _I32, (B,)))
     if workspace is not None:
         checks.append(("workspace", workspace, _U8, (workspace.numel(),)))
-    _need_here(func, checks)
+    dev = _need_here(func, checks)
     L = lib()
     if workspace is None:
-        nbytes = L.fa_cross_workspace_bytes(B, Hq, Hkv, Nq, Nk, d)
+        nbytes = _cross_workspace(dev, B, Hq, Hkv, Nq, Nk, d)
         if nbytes:
             workspace = _workspace_on(stream, nbytes, q.device)
     else:
         nbytes = workspace.numel()
     o_fp32 = o.dtype == torch.float32
     opts = ctypes.byref(FaCrossOpts(o_fp32, wait_budget_cycles)) if o_fp32 or wait_budget_cycles else None
-    _check(L.fa_cross_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, d,
-                          float(scale), _ptr(workspace), nbytes, _stream(stream), opts), func)
+    _check(L.fa_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_lens), o.data_ptr(), lse.data_ptr(), B, Hq,
+                          Hkv, Nq, Nk, d, float(scale), _ptr(workspace), nbytes, _stream_on(dev, stream), opts), func)
 
 
 def fa_cross_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
@@ -478,9 +491,9 @@ def fa_cross_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale: float, kv_lens=None, 
     dk and dv like k, bf16 or fp32 (from dq's dtype).  ``workspace``: a uint8 CUDA tensor of
     fa_cross_bwd_workspace_bytes() bytes; allocated here when None."""
     func = "fa_cross_bwd"
-    _need_4d(func, q=q, k=k, dq=dq)
-    B, Hq, Nq, d = qs = q.shape
-    _, Hkv, Nk, _ = k.shape
+    B, Hq, Nq, d = qs = _shape4(func, "q", q)
+    _, Hkv, Nk, _ = _shape4(func, "k", k)
+    _shape4(func, "dq", dq)
     ks, grad = (B, Hkv, Nk, d), (dq.dtype,) if dq.dtype in _OUT else _OUT
     checks = [("q", q, _BF16, qs), ("o", o, _BF16, qs), ("dout", dout, _BF16, qs), ("k", k, _BF16, ks),
               ("v", v, _BF16, ks), ("lse", lse, _F32, (B, Hq, Nq)), ("dq", dq, grad, qs), ("dk", dk, grad, ks),
@@ -489,14 +502,15 @@ def fa_cross_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale: float, kv_lens=None, 
         checks.append(("kv_lens", kv_lens, _I32, (B,)))
     if workspace is not None:
         checks.append(("workspace", workspace, _U8, (workspace.numel(),)))
-    _need_here(func, checks)
+    dev = _need_here(func, checks)
     L = lib()
     if workspace is None:
         workspace = _workspace_on(stream, L.fa_cross_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, d), q.device)
     opts = ctypes.byref(FaBwdOpts(wait_budget_cycles)) if wait_budget_cycles else None
-    _check(L.fa_cross_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
-                          _ptr(dk), _ptr(dv), B, Hq, Hkv, Nq, Nk, d, float(scale), dq.dtype == torch.float32,
-                          _ptr(workspace), workspace.numel(), _stream(stream), opts), func)
+    _check(L.fa_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_lens), o.data_ptr(), dout.data_ptr(),
+                          lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Nq, Nk, d,
+                          float(scale), dq.dtype == torch.float32, _ptr(workspace), workspace.numel(),
+                          _stream_on(dev, stream), opts), func)
 
 
 def fa_rope_axes_plan(d: int, sections, base: float = 10000.0, interleaved: bool = False, per_axis: bool = False,
@@ -521,14 +535,12 @@ def fa_rope_axes(q, k, pos, plan, q_out=None, k_out=None, inverse: bool = False,
     [axes, B, N] int32; in place where an output is None or its input.  inverse=True turns back: the
     gradients of q and k from those of q_out and k_out."""
     func = "fa_rope_axes"
-    _need_4d(func, q=q)
-    B, Hq, N, d = qs = q.shape
+    B, Hq, N, d = qs = _shape4(func, "q", q)
     q_out = q if q_out is None else q_out
     checks = [("q", q, _BF16, qs), ("q_out", q_out, _BF16, qs)]
     Hk = 0
     if k is not None:
-        _need_4d(func, k=k)
-        Hk = k.shape[1]
+        Hk = _shape4(func, "k", k)[1]
         k_out = k if k_out is None else k_out
         ks = (B, Hk, N, d)
         checks += [("k", k, _BF16, ks), ("k_out", k_out, _BF16, ks)]
@@ -536,9 +548,9 @@ def fa_rope_axes(q, k, pos, plan, q_out=None, k_out=None, inverse: bool = False,
         raise FattnError(FA_ERR_INVALID_ARG, func, "k_out without k")
     _need_plan(func, plan, d)
     checks.append(("pos", pos, _I32, (plan.n_axes, B, N)))
-    _need_here(func, checks)
-    _check(lib().fa_rope_axes(_ptr(q), _ptr(k), _ptr(pos), _ptr(q_out), _ptr(k_out), B, Hq, Hk, N, plan,
-                              bool(inverse), _stream(stream)), func)
+    dev = _need_here(func, checks)
+    _check(lib().fa_rope_axes(q.data_ptr(), _ptr(k), pos.data_ptr(), q_out.data_ptr(), _ptr(k_out), B, Hq, Hk, N, plan,
+                              bool(inverse), _stream_on(dev, stream)), func)
 
 
 def fa_rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table, seq_lens, new_lens=None,
@@ -547,10 +559,9 @@ def fa_rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table,
     v copied into the pools k_pages, v_pages [P, Hk, page_size, d] of fa_decode_paged, as keys seq_lens[b] ..
     of sequence b (int32 [B], the lengths before this call); tokens from new_lens[b] on are padding."""
     func = "fa_rope_axes_paged"
-    _need_4d(func, q=q, k=k, k_pages=k_pages)
-    B, Hq, N, d = qs = q.shape
-    Hk = k.shape[1]
-    P, _, page_size, _ = k_pages.shape
+    B, Hq, N, d = qs = _shape4(func, "q", q)
+    Hk = _shape4(func, "k", k)[1]
+    P, _, page_size, _ = _shape4(func, "k_pages", k_pages)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise FattnError(FA_ERR_INVALID_ARG, func, "block_table must be a 2-dimensional torch.Tensor")
     max_pages = block_table.shape[1]
@@ -562,10 +573,11 @@ def fa_rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table,
               ("pos", pos, _I32, (plan.n_axes, B, N))]
     if new_lens is not None:
         checks.append(("new_lens", new_lens, _I32, (B,)))
-    _need_here(func, checks)
-    _check(lib().fa_rope_axes_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(pos), _ptr(q_out), _ptr(k_pages), _ptr(v_pages),
-                                    _ptr(block_table), _ptr(seq_lens), _ptr(new_lens), B, Hq, Hk, N, page_size,
-                                    max_pages, P, plan, _stream(stream)), func)
+    dev = _need_here(func, checks)
+    _check(lib().fa_rope_axes_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), pos.data_ptr(), q_out.data_ptr(),
+                                    k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                                    seq_lens.data_ptr(), _ptr(new_lens), B, Hq, Hk, N, page_size, max_pages, P, plan,
+                                    _stream_on(dev, stream)), func)
 
 
 def fa_get_status(stream=None) -> int:
