@@ -166,6 +166,7 @@ _F32 = (torch.float32,)
 _OUT = (torch.bfloat16, torch.float32)
 _U8 = (torch.uint8,)
 _I32 = (torch.int32,)
+_Tensor = torch.Tensor
 
 
 def _need(func: str, name: str, t, dtypes, shape=None):
@@ -408,7 +409,7 @@ def _need_here(func: str, tensors):
     few microseconds, and their checks count.)"""
     dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
     for name, t, dtypes, shape in tensors:
-        if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+        if not (isinstance(t, _Tensor) and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
                 and t.get_device() == dev):
             _need(func, name, t, dtypes, shape)
             if t.get_device() != torch.cuda.current_device():
