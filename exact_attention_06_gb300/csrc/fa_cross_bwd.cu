@@ -330,14 +330,10 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
   const int n_keys = x.keys(bh);
   const int mine = min(x.tiles * kTile, n_keys - key0);
   if (x.part_stride) dq = static_cast<float*>(dq) + blockIdx.z * x.part_stride;
-  if (mine <= 0) {  // no key in this range
-    zero_rows<D>(dq, static_cast<size_t>(bh) * N + qt * kTile, min(kTile, N - qt * kTile), grad_fp32);
-    wait_as_last_block();
-    return;
-  }
-  const int n_h = (mine + kHalf - 1) / kHalf, n_j = (n_h + 1) / 2;
-  const bool k_tail = mine % kTile != 0 && n_keys < x.n_keys;  // rows behind the sequence in K's last tile
-  if (threadIdx.x == 0) {
+  // One thread sets the barriers up while the length is on its way, and starts the copies before TMEM is allocated.
+  // (Measured 92 -> 89 us at d = 64; the dK/dV kernel, whose blocks are longer, was slower with it.)
+  const bool producer = threadIdx.x == C::TMA * 32;
+  if (producer) {
     mbar_init(BAR(C::B_OWN), 1);
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(BAR(C::B_FULL + s), 1);
@@ -355,6 +351,31 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  if (mine <= 0) {  // no key in this range
+    zero_rows<D>(dq, static_cast<size_t>(bh) * N + qt * kTile, min(kTile, N - qt * kTile), grad_fp32);
+    wait_as_last_block();
+    return;
+  }
+  const int n_h = (mine + kHalf - 1) / kHalf, n_j = (n_h + 1) / 2;
+  const bool k_tail = mine % kTile != 0 && n_keys < x.n_keys;  // rows behind the sequence in K's last tile
+  auto load = [&](int j) {  // K_j, V_j
+    const int s = j % C::ST;
+    const uint32_t st = sRing + s * C::STAGE;
+    mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * C::TB);
+    for (int h = 0; h < C::NH; ++h) {
+      tma_load_3d(st + h * kBox, &tk, BAR(C::B_FULL + s), h * 64, key0 + j * kTile, bh);
+      tma_load_3d(st + C::TB + h * kBox, &tv, BAR(C::B_FULL + s), h * 64, key0 + j * kTile, bh);
+    }
+  };
+  int issued = 0;  // (the producer's)
+  if (producer) {
+    mbar_arrive_expect_tx(BAR(C::B_OWN), 2 * C::TB);
+    for (int h = 0; h < C::NH; ++h) {
+      tma_load_3d(sQ + h * kBox, &tq, BAR(C::B_OWN), h * 64, qt * kTile, bh);
+      tma_load_3d(sDO + h * kBox, &tdo, BAR(C::B_OWN), h * 64, qt * kTile, bh);
+    }
+    for (; issued < min(C::ST, n_j); ++issued) load(issued);
+  }
   if (warp == C::MMA) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -365,24 +386,10 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
   if (warp == C::TMA) {
-    int issued = 0;
     if (lane == 0) {
-      tma_prefetch_desc(&tk);
-      tma_prefetch_desc(&tv);
-      mbar_arrive_expect_tx(BAR(C::B_OWN), 2 * C::TB);
-      for (int h = 0; h < C::NH; ++h) {
-        tma_load_3d(sQ + h * kBox, &tq, BAR(C::B_OWN), h * 64, qt * kTile, bh);
-        tma_load_3d(sDO + h * kBox, &tdo, BAR(C::B_OWN), h * 64, qt * kTile, bh);
-      }
-      for (int j = 0; j < n_j; ++j) {
-        const int s = j % C::ST;
-        if (j >= C::ST && !bwait(BAR(C::B_EMPTY + s), ((j / C::ST) - 1) & 1, abort_flag, budget)) break;
-        mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * C::TB);
-        const uint32_t st = sRing + s * C::STAGE;
-        for (int h = 0; h < C::NH; ++h) {
-          tma_load_3d(st + h * kBox, &tk, BAR(C::B_FULL + s), h * 64, key0 + j * kTile, bh);
-          tma_load_3d(st + C::TB + h * kBox, &tv, BAR(C::B_FULL + s), h * 64, key0 + j * kTile, bh);
-        }
+      for (int j = issued; j < n_j; ++j) {
+        if (!bwait(BAR(C::B_EMPTY + j % C::ST), ((j / C::ST) - 1) & 1, abort_flag, budget)) break;
+        load(j);
         issued = j + 1;
       }
     }
