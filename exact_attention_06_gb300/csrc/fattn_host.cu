@@ -305,31 +305,32 @@ struct CrossPlan {
 };
 
 // The few-row kernel's blocks per key head.  Costs in the time a 64-key stage takes an SM at its share of
-// HBM: the whole call cannot be faster than all stages shared out, one block takes at least 0.73 a
-// stage (its chain of copies and products), set-up and join cost 3 a round of resident blocks, partials and the combine
-// kernel 3 more.  Clusters (up to 8 blocks) need neither partials nor a second kernel; of theirs the
-// largest within 5 % of the best is taken, since shorter blocks even out sequences of different lengths.
+// HBM: the whole call cannot be faster than all stages shared out; a block takes at least 0.73 a stage
+// (its chain of copies and products); set-up and join cost 3 a round of resident blocks and 0.12 a block of
+// the cluster, partials and the combine kernel 3 more.  Clusters (up to 8 blocks) need neither partials
+// nor a second kernel; of theirs the largest within 4 % of the best is taken, since shorter blocks even out
+// sequences of different lengths.
 // Measured (GB300, d = 128): 64 key heads x 577 keys, S = 1 / 2 / 4 / 5: 8.2 / 6.2 / 6.2 / 10.0 us;
 // 64 x 18k-32k keys, S = 2 / 4 / 8 / 19: 143 / 124 / 120 / 128 us; 8 x 16384, S = 8 / 16 / 32: 20.3 / 15.6 /
-// 17.7 us; 512 x 1500 at d = 64, S = 1 / 4 / 8: 41 / 43 / 60 us.
+// 17.7 us.
 void plan_few(CrossPlan* p, const CrossShape& c, int Nk, int d, int sms, bool allow_parts) {
-  constexpr double kBlock = 0.73, kFixed = 3.0, kJoin = 3.0;
+  constexpr double kBlock = 0.73, kFixed = 3.0, kMember = 0.12, kJoin = 3.0, kNear = 1.04;
   const int stages = (Nk + fattn::kRowsStageKeys - 1) / fattn::kRowsStageKeys;
   const long long slots = static_cast<long long>(sms) * fattn::cross_rows_per_sm(d, c.rows);
   const double all = static_cast<double>(c.bh) * stages / sms;
   auto cost = [&](int s) {
     const double rounds = static_cast<double>((c.bh * s + slots - 1) / slots);
-    return std::fmax(all, kBlock * rounds * ((stages + s - 1) / s)) + kFixed * rounds;
+    return std::fmax(all, kBlock * rounds * ((stages + s - 1) / s)) + kFixed * rounds + (s > 8 ? kJoin : kMember * s);
   };
   const int most = std::min(stages, 8);
   double best = cost(1);
   for (int s = 2; s <= most; ++s) best = std::fmin(best, cost(s));
   p->splits = 1;
   for (int s = 2; s <= most; ++s)
-    if (cost(s) <= 1.05 * best && c.bh * s <= INT_MAX) p->splits = s;
+    if (cost(s) <= kNear * best && c.bh * s <= INT_MAX) p->splits = s;
   for (int s = 9; allow_parts && s <= 256 && s <= stages && c.bh * s <= INT_MAX; ++s)
-    if (cost(s) + kJoin < best) {
-      best = cost(s) + kJoin;
+    if (cost(s) < best) {
+      best = cost(s);
       p->splits = s;
     }
   p->few = 1;
@@ -341,6 +342,9 @@ CrossPlan plan_cross(const CrossShape& c, int Nk, int d, int sms, bool workspace
   const int tiles = (Nk + 127) / 128;
   const long long rows = c.bh * c.rows;
   const bool can_join = workspace && rows <= INT_MAX;  // (the combine kernel's row count)
+  // At most 32 rows a key head take the few-row kernel.  Measured against the 128-row tiles (d = 128, 1 / 16 / 17 / 32
+  // rows): 64 key heads x 8192 keys 41 / 43 / 46 / 48 us against 51 / 53 / 53 / 54; 512 x 1500 keys 60 / 64 / 82 / 88
+  // against 83 / 87 / 87 / 88; 64 x 577 keys 5.9 / 7.5 / 8.2 / 9.6 against 10.8.
   if (c.rows <= fattn::kCrossRowsMax)
     plan_few(&p, c, Nk, d, sms, can_join);
   else if (can_join)

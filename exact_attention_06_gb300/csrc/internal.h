@@ -126,7 +126,8 @@ unsigned int decode_read_and_clear_status();
 // blocks of a key head are a cluster and write o and lse; else partial slots [BH * R, S].
 constexpr int kRowsStageKeys = 64;
 constexpr int kCrossRowsMax = 32;
-constexpr int cross_rows_per_sm(int d, int rows) { return d == 128 && rows > 16 ? 1 : 2; }
+// Resident blocks per SM: at d = 128 two by shared memory, one of 32 rows by registers; at d = 64 four, or two.
+constexpr int cross_rows_per_sm(int d, int rows) { return (d == 128 ? 2 : 4) / (rows > 16 ? 2 : 1); }
 struct CrossRowsArgs {
   const void* q;
   void* o;
