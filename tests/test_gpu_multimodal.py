@@ -114,3 +114,57 @@ def test_a_training_step_of_a_layer():
                            ("dv", dv, gv)):
         e = np.abs(got.cpu().double().numpy() - ref)
         assert e.max() <= 2e-2 * np.abs(ref).max() and e.mean() <= 1e-2 * np.abs(ref).mean(), name
+
+
+def test_a_training_step_captured_and_replayed():
+    """Forward and backward (with keys and queries cut into ranges) captured twice, in graphs with workspaces of
+    their own, and replayed in turn on new values and lengths: bitwise what eager calls give."""
+    ensure_built()
+    B, Hq, Hkv, Nq, Nk, d = 2, 4, 2, 700, 900, 128
+    scale = d ** -0.5
+    size = (B, Hq, Hkv, Nq, Nk, d)
+    plan = fattn.fa_rope_axes_plan(d, (16, 24, 24), cyclic=True)
+    kl = torch.tensor([900, 900], dtype=torch.int32, device=DEV)
+    pos = torch.randint(0, 500, (3, B, Nq), dtype=torch.int32, device=DEV)
+    q, do = _rand((B, Hq, Nq, d), 1), _rand((B, Hq, Nq, d), 2)
+    k, v = _rand((B, Hkv, Nk, d), 3), _rand((B, Hkv, Nk, d), 4)
+    assert fattn.fa_cross_bwd_workspace_bytes(*size) > B * Hq * Nq * 4 + 256  # ranges of queries or keys
+
+    def buffers():
+        return [torch.empty_like(q), torch.empty_like(q), torch.empty(B, Hq, Nq, device=DEV), torch.empty_like(q),
+                torch.empty_like(k), torch.empty_like(v),
+                torch.empty(max(256, fattn.fa_cross_workspace_bytes(*size)), dtype=torch.uint8, device=DEV),
+                torch.empty(fattn.fa_cross_bwd_workspace_bytes(*size), dtype=torch.uint8, device=DEV)]
+
+    def step(b, stream=None):
+        qr, o, lse, dq, dk, dv, w1, w2 = b
+        fattn.fa_rope_axes(q, None, pos, plan, qr, stream=stream)
+        fattn.fa_cross_fwd(qr, k, v, o, lse, scale, kv_lens=kl, workspace=w1, stream=stream)
+        fattn.fa_cross_bwd(qr, k, v, o, do, lse, dq, dk, dv, scale, kv_lens=kl, workspace=w2, stream=stream)
+        fattn.fa_rope_axes(dq, None, pos, plan, inverse=True, stream=stream)
+
+    one, two, eager = buffers(), buffers(), buffers()
+    step(eager)
+    torch.cuda.synchronize()
+    graphs = []
+    for b in (one, two):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(b)
+        graphs.append(g)
+    for t, lens in enumerate(([900, 333], [0, 128], [901, 1])):
+        for i, x in enumerate((q, k, v, do)):
+            x.copy_(_rand(x.shape, 20 + 4 * t + i))
+        kl.copy_(torch.tensor(lens, dtype=torch.int32))
+        for b in (one, two, eager):
+            for x in b[:6]:
+                x.fill_(float("nan"))
+        graphs[0].replay()
+        graphs[1].replay()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        step(eager, stream=side.cuda_stream)  # a raw handle
+        torch.cuda.synchronize()
+        assert fattn.fa_get_status() == fattn.FA_OK
+        for a, b, c in zip(one[:6], two[:6], eager[:6]):
+            assert torch.equal(a, c) and torch.equal(b, c) and torch.isfinite(a).logical_or(a == -float("inf")).all()
