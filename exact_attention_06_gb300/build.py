@@ -1,7 +1,8 @@
 """Build ``libfattn.so`` in-tree with nvcc for sm_103a.
 
 The translation units compile in parallel into ``_build/`` and link into
-``exact_attention_06_gb300/libfattn.so``.  The CUDA runtime is linked
+``exact_attention_06_gb300/libfattn.so``; beside them the host compiler builds the
+binding's module ``_calls.so`` against torch's headers.  The CUDA runtime is linked
 statically; the driver is reached through cudaGetDriverEntryPointByVersion,
 so no libcuda link is needed at build time.
 """
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfattn.so")
+CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["fa_fwd.cu", "fa_bwd.cu", "fa_cross_bwd.cu", "fa_cross_rows.cu", "fa_decode.cu", "fa_quant.cu", "fa_rope.cu",
            "fattn_host.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
@@ -45,10 +47,23 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _calls_command(out: str):
+    import sysconfig
+
+    import torch
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    top = os.path.dirname(torch.__file__)
+    inc, libs = os.path.join(top, "include"), os.path.join(top, "lib")
+    return [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall",
+            os.path.join(CSRC, "py_calls.cpp"), "-o", out, "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+            "-I", cuda, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+            f"-L{libs}", f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -65,9 +80,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    calls_tmp = CALLS + ".tmp"
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(subprocess.run, _calls_command(calls_tmp), capture_output=True, text=True)
         results = list(ex.map(compile_one, SOURCES))
+        calls = calls.result()
     errors = []
+    if calls.returncode != 0:
+        errors.append(f"py_calls.cpp:\n{calls.stdout}{calls.stderr}")
     for src, _obj, r in results:
         if verbose or ptxas_info:
             sys.stderr.write(r.stdout + r.stderr)
@@ -81,6 +101,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB)
+    os.replace(calls_tmp, CALLS)
     return LIB
 
 

@@ -1,15 +1,19 @@
-"""Thin ctypes binding of the libfattn C ABI (include/fattn.h).
+"""Thin binding of the libfattn C ABI (include/fattn.h).
 
 Argument marshalling only: every function takes torch CUDA tensors (or sizes),
 passes their device pointers and the current CUDA stream to the function of
 the same name in ``libfattn.so`` and raises ``FattnError`` on a non-OK status.
 All computation happens in the library's kernels; there is no fallback.
+
+The library is called through ctypes; cross attention and rotary positions go
+through the compiled module ``_calls`` (csrc/py_calls.cpp), which makes the
+same checks on the tensors in C++: a decode step's kernels take less time than
+these checks in Python.
 """
 
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -68,11 +72,12 @@ class FaRopeAxesPlan(ctypes.Structure):
 
 
 _lib = None
+_calls = None  # the compiled module, bound to the loaded library
 
 
 def lib() -> ctypes.CDLL:
     """The loaded library; raises if it has not been built."""
-    global _lib
+    global _lib, _calls
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise FattnError(FA_ERR_CUDA, "load", f"{LIB_PATH} is missing; build it with exact_attention_06_gb300.build")
@@ -126,6 +131,15 @@ def lib() -> ctypes.CDLL:
                      "fa_decode_paged_ex", "fa_combine", "fa_combine_ex", "fa_cross_fwd", "fa_cross_bwd",
                      "fa_rope_axes_plan", "fa_rope_axes", "fa_rope_axes_paged", "fa_get_status"):
             getattr(L, name).restype = i
+        try:
+            from . import _calls as calls
+        except ImportError as e:
+            raise FattnError(FA_ERR_CUDA, "load", f"{_HERE}/_calls.so cannot be loaded ({e}); build it with "
+                                                  "exact_attention_06_gb300.build") from e
+        calls.bind(*(ctypes.cast(getattr(L, name), vp).value for name in (
+            "fa_cross_fwd", "fa_cross_workspace_bytes", "fa_cross_bwd", "fa_cross_bwd_workspace_bytes",
+            "fa_rope_axes", "fa_rope_axes_paged")))
+        _calls = calls
         _lib = L
     return _lib
 
@@ -157,8 +171,7 @@ def _check(status: int, func: str):
 
 
 def _ptr(t):
-    """A tensor's device pointer for a c_void_p argument (an int converts faster than a c_void_p object)."""
-    return t.data_ptr() if t is not None else None
+    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
 _BF16 = (torch.bfloat16,)
@@ -166,7 +179,6 @@ _F32 = (torch.float32,)
 _OUT = (torch.bfloat16, torch.float32)
 _U8 = (torch.uint8,)
 _I32 = (torch.int32,)
-_Tensor = torch.Tensor
 
 
 def _need(func: str, name: str, t, dtypes, shape=None):
@@ -184,16 +196,10 @@ def _need(func: str, name: str, t, dtypes, shape=None):
         raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} must be a CUDA tensor")
 
 
-# The current stream's handle without building a torch Stream object (3 us of a 4 us call).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream(stream):
     if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
 def fa_fwd_workspace_bytes(B: int, H: int, N: int, d: int, causal: bool = False) -> int:
@@ -403,42 +409,36 @@ def fa_combine(u_part, m_part, l_part, o, lse, stream=None):
     _check(st, "fa_combine_ex")
 
 
-def _need_here(func: str, tensors):
-    """Check (name, tensor, dtypes, shape) entries as _need does, and that each tensor is on the current
-    device, where the kernels run; its ordinal.  (One pass of cheap comparisons: a decode step's calls take a
-    few microseconds, and their checks count.)"""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+def _need_here(func: str, *tensors):
+    """Find what is wrong among (name, tensor, dtypes, shape) entries, of which the compiled module refused one."""
     for name, t, dtypes, shape in tensors:
-        if not (isinstance(t, _Tensor) and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
-                and t.get_device() == dev):
-            _need(func, name, t, dtypes, shape)
-            if t.get_device() != torch.cuda.current_device():
-                raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} is on cuda:{t.get_device()}, the current device "
-                                                           f"is cuda:{torch.cuda.current_device()}")
-    return dev
+        _need(func, name, t, dtypes, shape)
+        if t.get_device() != torch.cuda.current_device():
+            raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} is on cuda:{t.get_device()}, the current device is "
+                                                       f"cuda:{torch.cuda.current_device()}")
 
 
 def _shape4(func: str, name: str, t):
-    try:
-        a, b, c, d = shape = t.shape
-    except (AttributeError, TypeError, ValueError):
-        raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} must be a 4-dimensional torch.Tensor") from None
-    return shape
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} must be a 4-dimensional torch.Tensor")
+    return t.shape
 
 
-def _stream_on(dev: int, stream):
-    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+def _refused(func: str):
+    raise FattnError(FA_ERR_INVALID_ARG, func, "an argument has the wrong type, or a size that does not fit an int")
 
 
 def _workspace_on(stream, nbytes: int, device):
     """Scratch that lives as long as the stream's work needs it: allocated on that stream, so that its
     memory goes to no other stream's tensor while the kernels may still use it."""
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def fa_cross_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
@@ -446,40 +446,49 @@ def fa_cross_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int
     return int(lib().fa_cross_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
 
 
-@functools.lru_cache(maxsize=1024)
-def _cross_workspace(dev: int, *sizes) -> int:
-    """fa_cross_workspace_bytes on device ``dev`` (the current one), which depends on nothing else."""
-    return lib().fa_cross_workspace_bytes(*sizes)
+def _cross_sizes(func: str, q, k, rest, kv_lens, workspace):
+    """Check a cross attention call's tensors (``rest``: those of q's, k's and lse's shapes); the call's sizes."""
+    B, Hq, Nq, d = _shape4(func, "q", q)
+    _, Hkv, Nk, _ = _shape4(func, "k", k)
+    shapes = {"q": (B, Hq, Nq, d), "k": (B, Hkv, Nk, d), "lse": (B, Hq, Nq)}
+    _need_here(func, ("q", q, _BF16, shapes["q"]), ("k", k, _BF16, shapes["k"]),
+               *((name, t, dtypes, shapes[like]) for name, t, dtypes, like in rest))
+    if kv_lens is not None:
+        _need_here(func, ("kv_lens", kv_lens, _I32, (B,)))
+    if workspace is not None:
+        _need_here(func, ("workspace", workspace, _U8, None))
+    return B, Hq, Hkv, Nq, Nk, d
+
+
+def _cross_fwd_sizes(q, k, v, o, lse, kv_lens, workspace):
+    return _cross_sizes("fa_cross_fwd", q, k, (("v", v, _BF16, "k"), ("o", o, _OUT, "q"), ("lse", lse, _F32, "lse")),
+                        kv_lens, workspace)
+
+
+def _cross_bwd_sizes(q, k, v, o, dout, lse, dq, dk, dv, kv_lens, workspace):
+    grad = (dq.dtype,) if isinstance(dq, torch.Tensor) and dq.dtype in _OUT else _OUT
+    return _cross_sizes("fa_cross_bwd", q, k, (
+        ("v", v, _BF16, "k"), ("o", o, _BF16, "q"), ("dout", dout, _BF16, "q"), ("lse", lse, _F32, "lse"),
+        ("dq", dq, grad, "q"), ("dk", dk, grad, "k"), ("dv", dv, grad, "k")), kv_lens, workspace)
 
 
 def fa_cross_fwd(q, k, v, o, lse, scale: float, kv_lens=None, workspace=None, stream=None,
                  wait_budget_cycles: int = 0):
     """Cross attention: q [B, Hq, Nq, d] against k, v [B, Hkv, Nk, d] (query head h reads key head
     h // (Hq // Hkv)), of which sequence b has the first kv_lens[b] (int32 [B]; None: all); o like q, bf16 or
-    fp32 (from its dtype); lse [B, Hq, Nq] fp32.  Nq = 1 is a decode step.  ``workspace``: a uint8 CUDA
-    tensor of fa_cross_workspace_bytes() bytes; allocated here when None."""
-    func = "fa_cross_fwd"
-    B, Hq, Nq, d = qs = _shape4(func, "q", q)
-    _, Hkv, Nk, _ = _shape4(func, "k", k)
-    ks = (B, Hkv, Nk, d)
-    checks = [("q", q, _BF16, qs), ("k", k, _BF16, ks), ("v", v, _BF16, ks), ("o", o, _OUT, qs),
-              ("lse", lse, _F32, (B, Hq, Nq))]
-    if kv_lens is not None:
-        checks.append(("kv_lens", kv_lens, _I32, (B,)))
-    if workspace is not None:
-        checks.append(("workspace", workspace, _U8, (workspace.numel(),)))
-    dev = _need_here(func, checks)
-    L = lib()
-    if workspace is None:
-        nbytes = _cross_workspace(dev, B, Hq, Hkv, Nq, Nk, d)
-        if nbytes:
-            workspace = _workspace_on(stream, nbytes, q.device)
-    else:
-        nbytes = workspace.numel()
-    o_fp32 = o.dtype == torch.float32
-    opts = ctypes.byref(FaCrossOpts(o_fp32, wait_budget_cycles)) if o_fp32 or wait_budget_cycles else None
-    _check(L.fa_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_lens), o.data_ptr(), lse.data_ptr(), B, Hq,
-                          Hkv, Nq, Nk, d, float(scale), _ptr(workspace), nbytes, _stream_on(dev, stream), opts), func)
+    fp32 (from its dtype); lse [B, Hq, Nq] fp32.  Nq = 1 is a decode step.  ``workspace``: a 1-dimensional uint8
+    CUDA tensor of fa_cross_workspace_bytes() bytes; allocated here when None."""
+    if _lib is None:
+        lib()
+    if stream is not None and workspace is None:
+        nbytes = fa_cross_workspace_bytes(*_cross_fwd_sizes(q, k, v, o, lse, kv_lens, workspace))
+        workspace = _workspace_on(stream, nbytes, q.device) if nbytes else None
+    st = _calls.cross_fwd(q, k, v, o, lse, scale, kv_lens, workspace, _handle(stream), wait_budget_cycles)
+    if st:
+        if st < 0:
+            _cross_fwd_sizes(q, k, v, o, lse, kv_lens, workspace)
+            _refused("fa_cross_fwd")
+        _check(st, "fa_cross_fwd")
 
 
 def fa_cross_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
@@ -489,29 +498,20 @@ def fa_cross_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d:
 def fa_cross_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale: float, kv_lens=None, workspace=None, stream=None,
                  wait_budget_cycles: int = 0):
     """Gradients of fa_cross_fwd (which produced the bf16 o, and lse, with the same kv_lens and scale): dq like q,
-    dk and dv like k, bf16 or fp32 (from dq's dtype).  ``workspace``: a uint8 CUDA tensor of
+    dk and dv like k, bf16 or fp32 (from dq's dtype).  ``workspace``: a 1-dimensional uint8 CUDA tensor of
     fa_cross_bwd_workspace_bytes() bytes; allocated here when None."""
-    func = "fa_cross_bwd"
-    B, Hq, Nq, d = qs = _shape4(func, "q", q)
-    _, Hkv, Nk, _ = _shape4(func, "k", k)
-    _shape4(func, "dq", dq)
-    ks, grad = (B, Hkv, Nk, d), (dq.dtype,) if dq.dtype in _OUT else _OUT
-    checks = [("q", q, _BF16, qs), ("o", o, _BF16, qs), ("dout", dout, _BF16, qs), ("k", k, _BF16, ks),
-              ("v", v, _BF16, ks), ("lse", lse, _F32, (B, Hq, Nq)), ("dq", dq, grad, qs), ("dk", dk, grad, ks),
-              ("dv", dv, grad, ks)]
-    if kv_lens is not None:
-        checks.append(("kv_lens", kv_lens, _I32, (B,)))
-    if workspace is not None:
-        checks.append(("workspace", workspace, _U8, (workspace.numel(),)))
-    dev = _need_here(func, checks)
-    L = lib()
-    if workspace is None:
-        workspace = _workspace_on(stream, L.fa_cross_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, d), q.device)
-    opts = ctypes.byref(FaBwdOpts(wait_budget_cycles)) if wait_budget_cycles else None
-    _check(L.fa_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_lens), o.data_ptr(), dout.data_ptr(),
-                          lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Nq, Nk, d,
-                          float(scale), dq.dtype == torch.float32, _ptr(workspace), workspace.numel(),
-                          _stream_on(dev, stream), opts), func)
+    if _lib is None:
+        lib()
+    if stream is not None and workspace is None:
+        sizes = _cross_bwd_sizes(q, k, v, o, dout, lse, dq, dk, dv, kv_lens, workspace)
+        workspace = _workspace_on(stream, fa_cross_bwd_workspace_bytes(*sizes), q.device)
+    st = _calls.cross_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale, kv_lens, workspace, _handle(stream),
+                          wait_budget_cycles)
+    if st:
+        if st < 0:
+            _cross_bwd_sizes(q, k, v, o, dout, lse, dq, dk, dv, kv_lens, workspace)
+            _refused("fa_cross_bwd")
+        _check(st, "fa_cross_bwd")
 
 
 def fa_rope_axes_plan(d: int, sections, base: float = 10000.0, interleaved: bool = False, per_axis: bool = False,
@@ -531,27 +531,49 @@ def _need_plan(func: str, plan, d: int):
         raise FattnError(FA_ERR_INVALID_ARG, func, f"plan must be fa_rope_axes_plan's for d={d}")
 
 
+def _refuse_rope(func: str, q, k, pos, plan, q_out, k_out):
+    B, Hq, N, d = qs = _shape4(func, "q", q)
+    _need_here(func, ("q", q, _BF16, qs), ("q_out", q_out, _BF16, qs))
+    if k is not None:
+        Hk = _shape4(func, "k", k)[1]
+        _need_here(func, ("k", k, _BF16, (B, Hk, N, d)), ("k_out", k_out, _BF16, (B, Hk, N, d)))
+    elif k_out is not None:
+        raise FattnError(FA_ERR_INVALID_ARG, func, "k_out without k")
+    _need_plan(func, plan, d)
+    _need_here(func, ("pos", pos, _I32, (plan.n_axes, B, N)))
+    _refused(func)
+
+
 def fa_rope_axes(q, k, pos, plan, q_out=None, k_out=None, inverse: bool = False, stream=None):
     """Turn q [B, Hq, N, d] into q_out and k [B, Hk, N, d] (or None) into k_out by the positions pos
     [axes, B, N] int32; in place where an output is None or its input.  inverse=True turns back: the
     gradients of q and k from those of q_out and k_out."""
-    func = "fa_rope_axes"
-    B, Hq, N, d = qs = _shape4(func, "q", q)
+    if _lib is None:
+        lib()
     q_out = q if q_out is None else q_out
-    checks = [("q", q, _BF16, qs), ("q_out", q_out, _BF16, qs)]
-    Hk = 0
-    if k is not None:
-        Hk = _shape4(func, "k", k)[1]
-        k_out = k if k_out is None else k_out
-        ks = (B, Hk, N, d)
-        checks += [("k", k, _BF16, ks), ("k_out", k_out, _BF16, ks)]
-    elif k_out is not None:
-        raise FattnError(FA_ERR_INVALID_ARG, func, "k_out without k")
+    k_out = k if k_out is None else k_out
+    st = _calls.rope_axes(q, k, pos, plan, q_out, k_out, inverse, _handle(stream))
+    if st:
+        if st < 0:
+            _refuse_rope("fa_rope_axes", q, k, pos, plan, q_out, k_out)
+        _check(st, "fa_rope_axes")
+
+
+def _refuse_paged(func: str, q, k, v, pos, plan, q_out, k_pages, v_pages, block_table, seq_lens, new_lens):
+    B, Hq, N, d = qs = _shape4(func, "q", q)
+    Hk = _shape4(func, "k", k)[1]
+    P, _, page_size, _ = _shape4(func, "k_pages", k_pages)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise FattnError(FA_ERR_INVALID_ARG, func, "block_table must be a 2-dimensional torch.Tensor")
     _need_plan(func, plan, d)
-    checks.append(("pos", pos, _I32, (plan.n_axes, B, N)))
-    dev = _need_here(func, checks)
-    _check(lib().fa_rope_axes(q.data_ptr(), _ptr(k), pos.data_ptr(), q_out.data_ptr(), _ptr(k_out), B, Hq, Hk, N, plan,
-                              bool(inverse), _stream_on(dev, stream)), func)
+    ks, pool = (B, Hk, N, d), (P, Hk, page_size, d)
+    _need_here(func, ("q", q, _BF16, qs), ("q_out", q_out, _BF16, qs), ("k", k, _BF16, ks), ("v", v, _BF16, ks),
+               ("k_pages", k_pages, _BF16, pool), ("v_pages", v_pages, _BF16, pool),
+               ("block_table", block_table, _I32, (B, block_table.shape[1])), ("seq_lens", seq_lens, _I32, (B,)),
+               ("pos", pos, _I32, (plan.n_axes, B, N)))
+    if new_lens is not None:
+        _need_here(func, ("new_lens", new_lens, _I32, (B,)))
+    _refused(func)
 
 
 def fa_rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table, seq_lens, new_lens=None,
@@ -559,26 +581,15 @@ def fa_rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table,
     """New tokens of a decode step or prompt chunk: q [B, Hq, N, d] turned into q_out, k [B, Hk, N, d] turned and
     v copied into the pools k_pages, v_pages [P, Hk, page_size, d] of fa_decode_paged, as keys seq_lens[b] ..
     of sequence b (int32 [B], the lengths before this call); tokens from new_lens[b] on are padding."""
-    func = "fa_rope_axes_paged"
-    B, Hq, N, d = qs = _shape4(func, "q", q)
-    Hk = _shape4(func, "k", k)[1]
-    P, _, page_size, _ = _shape4(func, "k_pages", k_pages)
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise FattnError(FA_ERR_INVALID_ARG, func, "block_table must be a 2-dimensional torch.Tensor")
-    max_pages = block_table.shape[1]
-    _need_plan(func, plan, d)
-    ks, pool = (B, Hk, N, d), (P, Hk, page_size, d)
-    checks = [("q", q, _BF16, qs), ("q_out", q_out, _BF16, qs), ("k", k, _BF16, ks), ("v", v, _BF16, ks),
-              ("k_pages", k_pages, _BF16, pool), ("v_pages", v_pages, _BF16, pool),
-              ("block_table", block_table, _I32, (B, max_pages)), ("seq_lens", seq_lens, _I32, (B,)),
-              ("pos", pos, _I32, (plan.n_axes, B, N))]
-    if new_lens is not None:
-        checks.append(("new_lens", new_lens, _I32, (B,)))
-    dev = _need_here(func, checks)
-    _check(lib().fa_rope_axes_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), pos.data_ptr(), q_out.data_ptr(),
-                                    k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-                                    seq_lens.data_ptr(), _ptr(new_lens), B, Hq, Hk, N, page_size, max_pages, P, plan,
-                                    _stream_on(dev, stream)), func)
+    if _lib is None:
+        lib()
+    st = _calls.rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table, seq_lens, new_lens,
+                                _handle(stream))
+    if st:
+        if st < 0:
+            _refuse_paged("fa_rope_axes_paged", q, k, v, pos, plan, q_out, k_pages, v_pages, block_table, seq_lens,
+                          new_lens)
+        _check(st, "fa_rope_axes_paged")
 
 
 def fa_get_status(stream=None) -> int:
