@@ -58,6 +58,7 @@ struct CrossArgs {
   const int* kv_lens;
   int kv_heads, n_keys, tiles;
   long long part_stride;
+  float* delta_out;  // dQ kernel, at most one key tile: D is computed here and written for the dK/dV kernel; else null
   __device__ __forceinline__ int keys(int bh) const {
     return kv_lens ? min(max(kv_lens[bh / kv_heads], 0), n_keys) : n_keys;
   }
@@ -81,6 +82,22 @@ __device__ __forceinline__ void clear_pairs(uint32_t (&pp)[16], uint32_t (&dp)[1
 // follows in the stream may: its last block ends only when that grid is complete.
 __device__ __forceinline__ void wait_as_last_block() {
   if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) grid_dep_wait();
+}
+
+// Sum of P dP over 32 keys of a query row (those past `lim` count for nothing, whatever they hold).
+template <bool MASK>
+__device__ __forceinline__ float dot_pairs(const uint32_t (&sv)[32], const uint32_t (&pv)[32], uint64_t c2, uint64_t nl2,
+                                           int key0, int lim) {
+  float acc0 = 0.f, acc1 = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nl2), x0, x1);
+    const float y0 = ex2(x0) * __uint_as_float(pv[e]), y1 = ex2(x1) * __uint_as_float(pv[e + 1]);
+    if (!MASK || key0 + e <= lim) acc0 += y0;
+    if (!MASK || key0 + e + 1 <= lim) acc1 += y1;
+  }
+  return acc0 + acc1;
 }
 
 // Products of a 128-row tile A with rows 64 q .. of a streamed tile: 128 x 64, K = d.
@@ -457,8 +474,33 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
     const uint32_t tS = lanes + kPair * g, tP = tS + 64;
     const bool in = row < N;
     const float lse2 = in ? lse[static_cast<size_t>(bh) * N + row] * kLog2e : INFINITY;
-    const float dd = in ? delta[static_cast<size_t>(bh) * N + row] : 0.f;
-    const uint64_t c2 = f2_pack(sl2, sl2), nl2 = f2_pack(-lse2, -lse2), nd2 = f2_pack(-dd, -dd);
+    const uint64_t c2 = f2_pack(sl2, sl2), nl2 = f2_pack(-lse2, -lse2);
+    float dd = 0.f;
+    if (!x.delta_out) {
+      if (in) dd = delta[static_cast<size_t>(bh) * N + row];
+    } else if (g < n_h) {
+      // One key tile: the row's D = sum of P dP is at hand (half g in this thread), and more exact than
+      // rowsum(O dO) with O rounded to bf16, whose error a softmax over few keys does not average out.
+      float part = 0.f;
+      if (bwait_all(BAR(C::B_SF + g), 0, abort_flag, budget)) {
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t sv[32], pv[32];
+          tmem_ld_x32(tS + 32 * c, sv);
+          tmem_ld_x32(tP + 32 * c, pv);
+          const int k0 = g * kHalf + 32 * c;
+          if (k0 + 32 > mine) part += dot_pairs<true>(sv, pv, c2, nl2, k0, mine - 1);
+          else part += dot_pairs<false>(sv, pv, c2, nl2, k0, mine - 1);
+        }
+      }
+      float* parts = reinterpret_cast<float*>(gbase + C::OFF_VEC);
+      parts[g * kTile + r] = part;
+      named_bar_sync(1, 128 * n_h);  // (reached after a timeout, too)
+      dd = parts[r] + (n_h > 1 ? parts[kTile + r] : 0.f);
+      if (g == 0 && in) x.delta_out[static_cast<size_t>(bh) * N + row] = dd;
+    }
+    const uint64_t nd2 = f2_pack(-dd, -dd);
     bool ok = true;
     for (int hh = g; ok && hh < n_h; hh += C::FLIGHT) {
       ok = bwait_all(BAR(C::B_SF + g), (hh / C::FLIGHT) & 1, abort_flag, budget);
@@ -541,39 +583,46 @@ template <int D>
 cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   using KV = CrossCfg<D, 2 * D>;
   using Q = CrossCfg<D, D>;
-  cudaError_t e = launch_delta(a.o, a.dout, a.delta, static_cast<long long>(a.BH) * a.N, D, stream);
-  if (e != cudaSuccess) return e;
   const long long kv_elems = static_cast<long long>(a.BH) * a.Nk * D, q_elems = static_cast<long long>(a.BH) * a.N * D;
   const int k_tiles = (a.Nk + kTile - 1) / kTile, q_tiles = (a.N + kTile - 1) / kTile;
   const bool kv_part = a.kv_splits > 1, q_part = a.q_splits > 1;
   auto k1 = cross_dkdv_kernel<D>;
-  if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, KV::SMEM)) != cudaSuccess) return e;
-  const dim3 g1(static_cast<unsigned>(a.BH), static_cast<unsigned>(k_tiles), static_cast<unsigned>(a.kv_splits));
-  float* dv_part = a.kv_part + a.kv_splits * kv_elems;
-  k1<<<g1, KV::THREADS, KV::SMEM, stream>>>(
-      a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, kv_part ? a.kv_part : a.dk, kv_part ? dv_part : a.dv, a.N, a.scale_log2,
-      a.scale, kv_part || a.grad_fp32, a.budget, a.tdk, a.tdv, head_groups(a.BH, k_tiles, false, a.sms),
-      CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.q_tiles, kv_part ? kv_elems : 0});
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   auto k2 = cross_dq_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, KV::SMEM);
+  if (e != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::SMEM)) != cudaSuccess) return e;
-  const dim3 g2(static_cast<unsigned>(a.BH), static_cast<unsigned>(q_tiles), static_cast<unsigned>(a.q_splits));
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = g2;
-  cfg.blockDim = dim3(Q::THREADS);
-  cfg.dynamicSmemBytes = Q::SMEM;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, k2, a.tq, a.tk, a.tv, a.tdo, a.lse, static_cast<const float*>(a.delta),
-                              q_part ? static_cast<void*>(a.q_part) : a.dq, a.N, a.scale_log2, a.scale,
-                              static_cast<int>(q_part || a.grad_fp32), a.budget, a.tdq,
-                              head_groups(a.BH, q_tiles, false, a.sms),
-                              CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.k_tiles, q_part ? q_elems : 0})) != cudaSuccess)
-    return e;
+  float* dv_part = a.kv_part + a.kv_splits * kv_elems;
+  auto dkdv = [&]() -> cudaError_t {
+    const dim3 grid(static_cast<unsigned>(a.BH), static_cast<unsigned>(k_tiles), static_cast<unsigned>(a.kv_splits));
+    k1<<<grid, KV::THREADS, KV::SMEM, stream>>>(
+        a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, kv_part ? a.kv_part : a.dk, kv_part ? dv_part : a.dv, a.N,
+        a.scale_log2, a.scale, kv_part || a.grad_fp32, a.budget, a.tdk, a.tdv, head_groups(a.BH, k_tiles, false, a.sms),
+        CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.q_tiles, kv_part ? kv_elems : 0, nullptr});
+    return cudaGetLastError();
+  };
+  auto dq = [&](bool behind_dkdv) -> cudaError_t {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.BH), static_cast<unsigned>(q_tiles), static_cast<unsigned>(a.q_splits));
+    cfg.blockDim = dim3(Q::THREADS);
+    cfg.dynamicSmemBytes = Q::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = behind_dkdv ? 1 : 0;
+    return cudaLaunchKernelEx(
+        &cfg, k2, a.tq, a.tk, a.tv, a.tdo, a.lse, static_cast<const float*>(a.delta),
+        q_part ? static_cast<void*>(a.q_part) : a.dq, a.N, a.scale_log2, a.scale,
+        static_cast<int>(q_part || a.grad_fp32), a.budget, a.tdq, head_groups(a.BH, q_tiles, false, a.sms),
+        CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.k_tiles, q_part ? q_elems : 0, behind_dkdv ? nullptr : a.delta});
+  };
+  if (k_tiles == 1) {  // dQ first: it finds D, which takes no kernel then and does not go through O
+    if ((e = dq(false)) != cudaSuccess || (e = dkdv()) != cudaSuccess) return e;
+  } else {
+    e = launch_delta(a.o, a.dout, a.delta, static_cast<long long>(a.BH) * a.N, D, stream);
+    if (e != cudaSuccess || (e = dkdv()) != cudaSuccess || (e = dq(true)) != cudaSuccess) return e;
+  }
   if (kv_part && (e = launch_sum(a.kv_part, a.dk, a.dv, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess)
     return e;
   if (q_part) return launch_sum(a.q_part, a.dq, nullptr, q_elems, a.q_splits, a.grad_fp32, stream);

@@ -372,7 +372,7 @@ CrossBwdPlan plan_cross_bwd(const CrossShape& c, int Nk, int d, int sms) {
   // d = 64: 193 / 204 / 215 / 222 us; B2 H16/4 1000 x 577: 40 / 33 / 36 / 35 us; B1 H8/2 4096 x 300, 1 / 8 / 16 / 32:
   // 134 / 28 / 26 / 32 us.
   p.q_splits = cut_scan(c.bh * qt, kt, sms, q);
-  p.kv_splits = cut_scan(c.bh * kt, qt, sms, kv, 0.75 * c.bh * qt * (kt + 3));
+  p.kv_splits = cut_scan(c.bh * kt, qt, sms, kv, kt > 1 ? 0.75 * c.bh * qt * (kt + 3) : 0.0);  // (kt = 1: dQ runs first)
   p.q_tiles = (qt + p.kv_splits - 1) / p.kv_splits;
   p.k_tiles = (kt + p.q_splits - 1) / p.q_splits;
   p.delta_bytes = round256(static_cast<size_t>(c.bh) * c.rows * sizeof(float));
