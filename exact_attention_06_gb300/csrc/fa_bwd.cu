@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(256) bwd_delta_kernel(const __nv_bfloat16* __r
                                                         const __nv_bfloat16* __restrict__ dout,
                                                         float* __restrict__ delta, long long rows) {
   constexpr int TPR = D / 8;  // threads per row, 8 elements (16 bytes) each
+  grid_dep_launch();          // a kernel launched programmatically after this one may set itself up meanwhile
   const long long gt = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   const long long row = gt / TPR;
   const int part = static_cast<int>(gt % TPR);

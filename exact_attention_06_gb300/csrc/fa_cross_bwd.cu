@@ -78,8 +78,9 @@ __device__ __forceinline__ void clear_pairs(uint32_t (&pp)[16], uint32_t (&dp)[1
   for (int i = 0; i < 16; ++i) pp[i] = dp[i] = 0;
 }
 
-// The dQ kernel needs nothing of the dK/dV kernel that it is launched programmatically after (and overlaps), but what
-// follows in the stream may: its last block ends only when that grid is complete.
+// The dQ kernel needs nothing of the dK/dV kernel that it is launched programmatically after (and overlaps), and a block
+// of padding needs nothing at all, but what follows in the stream may: a grid's last block ends only when the
+// grid before is complete.
 __device__ __forceinline__ void wait_as_last_block() {
   if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) grid_dep_wait();
 }
@@ -141,7 +142,6 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 4);
 #define BAR(i) (sBar + 8u * static_cast<uint32_t>(i))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_dep_launch();  // the dQ kernel may take SMs as this grid's last round leaves them idle
   int bh, kt;
   grouped_block(ng, bh, kt);
   const int row0 = static_cast<int>(blockIdx.z) * x.tiles * kTile;  // this block's query rows
@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
     const int rows = min(kTile, x.n_keys - kt * kTile);
     zero_rows<D>(dk, k0, rows, grad_fp32);
     zero_rows<D>(dv, k0, rows, grad_fp32);
+    wait_as_last_block();
     return;
   }
   if (threadIdx.x == 0) {
@@ -208,6 +209,12 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
           tma_load_3d(st + h * kBox, &tq, BAR(C::B_FULL + s), h * 64, row0 + i * kTile, bh);
           tma_load_3d(st + C::TB + h * kBox, &tdo, BAR(C::B_FULL + s), h * 64, row0 + i * kTile, bh);
         }
+      }
+      if (i == 0) {
+        // Launched programmatically: D comes from the kernel before.  The dQ kernel, which reads it too, may then take
+        // SMs as this grid's last round leaves them idle.
+        grid_dep_wait();
+        grid_dep_launch();
       }
       float* vs = vec + s * (2 * kTile);
 #pragma unroll
@@ -333,6 +340,7 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
                       float sl2, float scale, int grad_fp32, unsigned long long budget,
                       const __grid_constant__ CUtensorMap tdq, int ng, const CrossArgs x) {
   using C = CrossCfg<D, D>;
+  grid_dep_launch();  // (the dK/dV kernel behind this one, when there is one key tile)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -592,24 +600,28 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::SMEM)) != cudaSuccess) return e;
   float* dv_part = a.kv_part + a.kv_splits * kv_elems;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = &attr;
   auto dkdv = [&]() -> cudaError_t {
-    const dim3 grid(static_cast<unsigned>(a.BH), static_cast<unsigned>(k_tiles), static_cast<unsigned>(a.kv_splits));
-    k1<<<grid, KV::THREADS, KV::SMEM, stream>>>(
-        a.tq, a.tk, a.tv, a.tdo, a.lse, a.delta, kv_part ? a.kv_part : a.dk, kv_part ? dv_part : a.dv, a.N,
-        a.scale_log2, a.scale, kv_part || a.grad_fp32, a.budget, a.tdk, a.tdv, head_groups(a.BH, k_tiles, false, a.sms),
+    cfg.gridDim = dim3(static_cast<unsigned>(a.BH), static_cast<unsigned>(k_tiles), static_cast<unsigned>(a.kv_splits));
+    cfg.blockDim = dim3(KV::THREADS);
+    cfg.dynamicSmemBytes = KV::SMEM;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(
+        &cfg, k1, a.tq, a.tk, a.tv, a.tdo, a.lse, static_cast<const float*>(a.delta),
+        kv_part ? static_cast<void*>(a.kv_part) : a.dk, kv_part ? static_cast<void*>(dv_part) : a.dv, a.N, a.scale_log2,
+        a.scale, static_cast<int>(kv_part || a.grad_fp32), a.budget, a.tdk, a.tdv,
+        head_groups(a.BH, k_tiles, false, a.sms),
         CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.q_tiles, kv_part ? kv_elems : 0, nullptr});
-    return cudaGetLastError();
   };
   auto dq = [&](bool behind_dkdv) -> cudaError_t {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.BH), static_cast<unsigned>(q_tiles), static_cast<unsigned>(a.q_splits));
     cfg.blockDim = dim3(Q::THREADS);
     cfg.dynamicSmemBytes = Q::SMEM;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
     cfg.numAttrs = behind_dkdv ? 1 : 0;
     return cudaLaunchKernelEx(
         &cfg, k2, a.tq, a.tk, a.tv, a.tdo, a.lse, static_cast<const float*>(a.delta),
