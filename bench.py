@@ -64,18 +64,18 @@ def _peaks():
 
 # DRAM bytes per launch (dram__bytes_read.sum + dram__bytes_write.sum) from ncu captures summarised
 # under profiles/, keyed by kernel and workload, valid only while the kernel sources are unchanged.
-_FWD = "bf5065744ca54e1b253c2dc98ec99b932f320522aa698fdb3178cb9e91562e04"
-_BWD = "3100608144e05a1479f6d4eec6fe754549bc5e11c799049f40b136280dca76b6"
+_FWD = "a42d8c474ca6f4e08da13b623285a7aa8937d96c7bbbac76fa3477ba121c3074"
+_BWD = "cfd5e6d8f269fb875eb6196f0e05848be8dc3643e808bbe8f4907ae37fbe8129"
 _DEC = "238a9c1b2ffecb15b22cb24a1544220a197fcbdb2c867899597a0c8e4fa65d64"
 NCU_TRAFFIC = {
-    ("fwd_kernel", "ragged"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 559.377e6},
-    ("fwd_kernel", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 263.888e6},
-    ("fwd_kernel_fp8", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 136.481e6},
-    ("fwd_persist_kernel", "prefill"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 50.483e6},
+    ("fwd_kernel", "ragged"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 558.459e6},
+    ("fwd_kernel", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 263.884e6},
+    ("fwd_kernel_fp8", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 136.213e6},
+    ("fwd_persist_kernel", "prefill"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 50.643e6},
     # backward: the dominant kernel (dK/dV) on the causal workload
-    ("bwd_dkdv_kernel", "causal"): {"sources": {"fa_bwd.cu": _BWD}, "bytes": 372.482e6},
+    ("bwd_dkdv_kernel", "causal"): {"sources": {"fa_bwd.cu": _BWD}, "bytes": 375.680e6},
     # the four-shard step: four forward launches over the key shards and the combine, summed
-    ("causal_sharded4", "causal"): {"sources": {"fa_fwd.cu": _FWD, "fa_decode.cu": _DEC}, "bytes": 1108.970e6},
+    ("causal_sharded4", "causal"): {"sources": {"fa_fwd.cu": _FWD, "fa_decode.cu": _DEC}, "bytes": 1108.376e6},
     # decode: captured on the B4 slice (decode_small) and scaled by 16 to B64 (K/V streamed once)
     ("decode_split_kernel", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2151.001e6},
     ("decode_split_kernel_paged", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.928e6},
