@@ -3,16 +3,16 @@
 // since doing it in Python took longer (5-9 us a call) than the kernels of a small step.
 //
 // Every function returns the library's status, or -1 when an argument is not what the call takes (nothing has been
-// launched then; fattn.py finds out which one and raises).  No exception leaves a function except as a Python error.
+// launched then; fattn.py finds out which one and raises).  C++ exceptions (an allocation that fails) become torch's Python errors.
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
-#include <exception>
 #include <initializer_list>
 
 #include "fattn.h"
@@ -152,7 +152,8 @@ void* workspace(Args& a, int i, size_t* bytes) {
 }
 
 // q, k, v, o, lse, scale, kv_lens | None, workspace | None (allocated on the current stream), stream | None, cycles
-PyObject* cross_fwd(PyObject*, PyObject* const* argv, Py_ssize_t n) try {
+PyObject* cross_fwd(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
   if (n != 10) return status(-1);
   Args a{argv};
   int64_t q[4], k[4];
@@ -178,13 +179,12 @@ PyObject* cross_fwd(PyObject*, PyObject* const* argv, Py_ssize_t n) try {
   }
   return status(api.cross_fwd(pq, pk, pv, static_cast<const int*>(lens), po, static_cast<float*>(lse), B, Hq, Hkv, Nq,
                               Nk, d, scale, ws, bytes, stream, &opts));
-} catch (const std::exception& e) {
-  PyErr_SetString(PyExc_RuntimeError, e.what());
-  return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 
 // q, k, v, o, dout, lse, dq, dk, dv, scale, kv_lens | None, workspace | None, stream | None, cycles
-PyObject* cross_bwd(PyObject*, PyObject* const* argv, Py_ssize_t n) try {
+PyObject* cross_bwd(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
   if (n != 14) return status(-1);
   Args a{argv};
   int64_t q[4], k[4];
@@ -214,13 +214,12 @@ PyObject* cross_bwd(PyObject*, PyObject* const* argv, Py_ssize_t n) try {
   }
   return status(api.cross_bwd(pq, pk, pv, static_cast<const int*>(lens), po, pdo, static_cast<const float*>(lse), dq, dk,
                               dv, B, Hq, Hkv, Nq, Nk, d, scale, f0, ws, bytes, stream, &opts));
-} catch (const std::exception& e) {
-  PyErr_SetString(PyExc_RuntimeError, e.what());
-  return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 
 // q, k | None, pos, plan, q_out, k_out | None, inverse, stream | None
-PyObject* rope_axes(PyObject*, PyObject* const* argv, Py_ssize_t n) try {
+PyObject* rope_axes(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
   if (n != 8) return status(-1);
   Args a{argv};
   int64_t q[4], k[4] = {0, 0, 0, 0};
@@ -245,13 +244,12 @@ PyObject* rope_axes(PyObject*, PyObject* const* argv, Py_ssize_t n) try {
     return status(-1);
   }
   return status(api.rope(pq, pk, static_cast<const int*>(pos), qo, ko, q[0], q[1], k[1], q[2], plan.p, inverse, stream));
-} catch (const std::exception& e) {
-  PyErr_SetString(PyExc_RuntimeError, e.what());
-  return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 
 // q, k, v, pos, plan, q_out, k_pages, v_pages, block_table, seq_lens, new_lens | None, stream | None
-PyObject* rope_axes_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) try {
+PyObject* rope_axes_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
   if (n != 12) return status(-1);
   Args a{argv};
   int64_t q[4], k[4], pool[4];
@@ -276,9 +274,7 @@ PyObject* rope_axes_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) try {
   return status(api.rope_paged(pq, pk, pv, static_cast<const int*>(pos), qo, kp, vp, static_cast<const int*>(bt),
                                static_cast<const int*>(lens), static_cast<const int*>(news), q[0], q[1], k[1], q[2],
                                pool[2], max_pages, pool[0], plan.p, stream));
-} catch (const std::exception& e) {
-  PyErr_SetString(PyExc_RuntimeError, e.what());
-  return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 
 // Addresses of fa_cross_fwd, fa_cross_workspace_bytes, fa_cross_bwd, fa_cross_bwd_workspace_bytes, fa_rope_axes,

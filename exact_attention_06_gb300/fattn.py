@@ -432,13 +432,18 @@ def _workspace_on(stream, nbytes: int, device):
     """Scratch that lives as long as the stream's work needs it: allocated on that stream, so that its
     memory goes to no other stream's tensor while the kernels may still use it."""
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+        stream = torch.cuda.ExternalStream(stream)
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _handle(stream):
-    return None if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    """A torch stream's or a raw (int) handle; None: the current stream, which the compiled module looks up."""
+    if stream is None or isinstance(stream, int):
+        return stream
+    if not hasattr(stream, "cuda_stream"):
+        raise FattnError(FA_ERR_INVALID_ARG, "stream", "stream must be a torch.cuda.Stream, a handle (int) or None")
+    return stream.cuda_stream
 
 
 def fa_cross_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
@@ -480,10 +485,11 @@ def fa_cross_fwd(q, k, v, o, lse, scale: float, kv_lens=None, workspace=None, st
     CUDA tensor of fa_cross_workspace_bytes() bytes; allocated here when None."""
     if _lib is None:
         lib()
+    handle = _handle(stream)
     if stream is not None and workspace is None:
         nbytes = fa_cross_workspace_bytes(*_cross_fwd_sizes(q, k, v, o, lse, kv_lens, workspace))
         workspace = _workspace_on(stream, nbytes, q.device) if nbytes else None
-    st = _calls.cross_fwd(q, k, v, o, lse, scale, kv_lens, workspace, _handle(stream), wait_budget_cycles)
+    st = _calls.cross_fwd(q, k, v, o, lse, scale, kv_lens, workspace, handle, wait_budget_cycles)
     if st:
         if st < 0:
             _cross_fwd_sizes(q, k, v, o, lse, kv_lens, workspace)
@@ -502,11 +508,11 @@ def fa_cross_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale: float, kv_lens=None, 
     fa_cross_bwd_workspace_bytes() bytes; allocated here when None."""
     if _lib is None:
         lib()
+    handle = _handle(stream)
     if stream is not None and workspace is None:
         sizes = _cross_bwd_sizes(q, k, v, o, dout, lse, dq, dk, dv, kv_lens, workspace)
         workspace = _workspace_on(stream, fa_cross_bwd_workspace_bytes(*sizes), q.device)
-    st = _calls.cross_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale, kv_lens, workspace, _handle(stream),
-                          wait_budget_cycles)
+    st = _calls.cross_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale, kv_lens, workspace, handle, wait_budget_cycles)
     if st:
         if st < 0:
             _cross_bwd_sizes(q, k, v, o, dout, lse, dq, dk, dv, kv_lens, workspace)

@@ -425,7 +425,8 @@ size_t fa_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 
 /* fa_cross_fwd -- workspace: caller-owned device scratch of fa_cross_workspace_bytes() bytes,
  * 256-byte aligned (FA_ERR_WORKSPACE if smaller), or NULL: one kernel, the keys uncut.  O and lse
- * are the same function of the inputs either way, up to rounding order.  opts may be NULL. */
+ * are the same function of the inputs either way, up to rounding order.  A workspace serves one call at
+ * a time (calls that overlap on the GPU need one each).  opts may be NULL. */
 fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int* kv_lens, void* o, float* lse,
                          int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, void* workspace,
                          size_t ws_bytes, void* stream, const fa_cross_opts* opts);
