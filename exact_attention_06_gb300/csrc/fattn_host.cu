@@ -297,7 +297,8 @@ int cut_scan(long long units, int tiles, int sms, double part_bytes, double fill
 }
 
 struct CrossPlan {
-  int few = 0;  // 1: the few-row kernel; its splits are a cluster unless `parts`
+  int few = 0;    // 1: the few-row kernel; its splits are a cluster unless `parts`
+  int tiles = 0;  // > 0: the short-key kernel, this many query tiles a block
   int parts = 0;
   int splits = 1, kchunk = 0;
   size_t u_bytes = 0, m_bytes = 0;
@@ -337,6 +338,22 @@ void plan_few(CrossPlan* p, const CrossShape& c, int Nk, int d, int sms, bool al
   p->parts = p->splits > 8;
 }
 
+// The short-key kernel's query tiles per block: about 1 us a tile, 4 a block's set-up and end.
+int plan_short(const CrossShape& c, int sms) {
+  const int n = (c.rows + 127) / 128;
+  int best = 1;
+  double best_t = 0;
+  for (int tiles = 1; tiles <= n; tiles = tiles < 8 ? tiles + 1 : tiles + tiles / 8) {
+    const long long blocks = c.bh * ((n + tiles - 1) / tiles);
+    const double t = static_cast<double>((blocks + sms - 1) / sms) * (tiles + 4.0);
+    if (tiles == 1 || t < best_t) {
+      best_t = t;
+      best = tiles;
+    }
+  }
+  return best;
+}
+
 CrossPlan plan_cross(const CrossShape& c, int Nk, int d, int sms, bool workspace) {
   CrossPlan p;
   const int tiles = (Nk + 127) / 128;
@@ -347,6 +364,8 @@ CrossPlan plan_cross(const CrossShape& c, int Nk, int d, int sms, bool workspace
   // against 83 / 87 / 87 / 88; 64 x 577 keys 5.9 / 7.5 / 8.2 / 9.6 against 10.8.
   if (c.rows <= fattn::kCrossRowsMax)
     plan_few(&p, c, Nk, d, sms, can_join);
+  else if (Nk <= fattn::kCrossShortKeys)
+    p.tiles = plan_short(c, sms);
   else if (can_join)
     p.splits = cut_scan(c.bh * ((c.rows + 255) / 256), tiles, sms, static_cast<double>(rows) * (d + 2) * 4);
   if (!p.few) p.parts = p.splits > 1;
@@ -978,6 +997,20 @@ fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int*
     if (e != cudaSuccess) return cuda_fail(e, "fa_cross_fwd launch");
     return join();
   }
+  if (plan.tiles > 0) {
+    fattn::CrossShortLaunch f{};
+    if ((st = make_map(&f.tq, q, d, c.rows, c.bh, 128)) != FA_OK) return st;
+    if ((st = make_map(&f.tk, k, d, Nk, c.bh, 128)) != FA_OK) return st;
+    if ((st = make_map(&f.tv, v, d, Nk, c.bh, 128)) != FA_OK) return st;
+    if (!o_fp32 && (st = make_map(&f.to, o, d, c.rows, c.bh, 128)) != FA_OK) return st;
+    f.BH = static_cast<int>(c.bh);
+    f.d = d;
+    f.args = {o, lse, kv_lens, Hkv, c.rows, Nk, plan.tiles, o_fp32, scale_log2, budget};
+    cudaGetLastError();
+    const cudaError_t e = fattn::launch_cross_short(f, s);
+    if (e != cudaSuccess) return cuda_fail(e, "fa_cross_fwd launch");
+    return FA_OK;
+  }
   fattn::FwdLaunch a{};
   if ((st = make_map(&a.tq, q, d, c.rows, c.bh, 128)) != FA_OK) return st;
   if ((st = make_map(&a.tk, k, d, Nk, c.bh, 128)) != FA_OK) return st;
@@ -1199,7 +1232,7 @@ fa_status_t fa_get_status(void* stream) {
   if (e != cudaSuccess) return cuda_fail(e, "fa_get_status synchronize");
   const unsigned int bits = fattn::fwd_read_and_clear_status() | fattn::decode_read_and_clear_status() |
                             fattn::bwd_read_and_clear_status() | fattn::cross_bwd_read_and_clear_status() |
-                            fattn::cross_rows_read_and_clear_status();
+                            fattn::cross_rows_read_and_clear_status() | fattn::cross_short_read_and_clear_status();
   if (bits & fattn::kStatusTimeout) return fail(FA_ERR_TIMEOUT, "a kernel wait exceeded its budget");
   return FA_OK;
 }

@@ -121,6 +121,24 @@ cudaError_t launch_combine(const float* u_part, const float* m_part, const float
                            int R, int S, int d, int o_fp32, cudaStream_t stream);
 unsigned int decode_read_and_clear_status();
 
+// Cross attention over at most kCrossShortKeys keys: R rows of each of BH key heads, `tiles` tiles of 128 a block.
+constexpr int kCrossShortKeys = 128;
+struct CrossShortArgs {
+  void* o;
+  float* lse;
+  const int* kv_lens;
+  int kv_heads, R, Nk, tiles, o_fp32;
+  float sl2;  // scale * log2(e)
+  unsigned long long budget;
+};
+struct CrossShortLaunch {
+  CUtensorMap tq, tk, tv, to;  // 128-row boxes (to: bf16 O only)
+  CrossShortArgs args;
+  int BH, d;
+};
+cudaError_t launch_cross_short(const CrossShortLaunch& l, cudaStream_t stream);
+unsigned int cross_short_read_and_clear_status();
+
 // Cross attention of few rows: R <= kCrossRowsMax query rows of each of BH key heads against the first
 // kv_lens[bh / kv_heads] (null: Nk) of its keys, shared out over S blocks.  u_part == null: the S <= 8
 // blocks of a key head are a cluster and write o and lse; else partial slots [BH * R, S].

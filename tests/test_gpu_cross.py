@@ -135,7 +135,8 @@ def test_backward(B, Hq, Hkv, Nq, Nk, lens, d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("B,Hq,Hkv,Nq,Nk", [(64, 8, 8, 40, 100), (100, 6, 3, 70, 130), (30, 8, 8, 300, 257)])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,Nk", [(64, 8, 8, 40, 100), (100, 6, 3, 70, 130), (30, 8, 8, 300, 257),
+                                             (4, 16, 8, 1500, 77), (3, 8, 8, 3333, 64), (3, 4, 4, 7000, 1)])
 def test_many_blocks_of_few_keys(B, Hq, Hkv, Nq, Nk, d):
     """More blocks than SMs, each with a tile or two of keys and padding (or nothing) behind them."""
     g = torch.Generator().manual_seed(B)
@@ -211,7 +212,7 @@ def test_repeats_bitwise_and_matches_the_square_forward():
     assert all(torch.equal(x, y) for x, y in zip(*grads))
 
 
-@pytest.mark.parametrize("Nq,Nk", [(300, 700), (3, 700), (1, 20000)])
+@pytest.mark.parametrize("Nq,Nk", [(300, 700), (3, 700), (1, 20000), (5000, 77)])
 def test_a_wait_that_runs_out_is_reported(Nq, Nk):
     q, k, v, do, kl = _inputs(2, 4, 2, Nq, Nk, 128, [Nk, 650])
     o, lse = torch.empty_like(q), torch.empty(2, 4, Nq, device=DEV)
