@@ -3,9 +3,9 @@
 //
 // There is one tile of keys, so a block loads K and V once and streams query tiles past them: per tile
 // S = Q K^T, a softmax with nothing carried over, O = P~ V / l.  Bound by HBM (Q in, O out, 4 d + 4 bytes a row for
-// 4 d * keys flops), if the chain of a tile (about 2 us) is hidden: two tiles are in flight, each with its own S (P~ is
-// packed into it) and U in TMEM, four softmax warps (one thread per row) and MMA-issuing thread.  Measured beside
-// plan_short.
+// 4 d * keys flops), if the chain of a tile (about 2 us) is hidden: two or three tiles are in flight, each with its own
+// S (P~ is packed into it) and U in TMEM, four softmax warps (one thread per row) and MMA-issuing thread.  Measured
+// beside plan_short.
 //
 // Padding behind the sequence: its scores become -inf, and its rows of V are cleared in shared memory, once, since
 // P~ = 0 times what they hold would reach U.
@@ -26,26 +26,28 @@ constexpr int kTile = 128;              // query rows per tile
 constexpr uint32_t kBox = 128u * 128u;  // bytes of a 128-row x 64-column bf16 box
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kChains = 2;
-constexpr int kWarpMma = 4 * kChains, kWarpTma = kWarpMma + kChains, kThreads = (kWarpTma + 1) * 32;
 
-template <int D>
+// KT: keys of the tile that are computed (64 or 128).
+template <int D, int KT>
 struct ShortCfg {
+  // Tiles in flight (chains): two, or three where TMEM (S and U of each) and registers (98 a thread) hold them.
+  static constexpr int CH = D == 64 && KT == 64 ? 3 : 2;
+  static constexpr uint32_t COLS = CH == 2 ? 256 : 128;  // TMEM of a chain: S (P~ packed into it), U in the second half
+  static constexpr int WARP_MMA = 4 * CH, WARP_TMA = WARP_MMA + CH, THREADS = (WARP_TMA + 1) * 32;
   static constexpr int NH = D / 64;
   static constexpr uint32_t TB = NH * kBox;  // bytes of a 128 x d bf16 tile
-  // Ring stages of Q: tile k is chain k % 2's and in stage k % ST, so with an even ST a stage is always the same chain's,
-  // which then sees each of its phases.  (With three, a chain that waits for its phase p of a stage could find phase
-  // p - 2 when the other chain's p - 1 has not landed: a wait by parity must not skip phases.)
-  static constexpr int ST = D == 64 ? 4 : 2;
+  // Ring stages of Q: tile k is chain k % CH's and in stage k % ST, and ST is a multiple of CH, so that a stage is
+  // always the same chain's, which then sees each of its phases.  (Otherwise a chain that waits for phase p of a
+  // stage could find phase p - 2 when another chain's p - 1 has not landed: a wait by parity must not skip phases.)
+  static constexpr int ST = D == 64 ? 2 * CH : CH;
   static constexpr uint32_t OFF_K = 0, OFF_V = TB, OFF_Q = 2 * TB, OFF_O = OFF_Q + ST * TB;  // O: one tile a chain
-  static constexpr uint32_t OFF_BAR = OFF_O + kChains * TB;
-  static constexpr int B_KV = 0, B_VC = 1, B_QF = 2, B_QE = B_QF + ST, B_SF = B_QE + ST, B_PF = B_SF + kChains,
-                       B_OF = B_PF + kChains, B_OSF = B_OF + kChains, B_OW = B_OSF + kChains, B_DRAIN = B_OW + kChains,
-                       NBAR = B_DRAIN + kChains;
+  static constexpr uint32_t OFF_BAR = OFF_O + CH * TB;
+  static constexpr int B_KV = 0, B_VC = 1, B_QF = 2, B_QE = B_QF + ST, B_SF = B_QE + ST, B_PF = B_SF + CH,
+                       B_OF = B_PF + CH, B_OSF = B_OF + CH, B_OW = B_OSF + CH, B_DRAIN = B_OW + CH, NBAR = B_DRAIN + CH;
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR;
   static constexpr uint32_t SMEM = OFF_MISC + 16u + 1024u;
   static_assert(SMEM <= 232448, "shared memory");
-  static_assert(ST % kChains == 0, "a stage belongs to one chain");
+  static_assert(ST % CH == 0 && CH * COLS <= kTmemCols && KT <= COLS / 2 && D <= COLS / 2, "a stage belongs to one chain");
 };
 
 __device__ __forceinline__ bool swait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
@@ -85,13 +87,12 @@ __device__ __forceinline__ float max64(uint32_t (&s)[64], int valid) {
   return fmax3(a[0], a[1], fmaxf(a[2], a[3]));
 }
 
-// KT: keys of the tile that are computed (64 or 128).
 template <int D, int KT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(ShortCfg<D, KT>::THREADS, 1)
     cross_short_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
                        const CrossShortArgs a) {
-  using C = ShortCfg<D>;
+  using C = ShortCfg<D, KT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -116,8 +117,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rows = min(a.tiles * kTile, a.R - row0), row_bytes = D * (a.o_fp32 ? 4 : 2);
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.o) + frow0 * row_bytes);
     const long long vecs = static_cast<long long>(rows) * row_bytes / 16;
-    for (long long i = threadIdx.x; i < vecs; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
-    for (int i = threadIdx.x; i < rows; i += kThreads) a.lse[frow0 + i] = -INFINITY;
+    for (long long i = threadIdx.x; i < vecs; i += C::THREADS) dst[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < rows; i += C::THREADS) a.lse[frow0 + i] = -INFINITY;
     return;
   }
 
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(C::B_QF + s), 1);
       mbar_init(BAR(C::B_QE + s), 1);
     }
-    for (int c = 0; c < kChains; ++c) {
+    for (int c = 0; c < C::CH; ++c) {
       mbar_init(BAR(C::B_SF + c), 1);
       mbar_init(BAR(C::B_PF + c), 128);
       mbar_init(BAR(C::B_OF + c), 1);
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kWarpMma) {
+  if (warp == C::WARP_MMA) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
@@ -148,9 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  // TMEM: chain c has S at 256 c (P~ packed into its first columns), U at 256 c + 128.
 
-  if (warp == kWarpTma) {
+  if (warp == C::WARP_TMA) {
     // ------------------------------------------------------------ producer
     int issued = 0;
     auto load = [&](int k) {
@@ -185,16 +185,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       sdrain(BAR(C::B_KV), 0, a.budget);
       for (int k = max(0, issued - C::ST); k < issued; ++k) sdrain(BAR(C::B_QF + k % C::ST), (k / C::ST) & 1, a.budget);
     }
-  } else if (warp >= kWarpMma) {
-    // ------------------------------------------------------------ MMA issuer of a chain: tiles c, c + 2, ..
-    const int c = warp - kWarpMma;
+  } else if (warp >= C::WARP_MMA) {
+    // ------------------------------------------------------------ MMA issuer of a chain: tiles c, c + CH, ..
+    const int c = warp - C::WARP_MMA;
     if (lane == 0 && c < n) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, KT, 0), idesc_o = idesc_bf16_f32(kTile, D, 1);
       const uint64_t dq = sdesc_sw128(sQ, 16, 1024), dk = sdesc_sw128(sK, 16, 1024), dv = sdesc_sw128(sV, kBox, 1024);
-      const uint32_t t_s = tmem + 256u * c, t_u = t_s + 128;
+      const uint32_t t_s = tmem + C::COLS * c, t_u = t_s + C::COLS / 2;
       bool ok = swait(BAR(C::B_KV), 0, abort_flag, a.budget) &&
                 (len == a.Nk || swait(BAR(C::B_VC), 0, abort_flag, a.budget));
-      for (int k = c, i = 0; ok && k < n; k += kChains, ++i) {
+      for (int k = c, i = 0; ok && k < n; k += C::CH, ++i) {
         ok = swait(BAR(C::B_QF + k % C::ST), (k / C::ST) & 1, abort_flag, a.budget);
         if (!ok) break;
         tc_fence_after();
@@ -223,12 +223,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ softmax warps of a chain: thread = query row
     const int c = warp >> 2, r = 32 * (warp & 3) + lane;
-    const uint32_t t_s = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 256u * c, t_u = t_s + 128;
+    const uint32_t t_s = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + C::COLS * c, t_u = t_s + C::COLS / 2;
     const uint32_t stage = base + C::OFF_O + static_cast<uint32_t>(c) * C::TB;
     const uint64_t c2 = f2_pack(a.sl2, a.sl2);
     const bool issuer = (warp & 3) == 0 && lane == 0;  // of the chain's TMA stores
     bool ok = true;
-    for (int k = c, i = 0; ok && k < n; k += kChains, ++i) {
+    for (int k = c, i = 0; ok && k < n; k += C::CH, ++i) {
       if (issuer && !a.o_fp32) {  // the staging is free once the last store has read it
         bulk_wait_read_all();
         mbar_arrive(BAR(C::B_OSF + c));
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef BAR
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) {
+  if (warp == C::WARP_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, int KT>
 cudaError_t launch_t(const CrossShortLaunch& l, cudaStream_t stream) {
-  using C = ShortCfg<D>;
+  using C = ShortCfg<D, KT>;
   auto kern = cross_short_kernel<D, KT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
@@ -329,7 +329,7 @@ cudaError_t launch_t(const CrossShortLaunch& l, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(l.BH), static_cast<unsigned>((l.args.R + block_rows - 1) / block_rows));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cfg.attrs = &attr;
