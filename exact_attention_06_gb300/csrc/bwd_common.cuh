@@ -38,12 +38,6 @@ __device__ __forceinline__ void bdrain(uint32_t bar, uint32_t parity, unsigned l
   }
 }
 
-__device__ __forceinline__ void tmem_st1_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n"
-               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-                  "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
-}
-
 // One thread per row: a D-column fp32 tile row in TMEM * scale -> global (fp32), or as bf16 into the
 // staged tile (box0: columns 0..63, box1: 64..127, 128-byte swizzle).
 template <int D>

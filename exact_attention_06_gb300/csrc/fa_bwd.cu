@@ -435,8 +435,8 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           uint32_t pp[16], dp[16];
           if (diag) ew_pairs_dkdv<true>(sv, pv, nv, c2, 32 * c, qt * kTile, key, pp, dp);
           else ew_pairs_dkdv<false>(sv, pv, nv, c2, 32 * c, qt * kTile, key, pp, dp);
-          tmem_st1_x16(tA + 16 * c, pp);  // P^T packed
-          tmem_st1_x16(tB + 16 * c, dp);  // dS^T packed
+          tmem_st_x16(tA + 16 * c, pp);  // P^T packed
+          tmem_st_x16(tB + 16 * c, dp);  // dS^T packed
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(BAR(C::B_PF + c));  // chunk c ready: its gradient MMAs may start
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(BwdWarps<D>::THREADS, 1)
           const int key0 = j * kTile + 32 * c;
           if (key0 + 31 > lim) ew_pairs_dq<true>(sv, pv, c2, nl2, nd2, key0, lim, dp);
           else ew_pairs_dq<false>(sv, pv, c2, nl2, nd2, key0, lim, dp);
-          tmem_st1_x16(tB + 16 * c, dp);
+          tmem_st_x16(tB + 16 * c, dp);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(BAR(C::B_PF + c));  // chunk c ready: its gradient MMAs may start

@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
         uint32_t pp[16], dp[16];
         ew_pairs_dkdv<false>(sv, pv, nv, c2, kHalf * (hh & 1) + 32 * c, 0, 0, pp, dp);
         if (key >= lim) clear_pairs(pp, dp);
-        tmem_st1_x16(tS + 16 * c, pp);
-        tmem_st1_x16(tP + 16 * c, dp);
+        tmem_st_x16(tS + 16 * c, pp);
+        tmem_st_x16(tP + 16 * c, dp);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(BAR(C::B_PF + 2 * g + c));
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
         const int k0 = hh * kHalf + 32 * c;
         if (k0 + 32 > mine) ew_pairs_dq<true, true>(sv, pv, c2, nl2, nd2, k0, mine - 1, dp);
         else ew_pairs_dq<false>(sv, pv, c2, nl2, nd2, k0, mine - 1, dp);
-        tmem_st1_x16(tP + 16 * c, dp);
+        tmem_st_x16(tP + 16 * c, dp);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(BAR(C::B_PF + 2 * g + c));

@@ -339,6 +339,16 @@ void plan_few(CrossPlan* p, const CrossShape& c, int Nk, int d, int sms, bool al
 }
 
 // The short-key kernel's query tiles per block: about 1 us a tile, 4 a block's set-up and end.
+// At most 128 keys take that kernel.  Measured (GB300) against the kernels for any number of keys, us:
+//   heads, rows x keys        d = 64         d = 128
+//   2 x 16, 8192 x 64     29.8 -> 15.7    53.1 -> 27.0
+//   2 x 16, 8192 x 77     29.6 -> 19.1    53.1 -> 30.0
+//   2 x 16, 8192 x 128    26.4 -> 23.7    51.0 -> 31.4
+//   4 x 16, 2048 x 77     18.0 -> 12.6    31.2 -> 18.0
+//   1 x 8, 1000 x 77       5.9 ->  4.3     6.7 ->  5.2
+//   8 x 16/2, 5880 x 4    73.8 -> 35.8   137.7 -> 63.8
+//   8 x 64/16, 4595 x 49   216 ->  101     414 ->  198   (6.1 TB/s)
+// A tile has 64, 96 or 128 keys: at d = 64, 77 keys take 24.1 us where the tile has 128 (8192 rows).
 int plan_short(const CrossShape& c, int sms) {
   const int n = (c.rows + 127) / 128;
   int best = 1;

@@ -155,6 +155,17 @@ def test_many_blocks_of_few_keys(B, Hq, Hkv, Nq, Nk, d):
         _inside(x, want[n], bound[n] * (1 + 2.0 ** -6) + 1e-30, n)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nk,lens", [(64, None), (65, [65, 64]), (96, None), (97, [97, 96]), (128, [128, 33]),
+                                     (77, [0, 77])])
+def test_blocks_that_stream_many_query_tiles(Nk, lens, d):
+    """The edges of the key tiles (64, 96, 128), with more query tiles in a block than its ring holds."""
+    q, k, v, _, kl = _inputs(2, 8, 4, 9000, Nk, d, lens)
+    for o_fp32 in (False, True):
+        o, lse = _fwd(q, k, v, kl, d ** -0.5, o_fp32)
+        _check_fwd(o, lse, q, k, v, d ** -0.5, lens, f"fp32={o_fp32}")
+
+
 def test_a_peaked_softmax():
     """Keys x8 (scores far apart): the running maximum moves, most probabilities vanish."""
     B, H, Nq, Nk, d, lens = 1, 2, 200, 700, 128, [650]
