@@ -64,8 +64,8 @@ def _peaks():
 
 # DRAM bytes per launch (dram__bytes_read.sum + dram__bytes_write.sum) from ncu captures summarised
 # under profiles/, keyed by kernel and workload, valid only while the kernel sources are unchanged.
-_FWD = "a42d8c474ca6f4e08da13b623285a7aa8937d96c7bbbac76fa3477ba121c3074"
-_BWD = "cfd5e6d8f269fb875eb6196f0e05848be8dc3643e808bbe8f4907ae37fbe8129"
+_FWD = "def71c075ea239ac85c9d1b1efa3c201806bcb551a1d8758fee3fb49b281d6db"
+_BWD = "d9e547d73ab8a499068ac81cbc23865af85b744a32d660c9953b67ef10a8ba27"
 _DEC = "238a9c1b2ffecb15b22cb24a1544220a197fcbdb2c867899597a0c8e4fa65d64"
 NCU_TRAFFIC = {
     ("fwd_kernel", "ragged"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 558.459e6},

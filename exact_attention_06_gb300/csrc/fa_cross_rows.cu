@@ -1,5 +1,5 @@
-// Cross attention of few query rows (fa_cross_fwd with at most 32 rows per key head: a decode step and its
-// shared heads), for sm_103a.
+// Cross attention of few query rows (fa_cross_fwd with at most 32 rows per key head, or 16 over at most 128
+// keys: a decode step and its shared heads), for sm_103a.
 //
 // Such a call reads each key head's K and V once for 4 * rows * d flops a key: it is bound by HBM, and
 // what counts is bytes in flight and a short path from the last byte to the output.  A 128-row

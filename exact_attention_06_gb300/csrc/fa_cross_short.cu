@@ -1,4 +1,4 @@
-// Cross attention forward over at most 128 keys (fa_cross_fwd with more than 32 rows per key head), for sm_103a: a text
+// Cross attention forward over at most 128 keys (fa_cross_fwd with more than 16 rows per key head), for sm_103a: a text
 // prompt of 77 tokens or 64 latents under thousands of queries.
 //
 // There is one tile of keys, so a block loads K and V once and streams query tiles past them: per tile

@@ -372,9 +372,13 @@ CrossPlan plan_cross(const CrossShape& c, int Nk, int d, int sms, bool workspace
   // At most 32 rows a key head take the few-row kernel.  Measured against the 128-row tiles (d = 128, 1 / 16 / 17 / 32
   // rows): 64 key heads x 8192 keys 41 / 43 / 46 / 48 us against 51 / 53 / 53 / 54; 512 x 1500 keys 60 / 64 / 82 / 88
   // against 83 / 87 / 87 / 88; 64 x 577 keys 5.9 / 7.5 / 8.2 / 9.6 against 10.8.
-  if (c.rows <= fattn::kCrossRowsMax)
+  // Against the short-key kernel (d = 128, 77 keys, 1 / 8 / 17 / 32 rows): 16 key heads 4.6 / 4.8 / 6.1 / 7.3 against
+  // 4.5 / 4.8 / 4.8 / 4.7; 512 key heads 9.6 / 11.4 / 22.6 / 28.7 against 15.7 / 15.9 / 16.2 / 16.8.  At d = 64, 512
+  // key heads: 6.1 / 6.5 / 11.3 / 13.5 against 13.7 / 13.5 / 13.4 / 13.6.  So at most 128 keys: 16 rows, one row block.
+  const bool short_keys = Nk <= fattn::kCrossShortKeys;
+  if (c.rows <= (short_keys ? fattn::kCrossRowsMax / 2 : fattn::kCrossRowsMax))
     plan_few(&p, c, Nk, d, sms, can_join);
-  else if (Nk <= fattn::kCrossShortKeys)
+  else if (short_keys)
     p.tiles = plan_short(c, sms);
   else if (can_join)
     p.splits = cut_scan(c.bh * ((c.rows + 255) / 256), tiles, sms, static_cast<double>(rows) * (d + 2) * 4);
