@@ -22,8 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfattn.so")
 CALLS = os.path.join(PKG, "_calls.so")
-SOURCES = ["fa_fwd.cu", "fa_bwd.cu", "fa_cross_bwd.cu", "fa_cross_rows.cu", "fa_cross_short.cu", "fa_decode.cu",
-           "fa_quant.cu", "fa_rope.cu", "fattn_host.cu"]
+SOURCES = ["fa_fwd.cu", "fa_bwd.cu", "fa_cross_bwd.cu", "fa_cross_bwd_short.cu", "fa_cross_rows.cu", "fa_cross_short.cu",
+           "fa_decode.cu", "fa_quant.cu", "fa_rope.cu", "fattn_host.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 

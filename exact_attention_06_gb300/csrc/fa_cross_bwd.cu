@@ -1,5 +1,6 @@
-// Cross attention backward for sm_103a: dK, dV (one CTA per key tile and range of query tiles) and dQ (one per
-// query tile and range of key tiles), by the formulas of fa_bwd.cu, P recomputed from the forward's lse.
+// Cross attention backward over more than 128 keys for sm_103a: dK, dV (one CTA per key tile and range of query
+// tiles) and dQ (one per query tile and range of key tiles), by the formulas of fa_bwd.cu, P recomputed from the
+// forward's lse.
 //
 // A step -- products, their way through TMEM, exponentials, P and dS back, gradients -- is a chain several times
 // as long as its work on the tensor core, so these kernels keep several in flight.  The scanned side is taken
@@ -58,7 +59,6 @@ struct CrossArgs {
   const int* kv_lens;
   int kv_heads, n_keys, tiles;
   long long part_stride;
-  float* delta_out;  // dQ kernel, at most one key tile: D is computed here and written for the dK/dV kernel; else null
   __device__ __forceinline__ int keys(int bh) const {
     return kv_lens ? min(max(kv_lens[bh / kv_heads], 0), n_keys) : n_keys;
   }
@@ -83,22 +83,6 @@ __device__ __forceinline__ void clear_pairs(uint32_t (&pp)[16], uint32_t (&dp)[1
 // grid before is complete.
 __device__ __forceinline__ void wait_as_last_block() {
   if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) grid_dep_wait();
-}
-
-// Sum of P dP over 32 keys of a query row (those past `lim` count for nothing, whatever they hold).
-template <bool MASK>
-__device__ __forceinline__ float dot_pairs(const uint32_t (&sv)[32], const uint32_t (&pv)[32], uint64_t c2, uint64_t nl2,
-                                           int key0, int lim) {
-  float acc0 = 0.f, acc1 = 0.f;
-#pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    float x0, x1;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nl2), x0, x1);
-    const float y0 = ex2(x0) * __uint_as_float(pv[e]), y1 = ex2(x1) * __uint_as_float(pv[e + 1]);
-    if (!MASK || key0 + e <= lim) acc0 += y0;
-    if (!MASK || key0 + e + 1 <= lim) acc1 += y1;
-  }
-  return acc0 + acc1;
 }
 
 // Products of a 128-row tile A with rows 64 q .. of a streamed tile: 128 x 64, K = d.
@@ -340,7 +324,6 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
                       float sl2, float scale, int grad_fp32, unsigned long long budget,
                       const __grid_constant__ CUtensorMap tdq, int ng, const CrossArgs x) {
   using C = CrossCfg<D, D>;
-  grid_dep_launch();  // (the dK/dV kernel behind this one, when there is one key tile)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -483,31 +466,7 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
     const bool in = row < N;
     const float lse2 = in ? lse[static_cast<size_t>(bh) * N + row] * kLog2e : INFINITY;
     const uint64_t c2 = f2_pack(sl2, sl2), nl2 = f2_pack(-lse2, -lse2);
-    float dd = 0.f;
-    if (!x.delta_out) {
-      if (in) dd = delta[static_cast<size_t>(bh) * N + row];
-    } else if (g < n_h) {
-      // One key tile: the row's D = sum of P dP is at hand (half g in this thread), and more exact than
-      // rowsum(O dO) with O rounded to bf16, whose error a softmax over few keys does not average out.
-      float part = 0.f;
-      if (bwait_all(BAR(C::B_SF + g), 0, abort_flag, budget)) {
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t sv[32], pv[32];
-          tmem_ld_x32(tS + 32 * c, sv);
-          tmem_ld_x32(tP + 32 * c, pv);
-          const int k0 = g * kHalf + 32 * c;
-          if (k0 + 32 > mine) part += dot_pairs<true>(sv, pv, c2, nl2, k0, mine - 1);
-          else part += dot_pairs<false>(sv, pv, c2, nl2, k0, mine - 1);
-        }
-      }
-      float* parts = reinterpret_cast<float*>(gbase + C::OFF_VEC);
-      parts[g * kTile + r] = part;
-      named_bar_sync(1, 128 * n_h);  // (reached after a timeout, too)
-      dd = parts[r] + (n_h > 1 ? parts[kTile + r] : 0.f);
-      if (g == 0 && in) x.delta_out[static_cast<size_t>(bh) * N + row] = dd;
-    }
+    const float dd = in ? delta[static_cast<size_t>(bh) * N + row] : 0.f;
     const uint64_t nd2 = f2_pack(-dd, -dd);
     bool ok = true;
     for (int hh = g; ok && hh < n_h; hh += C::FLIGHT) {
@@ -581,12 +540,6 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(const float* __restrict_
         make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
 }
 
-cudaError_t launch_sum(const float* part, void* out, void* out2, long long n, int S, int fp32, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((n / 4 + 255) / 256), out2 ? 2 : 1);
-  cross_sum_kernel<<<grid, 256, 0, stream>>>(part, out, out2, n, S, fp32);
-  return cudaGetLastError();
-}
-
 template <int D>
 cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   using KV = CrossCfg<D, 2 * D>;
@@ -606,42 +559,44 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cfg.stream = stream;
   cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   auto dkdv = [&]() -> cudaError_t {
     cfg.gridDim = dim3(static_cast<unsigned>(a.BH), static_cast<unsigned>(k_tiles), static_cast<unsigned>(a.kv_splits));
     cfg.blockDim = dim3(KV::THREADS);
     cfg.dynamicSmemBytes = KV::SMEM;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(
         &cfg, k1, a.tq, a.tk, a.tv, a.tdo, a.lse, static_cast<const float*>(a.delta),
         kv_part ? static_cast<void*>(a.kv_part) : a.dk, kv_part ? static_cast<void*>(dv_part) : a.dv, a.N, a.scale_log2,
         a.scale, static_cast<int>(kv_part || a.grad_fp32), a.budget, a.tdk, a.tdv,
         head_groups(a.BH, k_tiles, false, a.sms),
-        CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.q_tiles, kv_part ? kv_elems : 0, nullptr});
+        CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.q_tiles, kv_part ? kv_elems : 0});
   };
-  auto dq = [&](bool behind_dkdv) -> cudaError_t {
+  auto dq = [&]() -> cudaError_t {
     cfg.gridDim = dim3(static_cast<unsigned>(a.BH), static_cast<unsigned>(q_tiles), static_cast<unsigned>(a.q_splits));
     cfg.blockDim = dim3(Q::THREADS);
     cfg.dynamicSmemBytes = Q::SMEM;
-    cfg.numAttrs = behind_dkdv ? 1 : 0;
     return cudaLaunchKernelEx(
         &cfg, k2, a.tq, a.tk, a.tv, a.tdo, a.lse, static_cast<const float*>(a.delta),
         q_part ? static_cast<void*>(a.q_part) : a.dq, a.N, a.scale_log2, a.scale,
         static_cast<int>(q_part || a.grad_fp32), a.budget, a.tdq, head_groups(a.BH, q_tiles, false, a.sms),
-        CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.k_tiles, q_part ? q_elems : 0, behind_dkdv ? nullptr : a.delta});
+        CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.k_tiles, q_part ? q_elems : 0});
   };
-  if (k_tiles == 1) {  // dQ first: it finds D, which takes no kernel then and does not go through O
-    if ((e = dq(false)) != cudaSuccess || (e = dkdv()) != cudaSuccess) return e;
-  } else {
-    e = launch_delta(a.o, a.dout, a.delta, static_cast<long long>(a.BH) * a.N, D, stream);
-    if (e != cudaSuccess || (e = dkdv()) != cudaSuccess || (e = dq(true)) != cudaSuccess) return e;
-  }
-  if (kv_part && (e = launch_sum(a.kv_part, a.dk, a.dv, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess)
+  e = launch_delta(a.o, a.dout, a.delta, static_cast<long long>(a.BH) * a.N, D, stream);
+  if (e != cudaSuccess || (e = dkdv()) != cudaSuccess || (e = dq()) != cudaSuccess) return e;
+  if (kv_part && (e = launch_cross_sum(a.kv_part, a.dk, a.dv, kv_elems, a.kv_splits, a.grad_fp32, stream)) != cudaSuccess)
     return e;
-  if (q_part) return launch_sum(a.q_part, a.dq, nullptr, q_elems, a.q_splits, a.grad_fp32, stream);
+  if (q_part) return launch_cross_sum(a.q_part, a.dq, nullptr, q_elems, a.q_splits, a.grad_fp32, stream);
   return cudaSuccess;
 }
 
 }  // namespace
+
+cudaError_t launch_cross_sum(const float* part, void* out, void* out2, long long n, int S, int fp32,
+                             cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((n / 4 + 255) / 256), out2 ? 2 : 1);
+  cross_sum_kernel<<<grid, 256, 0, stream>>>(part, out, out2, n, S, fp32);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_cross_bwd(const BwdLaunch& a, cudaStream_t stream) {
   return a.d == 64 ? launch_t<64>(a, stream) : launch_t<128>(a, stream);

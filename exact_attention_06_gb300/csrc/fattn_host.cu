@@ -393,19 +393,25 @@ struct CrossBwdPlan {
   int kv_splits = 1, q_tiles = 0;  // dK, dV: ranges of query tiles
   int q_splits = 1, k_tiles = 0;   // dQ: ranges of key tiles
   size_t delta_bytes = 0, kv_bytes = 0, q_bytes = 0;
-  size_t total() const { return delta_bytes + kv_bytes + q_bytes; }
+  size_t total() const { return std::max<size_t>(delta_bytes + kv_bytes + q_bytes, 256); }  // never none
 };
 
 CrossBwdPlan plan_cross_bwd(const CrossShape& c, int Nk, int d, int sms) {
   CrossBwdPlan p;
   const int qt = (c.rows + 127) / 128, kt = (Nk + 127) / 128;
   const double kv = 2.0 * c.bh * Nk * d * sizeof(float), q = 1.0 * c.bh * c.rows * d * sizeof(float);
+  if (Nk <= fattn::kCrossShortKeys) {  // one kernel
+    p.kv_splits = cut_scan(c.bh, qt, sms, kv);
+    p.q_tiles = (qt + p.kv_splits - 1) / p.kv_splits;
+    if (p.kv_splits > 1) p.kv_bytes = round256(static_cast<size_t>(kv) * p.kv_splits);
+    return p;
+  }
   // The dQ kernel fills the dK/dV kernel's last round; a step of it costs about 0.75 of the latter's.  Measured
   // (GB300, ranges of queries per key tile 1 / 2 / 3 / 4, both kernels and the join): B4 H16/4 2048 x 1500 at
   // d = 64: 193 / 204 / 215 / 222 us; B2 H16/4 1000 x 577: 40 / 33 / 36 / 35 us; B1 H8/2 4096 x 300, 1 / 8 / 16 / 32:
   // 134 / 28 / 26 / 32 us.
   p.q_splits = cut_scan(c.bh * qt, kt, sms, q);
-  p.kv_splits = cut_scan(c.bh * kt, qt, sms, kv, kt > 1 ? 0.75 * c.bh * qt * (kt + 3) : 0.0);  // (kt = 1: dQ runs first)
+  p.kv_splits = cut_scan(c.bh * kt, qt, sms, kv, 0.75 * c.bh * qt * (kt + 3));
   p.q_tiles = (qt + p.kv_splits - 1) / p.kv_splits;
   p.k_tiles = (kt + p.q_splits - 1) / p.q_splits;
   p.delta_bytes = round256(static_cast<size_t>(c.bh) * c.rows * sizeof(float));
@@ -1097,8 +1103,9 @@ fa_status_t fa_cross_bwd(const void* q, const void* k, const void* v, const int*
   fattn::BwdLaunch a{};
   a.sms = sms;
   if ((st = make_map(&a.tq, q, d, c.rows, c.bh, 128)) != FA_OK) return st;
-  if ((st = make_map(&a.tk, k, d, Nk, c.bh, 128)) != FA_OK) return st;
-  if ((st = make_map(&a.tv, v, d, Nk, c.bh, 128)) != FA_OK) return st;
+  const int key_box = Nk <= 64 ? 64 : 128;
+  if ((st = make_map(&a.tk, k, d, Nk, c.bh, key_box)) != FA_OK) return st;
+  if ((st = make_map(&a.tv, v, d, Nk, c.bh, key_box)) != FA_OK) return st;
   if ((st = make_map(&a.tdo, dout, d, c.rows, c.bh, 128)) != FA_OK) return st;
   if (!grad_fp32) {
     if ((st = make_map(&a.tdq, dq, d, c.rows, c.bh, 128)) != FA_OK) return st;
@@ -1130,7 +1137,8 @@ fa_status_t fa_cross_bwd(const void* q, const void* k, const void* v, const int*
   a.k_tiles = plan.k_tiles;
   a.q_splits = plan.q_splits;
   cudaGetLastError();
-  cudaError_t e = fattn::launch_cross_bwd(a, static_cast<cudaStream_t>(stream));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = Nk <= fattn::kCrossShortKeys ? fattn::launch_cross_bwd_short(a, s) : fattn::launch_cross_bwd(a, s);
   if (e != cudaSuccess) return cuda_fail(e, "fa_cross_bwd launch");
   return FA_OK;
 }
@@ -1246,7 +1254,8 @@ fa_status_t fa_get_status(void* stream) {
   if (e != cudaSuccess) return cuda_fail(e, "fa_get_status synchronize");
   const unsigned int bits = fattn::fwd_read_and_clear_status() | fattn::decode_read_and_clear_status() |
                             fattn::bwd_read_and_clear_status() | fattn::cross_bwd_read_and_clear_status() |
-                            fattn::cross_rows_read_and_clear_status() | fattn::cross_short_read_and_clear_status();
+                            fattn::cross_rows_read_and_clear_status() | fattn::cross_short_read_and_clear_status() |
+                            fattn::cross_bwd_short_read_and_clear_status();
   if (bits & fattn::kStatusTimeout) return fail(FA_ERR_TIMEOUT, "a kernel wait exceeded its budget");
   return FA_OK;
 }

@@ -166,6 +166,26 @@ def test_blocks_that_stream_many_query_tiles(Nk, lens, d):
         _check_fwd(o, lse, q, k, v, d ** -0.5, lens, f"fp32={o_fp32}")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nk,lens", [(1, None), (64, [64, 0]), (65, [65, 64]), (96, None), (97, [97, 96]), (128, [128, 33]),
+                                     (77, [0, 77]), (31, [32, 5])])
+def test_gradients_of_many_query_tiles_over_few_keys(Nk, lens, d):
+    B, Hq, Hkv, Nq = 2, 8, 4, 7001  # some twenty tiles a block, then ranges of them
+    q, k, v, do, kl = _inputs(B, Hq, Hkv, Nq, Nk, d, lens)
+    scale = d ** -0.5
+    o, lse = _fwd(q, k, v, kl, scale)
+    ref, _, otol, _, eps = _bounds(q, k, v, scale, lens)
+    want, bound = oc.cross_backward(q, k, v, do, scale, lens, rel=U + 4 * eps + 2.0 ** -10,
+                                    o_err=otol + U * (np.abs(ref) + otol))
+    for t in (torch.float32, torch.bfloat16):
+        got = {n: torch.full(x.shape, float("nan"), dtype=t, device=DEV) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+        fattn.fa_cross_bwd(q, k, v, o, do, lse, *got.values(), scale, kv_lens=kl)
+        assert fattn.fa_get_status() == fattn.FA_OK
+        for n, g in got.items():
+            tol = bound[n] * (1 + 2.0 ** -6) + 1e-30
+            _inside(g, want[n], tol + (U * (np.abs(want[n]) + tol) if t == torch.bfloat16 else 0), f"{n} {t}")
+
+
 def test_a_peaked_softmax():
     """Keys x8 (scores far apart): the running maximum moves, most probabilities vanish."""
     B, H, Nq, Nk, d, lens = 1, 2, 200, 700, 128, [650]
