@@ -520,6 +520,7 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
 __global__ void __launch_bounds__(256) cross_sum_kernel(const float* __restrict__ part, void* __restrict__ out,
                                                         void* __restrict__ out2, long long n, int S, int fp32) {
   const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  grid_dep_wait();  // launched programmatically after the kernel that leaves the partial sums
   if (i >= n) return;
   if (blockIdx.y) {
     part += S * n;
@@ -593,9 +594,16 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
 
 cudaError_t launch_cross_sum(const float* part, void* out, void* out2, long long n, int S, int fp32,
                              cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((n / 4 + 255) / 256), out2 ? 2 : 1);
-  cross_sum_kernel<<<grid, 256, 0, stream>>>(part, out, out2, n, S, fp32);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((n / 4 + 255) / 256), out2 ? 2 : 1);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cross_sum_kernel, part, out, out2, n, S, fp32);
 }
 
 cudaError_t launch_cross_bwd(const BwdLaunch& a, cudaStream_t stream) {

@@ -9,7 +9,7 @@
 // A row's keys are all there, so D takes no pass over O (and no rounding of O).  Bound by HBM: Q and dO in, dQ out,
 // 6 d + 4 bytes a row.  The chain of a tile (about 3 us) is hidden by two tiles in flight, a thread per row, where TMEM
 // holds them; else a row has two threads, one for each 64 keys, which exchange their halves of D.
-// One thread issues S and dP of all tiles, another the products with P and dS, whose sums want one order.
+// One thread issues S and dP, another the products with P and dS, whose sums want one order, a third dQ's stores.
 // Several blocks of a key head leave fp32 partial sums, which cross_sum_kernel adds in their order.  Measured beside
 // plan_cross_bwd.
 //
@@ -25,46 +25,61 @@ template <int D, int KT>
 struct BwdShortCfg {
   static constexpr int CH = KT == 64 || (D == 64 && KT == 96) ? 2 : 1;  // tiles in flight (chains)
   static constexpr int W = 2 / CH;                                      // threads per row
+  // One chain: dQ is written over dP alone, the next tile's S is computed and its exponentials are taken while this one's
+  // gradients are computed, and a stage's Q and dO come and go apart.
+  static constexpr bool EARLY = CH == 1;
   static constexpr int NH = D / 64;
   static constexpr uint32_t KBOX = (KT == 64 ? 64u : 128u) * 128u;  // bytes of a box of K or V
   static constexpr uint32_t TK = NH * KBOX, TQ = NH * kBox;
+  // dQ on its way out: in a place of its own, or that of the tile's dO, or in the chain's buffer, as shared memory allows.
+  enum Out { kOwn, kInDO, kInBuf };
+  static constexpr Out OUT = CH == 2 ? kInBuf : D == 64 ? kOwn : kInDO;
   static constexpr int ST = D == 64 ? 4 : 2;  // stages of dO and Q
   static constexpr uint32_t STAGE = 2 * TQ;
-  // A chain's buffer: P, then dS over it when dV's product has read P (at 64 keys beside it); at last dQ on its way out.
+  // A chain's buffer: P, then dS over it when dV's product has read P (at 64 keys beside it).
   static constexpr uint32_t BUF = 2 * kBox, OFF_DS = KT == 64 ? kBox : 0;
-  static constexpr uint32_t OFF_K = 0, OFF_V = TK, OFF_Q = 2 * TK, OFF_P = OFF_Q + ST * STAGE, OFF_BAR = OFF_P + CH * BUF;
+  static constexpr uint32_t OFF_K = 0, OFF_V = TK, OFF_Q = 2 * TK, OFF_P = OFF_Q + ST * STAGE, OFF_O = OFF_P + CH * BUF,
+                            OFF_BAR = OFF_O + (OUT == kOwn ? CH * TQ : 0);
   // TMEM: dV, dK, then per chain S and dP, over which dQ is written.
-  static constexpr uint32_t COL_DK = D, COL_C = 2 * D, COLS = 2 * KT;
-  static constexpr int WARP_S = 4 * CH * W, WARP_TMA = WARP_S + 2, THREADS = (WARP_TMA + 1) * 32;
-  static constexpr int B_KV = 0, B_KC = 1, B_ACC = 2, B_DRAIN = 3, B_QF = 5, B_QE = B_QF + ST, B_SF = B_QE + ST,
-                       B_PF = B_SF + CH, B_DV = B_PF + CH, B_DS = B_DV + CH, B_GF = B_DS + CH, B_QR = B_GF + CH,
+  static constexpr uint32_t COL_DK = D, COL_C = 2 * D, COL_DP = KT, COL_DQ = EARLY ? KT : 0;
+  static constexpr uint32_t COLS = EARLY && D > KT ? KT + D : 2 * KT;
+  static __device__ __forceinline__ uint32_t dq_place(uint32_t base, int c, int s) {
+    return base + (OUT == kOwn ? OFF_O + c * TQ : OUT == kInDO ? OFF_Q + s * STAGE : OFF_P + c * BUF);
+  }
+  static constexpr int WARP_S = 4 * CH * W, WARP_O = WARP_S + 2, WARP_TMA = WARP_S + (OUT == kInBuf ? 2 : 3), THREADS = (WARP_TMA + 1) * 32;
+  static constexpr int B_KV = 0, B_KC = 1, B_ACC = 2, B_DRAIN = 3, B_QF = 5, B_QE = B_QF + ST, B_DF = B_QE + ST,
+                       B_DE = B_DF + ST, B_SF = B_DE + ST,
+                       B_SR = B_SF + CH, B_SP = B_SR + CH, B_PF = B_SP + CH, B_DV = B_PF + CH, B_DS = B_DV + CH, B_GF = B_DS + CH, B_QR = B_GF + CH,
                        B_OW = B_QR + CH, B_OSF = B_OW + CH, B_DX = B_OSF + CH, NBAR = B_DX + 1;
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR, OFF_D = OFF_MISC + 16u;  // D's halves (two threads a row)
   static constexpr uint32_t SMEM = OFF_D + (W == 2 ? 2u * kTile * 4u : 0u) + 1024u;
   static_assert(SMEM <= 232448, "shared memory");
-  static_assert(COL_C + CH * COLS <= kTmemCols && D <= static_cast<int>(COLS) && TQ <= BUF, "TMEM, dQ's places");
+  static_assert(COL_C + CH * COLS <= kTmemCols && COL_DQ + D <= COLS && TQ <= BUF, "TMEM, dQ's places");
 };
 
-// 32 keys of this thread's row: p = 2^(s c - lse2), packed into pp; returns the sum of p dp.  MASK: keys from `valid`
-// on count nothing, whatever is there.
+// p = 2^(s c - lse2) of 32 keys of this thread's row.  MASK here and below: keys from `valid` on count nothing,
+// whatever is there.
 template <bool MASK>
-__device__ __forceinline__ float p_step(const uint32_t (&s)[32], const uint32_t (&dp)[32], uint64_t c2, uint64_t nl2,
-                                        int valid, float* p, uint32_t (&pp)[16]) {
+__device__ __forceinline__ void p_step(const uint32_t (&s)[32], uint64_t c2, uint64_t nl2, int valid, float* p) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, nl2), x0, x1);
+    p[e] = MASK && e >= valid ? 0.f : ex2(x0);
+    p[e + 1] = MASK && e + 1 >= valid ? 0.f : ex2(x1);
+  }
+}
+
+// Sum of p dp over them.
+template <bool MASK>
+__device__ __forceinline__ float dot_step(const float* p, const uint32_t (&dp)[32], int valid) {
   uint64_t a = f2_pack(0.f, 0.f), b = a;
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
-    float x0, x1, d0 = __uint_as_float(dp[e]), d1 = __uint_as_float(dp[e + 1]);
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, nl2), x0, x1);
-    float p0 = ex2(x0), p1 = ex2(x1);
-    if (MASK) {
-      if (e >= valid) p0 = d0 = 0.f;
-      if (e + 1 >= valid) p1 = d1 = 0.f;
-    }
-    if (e & 2) b = f2_fma(f2_pack(p0, p1), f2_pack(d0, d1), b);
-    else a = f2_fma(f2_pack(p0, p1), f2_pack(d0, d1), a);
-    p[e] = p0;
-    p[e + 1] = p1;
-    pp[e / 2] = pack_bf16(p0, p1);
+    const float d0 = MASK && e >= valid ? 0.f : __uint_as_float(dp[e]);
+    const float d1 = MASK && e + 1 >= valid ? 0.f : __uint_as_float(dp[e + 1]);
+    if (e & 2) b = f2_fma(f2_pack(p[e], p[e + 1]), f2_pack(d0, d1), b);
+    else a = f2_fma(f2_pack(p[e], p[e + 1]), f2_pack(d0, d1), a);
   }
   float s0, s1;
   f2_unpack(f2_add(a, b), s0, s1);
@@ -97,7 +112,7 @@ __device__ __forceinline__ void put_cols(uint32_t buf, int r, int c, const uint3
            v[4 * i + 2], v[4 * i + 3]);
 }
 
-// Columns [32 c0, 32 c1) of this thread's row of dQ out of TMEM: to global memory (fp32) or as bf16 into the buffer.
+// Columns [32 c0, 32 c1) of this thread's row of dQ out of TMEM: to global memory (fp32) or as bf16 into shared memory.
 template <int D>
 __device__ __forceinline__ void put_dq(void* out, size_t frow, bool valid, uint32_t buf, int r, uint32_t taddr, float scale,
                                        int c0, int c1, int fp32) {
@@ -207,16 +222,20 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(BAR(C::B_QF + s), 1);
       mbar_init(BAR(C::B_QE + s), 1);
+      mbar_init(BAR(C::B_DF + s), 1);
+      mbar_init(BAR(C::B_DE + s), 1);
     }
     for (int c = 0; c < C::CH; ++c) {
-      mbar_init(BAR(C::B_SF + c), 1);     // S, dP computed
+      mbar_init(BAR(C::B_SF + c), 1);     // S computed
+      mbar_init(BAR(C::B_SR + c), 128 * C::W);  // S read
+      mbar_init(BAR(C::B_SP + c), 1);     // dP computed
       mbar_init(BAR(C::B_PF + c), 128 * C::W);   // P in shared memory (more than 64 keys)
       mbar_init(BAR(C::B_DV + c), 1);     // P read (more than 64 keys)
       mbar_init(BAR(C::B_DS + c), 128 * C::W);   // dS in shared memory
       mbar_init(BAR(C::B_GF + c), 1);     // dQ computed, buffer read
       mbar_init(BAR(C::B_QR + c), 128 * C::W);   // dQ out of TMEM
-      mbar_init(BAR(C::B_OW + c), 128 * C::W);   // dQ in the buffer
-      mbar_init(BAR(C::B_OSF + c), 1);    // the buffer's dQ stored
+      mbar_init(BAR(C::B_OW + c), 128 * C::W);   // dQ in shared memory
+      mbar_init(BAR(C::B_OSF + c), 1);    // dQ's place free again
     }
     mbar_init(BAR(C::B_DX), 256);  // both halves of D written
     *abort_flag = 0;
@@ -234,15 +253,18 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
 
   if (warp == C::WARP_TMA) {
     // ------------------------------------------------------------ producer
-    int issued = 0;
-    auto load = [&](int k) {  // dO, then Q
-      const int s = k % C::ST;
-      const uint32_t st = sQ + s * C::STAGE;
-      mbar_arrive_expect_tx(BAR(C::B_QF + s), C::STAGE);
-      for (int h = 0; h < C::NH; ++h) {
-        tma_load_3d(st + h * kBox, &tdo, BAR(C::B_QF + s), h * 64, row0 + k * kTile, bh);
-        tma_load_3d(st + C::TQ + h * kBox, &tq, BAR(C::B_QF + s), h * 64, row0 + k * kTile, bh);
-      }
+    int issued = 0, q_only = 0;  // tiles asked for; 1: and one more without its dO (after a timeout)
+    auto load_q = [&](int k) {
+      const uint32_t full = BAR(C::B_QF + k % C::ST);
+      mbar_arrive_expect_tx(full, C::EARLY ? C::TQ : C::STAGE);
+      for (int h = 0; h < C::NH; ++h)
+        tma_load_3d(sQ + (k % C::ST) * C::STAGE + C::TQ + h * kBox, &tq, full, h * 64, row0 + k * kTile, bh);
+    };
+    auto load_do = [&](int k) {
+      const uint32_t full = BAR((C::EARLY ? C::B_DF : C::B_QF) + k % C::ST);
+      if (C::EARLY) mbar_arrive_expect_tx(full, C::TQ);
+      for (int h = 0; h < C::NH; ++h)
+        tma_load_3d(sQ + (k % C::ST) * C::STAGE + h * kBox, &tdo, full, h * 64, row0 + k * kTile, bh);
     };
     if (lane == 0) {
       mbar_arrive_expect_tx(BAR(C::B_KV), 2 * C::TK);
@@ -250,7 +272,10 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
         tma_load_3d(sK + h * C::KBOX, &tk, BAR(C::B_KV), h * 64, 0, bh);
         tma_load_3d(sV + h * C::KBOX, &tv, BAR(C::B_KV), h * 64, 0, bh);
       }
-      for (; issued < min(C::ST, n); ++issued) load(issued);
+      for (; issued < min(C::ST, n); ++issued) {
+        load_q(issued);
+        load_do(issued);
+      }
     }
     if (len < a.Nk) {  // K's rows behind the sequence
       __syncwarp();
@@ -263,12 +288,35 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
     }
     if (lane == 0) {
       for (; issued < n; ++issued) {
-        if (!bwait(BAR(C::B_QE + issued % C::ST), ((issued / C::ST) - 1) & 1, abort_flag, a.budget)) break;
-        load(issued);
+        const int s = issued % C::ST, last = ((issued / C::ST) - 1) & 1;
+        if (!bwait(BAR(C::B_QE + s), last, abort_flag, a.budget)) break;
+        load_q(issued);
+        if (C::EARLY && !bwait(BAR(C::B_DE + s), last, abort_flag, a.budget)) {
+          q_only = 1;
+          break;
+        }
+        load_do(issued);
       }
       // every copy lands before the shared memory is released
       bdrain(BAR(C::B_KV), 0, a.budget);
-      for (int k = max(0, issued - C::ST); k < issued; ++k) bdrain(BAR(C::B_QF + k % C::ST), (k / C::ST) & 1, a.budget);
+      const int q_end = issued + q_only;
+      for (int k = max(0, q_end - C::ST); k < q_end; ++k) bdrain(BAR(C::B_QF + k % C::ST), (k / C::ST) & 1, a.budget);
+      for (int k = max(0, issued - C::ST); C::EARLY && k < issued; ++k)
+        bdrain(BAR(C::B_DF + k % C::ST), (k / C::ST) & 1, a.budget);
+    }
+  } else if (C::OUT != C::kInBuf && warp == C::WARP_O) {
+    // ------------------------------------------------------------ dQ's stores (bf16; one chain)
+    if (lane == 0 && !a.q_fp32) {
+      for (int k = 0; k < n; ++k) {
+        const int s = k % C::ST;
+        if (!bwait(BAR(C::B_OW), k & 1, abort_flag, a.budget)) break;
+        for (int h = 0; h < C::NH; ++h)
+          tma_store_3d(&tdq, C::dq_place(base, 0, s) + h * kBox, h * 64, row0 + k * kTile, bh);
+        bulk_commit();
+        bulk_wait_read_all();
+        mbar_arrive(BAR(C::OUT == C::kInDO ? C::B_DE + s : C::B_OSF));
+      }
+      bulk_wait_all();  // complete before the CTA exits
     }
   } else if (warp >= C::WARP_S) {
     // ------------------------------------------------------------ MMA issuers
@@ -278,30 +326,35 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
       bool ok = bwait(BAR(C::B_KV), 0, abort_flag, a.budget) &&
                 (len == a.Nk || bwait(BAR(C::B_KC), 0, abort_flag, a.budget));
       if (warp == C::WARP_S) {  // S = Q K^T, dP = dO V^T
-        constexpr uint32_t idesc = idesc_bf16_f32(kTile, KT, 0);
+        auto product = [&](uint32_t t, uint64_t x, uint64_t y) {
+          constexpr uint32_t idesc = idesc_bf16_f32(kTile, KT, 0);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t ox = static_cast<uint32_t>(kk >> 2) * kBox + static_cast<uint32_t>(kk & 3) * 32u;
+            const uint32_t oy = static_cast<uint32_t>(kk >> 2) * C::KBOX + static_cast<uint32_t>(kk & 3) * 32u;
+            if (kk == 0) mma_ss_c<0>(t, sdesc_add(x, ox), sdesc_add(y, oy), idesc);
+            else mma_ss_c<1>(t, sdesc_add(x, ox), sdesc_add(y, oy), idesc);
+          }
+        };
         for (int k = 0; ok && k < n; ++k) {
-          const int c = k % C::CH, s = k % C::ST;
+          const int c = k % C::CH, s = k % C::ST, last = ((k / C::CH) - 1) & 1;
+          const uint32_t t = tmem + C::COL_C + C::COLS * c;
+          const uint64_t d_do = sdesc_add(dst_row, s * C::STAGE);
+          // the columns are free when the chain's last S is read, and its dQ
           ok = bwait(BAR(C::B_QF + s), (k / C::ST) & 1, abort_flag, a.budget) &&
-               (k < C::CH || bwait(BAR(C::B_QR + c), ((k / C::CH) - 1) & 1, abort_flag, a.budget));
+               (k < C::CH || bwait(BAR((C::EARLY ? C::B_SR : C::B_QR) + c), last, abort_flag, a.budget));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t t_s = tmem + C::COL_C + C::COLS * c;
-          const uint64_t d_do = sdesc_add(dst_row, s * C::STAGE), d_q = sdesc_add(d_do, C::TQ);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t oa = static_cast<uint32_t>(kk >> 2) * kBox + static_cast<uint32_t>(kk & 3) * 32u;
-            const uint32_t ob = static_cast<uint32_t>(kk >> 2) * C::KBOX + static_cast<uint32_t>(kk & 3) * 32u;
-            if (kk == 0) mma_ss_c<0>(t_s, sdesc_add(d_q, oa), sdesc_add(dk_row, ob), idesc);
-            else mma_ss_c<1>(t_s, sdesc_add(d_q, oa), sdesc_add(dk_row, ob), idesc);
+          product(t, sdesc_add(d_do, C::TQ), dk_row);
+          if (C::EARLY) {
+            tc_commit(BAR(C::B_SF + c));
+            ok = bwait(BAR(C::B_DF + s), (k / C::ST) & 1, abort_flag, a.budget) &&
+                 (k < C::CH || bwait(BAR(C::B_QR + c), last, abort_flag, a.budget));
+            if (!ok) break;
+            tc_fence_after();
           }
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t oa = static_cast<uint32_t>(kk >> 2) * kBox + static_cast<uint32_t>(kk & 3) * 32u;
-            const uint32_t ob = static_cast<uint32_t>(kk >> 2) * C::KBOX + static_cast<uint32_t>(kk & 3) * 32u;
-            if (kk == 0) mma_ss_c<0>(t_s + KT, sdesc_add(d_do, oa), sdesc_add(dv_row, ob), idesc);
-            else mma_ss_c<1>(t_s + KT, sdesc_add(d_do, oa), sdesc_add(dv_row, ob), idesc);
-          }
-          tc_commit(BAR(C::B_SF + c));
+          product(t + C::COL_DP, d_do, dv_row);
+          tc_commit(BAR((C::EARLY ? C::B_SP : C::B_SF) + c));
         }
       } else {  // dV += P^T dO, dK += dS^T Q, dQ = dS K
         const uint64_t dk_col = sdesc_sw128(sK, C::KBOX, 1024);
@@ -315,7 +368,7 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
         };
         for (int k = 0; ok && k < n; ++k) {
           const int c = k % C::CH, s = k % C::ST, i = k / C::CH;
-          const uint32_t buf = base + C::OFF_P + c * C::BUF, t_s = tmem + C::COL_C + C::COLS * c;
+          const uint32_t buf = base + C::OFF_P + c * C::BUF, t_q = tmem + C::COL_C + C::COLS * c + C::COL_DQ;
           const uint64_t d_do = sdesc_add(dst_col, s * C::STAGE), d_q = sdesc_add(d_do, C::TQ);
           if constexpr (KT > 64) {
             ok = bwait(BAR(C::B_PF + c), i & 1, abort_flag, a.budget);
@@ -323,6 +376,7 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
             tc_fence_after();
             sum(tmem, buf, d_do, idesc_bf16_f32(kTile, D, 1, 1), k == 0);
             tc_commit(BAR(C::B_DV + c));
+            if (C::OUT != C::kInDO || a.q_fp32) tc_commit(BAR(C::B_DE + s));
           }
           ok = bwait(BAR(C::B_DS + c), i & 1, abort_flag, a.budget);
           if (!ok) break;
@@ -331,8 +385,8 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
 #pragma unroll
           for (int kk = 0; kk < KT / 16; ++kk) {
             const uint32_t off = static_cast<uint32_t>(kk >> 2) * kBox + static_cast<uint32_t>(kk & 3) * 32u;
-            if (kk == 0) mma_ss_c<0>(t_s, ds, dk_col, idesc_bf16_f32(kTile, D, 1));
-            else mma_ss_c<1>(t_s, sdesc_add(ds, off), sdesc_add(dk_col, 2048u * kk), idesc_bf16_f32(kTile, D, 1));
+            if (kk == 0) mma_ss_c<0>(t_q, ds, dk_col, idesc_bf16_f32(kTile, D, 1));
+            else mma_ss_c<1>(t_q, sdesc_add(ds, off), sdesc_add(dk_col, 2048u * kk), idesc_bf16_f32(kTile, D, 1));
           }
           // At 64 keys [P dS]^T [dO Q] in one: dV is its upper left quarter and dK its lower right (the others would
           // be padding up to 128 rows).
@@ -353,39 +407,90 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
     constexpr int QN = C::W == 2 ? 2 : KT / 32;  // 32-key steps of a thread (KT = 96: the second thread has one)
     const int q0 = 2 * w, qn = min(KT / 32 - q0, QN);
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const uint32_t t_s = lanes + C::COL_C + C::COLS * c, buf = base + C::OFF_P + static_cast<uint32_t>(c) * C::BUF;
+    const uint32_t t_s = lanes + C::COL_C + C::COLS * c, t_dp = t_s + C::COL_DP;
+    const uint32_t buf = base + C::OFF_P + static_cast<uint32_t>(c) * C::BUF;
     float* halves = reinterpret_cast<float*>(gbase + C::OFF_D);
     const uint64_t c2 = f2_pack(a.sl2, a.sl2);
-    const bool issuer = (warp & 3) == 0 && lane == 0 && w == 0;  // of the chain's TMA stores
-    bool ok = true;
+    const bool issuer = C::OUT == C::kInBuf && !a.q_fp32 && (warp & 3) == 0 && lane == 0;  // of a chain's stores
+    float p[32 * QN];
+    auto row_lse = [&](int k) {  // rows past the last: P = 0
+      const int row = row0 + k * kTile + r;
+      return row < a.R ? a.lse[static_cast<size_t>(bh) * a.R + row] : INFINITY;
+    };
+    auto masked = [&](int q) { return 32 * (q0 + q) + 32 > len; };
+    auto p_of = [&](int q, float lse) {  // (this thread's step q)
+      const int k0 = 32 * (q0 + q);
+      const uint64_t nl2 = f2_pack(-lse * kLog2e, -lse * kLog2e);
+      uint32_t s[32];
+      tmem_ld_x32(t_s + k0, s);
+      if (masked(q)) p_step<true>(s, c2, nl2, len - k0, p + 32 * q);
+      else p_step<false>(s, c2, nl2, 32, p + 32 * q);
+    };
+    auto dot_of = [&](int q) {
+      const int k0 = 32 * (q0 + q);
+      uint32_t dp[32];
+      tmem_ld_x32(t_dp + k0, dp);
+      return masked(q) ? dot_step<true>(p + 32 * q, dp, len - k0) : dot_step<false>(p + 32 * q, dp, 32);
+    };
+    auto put_p = [&](int q) {
+      uint32_t pp[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) pp[e] = pack_bf16(p[32 * q + 2 * e], p[32 * q + 2 * e + 1]);
+      put_cols(buf, r, q0 + q, pp);
+    };
+    float lse = row_lse(c);  // of the chain's next tile, read a tile ahead
+    auto take_p = [&](int k) -> bool {
+      const float now = lse;
+      lse = row_lse(k + 1);
+      if (!bwait_all(BAR(C::B_SF), k & 1, abort_flag, a.budget)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < QN; ++q)
+        if (q < qn) p_of(q, now);
+      tc_fence_before();
+      mbar_arrive(BAR(C::B_SR));
+      return true;
+    };
+    bool ok = !C::EARLY || take_p(0);
     for (int k = c, i = 0; ok && k < n; k += C::CH, ++i) {
       const int row = row0 + k * kTile + r;
       const size_t frow = static_cast<size_t>(bh) * a.R + row;
-      const float lse2 = row < a.R ? a.lse[frow] * kLog2e : INFINITY;
-      const uint64_t nl2 = f2_pack(-lse2, -lse2);
-      if (issuer && !a.q_fp32) {  // the buffer is free once the last store has read it
-        bulk_wait_read_all();
-        mbar_arrive(BAR(C::B_OSF + c));
-      }
-      ok = bwait_all(BAR(C::B_SF + c), i & 1, abort_flag, a.budget);
-      if (ok && !a.q_fp32) ok = bwait_all(BAR(C::B_OSF + c), i & 1, abort_flag, a.budget);
-      if (!ok) break;
-      tc_fence_after();
-      float p[32 * QN], dd = 0.f;
+      float dd = 0.f;
+      if constexpr (C::EARLY) {
 #pragma unroll
-      for (int q = 0; q < QN; ++q) {
-        if (q >= qn) continue;
-        const int k0 = 32 * (q0 + q);
-        uint32_t s[32], dp[32], pp[16];
-        tmem_ld_x32(t_s + k0, s);
-        tmem_ld_x32(t_s + KT + k0, dp);
-        if (k0 + 32 > len) dd += p_step<true>(s, dp, c2, nl2, len - k0, p + 32 * q, pp);
-        else dd += p_step<false>(s, dp, c2, nl2, 32, p + 32 * q, pp);
-        put_cols(buf, r, q0 + q, pp);
-      }
-      if constexpr (KT > 64) {
+        for (int q = 0; q < QN; ++q)
+          if (q < qn) put_p(q);
         fence_proxy_async_smem();
-        mbar_arrive(BAR(C::B_PF + c));
+        ok = bwait_all(BAR(C::B_SP), k & 1, abort_flag, a.budget);
+        if (!ok) break;
+        tc_fence_after();
+        // Only now: dP computed says that dO has landed, which dV's issuer does not wait for, and that it is read, before
+        // dV's commit may give its place away.
+        mbar_arrive(BAR(C::B_PF));
+#pragma unroll
+        for (int q = 0; q < QN; ++q)
+          if (q < qn) dd += dot_of(q);
+      } else {
+        const float now = lse;
+        lse = row_lse(k + C::CH);
+        if (issuer) {  // the buffer is free once the last store has read it
+          bulk_wait_read_all();
+          mbar_arrive(BAR(C::B_OSF + c));
+        }
+        ok = bwait_all(BAR(C::B_SF + c), i & 1, abort_flag, a.budget);
+        if (ok && !a.q_fp32) ok = bwait_all(BAR(C::B_OSF + c), i & 1, abort_flag, a.budget);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < QN; ++q) {
+          p_of(q, now);
+          dd += dot_of(q);
+          put_p(q);
+        }
+        if constexpr (KT > 64) {
+          fence_proxy_async_smem();
+          mbar_arrive(BAR(C::B_PF + c));
+        }
       }
       if constexpr (C::W == 2) {
         halves[w * kTile + r] = dd;
@@ -401,8 +506,8 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
         if (q >= qn) continue;
         const int k0 = 32 * (q0 + q);
         uint32_t dp[32];
-        tmem_ld_x32(t_s + KT + k0, dp);
-        if (k0 + 32 > len) ds_step<true>(p + 32 * q, dp, nd2, len - k0, ds + 16 * q);
+        tmem_ld_x32(t_dp + k0, dp);
+        if (masked(q)) ds_step<true>(p + 32 * q, dp, nd2, len - k0, ds + 16 * q);
         else ds_step<false>(p + 32 * q, dp, nd2, 32, ds + 16 * q);
       }
       if constexpr (KT > 64) {
@@ -415,23 +520,25 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(BAR(C::B_DS + c));
+      if (C::EARLY && k + 1 < n && !(ok = take_p(k + 1))) break;
       ok = bwait_all(BAR(C::B_GF + c), i & 1, abort_flag, a.budget);
+      if (ok && C::OUT == C::kOwn && !a.q_fp32 && i > 0)
+        ok = bwait_all(BAR(C::B_OSF + c), (i - 1) & 1, abort_flag, a.budget);
       if (!ok) break;
       tc_fence_after();
-      put_dq<D>(a.dq, frow, row < a.R, buf, r, t_s, a.scale, w * (D / 32 / C::W), (w + 1) * (D / 32 / C::W), a.q_fp32);
+      put_dq<D>(a.dq, frow, row < a.R, C::dq_place(base, c, k % C::ST), r, t_s + C::COL_DQ, a.scale,
+                w * (D / 32 / C::W), (w + 1) * (D / 32 / C::W), a.q_fp32);
       tc_fence_before();
       mbar_arrive(BAR(C::B_QR + c));
       if (!a.q_fp32) {
         fence_proxy_async_smem();
         mbar_arrive(BAR(C::B_OW + c));
-        if (issuer) {
-          ok = bwait(BAR(C::B_OW + c), i & 1, abort_flag, a.budget);
-          if (ok) {
-            for (int h = 0; h < C::NH; ++h) tma_store_3d(&tdq, buf + h * kBox, h * 64, row0 + k * kTile, bh);
-            bulk_commit();
-          }
+        if (issuer && bwait(BAR(C::B_OW + c), i & 1, abort_flag, a.budget)) {
+          for (int h = 0; h < C::NH; ++h)
+            tma_store_3d(&tdq, C::dq_place(base, c, k % C::ST) + h * kBox, h * 64, row0 + k * kTile, bh);
+          bulk_commit();
         }
-        ok = __all_sync(0xffffffffu, ok);
+        __syncwarp();
       }
     }
     if (ok && (KT > 64 || g == 0) && bwait_all(BAR(C::B_ACC), 0, abort_flag, a.budget)) {
