@@ -7,11 +7,16 @@
 //   dV += P^T dO, dK += dS^T Q, dQ = dS K   P and dS as bf16 in shared memory, [query][key]: the first two take them
 //                                           with the keys as rows (MN-major), the last as they lie
 // A row's keys are all there, so D takes no pass over O (and no rounding of O).  Bound by HBM: Q and dO in, dQ out,
-// 6 d + 4 bytes a row.  The chain of a tile (about 3 us) is hidden by two tiles in flight, a thread per row, where TMEM
-// holds them; else a row has two threads, one for each 64 keys, which exchange their halves of D.
-// One thread issues S and dP, another the products with P and dS, whose sums want one order, a third dQ's stores.
-// Several blocks of a key head leave fp32 partial sums, which cross_sum_kernel adds in their order.  Measured beside
-// plan_cross_bwd.
+// 6 d + 4 bytes a row (8 x 64/16 heads, 4595 rows, 49 keys: 5.2 TB/s at d = 64, 5.7 at d = 128), where the chain of a
+// tile, about 2 us, is hidden:
+// - Two tiles in flight, a thread per row, where TMEM holds them (64 keys, and 96 at d = 64).
+// - Else one (bound by that chain: 3.6-3.9 TB/s at d = 128), shortened: a row has two threads, one for each 64 keys,
+//   which exchange their halves of D; the next tile's S is computed and its exponentials are taken while this one's
+//   gradients are; Q and dO come and go apart, and dQ leaves through dO's place, which is the one needed later.
+//   (2 x 16 heads, 8192 x 77, d = 128: 62 -> 51 us; with dQ in Q's place 62: the next loads then wait for the store.)
+// - lse is read a tile ahead (8 x 64/16, 4595 x 49, d = 64: 197 -> 176 us).
+// One thread issues S and dP, another the products with P and dS, whose sums want one order.  Several blocks of a key
+// head leave fp32 partial sums, which cross_sum_kernel adds in their order.  Measured beside plan_cross_bwd.
 //
 // Padding behind the sequence: P and dS become 0 after the arithmetic and K's rows are cleared in shared memory, once.
 #include "bwd_common.cuh"
@@ -25,13 +30,13 @@ template <int D, int KT>
 struct BwdShortCfg {
   static constexpr int CH = KT == 64 || (D == 64 && KT == 96) ? 2 : 1;  // tiles in flight (chains)
   static constexpr int W = 2 / CH;                                      // threads per row
-  // One chain: dQ is written over dP alone, the next tile's S is computed and its exponentials are taken while this one's
-  // gradients are computed, and a stage's Q and dO come and go apart.
+  // One chain: dQ is written over dP alone, the next tile's S comes early, and a stage's Q and dO come and go apart.
   static constexpr bool EARLY = CH == 1;
   static constexpr int NH = D / 64;
   static constexpr uint32_t KBOX = (KT == 64 ? 64u : 128u) * 128u;  // bytes of a box of K or V
   static constexpr uint32_t TK = NH * KBOX, TQ = NH * kBox;
-  // dQ on its way out: in a place of its own, or that of the tile's dO, or in the chain's buffer, as shared memory allows.
+  // dQ on its way out: in a place of its own, in that of the tile's dO, or in the chain's buffer, as shared memory allows
+  // (a store warp, or, from the buffer, the chain's first thread).
   enum Out { kOwn, kInDO, kInBuf };
   static constexpr Out OUT = CH == 2 ? kInBuf : D == 64 ? kOwn : kInDO;
   static constexpr int ST = D == 64 ? 4 : 2;  // stages of dO and Q
@@ -46,10 +51,11 @@ struct BwdShortCfg {
   static __device__ __forceinline__ uint32_t dq_place(uint32_t base, int c, int s) {
     return base + (OUT == kOwn ? OFF_O + c * TQ : OUT == kInDO ? OFF_Q + s * STAGE : OFF_P + c * BUF);
   }
-  static constexpr int WARP_S = 4 * CH * W, WARP_O = WARP_S + 2, WARP_TMA = WARP_S + (OUT == kInBuf ? 2 : 3), THREADS = (WARP_TMA + 1) * 32;
+  static constexpr int WARP_S = 4 * CH * W, WARP_O = WARP_S + 2, WARP_TMA = WARP_S + (OUT == kInBuf ? 2 : 3);
+  static constexpr int THREADS = (WARP_TMA + 1) * 32;
   static constexpr int B_KV = 0, B_KC = 1, B_ACC = 2, B_DRAIN = 3, B_QF = 5, B_QE = B_QF + ST, B_DF = B_QE + ST,
-                       B_DE = B_DF + ST, B_SF = B_DE + ST,
-                       B_SR = B_SF + CH, B_SP = B_SR + CH, B_PF = B_SP + CH, B_DV = B_PF + CH, B_DS = B_DV + CH, B_GF = B_DS + CH, B_QR = B_GF + CH,
+                       B_DE = B_DF + ST, B_SF = B_DE + ST, B_SR = B_SF + CH, B_SP = B_SR + CH, B_PF = B_SP + CH,
+                       B_DV = B_PF + CH, B_DS = B_DV + CH, B_GF = B_DS + CH, B_QR = B_GF + CH,
                        B_OW = B_QR + CH, B_OSF = B_OW + CH, B_DX = B_OSF + CH, NBAR = B_DX + 1;
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR, OFF_D = OFF_MISC + 16u;  // D's halves (two threads a row)
   static constexpr uint32_t SMEM = OFF_D + (W == 2 ? 2u * kTile * 4u : 0u) + 1024u;
@@ -88,7 +94,8 @@ __device__ __forceinline__ float dot_step(const float* p, const uint32_t (&dp)[3
 
 // dS = p (dp - D) of 32 keys, packed.
 template <bool MASK>
-__device__ __forceinline__ void ds_step(const float* p, const uint32_t (&dp)[32], uint64_t nd2, int valid, uint32_t* ds) {
+__device__ __forceinline__ void ds_step(const float* p, const uint32_t (&dp)[32], uint64_t nd2, int valid,
+                                        uint32_t* ds) {
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
     float s0, s1;
@@ -114,8 +121,8 @@ __device__ __forceinline__ void put_cols(uint32_t buf, int r, int c, const uint3
 
 // Columns [32 c0, 32 c1) of this thread's row of dQ out of TMEM: to global memory (fp32) or as bf16 into shared memory.
 template <int D>
-__device__ __forceinline__ void put_dq(void* out, size_t frow, bool valid, uint32_t buf, int r, uint32_t taddr, float scale,
-                                       int c0, int c1, int fp32) {
+__device__ __forceinline__ void put_dq(void* out, size_t frow, bool valid, uint32_t buf, int r, uint32_t taddr,
+                                       float scale, int c0, int c1, int fp32) {
 #pragma unroll 2
   for (int c = c0; c < c1; ++c) {
     uint32_t u[32];
@@ -226,16 +233,16 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
       mbar_init(BAR(C::B_DE + s), 1);
     }
     for (int c = 0; c < C::CH; ++c) {
-      mbar_init(BAR(C::B_SF + c), 1);     // S computed
+      mbar_init(BAR(C::B_SF + c), 1);           // S computed (two chains: and dP)
       mbar_init(BAR(C::B_SR + c), 128 * C::W);  // S read
-      mbar_init(BAR(C::B_SP + c), 1);     // dP computed
-      mbar_init(BAR(C::B_PF + c), 128 * C::W);   // P in shared memory (more than 64 keys)
-      mbar_init(BAR(C::B_DV + c), 1);     // P read (more than 64 keys)
-      mbar_init(BAR(C::B_DS + c), 128 * C::W);   // dS in shared memory
-      mbar_init(BAR(C::B_GF + c), 1);     // dQ computed, buffer read
-      mbar_init(BAR(C::B_QR + c), 128 * C::W);   // dQ out of TMEM
-      mbar_init(BAR(C::B_OW + c), 128 * C::W);   // dQ in shared memory
-      mbar_init(BAR(C::B_OSF + c), 1);    // dQ's place free again
+      mbar_init(BAR(C::B_SP + c), 1);           // dP computed
+      mbar_init(BAR(C::B_PF + c), 128 * C::W);  // P in shared memory (more than 64 keys)
+      mbar_init(BAR(C::B_DV + c), 1);           // P read (more than 64 keys)
+      mbar_init(BAR(C::B_DS + c), 128 * C::W);  // dS in shared memory
+      mbar_init(BAR(C::B_GF + c), 1);           // dQ computed, buffer read
+      mbar_init(BAR(C::B_QR + c), 128 * C::W);  // dQ out of TMEM
+      mbar_init(BAR(C::B_OW + c), 128 * C::W);  // dQ in shared memory
+      mbar_init(BAR(C::B_OSF + c), 1);          // dQ's place free again
     }
     mbar_init(BAR(C::B_DX), 256);  // both halves of D written
     *abort_flag = 0;
@@ -376,7 +383,7 @@ __global__ void __launch_bounds__(BwdShortCfg<D, KT>::THREADS, 1)
             tc_fence_after();
             sum(tmem, buf, d_do, idesc_bf16_f32(kTile, D, 1, 1), k == 0);
             tc_commit(BAR(C::B_DV + c));
-            if (C::OUT != C::kInDO || a.q_fp32) tc_commit(BAR(C::B_DE + s));
+            if (C::EARLY && (C::OUT != C::kInDO || a.q_fp32)) tc_commit(BAR(C::B_DE + s));
           }
           ok = bwait(BAR(C::B_DS + c), i & 1, abort_flag, a.budget);
           if (!ok) break;
@@ -571,7 +578,8 @@ cudaError_t launch_t(const BwdLaunch& l, cudaStream_t stream) {
   float* dv_part = l.kv_part + l.kv_splits * elems;
   const BwdShortArgs args{l.lse, l.dq, parts ? static_cast<void*>(l.kv_part) : l.dk,
                           parts ? static_cast<void*>(dv_part) : l.dv, parts ? elems : 0, l.kv_lens, l.kv_heads, l.N, l.Nk,
-                          l.q_tiles, l.grad_fp32, static_cast<int>(parts || l.grad_fp32), l.scale_log2, l.scale, l.budget};
+                          l.q_tiles, l.grad_fp32, static_cast<int>(parts || l.grad_fp32), l.scale_log2, l.scale,
+                          l.budget};
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

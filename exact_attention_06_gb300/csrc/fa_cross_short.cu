@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(ShortCfg<D, KT>::THREADS, 1)
         tc_fence_after();
         const uint64_t x = sdesc_add(dq, (k % C::ST) * C::TB);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {  // S = Q K^T (over the last P~, which PV below read: MMAs complete in order)
+        for (int kk = 0; kk < D / 16; ++kk) {  // S = Q K^T (over the last P~, which PV below read: MMAs are in order)
           const uint32_t off = static_cast<uint32_t>(kk >> 2) * kBox + static_cast<uint32_t>(kk & 3) * 32u;
           if (kk == 0) mma_ss_c<0>(t_s, sdesc_add(x, off), sdesc_add(dk, off), idesc_s);
           else mma_ss_c<1>(t_s, sdesc_add(x, off), sdesc_add(dk, off), idesc_s);
@@ -353,9 +353,12 @@ cudaError_t launch_t(const CrossShortLaunch& l, cudaStream_t stream) {
 
 cudaError_t launch_cross_short(const CrossShortLaunch& l, cudaStream_t stream) {
   const int Nk = l.args.Nk;
-  if (l.d == 64)
-    return Nk <= 64 ? launch_t<64, 64>(l, stream) : Nk <= 96 ? launch_t<64, 96>(l, stream) : launch_t<64, 128>(l, stream);
-  return Nk <= 64 ? launch_t<128, 64>(l, stream) : Nk <= 96 ? launch_t<128, 96>(l, stream) : launch_t<128, 128>(l, stream);
+  if (l.d == 64) {
+    if (Nk <= 64) return launch_t<64, 64>(l, stream);
+    return Nk <= 96 ? launch_t<64, 96>(l, stream) : launch_t<64, 128>(l, stream);
+  }
+  if (Nk <= 64) return launch_t<128, 64>(l, stream);
+  return Nk <= 96 ? launch_t<128, 96>(l, stream) : launch_t<128, 128>(l, stream);
 }
 
 unsigned int cross_short_read_and_clear_status() {

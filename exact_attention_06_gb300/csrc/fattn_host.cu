@@ -400,7 +400,19 @@ CrossBwdPlan plan_cross_bwd(const CrossShape& c, int Nk, int d, int sms) {
   CrossBwdPlan p;
   const int qt = (c.rows + 127) / 128, kt = (Nk + 127) / 128;
   const double kv = 2.0 * c.bh * Nk * d * sizeof(float), q = 1.0 * c.bh * c.rows * d * sizeof(float);
-  if (Nk <= fattn::kCrossShortKeys) {  // one kernel
+  // At most 128 keys take the one-pass kernel, whose step is a query tile.  Measured (GB300) against the dQ and dK/dV
+  // kernels of more keys, us:
+  //   heads, rows x keys        d = 64         d = 128
+  //   2 x 16, 8192 x 64        89 -> 27      117 -> 46
+  //   2 x 16, 8192 x 77       102 -> 37      133 -> 51
+  //   2 x 16, 8192 x 128      101 -> 44      134 -> 56
+  //   4 x 16, 2048 x 77        57 -> 23       73 -> 32
+  //   1 x 8, 1000 x 77       13.4 -> 9.5    16.5 -> 11.7
+  //   8 x 16/2, 5880 x 4      244 -> 61      313 -> 105
+  //   8 x 64/16, 4595 x 49    740 -> 176     960 -> 321
+  //   64 x 8, 40 x 100         40 -> 25       49 -> 34
+  // Ranges of queries per key head, 2 x 16 heads, 8192 x 77, d = 128, 1 / 2 / 4 / 8: 154 / 83 / 51 / 60 us.
+  if (Nk <= fattn::kCrossShortKeys) {
     p.kv_splits = cut_scan(c.bh, qt, sms, kv);
     p.q_tiles = (qt + p.kv_splits - 1) / p.kv_splits;
     if (p.kv_splits > 1) p.kv_bytes = round256(static_cast<size_t>(kv) * p.kv_splits);

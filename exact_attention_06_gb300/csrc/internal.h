@@ -205,7 +205,8 @@ cudaError_t launch_cross_bwd(const BwdLaunch& a, cudaStream_t stream);
 unsigned int cross_bwd_read_and_clear_status();
 // out (and out2, from the S sums after those) = the sum of S partial sums of n elements each
 cudaError_t launch_cross_sum(const float* part, void* out, void* out2, long long n, int S, int fp32, cudaStream_t stream);
-// The same over at most kCrossShortKeys keys (tk, tv: boxes of 64 rows for up to 64 keys), q_tiles and kv_splits as above.
+// The backward over at most kCrossShortKeys keys (tk, tv: boxes of 64 rows for up to 64 keys), q_tiles and kv_splits as
+// above.
 cudaError_t launch_cross_bwd_short(const BwdLaunch& a, cudaStream_t stream);
 unsigned int cross_bwd_short_read_and_clear_status();
 // delta[r] = rowsum(o_r * dout_r) of `rows` bf16 rows of d
