@@ -3,7 +3,8 @@
 // since doing it in Python took longer (5-9 us a call) than the kernels of a small step.
 //
 // Every function returns the library's status, or -1 when an argument is not what the call takes (nothing has been
-// launched then; fattn.py finds out which one and raises).  C++ exceptions (an allocation that fails) become torch's Python errors.
+// launched then; fattn.py finds out which one and raises).  C++ exceptions (an allocation that fails) become torch's
+// Python errors.
 #include <Python.h>
 
 #include <ATen/ops/empty.h>

@@ -431,9 +431,9 @@ fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int*
                          int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, void* workspace,
                          size_t ws_bytes, void* stream, const fa_cross_opts* opts);
 
-/* Scratch bytes of fa_cross_bwd on the current device: rowsum(O * dO) per query row, and fp32
- * partial gradients where it cuts a long scan into ranges (few key tiles under many queries, or
- * the reverse).  0 for invalid sizes or without a device. */
+/* Scratch bytes of fa_cross_bwd on the current device: rowsum(O * dO) per query row (of more than
+ * 128 keys), and fp32 partial gradients where it cuts a long scan into ranges (few key tiles under
+ * many queries, or the reverse).  Never 0 for valid sizes; 0 for invalid ones or without a device. */
 size_t fa_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 
 /* fa_cross_bwd -- the gradients, by the formulas of fa_bwd: dq like q, dk and dv like k and v (bf16,

@@ -269,7 +269,8 @@ def test_outputs_and_workspaces_keep_their_bounds():
     """Sentinels around every written buffer, workspaces of exactly the stated size."""
     for B, Hq, Hkv, Nq, Nk, d, lens in ((2, 6, 2, 43, 641, 64, [641, 200]), (1, 2, 2, 1, 1500, 128, [1400]),
                                         (1, 6, 2, 7, 20000, 128, [19000]),
-                                        (1, 4, 4, 900, 70, 128, None)):
+                                        (1, 4, 4, 900, 70, 128, None), (1, 8, 4, 3001, 77, 64, [60]),
+                                        (2, 4, 4, 700, 33, 128, [33, 0]), (1, 2, 2, 17, 97, 64, None)):
         q, k, v, do, kl = _inputs(B, Hq, Hkv, Nq, Nk, d, lens)
 
         def guarded(shape, dtype):
@@ -323,3 +324,79 @@ def test_calls_on_two_streams_keep_apart():
     for i, (o, lse) in enumerate(outs):
         q, k, v, _, kl = (a, b)[i % 2]
         _check_fwd(o, lse, q, k, v, 0.09, kl.tolist(), f"call {i}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nk", [50, 77, 128])
+def test_few_keys_captured_and_repeated(Nk, d):
+    """A training step over few keys, several blocks a key head: replayed with other inputs and lengths, on two streams
+    with the workspaces of their graphs, and the same gradients bit for bit."""
+    steps, size = [], (2, 8, 4, 4000, Nk, d)
+    for seed, lens in ((1, [Nk, Nk // 2]), (5, [0, Nk - 1])):
+        q, k, v, do, kl = _inputs(*size, lens, seed=seed)
+        buf = [x.clone() for x in (q, k, v, do, kl)]
+        out = [torch.empty_like(q), torch.empty(q.shape[:3], device=DEV), *(torch.empty_like(x) for x in (q, k, v))]
+        steps.append(((q, k, v, do, kl), buf, out))
+
+    def step(buf, out):
+        (q, k, v, do, kl), (o, lse, *g) = buf, out
+        fattn.fa_cross_fwd(q, k, v, o, lse, 0.1, kv_lens=kl)
+        fattn.fa_cross_bwd(q, k, v, o, do, lse, *g, 0.1, kv_lens=kl)
+    want = []
+    for first, buf, out in steps:
+        step(buf, out)
+        want.append([x.clone() for x in out])
+        step(buf, out)
+        assert all(torch.equal(x, y) for x, y in zip(want[-1], out))
+    streams, graphs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    torch.cuda.synchronize()
+    for s, (first, buf, out) in zip(streams, steps):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            step(buf, out)
+    for turn in range(4):  # each graph's buffers get the other's inputs in turn
+        for i, (_, buf, out) in enumerate(steps):
+            for x, y in zip(buf, steps[(i + turn) % 2][0]):
+                x.copy_(y)
+            for x in out:
+                x.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for i, (_, _, out) in enumerate(steps):
+            assert all(torch.equal(x, y) for x, y in zip(out, want[(i + turn) % 2])), f"graph {i}, turn {turn}"
+    assert fattn.fa_get_status() == fattn.FA_OK
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+def test_few_keys_past_32_bits(fp32):
+    """The last sequence lies behind 2^31 elements: what a call of its own gives."""
+    B, H, Nq, Nk, d = 66, 64, 8192, 77, 64
+    t = torch.float32 if fp32 else torch.bfloat16
+    q, do = (torch.zeros(B, H, Nq, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k, v = (torch.zeros(B, H, Nk, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    last = _inputs(1, H, H, Nq, Nk, d, None)
+    for x, y in zip((q, k, v, do), last):
+        x[-1:] = y
+
+    def step(q, k, v, do):
+        o, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=DEV)
+        fattn.fa_cross_fwd(q, k, v, o, lse, 0.1)
+        g = [torch.empty(x.shape, dtype=t, device=DEV) for x in (q, k, v)]
+        fattn.fa_cross_bwd(q, k, v, o, do, lse, *g, 0.1)
+        assert fattn.fa_get_status() == fattn.FA_OK
+        return o, lse, *g
+    got, want = step(q, k, v, do), step(*last[:4])
+    for x, y in zip(got[:3], want[:3]):
+        assert torch.equal(x[-1:], y)
+    # dK and dV: other ranges of queries, so the same terms in another order, each side within Nq 2^-24 of their
+    # absolute sum, and rounded to bf16.
+    q, k, v, do = (x.double() for x in last[:4])
+    p = (q @ k.mT * 0.1).softmax(-1)
+    dp = do @ v.mT
+    ds = p * (dp.abs() + (p * dp).sum(-1, keepdim=True).abs())
+    for x, y, terms in zip(got[3:], want[3:], (0.1 * ds.mT @ q.abs(), p.mT @ do.abs())):
+        slack = 2 * Nq * 2.0 ** -24 * (1 + 4 * U) * terms
+        assert ((x[-1:].double() - y.double()).abs() <= slack + (0 if fp32 else 2 * U * (y.double().abs() + slack))).all()
