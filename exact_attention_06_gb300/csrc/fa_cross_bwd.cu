@@ -1,6 +1,6 @@
 // Cross attention backward over more than 128 keys for sm_103a: dK, dV (one CTA per key tile and range of query
-// tiles) and dQ (one per query tile and range of key tiles), by the formulas of fa_bwd.cu, P recomputed from the
-// forward's lse.
+// tiles) and dQ (one per few query tiles, one after another, and range of key tiles), by the formulas of fa_bwd.cu,
+// P recomputed from the forward's lse.
 //
 // A step -- products, their way through TMEM, exponentials, P and dS back, gradients -- is a chain several times
 // as long as its work on the tensor core, so these kernels keep several in flight.  The scanned side is taken
@@ -33,20 +33,22 @@ struct CrossCfg {
   static constexpr int NH = D / 64;             // 128-byte boxes per row
   static constexpr uint32_t TB = NH * kBox;     // bytes of a 128 x d bf16 tile
   static constexpr int FLIGHT = (512 - ACC) / 128 < 3 ? (512 - ACC) / 128 : 3;  // half hh uses pair hh % FLIGHT
-  static constexpr uint32_t COL_ACC = 512 - ACC;
+  // dQ: places for a query tile's Q and dO, and for its accumulator (two at d = 64)
+  static constexpr int NB = ACC == 64 ? 2 : 1;
+  static constexpr uint32_t COL_ACC = 512 - NB * ACC;
   static constexpr int EW = 4 * FLIGHT;         // elementwise warps
   static constexpr int MMA = EW, TMA = EW + kIssuers, THREADS = (TMA + 1) * 32;
   static constexpr int ST = D == 64 ? 4 : 2;    // ring stages
   static constexpr uint32_t OFF_A = 0, OFF_B = TB;  // the block's own tiles: K, V or Q, dO
-  static constexpr uint32_t OFF_RING = 2 * TB;      // stage: Q_i, dO_i or K_j, V_j
+  static constexpr uint32_t OFF_RING = NB * 2 * TB;  // stage: Q_i, dO_i or K_j, V_j
   static constexpr uint32_t STAGE = 2 * TB;
   // dK/dV: per stage a float4 for each pair of its query rows, {-lse2, -lse2, -D, -D} (lse2 = lse * log2(e))
   static constexpr uint32_t OFF_VEC = OFF_RING + ST * STAGE;
   static constexpr uint32_t VEC = 2 * kTile * 4;
   static constexpr uint32_t OFF_BAR = OFF_VEC + ST * VEC;
-  static constexpr int B_OWN = 0, B_FULL = 1, B_EMPTY = B_FULL + ST, B_SF = B_EMPTY + ST, B_PF = B_SF + FLIGHT,
-                       B_GD = B_PF + 2 * FLIGHT, B_GF = B_GD + FLIGHT, B_DRAIN = B_GF + 1, B_OW = B_DRAIN + kIssuers,
-                       B_KC = B_OW + 2, NBAR = B_KC + 1;
+  static constexpr int B_OWN = 0, B_FULL = 2, B_EMPTY = B_FULL + ST, B_SF = B_EMPTY + ST, B_PF = B_SF + FLIGHT,
+                       B_GD = B_PF + 2 * FLIGHT, B_GF = B_GD + FLIGHT, B_DRAIN = B_GF + 2, B_OW = B_DRAIN + kIssuers,
+                       B_KC = B_OW + 2, NBAR = B_KC + ST;
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR;
   static constexpr uint32_t SMEM = OFF_MISC + 16u + 1024u;
   static_assert(SMEM <= 232448, "shared memory");
@@ -58,6 +60,7 @@ struct CrossCfg {
 struct CrossArgs {
   const int* kv_lens;
   int kv_heads, n_keys, tiles;
+  int own_tiles;  // dQ kernel: query tiles per block, one after another
   long long part_stride;
   __device__ __forceinline__ int keys(int bh) const {
     return kv_lens ? min(max(kv_lens[bh / kv_heads], 0), n_keys) : n_keys;
@@ -315,7 +318,9 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
   }
 }
 
-// One CTA per query tile and range of key tiles.  dS is packed into its dP.
+// One CTA per x.own_tiles query tiles and range of key tiles: it scans the keys for one tile after another, the next
+// one's Q, dO and first keys on their way meanwhile.  Halves (and stages) are counted over all its tiles, so that their
+// phases go on.  dS is packed into its dP.
 template <int D>
 __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
     cross_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -328,12 +333,13 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t sQ = base + C::OFF_A, sDO = base + C::OFF_B, sRing = base + C::OFF_RING, sBar = base + C::OFF_BAR;
+  const uint32_t sOwn = base + C::OFF_A, sRing = base + C::OFF_RING, sBar = base + C::OFF_BAR;  // own: Q, dO
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int bh, qt;
-  grouped_block(ng, bh, qt);
+  int bh, qb;
+  grouped_block(ng, bh, qb);
+  const int t0 = qb * x.own_tiles, nt = min(x.own_tiles, (N + kTile - 1) / kTile - t0);
   const int key0 = static_cast<int>(blockIdx.z) * x.tiles * kTile;  // this block's keys
   const int n_keys = x.keys(bh);
   const int mine = min(x.tiles * kTile, n_keys - key0);
@@ -342,47 +348,54 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
   // (Measured 92 -> 89 us at d = 64; the dK/dV kernel, whose blocks are longer, was slower with it.)
   const bool producer = threadIdx.x == C::TMA * 32;
   if (producer) {
-    mbar_init(BAR(C::B_OWN), 1);
+    for (int b = 0; b < C::NB; ++b) {
+      mbar_init(BAR(C::B_OWN + b), 1);
+      mbar_init(BAR(C::B_GF + b), 1);    // the tile's dQ is complete
+      mbar_init(BAR(C::B_OW + b), 128);  // and out of TMEM (bf16: in Q's place)
+    }
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(BAR(C::B_FULL + s), 1);
       mbar_init(BAR(C::B_EMPTY + s), 1);
+      mbar_init(BAR(C::B_KC + s), 32);  // K's last tile cleared behind the sequence
     }
     for (int g = 0; g < C::FLIGHT; ++g) {
       mbar_init(BAR(C::B_SF + g), 2);  // S and dP
       mbar_init(BAR(C::B_GD + g), 1);  // the pair's dQ MMAs are complete
     }
     for (int c = 0; c < 2 * C::FLIGHT; ++c) mbar_init(BAR(C::B_PF + c), 128);
-    mbar_init(BAR(C::B_GF), 1);
     for (int i = 0; i < kIssuers; ++i) mbar_init(BAR(C::B_DRAIN + i), 1);
-    mbar_init(BAR(C::B_OW), 128);
-    mbar_init(BAR(C::B_KC), 32);  // K's last tile cleared behind the sequence
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (mine <= 0) {  // no key in this range
-    zero_rows<D>(dq, static_cast<size_t>(bh) * N + qt * kTile, min(kTile, N - qt * kTile), grad_fp32);
+    zero_rows<D>(dq, static_cast<size_t>(bh) * N + t0 * kTile, min(nt * kTile, N - t0 * kTile), grad_fp32);
     wait_as_last_block();
     return;
   }
-  const int n_h = (mine + kHalf - 1) / kHalf, n_j = (n_h + 1) / 2;
+  const int n_h = (mine + kHalf - 1) / kHalf, n_j = (n_h + 1) / 2;  // per query tile
   const bool k_tail = mine % kTile != 0 && n_keys < x.n_keys;  // rows behind the sequence in K's last tile
-  auto load = [&](int j) {  // K_j, V_j
-    const int s = j % C::ST;
+  auto load = [&](int jj, int j) {  // K_j, V_j as the block's stage jj
+    const int s = jj % C::ST, row = key0 + j * kTile;
     const uint32_t st = sRing + s * C::STAGE;
     mbar_arrive_expect_tx(BAR(C::B_FULL + s), 2 * C::TB);
     for (int h = 0; h < C::NH; ++h) {
-      tma_load_3d(st + h * kBox, &tk, BAR(C::B_FULL + s), h * 64, key0 + j * kTile, bh);
-      tma_load_3d(st + C::TB + h * kBox, &tv, BAR(C::B_FULL + s), h * 64, key0 + j * kTile, bh);
+      tma_load_3d(st + h * kBox, &tk, BAR(C::B_FULL + s), h * 64, row, bh);
+      tma_load_3d(st + C::TB + h * kBox, &tv, BAR(C::B_FULL + s), h * 64, row, bh);
     }
   };
-  int issued = 0;  // (the producer's)
-  if (producer) {
-    mbar_arrive_expect_tx(BAR(C::B_OWN), 2 * C::TB);
+  auto load_own = [&](int t) {  // Q, dO of the block's tile t
+    const uint32_t full = BAR(C::B_OWN + t % C::NB), own = sOwn + t % C::NB * (2 * C::TB);
+    mbar_arrive_expect_tx(full, 2 * C::TB);
     for (int h = 0; h < C::NH; ++h) {
-      tma_load_3d(sQ + h * kBox, &tq, BAR(C::B_OWN), h * 64, qt * kTile, bh);
-      tma_load_3d(sDO + h * kBox, &tdo, BAR(C::B_OWN), h * 64, qt * kTile, bh);
+      tma_load_3d(own + h * kBox, &tq, full, h * 64, (t0 + t) * kTile, bh);
+      tma_load_3d(own + C::OFF_B + h * kBox, &tdo, full, h * 64, (t0 + t) * kTile, bh);
     }
-    for (; issued < min(C::ST, n_j); ++issued) load(issued);
+  };
+  const int first = min(C::ST, n_j);  // stages asked for at once
+  if (producer) {
+    load_own(0);
+    for (int j = 0; j < first; ++j) load(j, j);
+    if (C::NB > 1 && nt > 1) load_own(1);
   }
   if (warp == C::MMA) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -394,28 +407,52 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
   if (warp == C::TMA) {
-    if (lane == 0) {
-      for (int j = issued; j < n_j; ++j) {
-        if (!bwait(BAR(C::B_EMPTY + j % C::ST), ((j / C::ST) - 1) & 1, abort_flag, budget)) break;
-        load(j);
-        issued = j + 1;
-      }
-    }
+    int issued = first, owned = min(C::NB, nt);  // stages, tiles
+    bool ok = true;
+    auto take = [&](int before, int end) {  // stages up to before + end, of which `before` are of earlier tiles
+      if (lane == 0)
+        for (; ok && issued < before + end; ++issued) {
+          const int s = issued % C::ST;
+          if (issued >= C::ST) ok = bwait(BAR(C::B_EMPTY + s), ((issued / C::ST) - 1) & 1, abort_flag, budget);
+          if (!ok) break;
+          load(issued, issued - before);
+        }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    };
     // dQ = dS K multiplies the last tile's K rows behind the sequence by dS = 0: clear what the
     // caller's padding holds there (0 times an infinity or NaN).
-    issued = __shfl_sync(0xffffffffu, issued, 0);
-    if (k_tail && issued == n_j) {
-      const int last = n_j - 1;
-      if (bwait_all(BAR(C::B_FULL + last % C::ST), (last / C::ST) & 1, abort_flag, budget)) {
-        const uint32_t tile = sRing + (last % C::ST) * C::STAGE;
-        for (int i = (mine - last * kTile) * 8 + lane; i < kTile * 8; i += 32)
-          for (int h = 0; h < C::NH; ++h) sts128(tile + h * kBox + i * 16, 0, 0, 0, 0);
-        fence_proxy_async_smem();
-        mbar_arrive(BAR(C::B_KC));
+    auto clear = [&](int t) {
+      const int last = t * n_j + n_j - 1, s = last % C::ST;
+      ok = ok && bwait_all(BAR(C::B_FULL + s), (last / C::ST) & 1, abort_flag, budget);
+      if (!ok) return;
+      for (int i = (mine - (n_j - 1) * kTile) * 8 + lane; i < kTile * 8; i += 32)
+        for (int h = 0; h < C::NH; ++h) sts128(sRing + s * C::STAGE + h * kBox + i * 16, 0, 0, 0, 0);
+      fence_proxy_async_smem();
+      mbar_arrive(BAR(C::B_KC + s));
+    };
+    auto finish = [&](int t) {  // tile t's dQ: stored from Q's place, which is then free, as dO's
+      ok = bwait(BAR(C::B_OW + t % C::NB), (t / C::NB) & 1, abort_flag, budget);
+      if (!ok || grad_fp32) return;
+      for (int h = 0; h < C::NH; ++h)
+        tma_store_3d(&tdq, sOwn + t % C::NB * (2 * C::TB) + h * kBox, h * 64, (t0 + t) * kTile, bh);
+      bulk_commit();
+      bulk_wait_read_all();
+    };
+    int done = 0;  // tiles finished
+    for (int t = 0; ok && t < nt; ++t) {
+      take(t * n_j, first);
+      if (k_tail && first == n_j) clear(t);
+      if (lane == 0 && ok && t > 0) {
+        finish(done++);
+        if (ok && owned < nt) load_own(owned++);
       }
+      take(t * n_j, n_j);
+      if (k_tail && first < n_j) clear(t);
     }
     if (lane == 0) {
-      bdrain(BAR(C::B_OWN), 0, budget);
+      while (ok && done < nt) finish(done++);
+      bulk_wait_all();  // the stores complete before the CTA exits
+      for (int t = max(0, owned - C::NB); t < owned; ++t) bdrain(BAR(C::B_OWN + t % C::NB), (t / C::NB) & 1, budget);
       for (int j = max(0, issued - C::ST); j < issued; ++j) bdrain(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, budget);
     }
   } else if (warp >= C::MMA) {
@@ -423,54 +460,100 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
     if (lane == 0) {
       const int role = warp - C::MMA;
       bool ok = true;
+      int hc = 0, jc = 0;  // halves and stages of the tiles before
       if (role < 2) {  // S = Q K^T, dP = dO V^T
-        const uint64_t dA = sdesc_sw128(role == 0 ? sQ : sDO, 16, 1024);
+        const uint64_t dA = sdesc_add(sdesc_sw128(sOwn, 16, 1024), role == 0 ? 0u : C::OFF_B);
         const uint64_t dR = sdesc_add(sdesc_sw128(sRing, 16, 1024), role == 0 ? 0u : C::TB);
-        ok = bwait(BAR(C::B_OWN), 0, abort_flag, budget);
-        for (int hh = 0; ok && hh < n_h; ++hh) {
-          const int j = hh >> 1, g = hh % C::FLIGHT;
-          // the stage loaded (and cleared behind the sequence), and the pair's last dQ MMAs done with its columns
-          ok = bwait(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, abort_flag, budget) &&
-               (!k_tail || j + 1 < n_j || bwait(BAR(C::B_KC), 0, abort_flag, budget)) &&
-               (hh < C::FLIGHT || bwait(BAR(C::B_GD + g), ((hh / C::FLIGHT) - 1) & 1, abort_flag, budget));
-          if (!ok) break;
-          tc_fence_after();
-          issue_half_product<D>(tmem + kPair * g + 64 * role, dA, sdesc_add(dR, (j % C::ST) * C::STAGE), hh & 1);
-          tc_commit(BAR(C::B_SF + g));
+        uint32_t cleared = 0;  // parity of each stage's next clearing
+        for (int t = 0; ok && t < nt; ++t, hc += n_h, jc += n_j) {
+          ok = bwait(BAR(C::B_OWN + t % C::NB), (t / C::NB) & 1, abort_flag, budget);
+          for (int hh = 0; ok && hh < n_h; ++hh) {
+            const int H = hc + hh, J = jc + (hh >> 1), g = H % C::FLIGHT, s = J % C::ST;
+            // the stage loaded (and cleared behind the sequence), and the pair's last dQ MMAs done with its columns
+            ok = bwait(BAR(C::B_FULL + s), (J / C::ST) & 1, abort_flag, budget) &&
+                 (!k_tail || (hh >> 1) + 1 < n_j || bwait(BAR(C::B_KC + s), (cleared >> s) & 1, abort_flag, budget)) &&
+                 (H < C::FLIGHT || bwait(BAR(C::B_GD + g), ((H / C::FLIGHT) - 1) & 1, abort_flag, budget));
+            if (!ok) break;
+            tc_fence_after();
+            issue_half_product<D>(tmem + kPair * g + 64 * role, sdesc_add(dA, t % C::NB * (2 * C::TB)),
+                                  sdesc_add(dR, s * C::STAGE), hh & 1);
+            tc_commit(BAR(C::B_SF + g));
+          }
+          cleared ^= 1u << ((jc + n_j - 1) % C::ST);
         }
       } else {  // dQ += dS K
         const uint64_t dRmn = sdesc_sw128(sRing, kBox, 1024);
-        for (int hh = 0; ok && hh < n_h; ++hh) {
-          const int g = hh % C::FLIGHT;
-          for (int c = 0; ok && c < 2; ++c) {
-            ok = bwait(BAR(C::B_PF + 2 * g + c), (hh / C::FLIGHT) & 1, abort_flag, budget);
+        for (int t = 0; ok && t < nt; ++t, hc += n_h, jc += n_j) {
+          const int b = t % C::NB;
+          if (t >= C::NB) {  // the accumulator's last tile is out
+            ok = bwait(BAR(C::B_OW + b), ((t / C::NB) - 1) & 1, abort_flag, budget);
             if (!ok) break;
-            tc_fence_after();
-            issue_half_chunk<D>(tmem + C::COL_ACC, tmem + kPair * g + 64, sdesc_add(dRmn, ((hh >> 1) % C::ST) * C::STAGE),
-                             hh & 1, c, hh > 0 || c > 0);
           }
-          if (!ok) break;
-          tc_commit(BAR(C::B_GD + g));
-          if (hh & 1) tc_commit(BAR(C::B_EMPTY + (hh >> 1) % C::ST));
+          for (int hh = 0; ok && hh < n_h; ++hh) {
+            const int H = hc + hh, s = (jc + (hh >> 1)) % C::ST, g = H % C::FLIGHT;
+            for (int c = 0; ok && c < 2; ++c) {
+              ok = bwait(BAR(C::B_PF + 2 * g + c), (H / C::FLIGHT) & 1, abort_flag, budget);
+              if (!ok) break;
+              tc_fence_after();
+              issue_half_chunk<D>(tmem + C::COL_ACC + b * D, tmem + kPair * g + 64, sdesc_add(dRmn, s * C::STAGE),
+                                  hh & 1, c, hh > 0 || c > 0);
+            }
+            if (!ok) break;
+            tc_commit(BAR(C::B_GD + g));
+            if ((hh & 1) || hh + 1 == n_h) tc_commit(BAR(C::B_EMPTY + s));
+          }
+          if (ok) tc_commit(BAR(C::B_GF + b));
         }
-        tc_commit(BAR(C::B_GF));
       }
       tc_commit(BAR(C::B_DRAIN + role));
       bdrain(BAR(C::B_DRAIN + role), 0, budget);
     }
   } else {
     // ------------------------------------------------------------ elementwise warps: thread = query row
-    const int g = warp >> 2, r = 32 * (warp & 3) + lane, row = qt * kTile + r;
+    const int g = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const uint32_t tS = lanes + kPair * g, tP = tS + 64;
-    const bool in = row < N;
-    const float lse2 = in ? lse[static_cast<size_t>(bh) * N + row] * kLog2e : INFINITY;
-    const uint64_t c2 = f2_pack(sl2, sl2), nl2 = f2_pack(-lse2, -lse2);
-    const float dd = in ? delta[static_cast<size_t>(bh) * N + row] : 0.f;
-    const uint64_t nd2 = f2_pack(-dd, -dd);
+    const uint64_t c2 = f2_pack(sl2, sl2);
     bool ok = true;
-    for (int hh = g; ok && hh < n_h; hh += C::FLIGHT) {
-      ok = bwait_all(BAR(C::B_SF + g), (hh / C::FLIGHT) & 1, abort_flag, budget);
+    int out = 0;  // tiles whose dQ is out (the first four warps take them out of TMEM)
+    auto put_out = [&](int t) {
+      const int b = t % C::NB, row = (t0 + t) * kTile + r;
+      ok = bwait_all(BAR(C::B_GF + b), (t / C::NB) & 1, abort_flag, budget);
+      if (!ok) return;
+      tc_fence_after();
+      const uint32_t acc = lanes + C::COL_ACC + b * D, place = sOwn + b * (2 * C::TB);
+      if (grad_fp32) store_grad_row<D>(dq, static_cast<size_t>(bh) * N + row, row < N, acc, scale);
+      else stage_row_bf16<D>(place, place + kBox, r, acc, scale);  // (its Q is no longer read)
+      tc_fence_before();
+      mbar_arrive(BAR(C::B_OW + b));
+    };
+    auto row_of = [&](const float* v, int t, float past) {
+      const int row = (t0 + t) * kTile + r;
+      return row < N ? v[static_cast<size_t>(bh) * N + row] : past;
+    };
+    float lse_n = row_of(lse, 0, INFINITY), dd_n = row_of(delta, 0, 0.f);  // of tile t + 1, read a tile ahead
+    int t = -1, hh = g, i = 0;
+    uint64_t nl2 = 0, nd2 = 0;
+    for (int tile = 0; ok; hh += C::FLIGHT, ++i) {
+      while (hh >= n_h) {
+        hh -= n_h;
+        ++tile;
+      }
+      if (g == 0)
+        while (ok && out < min(tile, nt)) put_out(out++);
+      if (!ok || tile >= nt) break;
+      if (tile != t) {
+        const bool next = tile == t + 1;
+        t = tile;
+        const float lse2 = (next ? lse_n : row_of(lse, t, INFINITY)) * kLog2e, dd = next ? dd_n : row_of(delta, t, 0.f);
+        nl2 = f2_pack(-lse2, -lse2);
+        nd2 = f2_pack(-dd, -dd);
+        if (t + 1 < nt) {
+          lse_n = row_of(lse, t + 1, INFINITY);
+          dd_n = row_of(delta, t + 1, 0.f);
+        }
+      }
+      ok = bwait_all(BAR(C::B_SF + g), i & 1, abort_flag, budget);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
@@ -486,21 +569,6 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(BAR(C::B_PF + 2 * g + c));
-      }
-    }
-    if (ok) ok = bwait_all(BAR(C::B_GF), 0, abort_flag, budget);
-    if (ok && g == 0) {
-      tc_fence_after();
-      if (grad_fp32) {
-        store_grad_row<D>(dq, static_cast<size_t>(bh) * N + row, in, lanes + C::COL_ACC, scale);
-      } else {  // through shared memory: the Q tile has its shape and is no longer read
-        stage_row_bf16<D>(sQ, sQ + kBox, r, lanes + C::COL_ACC, scale);
-        mbar_arrive(BAR(C::B_OW));
-        if (warp == 0 && lane == 0 && bwait(BAR(C::B_OW), 0, abort_flag, budget)) {
-          for (int h = 0; h < C::NH; ++h) tma_store_3d(&tdq, sQ + h * kBox, h * 64, qt * kTile, bh);
-          bulk_commit();
-          bulk_wait_all();  // complete before the CTA exits
-        }
       }
     }
     tmem_wait_st();
@@ -546,7 +614,8 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   using KV = CrossCfg<D, 2 * D>;
   using Q = CrossCfg<D, D>;
   const long long kv_elems = static_cast<long long>(a.BH) * a.Nk * D, q_elems = static_cast<long long>(a.BH) * a.N * D;
-  const int k_tiles = (a.Nk + kTile - 1) / kTile, q_tiles = (a.N + kTile - 1) / kTile;
+  const int k_tiles = (a.Nk + kTile - 1) / kTile;
+  const int q_blocks = ((a.N + kTile - 1) / kTile + a.own_tiles - 1) / a.own_tiles;
   const bool kv_part = a.kv_splits > 1, q_part = a.q_splits > 1;
   auto k1 = cross_dkdv_kernel<D>;
   auto k2 = cross_dq_kernel<D>;
@@ -570,17 +639,17 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
         kv_part ? static_cast<void*>(a.kv_part) : a.dk, kv_part ? static_cast<void*>(dv_part) : a.dv, a.N, a.scale_log2,
         a.scale, static_cast<int>(kv_part || a.grad_fp32), a.budget, a.tdk, a.tdv,
         head_groups(a.BH, k_tiles, false, a.sms),
-        CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.q_tiles, kv_part ? kv_elems : 0});
+        CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.q_tiles, 0, kv_part ? kv_elems : 0});
   };
   auto dq = [&]() -> cudaError_t {
-    cfg.gridDim = dim3(static_cast<unsigned>(a.BH), static_cast<unsigned>(q_tiles), static_cast<unsigned>(a.q_splits));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.BH), static_cast<unsigned>(q_blocks), static_cast<unsigned>(a.q_splits));
     cfg.blockDim = dim3(Q::THREADS);
     cfg.dynamicSmemBytes = Q::SMEM;
     return cudaLaunchKernelEx(
         &cfg, k2, a.tq, a.tk, a.tv, a.tdo, a.lse, static_cast<const float*>(a.delta),
         q_part ? static_cast<void*>(a.q_part) : a.dq, a.N, a.scale_log2, a.scale,
-        static_cast<int>(q_part || a.grad_fp32), a.budget, a.tdq, head_groups(a.BH, q_tiles, false, a.sms),
-        CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.k_tiles, q_part ? q_elems : 0});
+        static_cast<int>(q_part || a.grad_fp32), a.budget, a.tdq, head_groups(a.BH, q_blocks, false, a.sms),
+        CrossArgs{a.kv_lens, a.kv_heads, a.Nk, a.k_tiles, a.own_tiles, q_part ? q_elems : 0});
   };
   e = launch_delta(a.o, a.dout, a.delta, static_cast<long long>(a.BH) * a.N, D, stream);
   if (e != cudaSuccess || (e = dkdv()) != cudaSuccess || (e = dq()) != cudaSuccess) return e;

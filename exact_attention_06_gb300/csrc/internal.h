@@ -197,6 +197,7 @@ struct BwdLaunch {
   int kv_heads;
   int q_tiles, kv_splits;
   int k_tiles, q_splits;
+  int own_tiles;  // query tiles that a block of the dQ kernel takes one after another
   float* kv_part;
   float* q_part;
 };

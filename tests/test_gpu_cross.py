@@ -168,9 +168,12 @@ def test_blocks_that_stream_many_query_tiles(Nk, lens, d):
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("Nk,lens", [(1, None), (64, [64, 0]), (65, [65, 64]), (96, None), (97, [97, 96]),
-                                     (128, [128, 33]), (77, [0, 77]), (31, [32, 5])])
+                                     (128, [128, 33]), (77, [0, 77]), (31, [32, 5]),
+                                     # more than one key tile: the dQ kernel's blocks take several query tiles
+                                     (129, None), (130, [130, 1]), (200, [65, 129]), (256, [256, 64]), (300, [193, 0]),
+                                     (600, [599, 300])])
 def test_gradients_of_many_query_tiles_over_few_keys(Nk, lens, d):
-    B, Hq, Hkv, Nq = 2, 8, 4, 7001  # some twenty tiles a block, then ranges of them
+    B, Hq, Hkv, Nq = 2, 8, 4, 7001  # some twenty query tiles a block, or ranges of them
     q, k, v, do, kl = _inputs(B, Hq, Hkv, Nq, Nk, d, lens)
     scale = d ** -0.5
     o, lse = _fwd(q, k, v, kl, scale)
