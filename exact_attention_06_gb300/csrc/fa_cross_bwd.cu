@@ -450,10 +450,11 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
       if (k_tail && first < n_j) clear(t);
     }
     if (lane == 0) {
-      while (ok && done < nt) finish(done++);
-      bulk_wait_all();  // the stores complete before the CTA exits
+      // every copy lands before the shared memory is released
       for (int t = max(0, owned - C::NB); t < owned; ++t) bdrain(BAR(C::B_OWN + t % C::NB), (t / C::NB) & 1, budget);
       for (int j = max(0, issued - C::ST); j < issued; ++j) bdrain(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, budget);
+      while (ok && done < nt) finish(done++);
+      bulk_wait_all();  // the stores complete before the CTA exits
     }
   } else if (warp >= C::MMA) {
     // ------------------------------------------------------------ MMA issuers: S, dP, dQ

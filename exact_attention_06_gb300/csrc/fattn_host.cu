@@ -392,7 +392,6 @@ CrossPlan plan_cross(const CrossShape& c, int Nk, int d, int sms, bool workspace
 struct CrossBwdPlan {
   int kv_splits = 1, q_tiles = 0;  // dK, dV: ranges of query tiles
   int q_splits = 1, k_tiles = 0;   // dQ: ranges of key tiles
-  int own_tiles = 1;               // dQ: query tiles a block
   size_t delta_bytes = 0, kv_bytes = 0, q_bytes = 0;
   size_t total() const { return std::max<size_t>(delta_bytes + kv_bytes + q_bytes, 256); }  // never none
 };
@@ -402,12 +401,14 @@ struct CrossBwdPlan {
 // number with which the last of them ends first, by these times in us of: a query tile of dK/dV, its blocks' fixed part,
 // a key tile of dQ, a query tile's part of its own, its blocks' fixed part.  Measured (GB300, the whole backward, us):
 //                                 tiles  1     2     3     4     6     8   (a kernel of one tile)
-//   d = 64, 2 x 16 heads, 8192 x 256   127   106   102    96    92    92   (116)
-//                         8192 x 512   187   160   150   146   141   153   (167)
-//           4 x 16/4, 2048 x 1500      201   197   190   194   218   234   (195)
-//   d = 128, 2 x 16, 8192 x 154        171   162   157   159   152   156   (164)
-//                    4096 x 2048       403   396   413   438   477   438   (396)
-int dq_own_tiles(const CrossBwdPlan& p, long long bh, int qt, int kt, int d, int sms) {
+//   d = 64, 2 x 16 heads, 8192 x 256   121   101    96    94    91    93   (116)
+//                         8192 x 512   176   153   147   144   141   153   (167)
+//           4 x 16/4, 2048 x 1500      199   196   191   195   220   236   (195)
+//   d = 128, 2 x 16, 8192 x 154        166   159   155   158   153   158   (164)
+//                    4096 x 2048       403   397   414   439   479   438   (396)
+// Where the sequences have lengths of their own (ragged), blocks end less evenly still: at most 24 key tiles a block
+// (4 x 16/4, 2048 x up to 1500, with the forward: 229 with two tiles, 232 with three, 233 with four).
+int dq_own_tiles(const CrossBwdPlan& p, long long bh, int qt, int kt, int d, int sms, bool ragged) {
   const double kv_step = d == 64 ? 1.16 : 1.8, kv_fixed = 3.5;
   const double q_step = d == 64 ? 0.87 : 1.34, q_tile = d == 64 ? 0.9 : 2.5, q_fixed = 3.0;
   const long long kv_blocks = bh * kt * p.kv_splits, busy = kv_blocks % sms;  // SMs with a block in dK/dV's last round
@@ -416,6 +417,7 @@ int dq_own_tiles(const CrossBwdPlan& p, long long bh, int qt, int kt, int d, int
   int best = 1;
   double best_t = 0;
   for (int own = 1; own <= qt && own <= 8; ++own) {
+    if (ragged && own > 1 && own * p.k_tiles > 24) break;
     const long long blocks = bh * ((qt + own - 1) / own) * p.q_splits;
     const double each = own * (p.k_tiles * q_step + q_tile) + q_fixed;
     auto done_by = [&](double t) {  // blocks
@@ -468,7 +470,6 @@ CrossBwdPlan plan_cross_bwd(const CrossShape& c, int Nk, int d, int sms) {
   p.kv_splits = cut_scan(c.bh * kt, qt, sms, kv, 0.75 * c.bh * qt * (kt + 3));
   p.q_tiles = (qt + p.kv_splits - 1) / p.kv_splits;
   p.k_tiles = (kt + p.q_splits - 1) / p.q_splits;
-  p.own_tiles = dq_own_tiles(p, c.bh, qt, kt, d, sms);
   p.delta_bytes = round256(static_cast<size_t>(c.bh) * c.rows * sizeof(float));
   if (p.kv_splits > 1) p.kv_bytes = round256(2ull * c.bh * Nk * d * sizeof(float) * p.kv_splits);
   if (p.q_splits > 1) p.q_bytes = round256(1ull * c.bh * c.rows * d * sizeof(float) * p.q_splits);
@@ -1191,10 +1192,12 @@ fa_status_t fa_cross_bwd(const void* q, const void* k, const void* v, const int*
   a.kv_splits = plan.kv_splits;
   a.k_tiles = plan.k_tiles;
   a.q_splits = plan.q_splits;
-  a.own_tiles = plan.own_tiles;
+  const bool short_keys = Nk <= fattn::kCrossShortKeys;
+  if (!short_keys)
+    a.own_tiles = dq_own_tiles(plan, c.bh, (c.rows + 127) / 128, (Nk + 127) / 128, d, sms, kv_lens != nullptr);
   cudaGetLastError();
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = Nk <= fattn::kCrossShortKeys ? fattn::launch_cross_bwd_short(a, s) : fattn::launch_cross_bwd(a, s);
+  cudaError_t e = short_keys ? fattn::launch_cross_bwd_short(a, s) : fattn::launch_cross_bwd(a, s);
   if (e != cudaSuccess) return cuda_fail(e, "fa_cross_bwd launch");
   return FA_OK;
 }
