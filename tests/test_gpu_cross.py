@@ -246,7 +246,7 @@ def test_repeats_bitwise_and_matches_the_square_forward():
     assert all(torch.equal(x, y) for x, y in zip(*grads))
 
 
-@pytest.mark.parametrize("Nq,Nk", [(300, 700), (3, 700), (1, 20000), (5000, 77)])
+@pytest.mark.parametrize("Nq,Nk", [(300, 700), (3, 700), (1, 20000), (5000, 77), (9000, 300)])
 def test_a_wait_that_runs_out_is_reported(Nq, Nk):
     q, k, v, do, kl = _inputs(2, 4, 2, Nq, Nk, 128, [Nk, 650])
     o, lse = torch.empty_like(q), torch.empty(2, 4, Nq, device=DEV)
