@@ -432,7 +432,9 @@ def _workspace_on(stream, nbytes: int, device):
     """Scratch that lives as long as the stream's work needs it: allocated on that stream, so that its
     memory goes to no other stream's tensor while the kernels may still use it."""
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(stream)
+        # A handle that is no pointer: 0 and 1 (cudaStreamLegacy) are the default stream, of which ExternalStream would
+        # make another (of 0 a new one from torch's pool).
+        stream = torch.cuda.default_stream(device) if stream in (0, 1) else torch.cuda.ExternalStream(stream, device)
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
