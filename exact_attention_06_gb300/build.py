@@ -2,9 +2,10 @@
 
 The translation units compile in parallel into ``_build/`` and link into
 ``exact_attention_06_gb300/libfattn.so``; beside them the host compiler builds the
-binding's module ``_calls.so`` against torch's headers.  The CUDA runtime is linked
-statically; the driver is reached through cudaGetDriverEntryPointByVersion,
-so no libcuda link is needed at build time.
+binding's module ``_calls.so`` against torch's headers, for this torch and Python only.
+The library needs neither, and is linked whether or not the module compiles.
+The CUDA runtime is linked statically; the driver is reached through
+cudaGetDriverEntryPointByVersion, so no libcuda link is needed at build time.
 """
 
 from __future__ import annotations
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfattn.so")
 CALLS = os.path.join(PKG, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "py_calls.cpp")
+CALLS_STAMP = os.path.join(BUILD, "_calls.stamp")  # what the module was built for and with
 SOURCES = ["fa_fwd.cu", "fa_bwd.cu", "fa_cross_bwd.cu", "fa_cross_bwd_short.cu", "fa_cross_rows.cu", "fa_cross_short.cu",
            "fa_decode.cu", "fa_quant.cu", "fa_rope.cu", "fattn_host.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
@@ -40,37 +44,93 @@ def _flags():
 
 
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != os.path.basename(CALLS_SRC)]
     files.append(os.path.join(INCLUDE, "fattn.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
-def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
+def _newer(out: str, files) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in files)
+
+
+def calls_abi() -> str:
+    """The torch and Python whose binary interfaces the module follows; compiled into it as ``BUILT_FOR``."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+def _cxx() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def _calls_key() -> str:
+    import torch
+    return "\n".join((calls_abi(), os.path.dirname(torch.__file__), _cxx()))
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def _calls_up_to_date() -> bool:
+    if not _newer(CALLS, [CALLS_SRC, os.path.join(INCLUDE, "fattn.h"), os.path.abspath(__file__)]):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    try:
+        with open(CALLS_STAMP) as f:
+            return f.read() == _calls_key()
+    except (OSError, ImportError):
+        return False
+
+
+def up_to_date() -> bool:
+    return _lib_up_to_date() and _calls_up_to_date()
 
 
 def _calls_command(out: str):
-    import sysconfig
-
     import torch
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     top = os.path.dirname(torch.__file__)
     inc, libs = os.path.join(top, "include"), os.path.join(top, "lib")
-    return [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall",
-            os.path.join(CSRC, "py_calls.cpp"), "-o", out, "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+    return [_cxx(), "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", f'-DFATTN_BUILT_FOR="{calls_abi()}"',
+            CALLS_SRC, "-o", out, "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
             "-I", cuda, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
             f"-L{libs}", f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
+def _build_calls():
+    """Compile the module; what went wrong, or None."""
+    tmp = CALLS + ".tmp"
+    try:
+        key = _calls_key()
+        r = subprocess.run(_calls_command(tmp), capture_output=True, text=True)
+    except (OSError, ImportError) as e:  # no torch, no compiler
+        return str(e)
+    if r.returncode != 0:
+        return f"{r.stdout}{r.stderr}"
+    os.replace(tmp, CALLS)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(key)
+    return None
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libfattn.so; returns its path.  Raises on failure."""
-    if not force and up_to_date():
+    """Compile what is out of date, link libfattn.so; returns its path.  Raises on failure."""
+    with_lib, with_calls = force or not _lib_up_to_date(), force or not _calls_up_to_date()
+    if not with_lib and not with_calls:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_build_calls) if with_calls else None
+        if with_lib:
+            _build_lib(ex, verbose, ptxas_info)
+        wrong = calls.result() if calls else None
+    if wrong:
+        raise RuntimeError(f"{LIB} is built, the binding's module is not: py_calls.cpp:\n{wrong}")
+    return LIB
+
+
+def _build_lib(ex, verbose: bool, ptxas_info: bool) -> None:
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
@@ -80,14 +140,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    calls_tmp = CALLS + ".tmp"
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(subprocess.run, _calls_command(calls_tmp), capture_output=True, text=True)
-        results = list(ex.map(compile_one, SOURCES))
-        calls = calls.result()
+    results = list(ex.map(compile_one, SOURCES))
     errors = []
-    if calls.returncode != 0:
-        errors.append(f"py_calls.cpp:\n{calls.stdout}{calls.stderr}")
     for src, _obj, r in results:
         if verbose or ptxas_info:
             sys.stderr.write(r.stdout + r.stderr)
@@ -101,8 +155,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB)
-    os.replace(calls_tmp, CALLS)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -8,7 +8,8 @@ All computation happens in the library's kernels; there is no fallback.
 The library is called through ctypes; cross attention and rotary positions go
 through the compiled module ``_calls`` (csrc/py_calls.cpp), which makes the
 same checks on the tensors in C++: a decode step's kernels take less time than
-these checks in Python.
+these checks in Python.  The module is loaded by the first of those calls; the
+others need the library alone.
 """
 
 from __future__ import annotations
@@ -17,6 +18,8 @@ import ctypes
 import os
 
 import torch
+
+from .build import calls_abi
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfattn.so")
@@ -77,7 +80,7 @@ _calls = None  # the compiled module, bound to the loaded library
 
 def lib() -> ctypes.CDLL:
     """The loaded library; raises if it has not been built."""
-    global _lib, _calls
+    global _lib
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise FattnError(FA_ERR_CUDA, "load", f"{LIB_PATH} is missing; build it with exact_attention_06_gb300.build")
@@ -131,17 +134,27 @@ def lib() -> ctypes.CDLL:
                      "fa_decode_paged_ex", "fa_combine", "fa_combine_ex", "fa_cross_fwd", "fa_cross_bwd",
                      "fa_rope_axes_plan", "fa_rope_axes", "fa_rope_axes_paged", "fa_get_status"):
             getattr(L, name).restype = i
-        try:
-            from . import _calls as calls
-        except ImportError as e:
-            raise FattnError(FA_ERR_CUDA, "load", f"{_HERE}/_calls.so cannot be loaded ({e}); build it with "
-                                                  "exact_attention_06_gb300.build") from e
-        calls.bind(*(ctypes.cast(getattr(L, name), vp).value for name in (
-            "fa_cross_fwd", "fa_cross_workspace_bytes", "fa_cross_bwd", "fa_cross_bwd_workspace_bytes",
-            "fa_rope_axes", "fa_rope_axes_paged")))
-        _calls = calls
         _lib = L
     return _lib
+
+
+def _load_calls():
+    """Load the compiled module and bind it to the library; raises if it has not been built for this torch and Python."""
+    global _calls
+    L = lib()
+    try:
+        from . import _calls as calls
+    except ImportError as e:
+        raise FattnError(FA_ERR_CUDA, "load", f"{_HERE}/_calls.so cannot be loaded ({e}); build it with "
+                                              "exact_attention_06_gb300.build") from e
+    built_for = getattr(calls, "BUILT_FOR", "an older library")
+    if built_for != calls_abi():
+        raise FattnError(FA_ERR_CUDA, "load", f"{_HERE}/_calls.so was built for {built_for}, this is {calls_abi()}; "
+                                              "build it with exact_attention_06_gb300.build")
+    calls.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+        "fa_cross_fwd", "fa_cross_workspace_bytes", "fa_cross_bwd", "fa_cross_bwd_workspace_bytes",
+        "fa_rope_axes", "fa_rope_axes_paged")))
+    _calls = calls
 
 
 _STATUS_NAMES = {FA_OK: "FA_OK", FA_ERR_INVALID_ARG: "FA_ERR_INVALID_ARG", FA_ERR_UNSUPPORTED: "FA_ERR_UNSUPPORTED",
@@ -485,8 +498,8 @@ def fa_cross_fwd(q, k, v, o, lse, scale: float, kv_lens=None, workspace=None, st
     h // (Hq // Hkv)), of which sequence b has the first kv_lens[b] (int32 [B]; None: all); o like q, bf16 or
     fp32 (from its dtype); lse [B, Hq, Nq] fp32.  Nq = 1 is a decode step.  ``workspace``: a 1-dimensional uint8
     CUDA tensor of fa_cross_workspace_bytes() bytes; allocated here when None."""
-    if _lib is None:
-        lib()
+    if _calls is None:
+        _load_calls()
     handle = _handle(stream)
     if stream is not None and workspace is None:
         nbytes = fa_cross_workspace_bytes(*_cross_fwd_sizes(q, k, v, o, lse, kv_lens, workspace))
@@ -508,8 +521,8 @@ def fa_cross_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale: float, kv_lens=None, 
     """Gradients of fa_cross_fwd (which produced the bf16 o, and lse, with the same kv_lens and scale): dq like q,
     dk and dv like k, bf16 or fp32 (from dq's dtype).  ``workspace``: a 1-dimensional uint8 CUDA tensor of
     fa_cross_bwd_workspace_bytes() bytes; allocated here when None."""
-    if _lib is None:
-        lib()
+    if _calls is None:
+        _load_calls()
     handle = _handle(stream)
     if stream is not None and workspace is None:
         sizes = _cross_bwd_sizes(q, k, v, o, dout, lse, dq, dk, dv, kv_lens, workspace)
@@ -556,8 +569,8 @@ def fa_rope_axes(q, k, pos, plan, q_out=None, k_out=None, inverse: bool = False,
     """Turn q [B, Hq, N, d] into q_out and k [B, Hk, N, d] (or None) into k_out by the positions pos
     [axes, B, N] int32; in place where an output is None or its input.  inverse=True turns back: the
     gradients of q and k from those of q_out and k_out."""
-    if _lib is None:
-        lib()
+    if _calls is None:
+        _load_calls()
     q_out = q if q_out is None else q_out
     k_out = k if k_out is None else k_out
     st = _calls.rope_axes(q, k, pos, plan, q_out, k_out, inverse, _handle(stream))
@@ -589,8 +602,8 @@ def fa_rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table,
     """New tokens of a decode step or prompt chunk: q [B, Hq, N, d] turned into q_out, k [B, Hk, N, d] turned and
     v copied into the pools k_pages, v_pages [P, Hk, page_size, d] of fa_decode_paged, as keys seq_lens[b] ..
     of sequence b (int32 [B], the lengths before this call); tokens from new_lens[b] on are padding."""
-    if _lib is None:
-        lib()
+    if _calls is None:
+        _load_calls()
     st = _calls.rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table, seq_lens, new_lens,
                                 _handle(stream))
     if st:
