@@ -131,7 +131,7 @@ struct PersistCfg : FwdCfg<64> {
   static constexpr int THREADS = (WARP_TMA + 1) * 32;
   static constexpr int B_Q = 0, B_QE = B_Q + 1, B_KF = B_QE + 1, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST,
                        B_SF = B_VE + VST, B_PF = B_SF + 2, B_SC = B_PF + 2, B_OF = B_SC + 2, B_DRAIN = B_OF + 2,
-                       B_OSF = B_DRAIN + N_ISSUERS, B_OW = B_OSF + 2, B_VC = B_OW + 2, NBAR = B_VC + VST;
+                       B_OSF = B_DRAIN + N_ISSUERS, B_OW = B_OSF + 2, B_VC = B_OW + 2, B_VT = B_VC + VST, NBAR = B_VT + 2;
   static constexpr uint32_t OFF_BAR = OFF_V + VST * KVB;
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR;
   static constexpr uint32_t OFF_O = (OFF_MISC + 16u + 1023u) & ~1023u;
@@ -1029,8 +1029,10 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
       mbar_init(BAR(C::B_OSF + t), 1);                 // O staging of tile t free again
       mbar_init(BAR(C::B_OW + t), kSoftmaxWarps * 32);  // O staging of tile t written
     }
-    if constexpr (CROSS)
+    if constexpr (CROSS) {
       for (int s = 0; s < C::VST; ++s) mbar_init(BAR(C::B_VC + s), kSoftmaxWarps * 32);  // V stage cleared
+      for (int t = 0; t < 2; ++t) mbar_init(BAR(C::B_VT + t), 1);  // tile t's threads may clear their next stage
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -1181,8 +1183,10 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
               mbar_arrive(BAR(C::B_VE + gv % C::VST));
               continue;
             }
+            const bool tail = CROSS && I.v_tail && j + 1 == n_max;
+            if (tail && (t == 0 || I.n0 == 0)) mbar_arrive(BAR(C::B_VT + t));  // the stage to clear has landed
             ok = wait(BAR(C::B_PF + t), (g + j) & 1);
-            if (CROSS && ok && I.v_tail && j + 1 == n_max) ok = wait(BAR(C::B_VC + gv % C::VST), (tails >> (gv % C::VST)) & 1);
+            if (tail && ok) ok = wait(BAR(C::B_VC + gv % C::VST), (tails >> (gv % C::VST)) & 1);
             if (!ok) break;
             tc_fence_after();
             issue_pv(t, gv, j == 0);
@@ -1194,7 +1198,7 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
         g0 += I.n0;
         g1 += I.n1;
         kc += n_max;
-        if (CROSS && I.v_tail) tails ^= 1u << ((kc - 1) % C::VST);
+        if (CROSS && I.v_tail && n_max > 0) tails ^= 1u << ((kc - 1) % C::VST);
       }
       if (issued) {  // all MMAs complete before TMEM is released
         tc_commit(BAR(C::B_DRAIN + role));
@@ -1220,6 +1224,7 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
     int g = 0;   // this tile's steps over the items so far: the phases of its SF and OF barriers
     int gi = 0;  // this tile's O tiles staged so far: the phases of its OSF and OW barriers
     int kc = 0;  // CROSS: the CTA's key tiles so far (ring stages)
+    int vt = 0;  // CROSS: stages of V this tile's threads have cleared: the phases of its VT barrier
     bool ok = true;
     for (int w = w0; ok && w < n_items; w += w_step) {
       const FwdItem I = item_at<CROSS>(w, aux, N);
@@ -1268,11 +1273,14 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
         l = fmaf(alpha, l, (s0 + s1) + (s2 + s3));
         if constexpr (CROSS) {
           // The last tile's V rows behind the sequence hold whatever the caller's padding does, and
-          // their P~ = 0 times an infinity or NaN there would reach U: one tile's threads clear them.
+          // their P~ = 0 times an infinity or NaN there would reach U: one tile's threads clear them.  That the
+          // stage has landed they learn from the tile's PV issuer, which sees every phase of the stage.  (They would
+          // see only those of tails, and a wait by parity returns at once when the phase before has yet to complete.)
           if (j + 1 == n && (t == 0 || I.n0 == 0) && I.v_tail) {
             const int gv = kc + j;
-            ok = wait_all(BAR(C::B_VF + gv % C::VST), (gv / C::VST) & 1, abort_flag, budget);
+            ok = wait_all(BAR(C::B_VT + t), vt & 1, abort_flag, budget);
             if (!ok) break;
+            ++vt;
             const uint32_t tile = sV + (gv % C::VST) * C::KVB;
             for (int i = (I.Nk - j * kBc) * 8 + (threadIdx.x % (kSoftmaxWarps * 32)); i < kBc * 8; i += kSoftmaxWarps * 32)
               sts128(tile + i * 16, 0, 0, 0, 0);
