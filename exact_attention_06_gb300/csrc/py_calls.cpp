@@ -133,6 +133,22 @@ struct Plan {
 
 PyObject* status(long st) { return PyLong_FromLong(st); }
 
+// The interpreter's lock is free while the library enqueues: a full launch queue makes the call wait for the GPU, and what
+// the GPU is waiting for may be a host function or another thread's call that needs the lock.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F>
+PyObject* enqueue(F f) {
+  long st;
+  {
+    const Unlocked unlocked;
+    st = f();
+  }
+  return status(st);
+}
+
 // Scratch for a call on torch's current stream: its memory returns to that stream's pool when the call has been queued.
 at::Tensor scratch(size_t bytes, int dev) {
   return at::empty({static_cast<int64_t>(bytes)},
@@ -173,13 +189,15 @@ PyObject* cross_fwd(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   const fa_cross_opts opts{fp32, a.cycles(9)};
   if (!a.ok) return status(-1);
   const int B = q[0], Hq = q[1], Hkv = k[1], Nq = q[2], Nk = k[2], d = q[3];
-  at::Tensor own;
-  if (argv[7] == Py_None && (bytes = api.cross_bytes(B, Hq, Hkv, Nq, Nk, d)) > 0) {
-    own = scratch(bytes, a.dev);
-    ws = own.data_ptr();
-  }
-  return status(api.cross_fwd(pq, pk, pv, static_cast<const int*>(lens), po, static_cast<float*>(lse), B, Hq, Hkv, Nq,
-                              Nk, d, scale, ws, bytes, stream, &opts));
+  return enqueue([&] {
+    at::Tensor own;
+    if (argv[7] == Py_None && (bytes = api.cross_bytes(B, Hq, Hkv, Nq, Nk, d)) > 0) {
+      own = scratch(bytes, a.dev);
+      ws = own.data_ptr();
+    }
+    return api.cross_fwd(pq, pk, pv, static_cast<const int*>(lens), po, static_cast<float*>(lse), B, Hq, Hkv, Nq, Nk, d,
+                         scale, ws, bytes, stream, &opts);
+  });
   END_HANDLE_TH_ERRORS
 }
 
@@ -208,13 +226,15 @@ PyObject* cross_bwd(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   const fa_bwd_opts opts{a.cycles(13)};
   if (!a.ok || f0 != f1 || f0 != f2) return status(-1);
   const int B = q[0], Hq = q[1], Hkv = k[1], Nq = q[2], Nk = k[2], d = q[3];
-  at::Tensor own;
-  if (argv[11] == Py_None && (bytes = api.cross_bwd_bytes(B, Hq, Hkv, Nq, Nk, d)) > 0) {
-    own = scratch(bytes, a.dev);
-    ws = own.data_ptr();
-  }
-  return status(api.cross_bwd(pq, pk, pv, static_cast<const int*>(lens), po, pdo, static_cast<const float*>(lse), dq, dk,
-                              dv, B, Hq, Hkv, Nq, Nk, d, scale, f0, ws, bytes, stream, &opts));
+  return enqueue([&] {
+    at::Tensor own;
+    if (argv[11] == Py_None && (bytes = api.cross_bwd_bytes(B, Hq, Hkv, Nq, Nk, d)) > 0) {
+      own = scratch(bytes, a.dev);
+      ws = own.data_ptr();
+    }
+    return api.cross_bwd(pq, pk, pv, static_cast<const int*>(lens), po, pdo, static_cast<const float*>(lse), dq, dk, dv, B,
+                         Hq, Hkv, Nq, Nk, d, scale, f0, ws, bytes, stream, &opts);
+  });
   END_HANDLE_TH_ERRORS
 }
 
@@ -244,7 +264,9 @@ PyObject* rope_axes(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     PyErr_Clear();
     return status(-1);
   }
-  return status(api.rope(pq, pk, static_cast<const int*>(pos), qo, ko, q[0], q[1], k[1], q[2], plan.p, inverse, stream));
+  return enqueue([&] {
+    return api.rope(pq, pk, static_cast<const int*>(pos), qo, ko, q[0], q[1], k[1], q[2], plan.p, inverse, stream);
+  });
   END_HANDLE_TH_ERRORS
 }
 
@@ -272,9 +294,11 @@ PyObject* rope_axes_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   void* news = a.ptr_or_none(10, kI32, {q[0]});
   void* stream = a.stream(11);
   if (!a.ok) return status(-1);
-  return status(api.rope_paged(pq, pk, pv, static_cast<const int*>(pos), qo, kp, vp, static_cast<const int*>(bt),
-                               static_cast<const int*>(lens), static_cast<const int*>(news), q[0], q[1], k[1], q[2],
-                               pool[2], max_pages, pool[0], plan.p, stream));
+  return enqueue([&] {
+    return api.rope_paged(pq, pk, pv, static_cast<const int*>(pos), qo, kp, vp, static_cast<const int*>(bt),
+                          static_cast<const int*>(lens), static_cast<const int*>(news), q[0], q[1], k[1], q[2], pool[2],
+                          max_pages, pool[0], plan.p, stream);
+  });
   END_HANDLE_TH_ERRORS
 }
 
