@@ -759,11 +759,8 @@ cudaError_t launch_bwd(const BwdLaunch& a, cudaStream_t stream) {
   return a.causal ? launch_bwd_t<128, true>(a, stream) : launch_bwd_t<128, false>(a, stream);
 }
 
-unsigned int bwd_read_and_clear_status() {
-  unsigned int v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_bwd_status, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_bwd_status, &zero, sizeof(zero));
-  return v;
+cudaError_t bwd_status_word(unsigned int** p) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_bwd_status);
 }
 
 }  // namespace fattn

@@ -680,11 +680,8 @@ cudaError_t launch_cross_bwd(const BwdLaunch& a, cudaStream_t stream) {
   return a.d == 64 ? launch_t<64>(a, stream) : launch_t<128>(a, stream);
 }
 
-unsigned int cross_bwd_read_and_clear_status() {
-  unsigned int v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_bwd_status, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_bwd_status, &zero, sizeof(zero));
-  return v;
+cudaError_t cross_bwd_status_word(unsigned int** p) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_bwd_status);
 }
 
 }  // namespace fattn

@@ -605,11 +605,8 @@ cudaError_t launch_cross_bwd_short(const BwdLaunch& l, cudaStream_t stream) {
   return l.Nk <= 96 ? launch_t<128, 96>(l, stream) : launch_t<128, 128>(l, stream);
 }
 
-unsigned int cross_bwd_short_read_and_clear_status() {
-  unsigned int v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_bwd_status, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_bwd_status, &zero, sizeof(zero));
-  return v;
+cudaError_t cross_bwd_short_status_word(unsigned int** p) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_bwd_status);
 }
 
 }  // namespace fattn

@@ -424,11 +424,8 @@ cudaError_t launch_cross_rows(const CrossRowsLaunch& a, cudaStream_t stream) {
   return two ? launch_t<128, 2, false>(a, stream) : launch_t<128, 1, false>(a, stream);
 }
 
-unsigned int cross_rows_read_and_clear_status() {
-  unsigned int v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_rows_status, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_rows_status, &zero, sizeof(zero));
-  return v;
+cudaError_t cross_rows_status_word(unsigned int** p) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_rows_status);
 }
 
 }  // namespace fattn

@@ -361,11 +361,8 @@ cudaError_t launch_cross_short(const CrossShortLaunch& l, cudaStream_t stream) {
   return Nk <= 96 ? launch_t<128, 96>(l, stream) : launch_t<128, 128>(l, stream);
 }
 
-unsigned int cross_short_read_and_clear_status() {
-  unsigned int v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_short_status, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_short_status, &zero, sizeof(zero));
-  return v;
+cudaError_t cross_short_status_word(unsigned int** p) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_short_status);
 }
 
 }  // namespace fattn

@@ -467,11 +467,8 @@ cudaError_t decode_noalloc_scratch(void** ptr) {
   return cudaSuccess;
 }
 
-unsigned int decode_read_and_clear_status() {
-  unsigned int v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_dec_status, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_dec_status, &zero, sizeof(zero));
-  return v;
+cudaError_t decode_status_word(unsigned int** p) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_dec_status);
 }
 
 }  // namespace fattn

@@ -1427,11 +1427,8 @@ cudaError_t launch_fwd(const FwdLaunch& a, cudaStream_t stream) {
   return a.causal ? launch_t<128, true>(a, stream) : launch_t<128, false>(a, stream);
 }
 
-unsigned int fwd_read_and_clear_status() {
-  unsigned int v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_fwd_status, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_fwd_status, &zero, sizeof(zero));
-  return v;
+cudaError_t fwd_status_word(unsigned int** p) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_fwd_status);
 }
 
 }  // namespace fattn

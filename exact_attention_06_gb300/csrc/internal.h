@@ -89,7 +89,8 @@ struct FwdLaunch {
   FwdAux aux;
 };
 cudaError_t launch_fwd(const FwdLaunch& a, cudaStream_t stream);
-unsigned int fwd_read_and_clear_status();
+// The current device's address of the word in which the kernels of fa_fwd.cu raise status bits; likewise below.
+cudaError_t fwd_status_word(unsigned int** p);
 
 // Split-KV decode launch description.  The tensor maps describe k, v as 3-D
 // tensors {d, L, B*H} with 64 x kDecodeStageKeys boxes and 128-byte swizzle.
@@ -119,7 +120,7 @@ constexpr int kDecodeCtasPerSm = 2;   // resident split CTAs per SM (shared-memo
 cudaError_t launch_decode_split(const DecodeLaunch& a, cudaStream_t stream);
 cudaError_t launch_combine(const float* u_part, const float* m_part, const float* l_part, void* o, float* lse,
                            int R, int S, int d, int o_fp32, cudaStream_t stream);
-unsigned int decode_read_and_clear_status();
+cudaError_t decode_status_word(unsigned int** p);
 
 // Cross attention over at most kCrossShortKeys keys: R rows of each of BH key heads, `tiles` tiles of 128 a block.
 constexpr int kCrossShortKeys = 128;
@@ -137,7 +138,7 @@ struct CrossShortLaunch {
   int BH, d;
 };
 cudaError_t launch_cross_short(const CrossShortLaunch& l, cudaStream_t stream);
-unsigned int cross_short_read_and_clear_status();
+cudaError_t cross_short_status_word(unsigned int** p);
 
 // Cross attention of few rows: R <= kCrossRowsMax query rows of each of BH key heads against the first
 // kv_lens[bh / kv_heads] (null: Nk) of its keys, shared out over S blocks.  u_part == null: the S <= 8
@@ -164,7 +165,7 @@ struct CrossRowsLaunch {
   int BH, d;
 };
 cudaError_t launch_cross_rows(const CrossRowsLaunch& a, cudaStream_t stream);
-unsigned int cross_rows_read_and_clear_status();
+cudaError_t cross_rows_status_word(unsigned int** p);
 
 // Backward launch description: q, k, v, dO as 3-D tensors {d, N, B*H} with
 // 64 x 128 boxes and 128-byte swizzle; delta is the caller's [B*H, N] fp32 scratch.
@@ -203,16 +204,16 @@ struct BwdLaunch {
 };
 cudaError_t launch_bwd(const BwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_cross_bwd(const BwdLaunch& a, cudaStream_t stream);
-unsigned int cross_bwd_read_and_clear_status();
+cudaError_t cross_bwd_status_word(unsigned int** p);
 // out (and out2, from the S sums after those) = the sum of S partial sums of n elements each
 cudaError_t launch_cross_sum(const float* part, void* out, void* out2, long long n, int S, int fp32, cudaStream_t stream);
 // The backward over at most kCrossShortKeys keys (tk, tv: boxes of 64 rows for up to 64 keys), q_tiles and kv_splits as
 // above.
 cudaError_t launch_cross_bwd_short(const BwdLaunch& a, cudaStream_t stream);
-unsigned int cross_bwd_short_read_and_clear_status();
+cudaError_t cross_bwd_short_status_word(unsigned int** p);
 // delta[r] = rowsum(o_r * dout_r) of `rows` bf16 rows of d
 cudaError_t launch_delta(const void* o, const void* dout, float* delta, long long rows, int d, cudaStream_t stream);
-unsigned int bwd_read_and_clear_status();
+cudaError_t bwd_status_word(unsigned int** p);
 
 // E4M3 block quantization: x [BH, N, d] bf16 -> codes [BH, N, d] bytes, scales [BH, ceil(N/128)].
 cudaError_t launch_quant_e4m3(const void* x, void* codes, float* scales, int BH, int N, int d, cudaStream_t stream);
