@@ -28,14 +28,7 @@ __device__ __forceinline__ bool bwait_all(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, bwait(bar, parity, abort_flag, budget));
 }
 __device__ __forceinline__ void bdrain(uint32_t bar, uint32_t parity, unsigned long long budget) {
-  if (budget < kDrainBudget) budget = kDrainBudget;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (static_cast<unsigned long long>(clock64() - t0) > budget) {
-      atomicOr(&g_bwd_status, kStatusTimeout);
-      return;
-    }
-  }
+  mbar_drain(bar, parity, budget, &g_bwd_status);
 }
 
 // One thread per row: a D-column fp32 tile row in TMEM * scale -> global (fp32), or as bf16 into the

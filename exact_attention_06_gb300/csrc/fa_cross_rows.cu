@@ -109,14 +109,7 @@ __device__ __forceinline__ bool rwait_all(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, budget, &g_rows_status));
 }
 __device__ __forceinline__ void rdrain(uint32_t bar, uint32_t parity, unsigned long long budget) {
-  if (budget < kDrainBudget) budget = kDrainBudget;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (static_cast<unsigned long long>(clock64() - t0) > budget) {
-      atomicOr(&g_rows_status, kStatusTimeout);
-      return;
-    }
-  }
+  mbar_drain(bar, parity, budget, &g_rows_status);
 }
 
 // Block blockIdx.x = key head * S + share.  CLUSTER: the S blocks of a key head are a cluster and write O and lse;

@@ -60,14 +60,7 @@ __device__ __forceinline__ bool swait_all(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, swait(bar, parity, abort_flag, budget));
 }
 __device__ __forceinline__ void sdrain(uint32_t bar, uint32_t parity, unsigned long long budget) {
-  if (budget < kDrainBudget) budget = kDrainBudget;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (static_cast<unsigned long long>(clock64() - t0) > budget) {
-      atomicOr(&g_short_status, kStatusTimeout);
-      return;
-    }
-  }
+  mbar_drain(bar, parity, budget, &g_short_status);
 }
 
 // N scores of this thread's row (raw fp32 bits); those from `valid` on become -inf.

@@ -73,15 +73,7 @@ __device__ __forceinline__ bool dwait_all(uint32_t bar, uint32_t parity, volatil
 }
 
 __device__ __forceinline__ void ddrain_wait(uint32_t bar, uint32_t parity, unsigned long long budget) {
-  // A drain never gets less than the default budget, however short the caller's wait budget is.
-  if (budget < kDrainBudget) budget = kDrainBudget;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (static_cast<unsigned long long>(clock64() - t0) > budget) {
-      atomicOr(&g_dec_status, kStatusTimeout);
-      return;
-    }
-  }
+  mbar_drain(bar, parity, budget, &g_dec_status);
 }
 
 __device__ __forceinline__ float dot8(const uint4& x, const float* q, float acc) {

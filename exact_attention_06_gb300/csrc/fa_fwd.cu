@@ -147,18 +147,8 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
   return __all_sync(0xffffffffu, ok);
 }
 
-// Bounded wait that ignores the abort flag: used to drain in-flight copies
-// and MMAs before the CTA releases its shared memory and TMEM.
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, unsigned long long budget) {
-  // A drain never gets less than the default budget, however short the caller's wait budget is.
-  if (budget < kDrainBudget) budget = kDrainBudget;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (static_cast<unsigned long long>(clock64() - t0) > budget) {
-      atomicOr(&g_fwd_status, kStatusTimeout);
-      return;
-    }
-  }
+  mbar_drain(bar, parity, budget, &g_fwd_status);
 }
 
 // This thread's half of a U_t row (D/2 columns) *= alpha, in one TMEM round trip.

@@ -67,6 +67,20 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// Bounded wait that ignores the abort flag: used to drain in-flight copies and MMAs before the CTA releases (or reuses) its
+// shared memory and TMEM.  It never gets less than the default budget, however short the caller's wait budget is.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, unsigned long long budget,
+                                           unsigned int* status) {
+  if (budget < kDrainBudget) budget = kDrainBudget;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (static_cast<unsigned long long>(clock64() - t0) > budget) {
+      atomicOr(status, kStatusTimeout);
+      return;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- block order
 // For a grid (B*H, P) of CTAs dispatched in linear order: the (head, work rank) of this CTA when
 // the heads are cut into ng groups of near-equal size (the first B*H mod ng groups one head
