@@ -31,6 +31,7 @@ import hashlib
 import json
 import math
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -63,37 +64,55 @@ def _peaks():
 
 
 # DRAM bytes per launch (dram__bytes_read.sum + dram__bytes_write.sum) from ncu captures summarised
-# under profiles/, keyed by kernel and workload, valid only while the kernel sources are unchanged.
-_FWD = "def71c075ea239ac85c9d1b1efa3c201806bcb551a1d8758fee3fb49b281d6db"
-_BWD = "d9e547d73ab8a499068ac81cbc23865af85b744a32d660c9953b67ef10a8ba27"
-_DEC = "238a9c1b2ffecb15b22cb24a1544220a197fcbdb2c867899597a0c8e4fa65d64"
+# under profiles/, keyed by kernel and workload, valid only while the kernels' code is unchanged: each source
+# with the digest (_code_digest) of it and all it includes.
+_FWD = "612b84ef8eaac17181b353fc5ae66ca3f857330e5dd29481c052a4b7bdb531a0"
+_BWD = "c6ff0b37c37d4af6feb5634dc39ff5ff3fe9ac504066ecc866c9a1f50ee6e413"
+_DEC = "f5eb7a7cf97578a63327f8468739b0ae62d5bf689a64dc9f5193ba35663904f1"
 NCU_TRAFFIC = {
-    ("fwd_kernel", "ragged"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 558.459e6},
-    ("fwd_kernel", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 263.884e6},
-    ("fwd_kernel_fp8", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 136.213e6},
-    ("fwd_persist_kernel", "prefill"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 50.643e6},
+    ("fwd_kernel", "ragged"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 559.038e6},
+    ("fwd_kernel", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 263.172e6},
+    ("fwd_kernel_fp8", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 136.563e6},
+    ("fwd_persist_kernel", "prefill"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 50.603e6},
     # backward: the dominant kernel (dK/dV) on the causal workload
-    ("bwd_dkdv_kernel", "causal"): {"sources": {"fa_bwd.cu": _BWD}, "bytes": 375.680e6},
+    ("bwd_dkdv_kernel", "causal"): {"sources": {"fa_bwd.cu": _BWD}, "bytes": 372.816e6},
     # the four-shard step: four forward launches over the key shards and the combine, summed
-    ("causal_sharded4", "causal"): {"sources": {"fa_fwd.cu": _FWD, "fa_decode.cu": _DEC}, "bytes": 1108.376e6},
+    ("causal_sharded4", "causal"): {"sources": {"fa_fwd.cu": _FWD, "fa_decode.cu": _DEC}, "bytes": 1108.964e6},
     # decode: captured on the B4 slice (decode_small) and scaled by 16 to B64 (K/V streamed once)
-    ("decode_split_kernel", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2151.001e6},
-    ("decode_split_kernel_paged", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.928e6},
+    ("decode_split_kernel", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.947e6},
+    ("decode_split_kernel_paged", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.934e6},
 }
+SOURCE_DIRS = (os.path.join(ROOT, "exact_attention_06_gb300", "csrc"), os.path.join(ROOT, "include"))
+
+
+def _code_digest(src: str) -> str:
+    """sha256 of a source's code, without comments and spacing, and of every file of this repository that it includes."""
+    found, left = {}, [src]
+    while left:
+        name = left.pop()
+        if name in found:
+            continue
+        path = next((p for p in (os.path.join(d, name) for d in SOURCE_DIRS) if os.path.exists(p)), None)
+        if path is None:
+            raise FileNotFoundError(name)
+        with open(path, encoding="utf-8") as f:
+            code = " ".join(re.sub(r"/\*.*?\*/|//[^\n]*", " ", f.read(), flags=re.S).split())
+        found[name] = code
+        left += re.findall(r'# ?include "([^"]+)"', code)
+    h = hashlib.sha256()
+    for name in sorted(found):
+        h.update(f"{name}\n{found[name]}\n".encode())
+    return h.hexdigest()
 
 
 def _traffic(kernel: str, workload: str):
     rec = NCU_TRAFFIC.get((kernel, workload))
     if rec is None:
         return None
-    for src, sha in rec["sources"].items():
-        try:
-            with open(os.path.join(ROOT, "exact_attention_06_gb300", "csrc", src), "rb") as f:
-                if hashlib.sha256(f.read()).hexdigest() != sha:
-                    return None
-        except OSError:
-            return None
-    return rec["bytes"]
+    try:
+        return rec["bytes"] if all(_code_digest(src) == sha for src, sha in rec["sources"].items()) else None
+    except OSError:
+        return None
 
 
 def _workload_label(w):
