@@ -215,6 +215,19 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _workspace_on(stream, nbytes: int, device):
+    """Scratch that lives as long as the stream's work needs it: allocated on that stream, so that its
+    memory goes to no other stream's tensor while the kernels may still use it.  None: the current stream."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        # A handle that is no pointer: 0 and 1 (cudaStreamLegacy) are the default stream, of which ExternalStream would
+        # make another (of 0 a new one from torch's pool).
+        stream = torch.cuda.default_stream(device) if stream in (0, 1) else torch.cuda.ExternalStream(stream, device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def fa_fwd_workspace_bytes(B: int, H: int, N: int, d: int, causal: bool = False) -> int:
     """Scratch bytes of the key split of fa_fwd_ex's last round on the current device (0: no key split)."""
     return int(lib().fa_fwd_workspace_bytes(B, H, N, d, int(bool(causal))))
@@ -321,7 +334,7 @@ def fa_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale: float, causal: bool = False
     for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         _need("fa_bwd", name, t, (dq.dtype,) if dq.dtype in _OUT else _OUT, (B, H, N, d))
     if workspace is None:
-        workspace = torch.empty(fa_bwd_workspace_bytes(B, H, N), dtype=torch.uint8, device=q.device)
+        workspace = _workspace_on(stream, fa_bwd_workspace_bytes(B, H, N), q.device)
     _need("fa_bwd", "workspace", workspace, _U8)
     ws_bytes = workspace.numel() * workspace.element_size()
     grad_fp32 = int(dq.dtype == torch.float32)
@@ -397,8 +410,8 @@ def fa_decode_paged(q, k_pages, v_pages, block_table, seq_lens, o, lse, scale: f
     _need("fa_decode_paged", "o", o, _OUT, (B, H, d))
     _need("fa_decode_paged", "lse", lse, _F32, (B, H))
     if workspace is None:
-        workspace = torch.empty(fa_decode_paged_workspace_bytes(B, H, max_seq_len, d, page_size, max_pages, splits),
-                                dtype=torch.uint8, device=q.device)
+        nbytes = fa_decode_paged_workspace_bytes(B, H, max_seq_len, d, page_size, max_pages, splits)
+        workspace = _workspace_on(stream, nbytes, q.device)
     _need("fa_decode_paged", "workspace", workspace, _U8)
     ws_bytes = workspace.numel() * workspace.element_size()
     opts = FaDecodeOpts(int(o.dtype == torch.float32), int(wait_budget_cycles))
@@ -439,17 +452,6 @@ def _shape4(func: str, name: str, t):
 
 def _refused(func: str):
     raise FattnError(FA_ERR_INVALID_ARG, func, "an argument has the wrong type, or a size that does not fit an int")
-
-
-def _workspace_on(stream, nbytes: int, device):
-    """Scratch that lives as long as the stream's work needs it: allocated on that stream, so that its
-    memory goes to no other stream's tensor while the kernels may still use it."""
-    if not hasattr(stream, "cuda_stream"):
-        # A handle that is no pointer: 0 and 1 (cudaStreamLegacy) are the default stream, of which ExternalStream would
-        # make another (of 0 a new one from torch's pool).
-        stream = torch.cuda.default_stream(device) if stream in (0, 1) else torch.cuda.ExternalStream(stream, device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _handle(stream):

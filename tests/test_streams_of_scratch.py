@@ -84,3 +84,53 @@ def test_a_call_with_scratch_of_its_own_keeps_to_its_stream(kind):
     assert kind in ("none", "default", "legacy") or new
     assert fattn.fa_get_status() == fattn.FA_OK
     assert all(torch.equal(x, y) for x, y in zip(*grads))
+
+
+class _Library:
+    """Every size is 512 bytes and every call succeeds."""
+
+    def __getattr__(self, name):
+        return lambda *args: 512 if name.endswith("bytes") else 0
+
+
+@pytest.mark.parametrize("handle,owner", [(0, 0), (0x7f00deadbe00, 0x7f00deadbe00), (None, None)])
+@pytest.mark.parametrize("call", ["fa_bwd", "fa_decode_paged"])
+def test_the_other_calls_allocate_on_their_stream_too(monkeypatch, call, handle, owner):
+    seen = _Recorder(monkeypatch)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: type("Stream", (), {"cuda_stream": 0})())
+    monkeypatch.setattr(fattn, "_need", lambda *args: None)
+    monkeypatch.setattr(fattn, "lib", _Library)
+    x, lse = torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16), torch.zeros(1, 2, 64)
+    if call == "fa_bwd":
+        fattn.fa_bwd(x, x, x, x, x, lse, x, x, x, 0.1, stream=handle)
+    else:
+        table = torch.zeros(1, 1, dtype=torch.int32)
+        fattn.fa_decode_paged(x[:, :, 0], x, x, table, table[0], x[:, :, 0], lse[:, :, 0], 0.1, 64, stream=handle)
+    assert seen.entered == ([] if owner is None else [owner])
+
+
+@pytest.mark.gpu
+def test_a_backward_on_a_side_stream_keeps_its_scratch():
+    """fa_bwd's row sums, on a side stream behind a long wait: a tensor that the current stream allocates and fills after
+    the call must not lie in them."""
+    ensure_built()
+    B, H, N, d = 2, 8, 4096, 64
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q, k, v, do = (torch.randn(B, H, N, d, generator=g, device="cuda").bfloat16() for _ in range(4))
+    o, lse = torch.empty_like(q), torch.empty(B, H, N, device="cuda")
+    fattn.fa_fwd(q, k, v, o, lse, 0.1)
+    want, got = ([torch.empty_like(q) for _ in range(3)] for _ in range(2))
+    fattn.fa_bwd(q, k, v, o, do, lse, *want, 0.1)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    n = fattn.fa_bwd_workspace_bytes(B, H, N)
+    for stream in (side, side.cuda_stream):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # some 10 ms
+        fattn.fa_bwd(q, k, v, o, do, lse, *got, 0.1, stream=stream)
+        other = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert fattn.fa_get_status() == fattn.FA_OK
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+        assert all((t == 255).all() for t in other)
+        del other
