@@ -448,8 +448,19 @@ struct CrossBwdPlan {
 //           4 x 16/4, 2048 x 1500      199   196   191   195   220   236   (195)
 //   d = 128, 2 x 16, 8192 x 154        166   159   155   158   153   158   (164)
 //                    4096 x 2048       403   397   414   439   479   438   (396)
-// Where the sequences have lengths of their own (ragged), blocks end less evenly still: at most 24 key tiles a block
-// (4 x 16/4, 2048 x up to 1500, with the forward: 229 with two tiles, 232 with three, 233 with four).
+// Where kv_lens is given (ragged), blocks end less evenly still, and a block takes at most 24 key tiles.  The lengths are
+// device data, so the rule cannot see that they are all alike.  Measured (the whole backward, us, with the rule / without):
+//                                      lengths from 1 to Nk   from Nk/2 to Nk   all Nk
+//   d = 64,  4 x 32/8, 1024 x 640           70 / 82               90 / 90        95 / 91
+//            8 x 16/4, 1000 x 577           67 / 81               87 / 89        94 / 92
+//            8 x 8/2,  4096 x 1024         192 / 196             214 / 220      250 / 253
+//            4 x 16/4, 2048 x 1500          97 / 95              167 / 171      199 / 191
+//            2 x 16,   4096 x 2048          95 / 87              231 / 229      263 / 249
+//   d = 128, 4 x 32/8, 1024 x 640          118 / 154             149 / 153      159 / 157
+//            8 x 16/4, 1000 x 577          112 / 141             145 / 153      159 / 158
+//            8 x 8/2,  4096 x 1024         317 / 334             348 / 373      416 / 413
+//            4 x 16/4, 2048 x 1500         158 / 159             269 / 275      312 / 305
+//            2 x 16,   4096 x 2048         142 / 141             357 / 363      407 / 402
 int dq_own_tiles(const CrossBwdPlan& p, long long bh, int qt, int kt, int d, int sms, bool ragged) {
   const double kv_step = d == 64 ? 1.16 : 1.8, kv_fixed = 3.5;
   const double q_step = d == 64 ? 0.87 : 1.34, q_tile = d == 64 ? 0.9 : 2.5, q_fixed = 3.0;

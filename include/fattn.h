@@ -17,9 +17,9 @@
  * Conventions shared by every entry point
  *   - Device pointers only (memory the caller allocated with the CUDA runtime
  *     on the current device).  The library allocates nothing, frees nothing
- *     and keeps no state beyond a cached per-device query (arch, SM count),
- *     a per-device status word read by fa_get_status() and the fixed scratch
- *     array of fa_decode_splitkv_noalloc.
+ *     and keeps no state beyond cached per-device queries (arch, SM count,
+ *     addresses), the per-device status words taken by fa_get_status() and the
+ *     fixed scratch array of fa_decode_splitkv_noalloc.
  *   - All tensors are contiguous, row-major in the head dimension d.
  *   - `stream` is a cudaStream_t (CUstream) handle; NULL is the legacy
  *     default stream.  Every call is asynchronous on that stream.
@@ -400,8 +400,9 @@ fa_status_t fa_bwd_ex(const void* q, const void* k, const void* v, const void* o
  * Cross attention: queries of a decoder against an encoder's states, whose count differs from the
  * queries' and from sequence to sequence (the scaled-dot-product interface takes k and v of another
  * length than q: xuesongtap §6).  Not causal.  Query heads may share key heads: query head h reads
- * key head h / (Hq / Hkv).  With Nq = 1 it is the single-token form: the same call, its keys cut
- * into ranges whose partials the combine kernel joins.
+ * key head h / (Hq / Hkv).  With Nq = 1 it is the single-token form, by the same call: where a key
+ * head has few query rows, up to eight blocks (a thread-block cluster) share its keys and join their
+ * partials themselves.
  *
  *   q         [B, Hq, Nq, d] bf16, 16-byte aligned.
  *   k, v      [B, Hkv, Nk, d] bf16, 16-byte aligned.  Hq a multiple of Hkv.
@@ -418,15 +419,17 @@ typedef struct {
   unsigned long long wait_budget_cycles; /* per-wait budget in SM cycles, as in fa_fwd_opts (0 = default) */
 } fa_cross_opts;
 
-/* Scratch bytes with which fa_cross_fwd cuts the keys into ranges on the current device, so that
- * few query rows still fill the SMs; 0 when it would not cut them (or for invalid sizes, or
- * without a device). */
+/* Scratch bytes for the partials of fa_cross_fwd where it cuts the keys into ranges that a second
+ * kernel joins, so that few query rows still fill the SMs: more than eight ranges of a few rows, or
+ * ranges of many rows' long keys.  0 when the call leaves no partials (keys uncut, or shared within
+ * a cluster), for invalid sizes, or without a device. */
 size_t fa_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 
 /* fa_cross_fwd -- workspace: caller-owned device scratch of fa_cross_workspace_bytes() bytes,
- * 256-byte aligned (FA_ERR_WORKSPACE if smaller), or NULL: one kernel, the keys uncut.  O and lse
- * are the same function of the inputs either way, up to rounding order.  A workspace serves one call at
- * a time (calls that overlap on the GPU need one each).  opts may be NULL. */
+ * 256-byte aligned (FA_ERR_WORKSPACE if smaller), or NULL: one kernel without partials (the keys of a
+ * few rows may still be shared within a cluster).  O and lse are the same function of the inputs either
+ * way, up to rounding order.  A workspace serves one call at a time (calls that overlap on the GPU need
+ * one each).  opts may be NULL. */
 fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int* kv_lens, void* o, float* lse,
                          int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, void* workspace,
                          size_t ws_bytes, void* stream, const fa_cross_opts* opts);
@@ -493,8 +496,8 @@ fa_status_t fa_rope_axes(const void* q, const void* k, const int* pos, void* q_o
  *   seq_lens   [B] int32: keys that sequence b had before; its token t becomes key seq_lens[b] + t.
  *   new_lens   [B] int32 or NULL: tokens of sequence b in this call; those from new_lens[b] on are
  *              padding, for which nothing is written (not to q_out either).
- *   A token whose key has no page (a negative length, a key past max_pages * page_size, an id
- *   outside [0, num_pages)) is not written to the pools.  page_size as for fa_decode_paged; Hk >= 1.
+ *   A token whose key has no page (seq_lens[b] + t negative, or at or past max_pages * page_size, or
+ *   an id outside [0, num_pages)) is not written to the pools.  page_size as for fa_decode_paged; Hk >= 1.
  *   The pools are written only at the new tokens' rows; two tokens of one call must not share a row.
  */
 fa_status_t fa_rope_axes_paged(const void* q, const void* k, const void* v, const int* pos, void* q_out,
@@ -504,9 +507,10 @@ fa_status_t fa_rope_axes_paged(const void* q, const void* k, const void* v, cons
 
 /*
  * fa_get_status -- synchronise `stream`, then read and clear the current
- * device's kernel status word.  Returns FA_ERR_TIMEOUT if any kernel of this
- * library ran out of its wait budget since the last call, FA_ERR_CUDA if the
- * synchronisation itself failed, else FA_OK.
+ * device's kernel status words (by a small kernel and a copy on `stream`, and
+ * a second synchronisation).  Returns FA_ERR_TIMEOUT if any kernel of this
+ * library ran out of its wait budget since the last call, FA_ERR_CUDA if a
+ * synchronisation, the kernel or the copy failed, else FA_OK.
  */
 fa_status_t fa_get_status(void* stream);
 

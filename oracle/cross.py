@@ -50,8 +50,8 @@ def cross_attention(q, k, v, scale, kv_lens=None):
 
 def cross_backward(q, k, v, do, scale, kv_lens=None, rel=0.0, o_err=None):
     """dQ, dK, dV, and bounds on what an implementation may be off by whose P and dS are each off by
-    ``rel`` of themselves, whose score, dP and row sums are off by ``rel`` / 16 of the sums of their
-    terms' absolute values, and whose O is off by ``o_err``."""
+    ``rel`` of themselves, whose dP - D is off by ``rel`` / 16 of itself (P's share of it) and by ``rel`` / 1024
+    of the sums of dP's and D's terms' absolute values, and whose O is off by ``o_err``."""
     q, k, v, do = _f64(q), _f64(k), _f64(v), _f64(do)
     B, Hq, Nq, d = q.shape
     G, Nk = Hq // k.shape[1], k.shape[2]
