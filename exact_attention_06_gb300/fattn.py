@@ -223,7 +223,8 @@ def _workspace_on(stream, nbytes: int, device):
     if not hasattr(stream, "cuda_stream"):
         # A handle that is no pointer: 0 and 1 (cudaStreamLegacy) are the default stream, of which ExternalStream would
         # make another (of 0 a new one from torch's pool).
-        stream = torch.cuda.default_stream(device) if stream in (0, 1) else torch.cuda.ExternalStream(stream, device)
+        handle = int(stream)
+        stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device)
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 

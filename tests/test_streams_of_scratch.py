@@ -134,3 +134,12 @@ def test_a_backward_on_a_side_stream_keeps_its_scratch():
         assert all(torch.equal(x, y) for x, y in zip(want, got))
         assert all((t == 255).all() for t in other)
         del other
+
+
+@pytest.mark.parametrize("handle,owner", [(0, 0), (1, 0), (0x7f00deadbe00, 0x7f00deadbe00)])
+def test_a_handle_may_be_an_object_that_is_a_number(monkeypatch, handle, owner):
+    """(fa_bwd and fa_decode_paged take whatever int() does.)"""
+    seen = _Recorder(monkeypatch)
+    number = type("Handle", (), {"__int__": lambda self: handle})()
+    fattn._workspace_on(number, 512, "cpu")
+    assert seen.entered == [owner]
