@@ -28,6 +28,12 @@
  *     exception crosses this boundary.  There is no CPU fallback and no
  *     other backend: an unsupported request is an error.
  *   - Supported head dimensions: d = 64 and d = 128 (the FP8 forward: 128).
+ *   - Scaled scores: below 2^29 in magnitude.  An exponent is the difference
+ *     of a score and its row's maximum, both times log2(e), of which the
+ *     maximum is rounded to fp32: by up to 2^-24 of it, in all the row's
+ *     exponents alike, so it cancels in O and lse -- until, from 2^31 on, that
+ *     alone takes 2^x out of fp32's range (O NaN or 0).  Gradients start from
+ *     the fp32 lse, whose rounding does not cancel: P is off by 2^-23 |lse|.
  *   - Device: compute capability 10.3 (GB300).  Anything else gives
  *     FA_ERR_ARCH.
  */
