@@ -27,7 +27,8 @@ CALLS = os.path.join(PKG, "_calls.so")
 CALLS_SRC = os.path.join(CSRC, "py_calls.cpp")
 CALLS_STAMP = os.path.join(BUILD, "_calls.stamp")  # what the module was built for and with
 SOURCES = ["fa_fwd.cu", "fa_bwd.cu", "fa_cross_bwd.cu", "fa_cross_bwd_short.cu", "fa_cross_rows.cu", "fa_cross_short.cu",
-           "fa_decode.cu", "fa_quant.cu", "fa_rope.cu", "fattn_host.cu"]
+           "fa_decode.cu", "fa_quant.cu", "fa_rope.cu", "fa_window_fwd.cu", "fa_window_bwd.cu", "fa_norm_rope.cu",
+           "fa_pages.cu", "fattn_host.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 

@@ -1,5 +1,6 @@
 // Cross attention of few query rows (fa_cross_fwd with at most 32 rows per key head, or 16 over at most 128
-// keys: a decode step and its shared heads), for sm_103a.
+// keys: a decode step and its shared heads), and the decode step over a paged cache in which a token sees a sliding
+// window and sinks (fa_window_decode_paged), for sm_103a.
 //
 // Such a call reads each key head's K and V once for 4 * rows * d flops a key: it is bound by HBM, and
 // what counts is bytes in flight and a short path from the last byte to the output.  A 128-row
@@ -18,10 +19,17 @@
 //
 // Padding.  Scores behind the sequence are replaced by -inf; V's words behind it are cleared in the
 // fragments, so that 0 times what the padding holds never reaches U.
+//
+// Paged.  A stage is 64 keys of one page (page sizes are multiples of 64).  A sequence's stages are those of the sinks
+// before its window and those from the window's first key on; nothing between them is read, neither table nor
+// pages.  The producer's lanes look up the pages of 32 stages at once, a batch ahead.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "window.cuh"
 
 namespace fattn {
 
@@ -114,7 +122,8 @@ __device__ __forceinline__ void rdrain(uint32_t bar, uint32_t parity, unsigned l
 
 // Block blockIdx.x = key head * S + share.  CLUSTER: the S blocks of a key head are a cluster and write O and lse;
 // otherwise they write partial slots (rows, S) for the combine kernel.
-template <int D, int RB, bool CLUSTER>
+// PAGED: the keys of a sequence are in pages, and those before its window but for the sinks are hidden.
+template <int D, int RB, bool CLUSTER, bool PAGED>
 __global__ void __launch_bounds__(RowsCfg<D, RB>::THREADS, RowsCfg<D, RB>::PER_SM)
     cross_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                       const CrossRowsArgs a) {
@@ -145,24 +154,51 @@ __global__ void __launch_bounds__(RowsCfg<D, RB>::THREADS, RowsCfg<D, RB>::PER_S
   }
   grid_dep_wait();  // every global access below comes after the previous kernel in the stream
   const int len = a.kv_lens ? min(max(a.kv_lens[bh / a.kv_heads], 0), a.Nk) : a.Nk;
-  const long long stages = (static_cast<long long>(len) + kSk - 1) / kSk;
+  // PAGED: keys from lo on and below a.sinks; the sequence's stages are ns of the sinks, then those from w0 on
+  const int lo = PAGED ? max(len - a.window, 0) : 0, w0 = lo / kSk;
+  const int ns = PAGED ? min((min(a.sinks, lo) + kSk - 1) / kSk, w0) : 0;
+  auto key_of = [&](int st) { return (PAGED && st >= ns ? st - ns + w0 : st) * kSk; };
+  const long long stages = (static_cast<long long>(len) + kSk - 1) / kSk - w0 + ns;
   const int st0 = static_cast<int>(stages * sp / S), n_st = static_cast<int>(stages * (sp + 1) / S) - st0;
   __syncthreads();
 
   if (warp == C::NW) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int issued = 0;
-      for (int i = 0; i < n_st; ++i) {
-        const int s = i % kSt;
-        if (i >= kSt && !mbar_wait(BAR(C::B_EMPTY + s), ((i / kSt) - 1) & 1, abort_flag, a.budget, &g_rows_status)) break;
-        const int key = (st0 + i) * kSk;
-        mbar_arrive_expect_tx(BAR(C::B_KF + s), C::TB);
-        for (int h = 0; h < C::NH; ++h) tma_load_3d(sK + s * C::TB + h * C::BOX, &tk, BAR(C::B_KF + s), h * 64, key, bh);
-        mbar_arrive_expect_tx(BAR(C::B_VF + s), C::TB);
-        for (int h = 0; h < C::NH; ++h) tma_load_3d(sV + s * C::TB + h * C::BOX, &tv, BAR(C::B_VF + s), h * 64, key, bh);
-        issued = i + 1;
+    int issued = 0;
+    auto stage = [&](int i, int row, int z) {  // the block's i-th stage: rows of plane z of the tensor maps
+      const int s = i % kSt;
+      if (i >= kSt && !mbar_wait(BAR(C::B_EMPTY + s), ((i / kSt) - 1) & 1, abort_flag, a.budget, &g_rows_status))
+        return false;
+      mbar_arrive_expect_tx(BAR(C::B_KF + s), C::TB);
+      for (int h = 0; h < C::NH; ++h) tma_load_3d(sK + s * C::TB + h * C::BOX, &tk, BAR(C::B_KF + s), h * 64, row, z);
+      mbar_arrive_expect_tx(BAR(C::B_VF + s), C::TB);
+      for (int h = 0; h < C::NH; ++h) tma_load_3d(sV + s * C::TB + h * C::BOX, &tv, BAR(C::B_VF + s), h * 64, row, z);
+      issued = i + 1;
+      return true;
+    };
+    if constexpr (PAGED) {
+      const int* table = a.block_table + static_cast<size_t>(bh / a.kv_heads) * a.max_pages;
+      const int head = bh % a.kv_heads;
+      auto plane = [&](int i) {  // of the pools [pages * heads]; -1: outside, where rows read as zeros
+        if (i >= n_st) return -1;
+        const int id = table[key_of(st0 + i) / a.page_size];
+        return id >= 0 && id < a.num_pages ? id * a.kv_heads + head : -1;
+      };
+      bool ok = true;
+      int next = plane(lane);
+      for (int i0 = 0; i0 < n_st; i0 += 32) {
+        const int mine = next;
+        next = plane(i0 + 32 + lane);
+        for (int i = i0; i < min(i0 + 32, n_st); ++i) {
+          const int z = __shfl_sync(0xffffffffu, mine, i - i0);
+          if (lane == 0 && ok) ok = stage(i, key_of(st0 + i) % a.page_size, z);
+        }
       }
+    } else if (lane == 0) {
+      for (int i = 0; i < n_st && stage(i, (st0 + i) * kSk, bh); ++i) {
+      }
+    }
+    if (lane == 0) {
       for (int i = max(issued - kSt, 0); i < issued; ++i) {  // every copy lands before the ring is reused
         rdrain(BAR(C::B_KF + i % kSt), (i / kSt) & 1, a.budget);
         rdrain(BAR(C::B_VF + i % kSt), (i / kSt) & 1, a.budget);
@@ -218,14 +254,18 @@ __global__ void __launch_bounds__(RowsCfg<D, RB>::THREADS, RowsCfg<D, RB>::PER_S
           mma16816(c[n], qf[kk + 1][0], qf[kk + 1][1], qf[kk + 1][2], qf[kk + 1][3], b[2], b[3]);
         }
       }
-      const int left = len - (st0 + i) * kSk - 16 * kw;  // keys of the sequence from the warp's first on
-      const bool tail = left < 16;
+      // the warp's 16 keys that count, from its lane's first on: bits 0, 1, 8, 9
+      const int key0 = key_of(st0 + i) + 16 * kw;
+      uint32_t seen = low_bits(len - key0);
+      if constexpr (PAGED) seen = visible_keys(key0, len - 1, a.window, a.sinks);
+      const bool tail = (seen & 0xffffu) != 0xffffu;
+      seen >>= 2 * t;
       if (tail) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            if (8 * n + 2 * t + j >= left) c[n][j] = c[n][2 + j] = -INFINITY;
+            if (!(seen >> (8 * n + j) & 1u)) c[n][j] = c[n][2 + j] = -INFINITY;
       }
       float x0 = fmaxf(fmaxf(c[0][0], c[0][1]), fmaxf(c[1][0], c[1][1]));
       float x1 = fmaxf(fmaxf(c[0][2], c[0][3]), fmaxf(c[1][2], c[1][3]));
@@ -262,9 +302,9 @@ __global__ void __launch_bounds__(RowsCfg<D, RB>::THREADS, RowsCfg<D, RB>::PER_S
       }
       if (!rwait_all(BAR(C::B_VF + s), par, abort_flag, a.budget)) break;
       const uint32_t vb = sV + s * C::TB + vrow;
-      // keys 2t, 2t + 1 (and 8 more) of a V fragment word: the halves behind the sequence are cleared
-      const uint32_t keep0 = (2 * t < left ? 0xFFFFu : 0u) | (2 * t + 1 < left ? 0xFFFF0000u : 0u);
-      const uint32_t keep1 = (8 + 2 * t < left ? 0xFFFFu : 0u) | (9 + 2 * t < left ? 0xFFFF0000u : 0u);
+      // keys 2t, 2t + 1 (and 8 more) of a V fragment word: the halves of hidden keys are cleared
+      const uint32_t keep0 = (seen & 1u ? 0xFFFFu : 0u) | (seen & 2u ? 0xFFFF0000u : 0u);
+      const uint32_t keep1 = (seen & 256u ? 0xFFFFu : 0u) | (seen & 512u ? 0xFFFF0000u : 0u);
 #pragma unroll
       for (int n = 0; n < D / 8; n += 2) {
         const uint32_t ch = static_cast<uint32_t>(n) + vchunk;
@@ -382,11 +422,11 @@ __global__ void __launch_bounds__(RowsCfg<D, RB>::THREADS, RowsCfg<D, RB>::PER_S
 #undef BAR
 }
 
-template <int D, int RB, bool CLUSTER>
+template <int D, int RB, bool CLUSTER, bool PAGED>
 cudaError_t launch_t(const CrossRowsLaunch& l, cudaStream_t stream) {
   using C = RowsCfg<D, RB>;
   const CrossRowsArgs& a = l.args;
-  auto kern = cross_rows_kernel<D, RB, CLUSTER>;
+  auto kern = cross_rows_kernel<D, RB, CLUSTER, PAGED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2]{};
@@ -408,13 +448,20 @@ cudaError_t launch_t(const CrossRowsLaunch& l, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_cross_rows(const CrossRowsLaunch& a, cudaStream_t stream) {
-  const bool two = a.args.R > 16, cluster = a.args.u_part == nullptr;
-  if (a.d == 64) {
-    if (cluster) return two ? launch_t<64, 2, true>(a, stream) : launch_t<64, 1, true>(a, stream);
-    return two ? launch_t<64, 2, false>(a, stream) : launch_t<64, 1, false>(a, stream);
-  }
-  if (cluster) return two ? launch_t<128, 2, true>(a, stream) : launch_t<128, 1, true>(a, stream);
-  return two ? launch_t<128, 2, false>(a, stream) : launch_t<128, 1, false>(a, stream);
+  auto go = [&](auto dim, auto paged) {
+    constexpr int D = decltype(dim)::value;
+    constexpr bool P = decltype(paged)::value;
+    const bool two = a.args.R > 16;
+    if (a.args.u_part == nullptr) return two ? launch_t<D, 2, true, P>(a, stream) : launch_t<D, 1, true, P>(a, stream);
+    return two ? launch_t<D, 2, false, P>(a, stream) : launch_t<D, 1, false, P>(a, stream);
+  };
+  using std::integral_constant;
+  using std::bool_constant;
+  if (a.args.block_table)
+    return a.d == 64 ? go(integral_constant<int, 64>{}, bool_constant<true>{})
+                     : go(integral_constant<int, 128>{}, bool_constant<true>{});
+  return a.d == 64 ? go(integral_constant<int, 64>{}, bool_constant<false>{})
+                   : go(integral_constant<int, 128>{}, bool_constant<false>{});
 }
 
 cudaError_t cross_rows_status_word(unsigned int** p) {

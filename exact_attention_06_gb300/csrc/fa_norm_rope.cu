@@ -1,0 +1,354 @@
+// RMS norm of each head's queries and keys and their rotation (fa_rope.cu) in one pass, and its gradient:
+//     r = (mean(x^2) + eps)^(-1/2),   n = x r,   y = R (w n)
+//     g = R^T dy,   h = w g,   dx = r (h - n mean(h n)),   dw = sum over rows of g n
+// with R the rotation of the row's position and w the weights of q or of k.  One rounding to bf16, of y (dx).
+//
+// Bound by memory: 4 bytes an element forward, 6 backward.  A thread holds the 16 elements of 8 pairs of a row (2
+// 16-byte vectors), the d / 16 threads of a row add their squares up by shuffles, and the row's angles serve several
+// heads, as in fa_rope.cu.
+//
+// dw adds up every row of every head.  A block of the backward kernel takes a few heads of many rows, adds in registers,
+// joins its threads through shared memory and leaves one partial sum; a second kernel adds those in a fixed
+// order.  No atomics: the gradients are bitwise repeatable.
+#include "rope_common.cuh"
+
+namespace fattn {
+namespace {
+
+constexpr int kElems = 2 * kPairs;  // elements per thread and row
+
+template <int D>
+__device__ __forceinline__ void load_weights(const NormRopeLaunch& a, float (*w)[D]) {
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    const void* src = i < D ? a.q_weight : a.k_weight;
+    float v = 1.f;
+    if (src)
+      v = a.weight_fp32 ? static_cast<const float*>(src)[i % D]
+                        : __bfloat162float(static_cast<const __nv_bfloat16*>(src)[i % D]);
+    w[i / D][i % D] = v;
+  }
+}
+
+// The sum of x over the threads of the row (TPR of them, side by side).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float x, unsigned int mask) {
+#pragma unroll
+  for (int o = TPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(mask, x, o);
+  return x;
+}
+// The lanes of this thread's row.
+template <int TPR>
+__device__ __forceinline__ unsigned int row_mask() {
+  return ((1u << TPR) - 1u) << (threadIdx.x & 31 & ~(TPR - 1));
+}
+
+__device__ __forceinline__ void unpack(const uint4& a, const uint4& b, float (&f)[kElems]) {
+  const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    f[2 * i] = bf16lo(x[i]);
+    f[2 * i + 1] = bf16hi(x[i]);
+  }
+}
+__device__ __forceinline__ void pack(const float (&f)[kElems], uint4& a, uint4& b) {
+  a = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+  b = make_uint4(pack_bf16(f[8], f[9]), pack_bf16(f[10], f[11]), pack_bf16(f[12], f[13]), pack_bf16(f[14], f[15]));
+}
+
+// Turn the thread's 8 pairs: elements (2i, 2i + 1), or (i, i + 8).
+template <bool INTER>
+__device__ __forceinline__ void turn(float (&f)[kElems], const float (&c)[kPairs], const float (&s)[kPairs]) {
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    float &a = f[INTER ? 2 * i : i], &b = f[INTER ? 2 * i + 1 : i + kPairs];
+    const float x = a, y = b;
+    a = fmaf(x, c[i], -y * s[i]);
+    b = fmaf(x, s[i], y * c[i]);
+  }
+}
+
+// The thread's 16 weights (w: a row of D in shared memory).
+__device__ __forceinline__ void weights_of(const float* w, int e0, int e1, float (&f)[kElems]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    reinterpret_cast<float4*>(f)[i] = reinterpret_cast<const float4*>(w + e0)[i];
+    reinterpret_cast<float4*>(f)[2 + i] = reinterpret_cast<const float4*>(w + e1)[i];
+  }
+}
+
+__device__ __forceinline__ void positions(const RopeLaunch& a, long long rows, long long r, int (&p)[FA_ROPE_MAX_AXES]) {
+#pragma unroll
+  for (int k = 0; k < FA_ROPE_MAX_AXES; ++k) p[k] = k < a.plan.n_axes ? a.pos[k * rows + r] : 0;
+}
+
+// Heads 0 .. Hq - 1 are q's, the next Hk k's; PAGED: k's go to the pools, as do v's, the last Hk, as they are.
+template <int D, bool INTER, bool PAGED>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeLaunch n) {
+  using C = RopeCfg<D>;
+  const RopeLaunch& a = n.r;
+  __shared__ unsigned long long turns[D / 2];
+  __shared__ unsigned char axis[D / 2];
+  __shared__ __align__(16) float w[2][D];
+  grid_dep_launch();
+  grid_dep_wait();
+  load_weights<D>(n, w);
+  load_tables(a.plan, D, turns, axis);
+  const int t = threadIdx.x % C::TPR;
+  const long long rows = static_cast<long long>(a.B) * a.N;
+  const long long r = static_cast<long long>(blockIdx.x) * C::ROWS + threadIdx.x / C::TPR;
+  if (r >= rows) return;
+  const long long b = r / a.N, tok = r - b * a.N;
+  if (PAGED && a.new_lens && tok >= a.new_lens[b]) return;  // a padded token: nothing of it is written
+  const unsigned int mask = row_mask<C::TPR>();
+  // The token's row in the pools (of head 0), or none.
+  bool has_page = false;
+  long long page_row = 0;
+  if constexpr (PAGED) {
+    const long long slot = n.slots[r], page = slot >= 0 ? slot / a.page_size : a.num_pages;
+    has_page = page < a.num_pages;
+    page_row = page * a.Hk * a.page_size + (slot - page * a.page_size);
+  }
+  int p[FA_ROPE_MAX_AXES];
+  positions(a, rows, r, p);
+  float c[kPairs], s[kPairs];
+  angles(turns, axis, t, p, 1.f, c, s);
+  const int heads = a.Hq + a.Hk * (PAGED ? 2 : 1);
+  const int h0 = static_cast<int>(blockIdx.y) * a.heads, h1 = min(h0 + a.heads, heads);
+  const int e0 = first_vec<D, INTER>(t), e1 = e0 + second_vec<D, INTER>();
+  for (int h = h0; h < h1; h += kUnroll) {
+    uint4 x0[kUnroll], x1[kUnroll];
+    __nv_bfloat16* dst[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int hh = min(h + i, h1 - 1);
+      const __nv_bfloat16* src;
+      if (hh < a.Hq) {
+        const long long off = ((b * a.Hq + hh) * a.N + tok) * D;
+        src = a.q + off;
+        dst[i] = a.q_out + off;
+      } else {
+        const bool is_v = PAGED && hh >= a.Hq + a.Hk;
+        const int hk = hh - a.Hq - (is_v ? a.Hk : 0);
+        const long long off = ((b * a.Hk + hk) * a.N + tok) * D;
+        src = (is_v ? a.v : a.k) + off;
+        if constexpr (PAGED)
+          dst[i] = has_page ? (is_v ? a.v_out : a.k_out) + (page_row + static_cast<long long>(hk) * a.page_size) * D
+                            : nullptr;
+        else
+          dst[i] = a.k_out + off;
+      }
+      if (h + i >= h1) dst[i] = nullptr;
+      if (dst[i]) {
+        x0[i] = *reinterpret_cast<const uint4*>(src + e0);
+        x1[i] = *reinterpret_cast<const uint4*>(src + e1);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i)
+      if (dst[i]) {  // (the same for all threads of the row)
+        if (!PAGED || h + i < a.Hq + a.Hk) {
+          float f[kElems], wf[kElems], ss = 0.f;
+          unpack(x0[i], x1[i], f);
+#pragma unroll
+          for (int e = 0; e < kElems; ++e) ss = fmaf(f[e], f[e], ss);
+          const float rs = rsqrtf(fmaf(row_sum<C::TPR>(ss, mask), 1.f / D, n.eps));
+          weights_of(w[h + i < a.Hq ? 0 : 1], e0, e1, wf);
+#pragma unroll
+          for (int e = 0; e < kElems; ++e) f[e] = f[e] * rs * wf[e];
+          turn<INTER>(f, c, s);
+          pack(f, x0[i], x1[i]);
+        }
+        *reinterpret_cast<uint4*>(dst[i] + e0) = x0[i];
+        *reinterpret_cast<uint4*>(dst[i] + e1) = x1[i];
+      }
+  }
+}
+
+// How the backward kernel's blocks share the work: `gx` blocks along the rows for each group of `heads` heads, of
+// which the first yq are q's and the next yk k's.
+struct BwdGrid {
+  int heads, yq, yk, gx;
+};
+
+BwdGrid bwd_grid(int B, int Hq, int Hk, int N, int d, int sms) {
+  BwdGrid g;
+  const long long groups = (static_cast<long long>(B) * N + kThreads / (d / kElems) - 1) / (kThreads / (d / kElems));
+  g.heads = 4;
+  auto ys = [&] {
+    g.yq = (Hq + g.heads - 1) / g.heads;
+    g.yk = (Hk + g.heads - 1) / g.heads;
+    return g.yq + g.yk;
+  };
+  while (ys() && g.heads > 1 && groups * ys() < 4LL * sms) g.heads /= 2;
+  long long gx = 8LL * sms / ys();
+  if (gx < 1) gx = 1;
+  g.gx = static_cast<int>(gx < groups ? gx : groups);
+  return g;
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeLaunch n, const BwdGrid g) {
+  using C = RopeCfg<D>;
+  constexpr int kTwo = 2;  // heads whose loads are in flight together
+  const RopeLaunch& a = n.r;
+  __shared__ unsigned long long turns[D / 2];
+  __shared__ unsigned char axis[D / 2];
+  __shared__ __align__(16) float w[2][D];
+  __shared__ __align__(16) float sum[C::ROWS][D + 4];
+  grid_dep_wait();
+  load_weights<D>(n, w);
+  load_tables(a.plan, D, turns, axis);
+  grid_dep_launch();
+  const int t = threadIdx.x % C::TPR, y = static_cast<int>(blockIdx.y);
+  const bool is_q = y < g.yq;
+  const int H = is_q ? a.Hq : a.Hk, h0 = (is_q ? y : y - g.yq) * g.heads, h1 = min(h0 + g.heads, H);
+  const __nv_bfloat16* const x = is_q ? a.q : a.k;
+  const __nv_bfloat16* const dy = is_q ? n.dq_out : n.dk_out;
+  __nv_bfloat16* const dx = is_q ? n.dq : n.dk;
+  const unsigned int mask = row_mask<C::TPR>();
+  const int e0 = first_vec<D, INTER>(t), e1 = e0 + second_vec<D, INTER>();
+  float wf[kElems], acc[kElems];
+  weights_of(w[is_q ? 0 : 1], e0, e1, wf);
+#pragma unroll
+  for (int e = 0; e < kElems; ++e) acc[e] = 0.f;
+  const long long rows = static_cast<long long>(a.B) * a.N;
+  for (long long r = static_cast<long long>(blockIdx.x) * C::ROWS + threadIdx.x / C::TPR; r < rows;
+       r += static_cast<long long>(g.gx) * C::ROWS) {
+    const long long b = r / a.N, tok = r - b * a.N;
+    const long long off = (b * H * a.N + tok) * D;
+    int p[FA_ROPE_MAX_AXES];
+    positions(a, rows, r, p);
+    float c[kPairs], s[kPairs];
+    angles(turns, axis, t, p, -1.f, c, s);
+    for (int h = h0; h < h1; h += kTwo) {
+      uint4 x0[kTwo], x1[kTwo], y0[kTwo], y1[kTwo];
+#pragma unroll
+      for (int i = 0; i < kTwo; ++i) {
+        const long long at = off + static_cast<long long>(min(h + i, h1 - 1)) * a.N * D;
+        x0[i] = *reinterpret_cast<const uint4*>(x + at + e0);
+        x1[i] = *reinterpret_cast<const uint4*>(x + at + e1);
+        y0[i] = *reinterpret_cast<const uint4*>(dy + at + e0);
+        y1[i] = *reinterpret_cast<const uint4*>(dy + at + e1);
+      }
+#pragma unroll
+      for (int i = 0; i < kTwo; ++i)
+        if (h + i < h1) {
+          float f[kElems], gr[kElems], ss = 0.f, hn = 0.f;
+          unpack(x0[i], x1[i], f);
+          unpack(y0[i], y1[i], gr);
+          turn<INTER>(gr, c, s);  // g
+#pragma unroll
+          for (int e = 0; e < kElems; ++e) {
+            ss = fmaf(f[e], f[e], ss);
+            hn = fmaf(gr[e] * wf[e], f[e], hn);
+          }
+          ss = row_sum<C::TPR>(ss, mask);
+          hn = row_sum<C::TPR>(hn, mask);
+          const float rs = rsqrtf(fmaf(ss, 1.f / D, n.eps));
+          const float m = hn * rs * (1.f / D);  // mean(h n)
+#pragma unroll
+          for (int e = 0; e < kElems; ++e) {
+            const float nn = f[e] * rs;
+            acc[e] = fmaf(gr[e], nn, acc[e]);
+            f[e] = rs * fmaf(gr[e], wf[e], -nn * m);
+          }
+          pack(f, x0[i], x1[i]);
+          __nv_bfloat16* const to = dx + off + static_cast<long long>(h + i) * a.N * D;
+          *reinterpret_cast<uint4*>(to + e0) = x0[i];
+          *reinterpret_cast<uint4*>(to + e1) = x1[i];
+        }
+    }
+  }
+  if (!n.part) return;
+  float* const mine = sum[threadIdx.x / C::TPR];
+#pragma unroll
+  for (int e = 0; e < kElems / 2; ++e) {
+    mine[e0 + e] = acc[e];
+    mine[e1 + e] = acc[kElems / 2 + e];
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < C::ROWS; ++i) v += sum[i][threadIdx.x];
+    n.part[(static_cast<size_t>(y) * g.gx + blockIdx.x) * D + threadIdx.x] = v;
+  }
+}
+
+// dw of q (blockIdx.y = 0) and k (1): 8 columns a block, 32 threads a column, which add every 32nd partial sum each and are
+// joined in their order.
+template <int D>
+__global__ void __launch_bounds__(256) norm_rope_weights_kernel(const NormRopeLaunch n, const BwdGrid g) {
+  __shared__ float sum[32][9];
+  grid_dep_wait();  // launched programmatically after the kernel that leaves the partial sums
+  float* const out = blockIdx.y ? n.dk_weight : n.dq_weight;
+  const int first = blockIdx.y ? g.yq * g.gx : 0, count = (blockIdx.y ? g.yk : g.yq) * g.gx;
+  const int col = threadIdx.x % 8, lane = threadIdx.x / 8;
+  const float* p = n.part + static_cast<size_t>(first) * D + blockIdx.x * 8 + col;
+  float v = 0.f;
+#pragma unroll 8
+  for (int i = lane; i < count; i += 32) v += p[static_cast<size_t>(i) * D];
+  sum[lane][col] = v;
+  __syncthreads();
+  if (lane || !out) return;
+  double total = 0.0;
+  for (int i = 0; i < 32; ++i) total += sum[i][col];
+  out[blockIdx.x * 8 + col] = static_cast<float>(total);
+}
+
+template <typename Kern, typename... Args>
+cudaError_t launch_kernel(Kern kern, dim3 grid, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D, bool INTER>
+cudaError_t launch_t(NormRopeLaunch n, cudaStream_t stream) {
+  RopeLaunch& a = n.r;
+  const long long bx = (static_cast<long long>(a.B) * a.N + RopeCfg<D>::ROWS - 1) / RopeCfg<D>::ROWS;
+  const int heads = a.Hq + a.Hk * (n.slots ? 2 : 1);
+  a.heads = kUnroll;
+  while (a.heads > 1 && bx * ((heads + a.heads - 1) / a.heads) < 4LL * a.sms) a.heads /= 2;
+  const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>((heads + a.heads - 1) / a.heads));
+  return n.slots ? launch_kernel(norm_rope_kernel<D, INTER, true>, grid, kThreads, stream, n)
+                 : launch_kernel(norm_rope_kernel<D, INTER, false>, grid, kThreads, stream, n);
+}
+
+template <int D, bool INTER>
+cudaError_t launch_bwd_t(const NormRopeLaunch& n, cudaStream_t stream) {
+  const RopeLaunch& a = n.r;
+  const BwdGrid g = bwd_grid(a.B, a.Hq, a.Hk, a.N, D, a.sms);
+  cudaError_t e = launch_kernel(norm_rope_bwd_kernel<D, INTER>,
+                                dim3(static_cast<unsigned>(g.gx), static_cast<unsigned>(g.yq + g.yk)), kThreads, stream, n, g);
+  if (e != cudaSuccess || !n.part) return e;
+  return launch_kernel(norm_rope_weights_kernel<D>, dim3(D / 8, a.Hk > 0 ? 2 : 1), 256, stream, n, g);
+}
+
+}  // namespace
+
+int norm_rope_partials(int B, int Hq, int Hk, int N, int d, int sms) {
+  const BwdGrid g = bwd_grid(B, Hq, Hk, N, d, sms);
+  return g.gx * (g.yq + g.yk);
+}
+
+cudaError_t launch_norm_rope(const NormRopeLaunch& a, cudaStream_t stream) {
+  const fa_rope_axes_plan_t& plan = a.r.plan;
+  if (plan.d == 64) return plan.interleaved ? launch_t<64, true>(a, stream) : launch_t<64, false>(a, stream);
+  return plan.interleaved ? launch_t<128, true>(a, stream) : launch_t<128, false>(a, stream);
+}
+
+cudaError_t launch_norm_rope_bwd(const NormRopeLaunch& a, cudaStream_t stream) {
+  const fa_rope_axes_plan_t& plan = a.r.plan;
+  if (plan.d == 64) return plan.interleaved ? launch_bwd_t<64, true>(a, stream) : launch_bwd_t<64, false>(a, stream);
+  return plan.interleaved ? launch_bwd_t<128, true>(a, stream) : launch_bwd_t<128, false>(a, stream);
+}
+
+}  // namespace fattn

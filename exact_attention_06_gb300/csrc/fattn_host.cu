@@ -69,8 +69,8 @@ fa_status_t check_device(int* sms) {
 
 // ---------------------------------------------------------------- status words
 // Each kernel file has a status word of its own.  One kernel takes (reads and clears) them all: a copy from and one to each
-// of the seven words took fa_get_status 94 us; this takes 22.
-constexpr int kStatusWords = 7;
+// of seven words took fa_get_status 94 us; this takes 22.
+constexpr int kStatusWords = 9;
 struct StatusWords {
   unsigned int* p[kStatusWords];
 };
@@ -88,7 +88,7 @@ cudaError_t take_status(cudaStream_t stream, unsigned int* bits) {
   constexpr Word kWord[kStatusWords] = {
       fattn::fwd_status_word,        fattn::decode_status_word,      fattn::bwd_status_word,
       fattn::cross_bwd_status_word,  fattn::cross_rows_status_word,  fattn::cross_short_status_word,
-      fattn::cross_bwd_short_status_word};
+      fattn::cross_bwd_short_status_word, fattn::window_fwd_status_word, fattn::window_bwd_status_word};
   static std::mutex mu;
   static StatusWords words[kMaxDevices];
   static bool known[kMaxDevices] = {};
@@ -130,12 +130,13 @@ EncodeTiledFn encode_fn() {
 
 // A tensor [batches, rows, d] (d innermost) of bf16 (esz = 2) or bytes (esz = 1, E4M3
 // codes) seen as 3-D {d, rows, batches}, loaded in boxes of 128 bytes (64 bf16 or 128
-// E4M3 columns) x box_rows rows with 128-byte swizzle.  Rows past `rows` read as zeros.
+// E4M3 columns) x box_rows rows with 128-byte swizzle.  Rows past `rows` read as zeros, as do those from
+// `shown` on, if it is not 0.
 fa_status_t make_map(CUtensorMap* map, const void* base, int d, long long rows, long long batches, int box_rows,
-                     int esz = 2) {
+                     int esz = 2, int shown = 0) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(shown ? shown : rows),
                               static_cast<cuuint64_t>(batches)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * esz, static_cast<cuuint64_t>(rows) * d * esz};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / esz), static_cast<cuuint32_t>(box_rows), 1};
@@ -527,6 +528,94 @@ CrossBwdPlan plan_cross_bwd(const CrossShape& c, int Nk, int d, int sms) {
   if (p.kv_splits > 1) p.kv_bytes = round256(2ull * c.bh * Nk * d * sizeof(float) * p.kv_splits);
   if (p.q_splits > 1) p.q_bytes = round256(1ull * c.bh * c.rows * d * sizeof(float) * p.q_splits);
   return p;
+}
+
+// Sliding windows.
+constexpr int kMaxSinks = 128;  // one key tile
+
+fa_status_t check_window(int window, int sinks) {
+  if (window < 1) return fail(FA_ERR_INVALID_ARG, "window=%d must be >= 1", window);
+  if (sinks < 0) return fail(FA_ERR_INVALID_ARG, "sinks=%d must be >= 0", sinks);
+  if (sinks > kMaxSinks) return fail(FA_ERR_UNSUPPORTED, "sinks=%d exceeds %d", sinks, kMaxSinks);
+  return FA_OK;
+}
+
+fa_status_t check_window_args(int B, int Hq, int Hkv, int N, int Nk, int d, int window, int sinks) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || N < 1 || Nk < 1)
+    return fail(FA_ERR_INVALID_ARG, "B, Hq, Hkv, N and Nk must be >= 1 (got %d, %d, %d, %d, %d)", B, Hq, Hkv, N, Nk);
+  if (Hq % Hkv != 0) return fail(FA_ERR_INVALID_ARG, "Hq=%d must be a multiple of Hkv=%d", Hq, Hkv);
+  if (N > Nk) return fail(FA_ERR_INVALID_ARG, "N=%d queries need at least as many keys (Nk=%d)", N, Nk);
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dimension d=%d is not supported (64 or 128)", d);
+  if (static_cast<long long>(B) * Hq > INT_MAX)
+    return fail(FA_ERR_UNSUPPORTED, "B*Hq=%lld exceeds the grid limit", static_cast<long long>(B) * Hq);
+  if ((Nk + 127LL) / 128 > 60000) return fail(FA_ERR_UNSUPPORTED, "Nk=%d exceeds the 60000 key-tile grid limit", Nk);
+  return check_window(window, sinks);
+}
+
+struct WindowBwdPlan {
+  int splits0 = 1, stages0 = 0, splits = 1, stages = 0, own_tiles = 1;
+  size_t delta_bytes = 0, part0_bytes = 0, part_bytes = 0;
+  size_t total() const { return std::max<size_t>(delta_bytes + part0_bytes + part_bytes, 256); }
+};
+
+WindowBwdPlan plan_window_bwd(int B, int Hq, int Hkv, int N, int Nk, int d, int window, int sinks, int sms) {
+  WindowBwdPlan p;
+  const int W = std::min(window, Nk), G = Hq / Hkv;
+  const long long bh = static_cast<long long>(B) * Hkv;
+  const int kt = (Nk + 127) / 128, qt = (N + 127) / 128;
+  // The dK/dV kernel's stages (128 query rows): of a key tile inside, for its query heads one after another.
+  const long long per_head = std::min<long long>(qt, (127LL + W + 127) / 128);
+  const long long inner = per_head * G;
+  const double kv = 2.0 * bh * Nk * d * sizeof(float);
+  p.splits = cut_scan(bh * kt, static_cast<int>(std::min<long long>(inner, INT_MAX)), sms, kv);
+  p.stages = static_cast<int>((inner + p.splits - 1) / p.splits);
+  // Key tile 0 with sinks is seen by all queries: ranges as long as the other tiles' blocks, at least 8 stages, and
+  // at most 128 of them.
+  const long long all = sinks > 0 ? static_cast<long long>(qt) * G : inner;
+  long long each = std::max<long long>(p.stages, 8);
+  each = std::max(each, (all + 127) / 128);
+  p.splits0 = static_cast<int>((all + each - 1) / each);
+  p.stages0 = static_cast<int>(each);
+  if (sinks == 0) {
+    p.splits0 = p.splits;
+    p.stages0 = p.stages;
+  }
+  p.delta_bytes = round256(static_cast<size_t>(B) * Hq * N * sizeof(float));
+  if (p.splits0 > 1) p.part0_bytes = round256(2ull * p.splits0 * bh * 128 * d * sizeof(float));
+  if (p.splits > 1) p.part_bytes = round256(2ull * p.splits * bh * Nk * d * sizeof(float));
+  // Query tiles that a block of the dQ kernel takes: each saves most of a block's set-up and end, but longer blocks
+  // end less evenly.
+  const long long steps = (127LL + W + 127) / 128 + (sinks > 0 ? 1 : 0);
+  while (p.own_tiles < 8 && static_cast<long long>(B) * Hq * ((qt + 2 * p.own_tiles - 1) / (2 * p.own_tiles)) >= 3LL * sms &&
+         2 * p.own_tiles * steps <= 24)
+    p.own_tiles *= 2;
+  return p;
+}
+
+// Stages of 64 keys that fa_window_decode_paged reads of a sequence at most.
+int window_stages(int max_seq_len, int window, int sinks) {
+  const long long all = (static_cast<long long>(max_seq_len) + 63) / 64;
+  return static_cast<int>(std::min(all, (static_cast<long long>(window) + 63) / 64 + 1 + (sinks + 63) / 64));
+}
+
+fa_status_t plan_window_decode(int B, int Hq, int Hkv, int d, int page_size, int max_pages, int num_pages, int max_seq_len,
+                               int window, int sinks, bool workspace, CrossShape* c, CrossPlan* p) {
+  if (B < 1 || Hq < 1 || Hkv < 1) return fail(FA_ERR_INVALID_ARG, "B, Hq and Hkv must be >= 1 (got %d, %d, %d)", B, Hq, Hkv);
+  if (Hq % Hkv != 0) return fail(FA_ERR_INVALID_ARG, "Hq=%d must be a multiple of Hkv=%d", Hq, Hkv);
+  fa_status_t st = check_paged_args(B, Hkv, d, page_size, max_pages, num_pages, max_seq_len);
+  if (st != FA_OK || (st = check_window(window, sinks)) != FA_OK) return st;
+  if (Hq / Hkv > fattn::kCrossRowsMax)
+    return fail(FA_ERR_UNSUPPORTED, "Hq/Hkv=%d exceeds %d query heads a key head", Hq / Hkv, fattn::kCrossRowsMax);
+  c->bh = static_cast<long long>(B) * Hkv;
+  c->rows = Hq / Hkv;
+  if (c->bh * c->rows > INT_MAX) return fail(FA_ERR_UNSUPPORTED, "B*Hq=%lld exceeds the grid limit", c->bh * c->rows);
+  int sms = 0;
+  if ((st = check_device(&sms)) != FA_OK) return st;
+  plan_few(p, *c, window_stages(max_seq_len, window, sinks) * fattn::kRowsStageKeys, d, sms, workspace);
+  const long long rows = c->bh * c->rows;
+  p->u_bytes = round256(static_cast<size_t>(rows) * p->splits * d * sizeof(float));
+  p->m_bytes = round256(static_cast<size_t>(rows) * p->splits * sizeof(float));
+  return FA_OK;
 }
 
 fa_status_t check_rope_args(const fa_rope_axes_plan_t* plan, const int* pos, int B, int Hq, int Hk, int N, int inverse) {
@@ -1120,7 +1209,8 @@ fa_status_t fa_cross_fwd(const void* q, const void* k, const void* v, const int*
     if ((st = make_map(&f.tv, v, d, Nk, c.bh, fattn::kRowsStageKeys)) != FA_OK) return st;
     f.BH = static_cast<int>(c.bh);
     f.d = d;
-    f.args = {q, o, lse, u_part, m_part, l_part, kv_lens, Hkv, c.rows, Nk, plan.splits, o_fp32, scale_log2, budget};
+    f.args = {q, o, lse, u_part, m_part, l_part, kv_lens, Hkv, c.rows, Nk, plan.splits, o_fp32, scale_log2, budget,
+              nullptr, 0, 0, 0, 0, 0};
     cudaGetLastError();
     const cudaError_t e = fattn::launch_cross_rows(f, s);
     if (e != cudaSuccess) return cuda_fail(e, "fa_cross_fwd launch");
@@ -1358,6 +1448,320 @@ fa_status_t fa_rope_axes_paged(const void* q, const void* k, const void* v, cons
   cudaError_t e = fattn::launch_rope(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fa_rope_axes_paged launch");
   return FA_OK;
+}
+
+fa_status_t fa_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int N,
+                          int Nk, int d, float scale, int window, int sinks, void* stream, const fa_window_opts* opts) {
+  g_last_error[0] = '\0';
+  if (!q || !k || !v || !o || !lse) return fail(FA_ERR_INVALID_ARG, "null tensor pointer");
+  const int o_fp32 = opts ? opts->o_fp32 : 0;
+  if (o_fp32 != 0 && o_fp32 != 1) return fail(FA_ERR_INVALID_ARG, "opts->o_fp32 must be 0 or 1");
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16))
+    return fail(FA_ERR_INVALID_ARG, "q, k, v and o must be 16-byte aligned");
+  if (!aligned(lse, 4)) return fail(FA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  fa_status_t st = check_window_args(B, Hq, Hkv, N, Nk, d, window, sinks);
+  if (st != FA_OK) return st;
+  fattn::WindowFwdLaunch l{};
+  if ((st = check_device(&l.sms)) != FA_OK) return st;
+  const int heads = B * Hq, kv_heads = B * Hkv, shown = std::min(sinks, Nk);
+  if ((st = make_map(&l.tq, q, d, N, heads, 128)) != FA_OK) return st;
+  if ((st = make_map(&l.tk, k, d, Nk, kv_heads, 128)) != FA_OK) return st;
+  if ((st = make_map(&l.tv, v, d, Nk, kv_heads, 128)) != FA_OK) return st;
+  if (sinks > 0) {
+    if ((st = make_map(&l.tks, k, d, Nk, kv_heads, 128, 2, shown)) != FA_OK) return st;
+    if ((st = make_map(&l.tvs, v, d, Nk, kv_heads, 128, 2, shown)) != FA_OK) return st;
+  }
+  if (!o_fp32 && (st = make_map(&l.to, o, d, N, heads, 128)) != FA_OK) return st;
+  l.args = {o, lse, N, Nk, Hq / Hkv, std::min(window, Nk), shown, o_fp32, scale * 1.4426950408889634f,
+            opts && opts->wait_budget_cycles ? opts->wait_budget_cycles : kDefaultBudget, 0};
+  l.BH = heads;
+  l.d = d;
+  cudaGetLastError();
+  const cudaError_t e = fattn::launch_window_fwd(l, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_window_fwd launch");
+}
+
+size_t fa_window_bwd_workspace_bytes(int B, int Hq, int Hkv, int N, int Nk, int d, int window, int sinks) {
+  const int saved = g_last_error[0];
+  int sms = 0;
+  fa_status_t st = check_window_args(B, Hq, Hkv, N, Nk, d, window, sinks);
+  if (st == FA_OK) st = check_device(&sms);
+  if (!saved) g_last_error[0] = '\0';
+  return st == FA_OK ? plan_window_bwd(B, Hq, Hkv, N, Nk, d, window, std::min(sinks, Nk), sms).total() : 0;
+}
+
+fa_status_t fa_window_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                          void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int Nk, int d, float scale,
+                          int window, int sinks, int grad_fp32, void* workspace, size_t ws_bytes, void* stream,
+                          const fa_bwd_opts* opts) {
+  g_last_error[0] = '\0';
+  if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv) return fail(FA_ERR_INVALID_ARG, "null tensor pointer");
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (grad_fp32 != 0 && grad_fp32 != 1) return fail(FA_ERR_INVALID_ARG, "grad_fp32 must be 0 or 1");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(dout, 16) ||
+      !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16))
+    return fail(FA_ERR_INVALID_ARG, "q, k, v, o, dout, dq, dk and dv must be 16-byte aligned");
+  if (!aligned(lse, 4)) return fail(FA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  fa_status_t st = check_window_args(B, Hq, Hkv, N, Nk, d, window, sinks);
+  if (st != FA_OK) return st;
+  if (!workspace) return fail(FA_ERR_WORKSPACE, "fa_window_bwd needs a workspace (fa_window_bwd_workspace_bytes)");
+  if (!aligned(workspace, 256)) return fail(FA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  fattn::WindowBwdLaunch l{};
+  if ((st = check_device(&l.sms)) != FA_OK) return st;
+  const int heads = B * Hq, kv_heads = B * Hkv, shown = std::min(sinks, Nk);
+  const WindowBwdPlan plan = plan_window_bwd(B, Hq, Hkv, N, Nk, d, window, shown, l.sms);
+  if (ws_bytes < plan.total())
+    return fail(FA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes, plan.total());
+  if ((st = make_map(&l.tq, q, d, N, heads, 128)) != FA_OK) return st;
+  if ((st = make_map(&l.tdo, dout, d, N, heads, 128)) != FA_OK) return st;
+  if ((st = make_map(&l.tk, k, d, Nk, kv_heads, 128)) != FA_OK) return st;
+  if ((st = make_map(&l.tv, v, d, Nk, kv_heads, 128)) != FA_OK) return st;
+  if (sinks > 0) {
+    if ((st = make_map(&l.tks, k, d, Nk, kv_heads, 128, 2, shown)) != FA_OK) return st;
+    if ((st = make_map(&l.tvs, v, d, Nk, kv_heads, 128, 2, shown)) != FA_OK) return st;
+  }
+  if (!grad_fp32) {
+    if ((st = make_map(&l.tdq, dq, d, N, heads, 128)) != FA_OK) return st;
+    if ((st = make_map(&l.tdk, dk, d, Nk, kv_heads, 128)) != FA_OK) return st;
+    if ((st = make_map(&l.tdv, dv, d, Nk, kv_heads, 128)) != FA_OK) return st;
+  }
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  fattn::WindowBwdArgs& a = l.args;
+  l.o = o;
+  l.dout = dout;
+  l.delta = reinterpret_cast<float*>(w);
+  l.d = d;
+  a.lse = lse;
+  a.delta = l.delta;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.part0 = reinterpret_cast<float*>(w + plan.delta_bytes);
+  a.part = reinterpret_cast<float*>(w + plan.delta_bytes + plan.part0_bytes);
+  a.stride0 = static_cast<long long>(kv_heads) * 128 * d;
+  a.stride = static_cast<long long>(kv_heads) * Nk * d;
+  a.N = N;
+  a.Nk = Nk;
+  a.group = Hq / Hkv;
+  a.window = std::min(window, Nk);
+  a.sinks = shown;
+  a.grad_fp32 = grad_fp32;
+  a.kv_heads = kv_heads;
+  a.splits0 = plan.splits0;
+  a.stages0 = plan.stages0;
+  a.splits = plan.splits;
+  a.stages = plan.stages;
+  a.own_tiles = plan.own_tiles;
+  a.sl2 = scale * 1.4426950408889634f;
+  a.scale = scale;
+  a.budget = opts && opts->wait_budget_cycles ? opts->wait_budget_cycles : kDefaultBudget;
+  cudaGetLastError();
+  const cudaError_t e = fattn::launch_window_bwd(l, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_window_bwd launch");
+}
+
+size_t fa_window_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int page_size, int max_pages, int max_seq_len,
+                                              int window, int sinks) {
+  const int saved = g_last_error[0];
+  CrossShape c;
+  CrossPlan p;
+  const fa_status_t st = plan_window_decode(B, Hq, Hkv, d, page_size, max_pages, 1, max_seq_len, window, sinks, true, &c, &p);
+  if (!saved) g_last_error[0] = '\0';
+  return st == FA_OK ? p.total() : 0;
+}
+
+fa_status_t fa_window_decode_paged(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                                   const int* seq_lens, void* o, float* lse, int B, int Hq, int Hkv, int d, int page_size,
+                                   int max_pages, int num_pages, int max_seq_len, float scale, int window, int sinks,
+                                   void* workspace, size_t ws_bytes, void* stream, const fa_decode_opts* opts) {
+  g_last_error[0] = '\0';
+  if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !o || !lse)
+    return fail(FA_ERR_INVALID_ARG, "null tensor pointer");
+  const int o_fp32 = opts ? opts->o_fp32 : 0;
+  if (o_fp32 != 0 && o_fp32 != 1) return fail(FA_ERR_INVALID_ARG, "opts->o_fp32 must be 0 or 1");
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16))
+    return fail(FA_ERR_INVALID_ARG, "q, k_pages, v_pages and o must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
+    return fail(FA_ERR_INVALID_ARG, "lse, block_table and seq_lens must be 4-byte aligned");
+  if (workspace && !aligned(workspace, 256)) return fail(FA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  CrossShape c;
+  CrossPlan plan;
+  fa_status_t st = plan_window_decode(B, Hq, Hkv, d, page_size, max_pages, num_pages, max_seq_len, window, sinks,
+                                      workspace != nullptr, &c, &plan);
+  if (st != FA_OK) return st;
+  if (workspace && ws_bytes < plan.total())
+    return fail(FA_ERR_WORKSPACE,
+                "workspace of %zu bytes is smaller than the %zu bytes fa_window_decode_paged_workspace_bytes gives", ws_bytes,
+                plan.total());
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  float* u_part = plan.parts ? reinterpret_cast<float*>(w) : nullptr;
+  float* m_part = plan.parts ? reinterpret_cast<float*>(w + plan.u_bytes) : nullptr;
+  float* l_part = plan.parts ? reinterpret_cast<float*>(w + plan.u_bytes + plan.m_bytes) : nullptr;
+  fattn::CrossRowsLaunch f{};
+  const long long planes = static_cast<long long>(num_pages) * Hkv;
+  if ((st = make_map(&f.tk, k_pages, d, page_size, planes, fattn::kRowsStageKeys)) != FA_OK) return st;
+  if ((st = make_map(&f.tv, v_pages, d, page_size, planes, fattn::kRowsStageKeys)) != FA_OK) return st;
+  f.BH = static_cast<int>(c.bh);
+  f.d = d;
+  f.args = {q, o, lse, u_part, m_part, l_part, seq_lens, Hkv, c.rows, max_seq_len, plan.splits, o_fp32,
+            scale * 1.4426950408889634f, opts && opts->wait_budget_cycles ? opts->wait_budget_cycles : kDefaultBudget,
+            block_table, page_size, max_pages, num_pages, std::min(window, max_seq_len), sinks};
+  cudaGetLastError();
+  cudaError_t e = fattn::launch_cross_rows(f, s);
+  if (e != cudaSuccess) return cuda_fail(e, "fa_window_decode_paged launch");
+  if (!plan.parts) return FA_OK;
+  e = fattn::launch_combine(u_part, m_part, l_part, o, lse, static_cast<int>(c.bh * c.rows), plan.splits, d, o_fp32, s);
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_window_decode_paged combine launch");
+}
+
+// The tensors and weights that the norm's calls share.
+static fa_status_t check_norm_args(const void* q, const void* k, const void* q_out, const void* k_out, const void* q_weight,
+                                   const void* k_weight, int weight_fp32, float eps, int Hk) {
+  if (!q || !q_out || (Hk > 0 && (!k || !k_out))) return fail(FA_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned(q, 16) || !aligned(q_out, 16) || (Hk > 0 && (!aligned(k, 16) || !aligned(k_out, 16))))
+    return fail(FA_ERR_INVALID_ARG, "q, k and their outputs must be 16-byte aligned");
+  if (weight_fp32 != 0 && weight_fp32 != 1) return fail(FA_ERR_INVALID_ARG, "weight_fp32 must be 0 or 1");
+  if (!aligned(q_weight, weight_fp32 ? 4 : 2) || !aligned(k_weight, weight_fp32 ? 4 : 2))
+    return fail(FA_ERR_INVALID_ARG, "q_weight and k_weight must be aligned to their type");
+  if (!std::isfinite(eps) || !(eps > 0.f)) return fail(FA_ERR_INVALID_ARG, "eps must be finite and > 0");
+  return FA_OK;
+}
+
+static fattn::NormRopeLaunch norm_launch(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                                         int weight_fp32, const int* pos, int B, int Hq, int Hk, int N, float eps,
+                                         const fa_rope_axes_plan_t* plan) {
+  fattn::NormRopeLaunch l{};
+  l.r.plan = *plan;
+  l.r.q = static_cast<const __nv_bfloat16*>(q);
+  l.r.k = static_cast<const __nv_bfloat16*>(k);
+  l.r.pos = pos;
+  l.r.B = B;
+  l.r.Hq = Hq;
+  l.r.Hk = Hk;
+  l.r.N = N;
+  l.q_weight = q_weight;
+  l.k_weight = k_weight;
+  l.weight_fp32 = weight_fp32;
+  l.eps = eps;
+  return l;
+}
+
+fa_status_t fa_norm_rope_axes(const void* q, const void* k, const void* q_weight, const void* k_weight, int weight_fp32,
+                              const int* pos, void* q_out, void* k_out, int B, int Hq, int Hk, int N, float eps,
+                              const fa_rope_axes_plan_t* plan, void* stream) {
+  g_last_error[0] = '\0';
+  fa_status_t st = check_rope_args(plan, pos, B, Hq, Hk, N, 0);
+  if (st != FA_OK) return st;
+  if ((st = check_norm_args(q, k, q_out, k_out, q_weight, k_weight, weight_fp32, eps, Hk)) != FA_OK) return st;
+  fattn::NormRopeLaunch l = norm_launch(q, k, q_weight, k_weight, weight_fp32, pos, B, Hq, Hk, N, eps, plan);
+  if ((st = check_device(&l.r.sms)) != FA_OK) return st;
+  l.r.q_out = static_cast<__nv_bfloat16*>(q_out);
+  l.r.k_out = static_cast<__nv_bfloat16*>(k_out);
+  cudaGetLastError();
+  const cudaError_t e = fattn::launch_norm_rope(l, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_norm_rope_axes launch");
+}
+
+size_t fa_norm_rope_axes_bwd_workspace_bytes(int B, int Hq, int Hk, int N, int d) {
+  const int saved = g_last_error[0];
+  int sms = 0;
+  const bool fits = B >= 1 && Hq >= 1 && Hk >= 0 && N >= 1 && (d == 64 || d == 128) &&
+                    static_cast<long long>(B) * N <= INT_MAX && static_cast<long long>(Hq) + 2LL * Hk <= 65535;
+  const bool ok = fits && check_device(&sms) == FA_OK;
+  if (!saved) g_last_error[0] = '\0';
+  return ok ? round256(static_cast<size_t>(fattn::norm_rope_partials(B, Hq, Hk, N, d, sms)) * d * sizeof(float)) : 0;
+}
+
+fa_status_t fa_norm_rope_axes_bwd(const void* q, const void* k, const void* q_weight, const void* k_weight, int weight_fp32,
+                                  const int* pos, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                  float* dq_weight, float* dk_weight, int B, int Hq, int Hk, int N, float eps,
+                                  const fa_rope_axes_plan_t* plan, void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error[0] = '\0';
+  fa_status_t st = check_rope_args(plan, pos, B, Hq, Hk, N, 0);
+  if (st != FA_OK) return st;
+  if ((st = check_norm_args(q, k, dq, dk, q_weight, k_weight, weight_fp32, eps, Hk)) != FA_OK) return st;
+  if (!dq_out || (Hk > 0 && !dk_out)) return fail(FA_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned(dq_out, 16) || (Hk > 0 && !aligned(dk_out, 16)))
+    return fail(FA_ERR_INVALID_ARG, "dq_out and dk_out must be 16-byte aligned");
+  if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4))
+    return fail(FA_ERR_INVALID_ARG, "dq_weight and dk_weight must be 4-byte aligned");
+  fattn::NormRopeLaunch l = norm_launch(q, k, q_weight, k_weight, weight_fp32, pos, B, Hq, Hk, N, eps, plan);
+  if ((st = check_device(&l.r.sms)) != FA_OK) return st;
+  if (dq_weight || (Hk > 0 && dk_weight)) {
+    const size_t need = fa_norm_rope_axes_bwd_workspace_bytes(B, Hq, Hk, N, plan->d);
+    if (!workspace || ws_bytes < need)
+      return fail(FA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes, need);
+    if (!aligned(workspace, 256)) return fail(FA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    l.part = static_cast<float*>(workspace);
+  }
+  l.dq_out = static_cast<const __nv_bfloat16*>(dq_out);
+  l.dk_out = static_cast<const __nv_bfloat16*>(dk_out);
+  l.dq = static_cast<__nv_bfloat16*>(dq);
+  l.dk = static_cast<__nv_bfloat16*>(dk);
+  l.dq_weight = dq_weight;
+  l.dk_weight = Hk > 0 ? dk_weight : nullptr;
+  cudaGetLastError();
+  const cudaError_t e = fattn::launch_norm_rope_bwd(l, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_norm_rope_axes_bwd launch");
+}
+
+fa_status_t fa_norm_rope_axes_paged(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
+                                    int weight_fp32, const int* pos, void* q_out, void* k_pages, void* v_pages,
+                                    const long long* slots, const int* new_lens, int B, int Hq, int Hk, int N, int page_size,
+                                    int num_pages, float eps, const fa_rope_axes_plan_t* plan, void* stream) {
+  g_last_error[0] = '\0';
+  if (!v || !v_pages || !slots) return fail(FA_ERR_INVALID_ARG, "null tensor pointer");
+  fa_status_t st = check_rope_args(plan, pos, B, Hq, Hk, N, 0);
+  if (st != FA_OK) return st;
+  if ((st = check_paged_args(B, Hk, plan->d, page_size, 1, num_pages, 1)) != FA_OK) return st;
+  if ((st = check_norm_args(q, k, q_out, k_pages, q_weight, k_weight, weight_fp32, eps, Hk)) != FA_OK) return st;
+  if (!aligned(v, 16) || !aligned(v_pages, 16)) return fail(FA_ERR_INVALID_ARG, "v and v_pages must be 16-byte aligned");
+  if (!aligned(slots, 8) || !aligned(new_lens, 4))
+    return fail(FA_ERR_INVALID_ARG, "slots must be 8-byte aligned, new_lens 4-byte aligned");
+  fattn::NormRopeLaunch l = norm_launch(q, k, q_weight, k_weight, weight_fp32, pos, B, Hq, Hk, N, eps, plan);
+  if ((st = check_device(&l.r.sms)) != FA_OK) return st;
+  l.r.v = static_cast<const __nv_bfloat16*>(v);
+  l.r.q_out = static_cast<__nv_bfloat16*>(q_out);
+  l.r.k_out = static_cast<__nv_bfloat16*>(k_pages);
+  l.r.v_out = static_cast<__nv_bfloat16*>(v_pages);
+  l.r.new_lens = new_lens;
+  l.r.page_size = page_size;
+  l.r.num_pages = num_pages;
+  l.slots = slots;
+  cudaGetLastError();
+  const cudaError_t e = fattn::launch_norm_rope(l, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_norm_rope_axes_paged launch");
+}
+
+fa_status_t fa_pages_extend(int* block_table, int* seq_lens, const int* new_lens, int* free_pages, int* n_free, int* granted,
+                            long long* slots, int B, int N, int page_size, int max_pages, int num_pages, void* stream) {
+  g_last_error[0] = '\0';
+  if (!block_table || !seq_lens || !new_lens || !free_pages || !n_free || !granted)
+    return fail(FA_ERR_INVALID_ARG, "null pointer");
+  if (B < 1 || max_pages < 1 || num_pages < 1 || (slots && N < 1))
+    return fail(FA_ERR_INVALID_ARG, "B, max_pages, num_pages and (with slots) N must be >= 1 (got %d, %d, %d, %d)", B,
+                max_pages, num_pages, N);
+  if (page_size < 64 || page_size % 64 != 0)
+    return fail(FA_ERR_UNSUPPORTED, "page_size=%d must be a positive multiple of 64", page_size);
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) ||
+      !aligned(n_free, 4) || !aligned(granted, 4) || !aligned(slots, 8))
+    return fail(FA_ERR_INVALID_ARG, "slots must be 8-byte aligned, the other arrays 4-byte aligned");
+  if (granted == new_lens || granted == seq_lens || new_lens == seq_lens)
+    return fail(FA_ERR_INVALID_ARG, "seq_lens, new_lens and granted must be arrays of their own");
+  if (static_cast<long long>(max_pages) * page_size > INT_MAX)
+    return fail(FA_ERR_UNSUPPORTED, "max_pages*page_size=%lld exceeds the length range",
+                static_cast<long long>(max_pages) * page_size);
+  if (static_cast<long long>(B) * max_pages > INT_MAX || (slots && static_cast<long long>(B) * ((N + 1023LL) / 1024) > INT_MAX))
+    return fail(FA_ERR_UNSUPPORTED, "B=%d with max_pages=%d, N=%d exceeds the grid limit", B, max_pages, N);
+  fa_status_t st = check_device(nullptr);
+  if (st != FA_OK) return st;
+  cudaGetLastError();
+  const cudaError_t e = fattn::launch_pages({block_table, seq_lens, new_lens, free_pages, n_free, granted, slots, B, N,
+                                             page_size, max_pages, num_pages}, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_pages_extend launch");
 }
 
 fa_status_t fa_get_status(void* stream) {

@@ -158,6 +158,10 @@ struct CrossRowsArgs {
   int kv_heads, R, Nk, S, o_fp32;
   float sl2;  // scale * log2(e)
   unsigned long long budget;
+  // Paged cache (block_table != nullptr): tk, tv map pools [num_pages * kv_heads, page_size, d], kv_lens (not null) has
+  // at most Nk keys a sequence, of which the last `window` and the first `sinks` count.
+  const int* block_table;  // [B, max_pages]
+  int page_size, max_pages, num_pages, window, sinks;
 };
 struct CrossRowsLaunch {
   CUtensorMap tk, tv;  // 64-key boxes
@@ -240,6 +244,96 @@ struct RopeLaunch {
   int page_size, max_pages, num_pages;
 };
 cudaError_t launch_rope(const RopeLaunch& a, cudaStream_t stream);
+
+// Causal attention with a sliding window and sinks: N queries of each of the query heads, `group` of which share a key
+// head, against its Nk >= N keys.
+struct WindowFwdArgs {
+  void* o;
+  float* lse;
+  int N, Nk, group, window, sinks, o_fp32;
+  float sl2;  // scale * log2(e)
+  unsigned long long budget;
+  int ng;  // head groups; set by launch_window_fwd
+};
+struct WindowFwdLaunch {
+  CUtensorMap tq, tk, tv;  // 128-row boxes
+  CUtensorMap tks, tvs;    // k and v up to their first `sinks` rows
+  CUtensorMap to;          // bf16 O only
+  WindowFwdArgs args;
+  int BH, d, sms;          // BH: B * Hq
+};
+cudaError_t launch_window_fwd(const WindowFwdLaunch& l, cudaStream_t stream);
+cudaError_t window_fwd_status_word(unsigned int** p);
+
+// Its backward.  Key tile 0's list of query stages (128 rows each) is cut into splits0 ranges of stages0, the other key
+// tiles' into `splits` of `stages`; where there are more than one, each leaves fp32 partial sums in part0 [2 (dK, dV)]
+// [splits0][kv_heads * 128, d] or part [2][splits][kv_heads * Nk, d], which a last kernel adds up.
+struct WindowBwdArgs {
+  const float* lse;
+  const float* delta;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* part0;
+  float* part;
+  long long stride0, stride;  // floats from one partial sum to the next
+  int N, Nk, group, window, sinks, grad_fp32;
+  int kv_heads;               // B * Hkv
+  int splits0, stages0, splits, stages;
+  int own_tiles;              // query tiles that a block of the dQ kernel takes one after another
+  float sl2, scale;
+  unsigned long long budget;
+  int ng, ng_q;               // head groups; set by launch_window_bwd
+};
+struct WindowBwdLaunch {
+  CUtensorMap tq, tk, tv, tks, tvs, tdo;  // as WindowFwdLaunch
+  CUtensorMap tdq, tdk, tdv;              // bf16 gradients only
+  WindowBwdArgs args;
+  const void* o;
+  const void* dout;
+  float* delta;
+  int d, sms;
+};
+cudaError_t launch_window_bwd(const WindowBwdLaunch& l, cudaStream_t stream);
+cudaError_t window_bwd_status_word(unsigned int** p);
+
+// RMS norm of each head's q and k, then the rotation: tensors and plan as RopeLaunch (block_table, seq_lens and
+// max_pages unused), weights [d] bf16 or fp32 (null: ones).  slots [B, N] (not null): k and v go to the pools, token n
+// of sequence b to row slots[b * N + n] of the pages' keys.
+struct NormRopeLaunch {
+  RopeLaunch r;
+  const void* q_weight;
+  const void* k_weight;
+  int weight_fp32;
+  float eps;
+  const long long* slots;
+  // backward: the gradients of q_out and k_out, those of q and k, and those of the weights (null: not wanted) by way
+  // of `part`, fp32 partial sums [norm_rope_partials()][d]
+  const __nv_bfloat16* dq_out;
+  const __nv_bfloat16* dk_out;
+  __nv_bfloat16* dq;
+  __nv_bfloat16* dk;
+  float* dq_weight;
+  float* dk_weight;
+  float* part;
+};
+cudaError_t launch_norm_rope(const NormRopeLaunch& a, cudaStream_t stream);
+cudaError_t launch_norm_rope_bwd(const NormRopeLaunch& a, cudaStream_t stream);
+// Partial sums of the weights' gradients that launch_norm_rope_bwd leaves for these sizes.
+int norm_rope_partials(int B, int Hq, int Hk, int N, int d, int sms);
+
+// Pages for new_lens[b] more tokens of each sequence (fewer where negative): see fa_pages_extend.
+struct PagesLaunch {
+  int* block_table;  // [B, max_pages]
+  int* seq_lens;
+  const int* new_lens;
+  int* free_pages;  // [num_pages]
+  int* n_free;
+  int* granted;
+  long long* slots;  // [B, N], or null
+  int B, N, page_size, max_pages, num_pages;
+};
+cudaError_t launch_pages(const PagesLaunch& a, cudaStream_t stream);
 
 // Fixed device scratch used by fa_decode_splitkv_noalloc in place of a
 // caller-provided workspace.  Size limit of that entry point.

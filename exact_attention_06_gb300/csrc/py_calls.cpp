@@ -1,5 +1,5 @@
-// The binding's side of the calls that a decode or training step makes most often (cross attention, rotary
-// positions), as a CPython module: argument checks, pointers and the stream are taken from the torch tensors here,
+// The binding's side of the calls that a decode or training step makes most often (cross attention, sliding windows,
+// rotary positions and norms, the cache's pages), as a CPython module: argument checks, pointers and the stream are taken from the torch tensors here,
 // since doing it in Python took longer (5-9 us a call) than the kernels of a small step.
 //
 // Every function returns the library's status, or -1 when an argument is not what the call takes (nothing has been
@@ -15,6 +15,7 @@
 
 #include <cstdint>
 #include <initializer_list>
+#include <type_traits>
 
 #include "fattn.h"
 
@@ -28,9 +29,19 @@ struct Api {
   decltype(&fa_cross_bwd_workspace_bytes) cross_bwd_bytes;
   decltype(&fa_rope_axes) rope;
   decltype(&fa_rope_axes_paged) rope_paged;
+  decltype(&fa_window_fwd) window_fwd;
+  decltype(&fa_window_bwd) window_bwd;
+  decltype(&fa_window_bwd_workspace_bytes) window_bwd_bytes;
+  decltype(&fa_window_decode_paged) window_decode;
+  decltype(&fa_window_decode_paged_workspace_bytes) window_decode_bytes;
+  decltype(&fa_norm_rope_axes) norm_rope;
+  decltype(&fa_norm_rope_axes_bwd) norm_rope_bwd;
+  decltype(&fa_norm_rope_axes_bwd_workspace_bytes) norm_rope_bwd_bytes;
+  decltype(&fa_norm_rope_axes_paged) norm_rope_paged;
+  decltype(&fa_pages_extend) pages_extend;
 } api{};
 
-constexpr auto kBf16 = at::kBFloat16, kF32 = at::kFloat, kI32 = at::kInt, kU8 = at::kByte;
+constexpr auto kBf16 = at::kBFloat16, kF32 = at::kFloat, kI32 = at::kInt, kI64 = at::kLong, kU8 = at::kByte;
 using Shape = std::initializer_list<int64_t>;
 
 // Reads tensors out of Python arguments; after the first that does not fit, `ok` stays false.
@@ -94,6 +105,28 @@ struct Args {
       ok = false;
     }
     return s;
+  }
+  // An int; the library checks its range.
+  int integer(int i) {
+    const long x = PyLong_AsLong(argv[i]);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      ok = false;
+    } else if (x != static_cast<int>(x)) {
+      ok = false;
+    }
+    return static_cast<int>(x);
+  }
+  // Two weights [d], both bf16 or both fp32 (then *fp32 = 1), either of them None.
+  void weights(int i, int64_t d, void** w0, void** w1, int* fp32) {
+    *fp32 = 0;
+    for (int k = i; k < i + 2; ++k)
+      if (ok && argv[k] != Py_None) {
+        const at::Tensor* t = tensor(k);
+        if (t) *fp32 = t->scalar_type() == kF32;
+      }
+    *w0 = ptr_or_none(i, *fp32 ? kF32 : kBf16, {d});
+    *w1 = ptr_or_none(i + 1, *fp32 ? kF32 : kBf16, {d});
   }
   float number(int i) {
     const double x = PyFloat_AsDouble(argv[i]);
@@ -302,24 +335,283 @@ PyObject* rope_axes_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// Addresses of fa_cross_fwd, fa_cross_workspace_bytes, fa_cross_bwd, fa_cross_bwd_workspace_bytes, fa_rope_axes,
-// fa_rope_axes_paged in the loaded library.
+// q, k, v, o, lse, scale, window, sinks, stream | None, cycles
+PyObject* window_fwd(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 10) return status(-1);
+  Args a{argv};
+  int64_t q[4], k[4];
+  int fp32 = 0;
+  void* pq = a.sized(0, 4, q);
+  void* pk = a.sized(1, 4, k);
+  if (!a.ok || k[0] != q[0] || k[3] != q[3]) return status(-1);
+  void* pv = a.ptr(2, kBf16, {k[0], k[1], k[2], k[3]});
+  void* po = a.out(3, {q[0], q[1], q[2], q[3]}, &fp32);
+  void* lse = a.ptr(4, kF32, {q[0], q[1], q[2]});
+  const float scale = a.number(5);
+  const int window = a.integer(6), sinks = a.integer(7);
+  void* stream = a.stream(8);
+  const fa_window_opts opts{fp32, a.cycles(9)};
+  if (!a.ok) return status(-1);
+  return enqueue([&] {
+    return api.window_fwd(pq, pk, pv, po, static_cast<float*>(lse), q[0], q[1], k[1], q[2], k[2], q[3], scale, window, sinks,
+                          stream, &opts);
+  });
+  END_HANDLE_TH_ERRORS
+}
+
+// q, k, v, o, dout, lse, dq, dk, dv, scale, window, sinks, workspace | None, stream | None, cycles
+PyObject* window_bwd(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 15) return status(-1);
+  Args a{argv};
+  int64_t q[4], k[4];
+  void* pq = a.sized(0, 4, q);
+  void* pk = a.sized(1, 4, k);
+  if (!a.ok || k[0] != q[0] || k[3] != q[3]) return status(-1);
+  int f0 = 0, f1 = 0, f2 = 0;
+  void* pv = a.ptr(2, kBf16, {k[0], k[1], k[2], k[3]});
+  void* po = a.ptr(3, kBf16, {q[0], q[1], q[2], q[3]});
+  void* pdo = a.ptr(4, kBf16, {q[0], q[1], q[2], q[3]});
+  void* lse = a.ptr(5, kF32, {q[0], q[1], q[2]});
+  void* dq = a.out(6, {q[0], q[1], q[2], q[3]}, &f0);
+  void* dk = a.out(7, {k[0], k[1], k[2], k[3]}, &f1);
+  void* dv = a.out(8, {k[0], k[1], k[2], k[3]}, &f2);
+  const float scale = a.number(9);
+  const int window = a.integer(10), sinks = a.integer(11);
+  size_t bytes = 0;
+  void* ws = workspace(a, 12, &bytes);
+  void* stream = a.stream(13);
+  const fa_bwd_opts opts{a.cycles(14)};
+  if (!a.ok || f0 != f1 || f0 != f2) return status(-1);
+  const int B = q[0], Hq = q[1], Hkv = k[1], N = q[2], Nk = k[2], d = q[3];
+  return enqueue([&] {
+    at::Tensor own;
+    if (argv[12] == Py_None && (bytes = api.window_bwd_bytes(B, Hq, Hkv, N, Nk, d, window, sinks)) > 0) {
+      own = scratch(bytes, a.dev);
+      ws = own.data_ptr();
+    }
+    return api.window_bwd(pq, pk, pv, po, pdo, static_cast<const float*>(lse), dq, dk, dv, B, Hq, Hkv, N, Nk, d, scale, window,
+                          sinks, f0, ws, bytes, stream, &opts);
+  });
+  END_HANDLE_TH_ERRORS
+}
+
+// q, k_pages, v_pages, block_table, seq_lens, o, lse, scale, max_seq_len, window, sinks, workspace | None, stream | None,
+// cycles
+PyObject* window_decode_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 14) return status(-1);
+  Args a{argv};
+  int64_t q[3], pool[4];
+  int fp32 = 0;
+  void* pq = a.sized(0, 3, q);
+  void* kp = a.sized(1, 4, pool);
+  if (!a.ok || pool[3] != q[2]) return status(-1);
+  const at::Tensor* table = a.tensor(3);
+  if (!table || table->dim() != 2) return status(-1);
+  const int64_t max_pages = table->size(1);
+  if (max_pages > INT32_MAX) return status(-1);
+  void* vp = a.ptr(2, kBf16, {pool[0], pool[1], pool[2], pool[3]});
+  void* bt = a.ptr(3, kI32, {q[0], max_pages});
+  void* lens = a.ptr(4, kI32, {q[0]});
+  void* po = a.out(5, {q[0], q[1], q[2]}, &fp32);
+  void* lse = a.ptr(6, kF32, {q[0], q[1]});
+  const float scale = a.number(7);
+  const int max_seq_len = a.integer(8), window = a.integer(9), sinks = a.integer(10);
+  size_t bytes = 0;
+  void* ws = workspace(a, 11, &bytes);
+  void* stream = a.stream(12);
+  const fa_decode_opts opts{fp32, a.cycles(13)};
+  if (!a.ok) return status(-1);
+  const int B = q[0], Hq = q[1], Hkv = pool[1], d = q[2], page_size = pool[2];
+  return enqueue([&] {
+    at::Tensor own;
+    if (argv[11] == Py_None &&
+        (bytes = api.window_decode_bytes(B, Hq, Hkv, d, page_size, max_pages, max_seq_len, window, sinks)) > 0) {
+      own = scratch(bytes, a.dev);
+      ws = own.data_ptr();
+    }
+    return api.window_decode(pq, kp, vp, static_cast<const int*>(bt), static_cast<const int*>(lens), po,
+                             static_cast<float*>(lse), B, Hq, Hkv, d, page_size, max_pages, pool[0], max_seq_len, scale,
+                             window, sinks, ws, bytes, stream, &opts);
+  });
+  END_HANDLE_TH_ERRORS
+}
+
+// q and k (or None) of a norm's call: pointers and sizes, k[1] = 0 without k.
+bool norm_inputs(Args& a, int64_t* q, int64_t* k, void** pq, void** pk) {
+  k[1] = 0;
+  *pk = nullptr;
+  *pq = a.sized(0, 4, q);
+  if (a.ok && a.argv[1] != Py_None) {
+    *pk = a.sized(1, 4, k);
+    if (a.ok && (k[0] != q[0] || k[2] != q[2] || k[3] != q[3])) a.ok = false;
+  }
+  return a.ok;
+}
+
+// q, k | None, q_weight | None, k_weight | None, pos, plan, q_out, k_out | None, eps, stream | None
+PyObject* norm_rope_axes(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 10) return status(-1);
+  Args a{argv};
+  int64_t q[4], k[4];
+  void *pq, *pk, *wq, *wk, *ko = nullptr;
+  int fp32 = 0;
+  if (!norm_inputs(a, q, k, &pq, &pk) || (!pk && argv[7] != Py_None)) return status(-1);
+  const Plan plan(argv[5], q[3]);
+  if (!plan.p) return status(-1);
+  a.weights(2, q[3], &wq, &wk, &fp32);
+  void* pos = a.ptr(4, kI32, {plan.p->n_axes, q[0], q[2]});
+  void* qo = a.ptr(6, kBf16, {q[0], q[1], q[2], q[3]});
+  if (pk) ko = a.ptr(7, kBf16, {k[0], k[1], k[2], k[3]});
+  const float eps = a.number(8);
+  void* stream = a.stream(9);
+  if (!a.ok) return status(-1);
+  return enqueue([&] {
+    return api.norm_rope(pq, pk, wq, wk, fp32, static_cast<const int*>(pos), qo, ko, q[0], q[1], k[1], q[2], eps, plan.p,
+                         stream);
+  });
+  END_HANDLE_TH_ERRORS
+}
+
+// q, k | None, q_weight | None, k_weight | None, pos, plan, dq_out, dk_out | None, dq, dk | None, dq_weight | None,
+// dk_weight | None, eps, workspace | None, stream | None
+PyObject* norm_rope_axes_bwd(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 15) return status(-1);
+  Args a{argv};
+  int64_t q[4], k[4];
+  void *pq, *pk, *wq, *wk, *gk = nullptr, *dk = nullptr;
+  int fp32 = 0;
+  if (!norm_inputs(a, q, k, &pq, &pk)) return status(-1);
+  if (!pk && (argv[7] != Py_None || argv[9] != Py_None || argv[11] != Py_None)) return status(-1);
+  const Plan plan(argv[5], q[3]);
+  if (!plan.p) return status(-1);
+  a.weights(2, q[3], &wq, &wk, &fp32);
+  void* pos = a.ptr(4, kI32, {plan.p->n_axes, q[0], q[2]});
+  void* gq = a.ptr(6, kBf16, {q[0], q[1], q[2], q[3]});
+  void* dq = a.ptr(8, kBf16, {q[0], q[1], q[2], q[3]});
+  if (pk) {
+    gk = a.ptr(7, kBf16, {k[0], k[1], k[2], k[3]});
+    dk = a.ptr(9, kBf16, {k[0], k[1], k[2], k[3]});
+  }
+  void* dwq = a.ptr_or_none(10, kF32, {q[3]});
+  void* dwk = a.ptr_or_none(11, kF32, {q[3]});
+  const float eps = a.number(12);
+  size_t bytes = 0;
+  void* ws = workspace(a, 13, &bytes);
+  void* stream = a.stream(14);
+  if (!a.ok) return status(-1);
+  return enqueue([&] {
+    at::Tensor own;
+    if (argv[13] == Py_None && (dwq || dwk) && (bytes = api.norm_rope_bwd_bytes(q[0], q[1], k[1], q[2], q[3])) > 0) {
+      own = scratch(bytes, a.dev);
+      ws = own.data_ptr();
+    }
+    return api.norm_rope_bwd(pq, pk, wq, wk, fp32, static_cast<const int*>(pos), gq, gk, dq, dk, static_cast<float*>(dwq),
+                             static_cast<float*>(dwk), q[0], q[1], k[1], q[2], eps, plan.p, ws, bytes, stream);
+  });
+  END_HANDLE_TH_ERRORS
+}
+
+// q, k, v, q_weight | None, k_weight | None, pos, plan, q_out, k_pages, v_pages, slots, new_lens | None, eps, stream | None
+PyObject* norm_rope_axes_paged(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 14) return status(-1);
+  Args a{argv};
+  int64_t q[4], k[4], pool[4];
+  void *pq, *pk, *wq, *wk;
+  int fp32 = 0;
+  if (!norm_inputs(a, q, k, &pq, &pk) || !pk) return status(-1);
+  void* kp = a.sized(8, 4, pool);
+  if (!a.ok || pool[1] != k[1] || pool[3] != q[3]) return status(-1);
+  const Plan plan(argv[6], q[3]);
+  if (!plan.p) return status(-1);
+  a.weights(3, q[3], &wq, &wk, &fp32);
+  void* pv = a.ptr(2, kBf16, {k[0], k[1], k[2], k[3]});
+  void* pos = a.ptr(5, kI32, {plan.p->n_axes, q[0], q[2]});
+  void* qo = a.ptr(7, kBf16, {q[0], q[1], q[2], q[3]});
+  void* vp = a.ptr(9, kBf16, {pool[0], pool[1], pool[2], pool[3]});
+  void* slots = a.ptr(10, kI64, {q[0], q[2]});
+  void* news = a.ptr_or_none(11, kI32, {q[0]});
+  const float eps = a.number(12);
+  void* stream = a.stream(13);
+  if (!a.ok) return status(-1);
+  return enqueue([&] {
+    return api.norm_rope_paged(pq, pk, pv, wq, wk, fp32, static_cast<const int*>(pos), qo, kp, vp,
+                               static_cast<const long long*>(slots), static_cast<const int*>(news), q[0], q[1], k[1], q[2],
+                               pool[2], pool[0], eps, plan.p, stream);
+  });
+  END_HANDLE_TH_ERRORS
+}
+
+// block_table, seq_lens, new_lens, free_pages, n_free, granted, slots | None, page_size, stream | None
+PyObject* pages_extend(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 9) return status(-1);
+  Args a{argv};
+  const at::Tensor* table = a.tensor(0);
+  if (!table || table->dim() != 2) return status(-1);
+  const at::Tensor* stack = a.tensor(3);
+  if (!stack || stack->dim() != 1) return status(-1);
+  const int64_t B = table->size(0), max_pages = table->size(1), num_pages = stack->size(0);
+  int64_t N = 0;
+  if (argv[6] != Py_None) {
+    const at::Tensor* slots = a.tensor(6);
+    if (!slots || slots->dim() != 2) return status(-1);
+    N = slots->size(1);
+  }
+  if (B > INT32_MAX || max_pages > INT32_MAX || num_pages > INT32_MAX || N > INT32_MAX) return status(-1);
+  void* bt = a.ptr(0, kI32, {B, max_pages});
+  void* lens = a.ptr(1, kI32, {B});
+  void* news = a.ptr(2, kI32, {B});
+  void* free = a.ptr(3, kI32, {num_pages});
+  void* n_free = a.ptr(4, kI32, {1});
+  void* granted = a.ptr(5, kI32, {B});
+  void* slots = a.ptr_or_none(6, kI64, {B, N});
+  const int page_size = a.integer(7);
+  void* stream = a.stream(8);
+  if (!a.ok) return status(-1);
+  return enqueue([&] {
+    return api.pages_extend(static_cast<int*>(bt), static_cast<int*>(lens), static_cast<const int*>(news),
+                            static_cast<int*>(free), static_cast<int*>(n_free), static_cast<int*>(granted),
+                            static_cast<long long*>(slots), B, N, page_size, max_pages, num_pages, stream);
+  });
+  END_HANDLE_TH_ERRORS
+}
+
+// Addresses of the library's entry points, in the order of Api.
 PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t n) {
-  void* p[6];
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind takes 6 addresses");
+  constexpr int kCount = 16;
+  void* p[kCount];
+  if (n != kCount) {
+    PyErr_Format(PyExc_TypeError, "bind takes %d addresses", kCount);
     return nullptr;
   }
-  for (int i = 0; i < 6; ++i) {
+  for (int i = 0; i < kCount; ++i) {
     p[i] = PyLong_AsVoidPtr(argv[i]);
     if (PyErr_Occurred()) return nullptr;
   }
-  api.cross_fwd = reinterpret_cast<decltype(api.cross_fwd)>(p[0]);
-  api.cross_bytes = reinterpret_cast<decltype(api.cross_bytes)>(p[1]);
-  api.cross_bwd = reinterpret_cast<decltype(api.cross_bwd)>(p[2]);
-  api.cross_bwd_bytes = reinterpret_cast<decltype(api.cross_bwd_bytes)>(p[3]);
-  api.rope = reinterpret_cast<decltype(api.rope)>(p[4]);
-  api.rope_paged = reinterpret_cast<decltype(api.rope_paged)>(p[5]);
+  int i = 0;
+  auto set = [&](auto& f) { f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(p[i++]); };
+  set(api.cross_fwd);
+  set(api.cross_bytes);
+  set(api.cross_bwd);
+  set(api.cross_bwd_bytes);
+  set(api.rope);
+  set(api.rope_paged);
+  set(api.window_fwd);
+  set(api.window_bwd);
+  set(api.window_bwd_bytes);
+  set(api.window_decode);
+  set(api.window_decode_bytes);
+  set(api.norm_rope);
+  set(api.norm_rope_bwd);
+  set(api.norm_rope_bwd_bytes);
+  set(api.norm_rope_paged);
+  set(api.pages_extend);
   Py_RETURN_NONE;
 }
 
@@ -333,6 +625,13 @@ PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"cross_bwd", fast(cross_bwd), METH_FASTCALL, nullptr},
                          {"rope_axes", fast(rope_axes), METH_FASTCALL, nullptr},
                          {"rope_axes_paged", fast(rope_axes_paged), METH_FASTCALL, nullptr},
+                         {"window_fwd", fast(window_fwd), METH_FASTCALL, nullptr},
+                         {"window_bwd", fast(window_bwd), METH_FASTCALL, nullptr},
+                         {"window_decode_paged", fast(window_decode_paged), METH_FASTCALL, nullptr},
+                         {"norm_rope_axes", fast(norm_rope_axes), METH_FASTCALL, nullptr},
+                         {"norm_rope_axes_bwd", fast(norm_rope_axes_bwd), METH_FASTCALL, nullptr},
+                         {"norm_rope_axes_paged", fast(norm_rope_axes_paged), METH_FASTCALL, nullptr},
+                         {"pages_extend", fast(pages_extend), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -5,9 +5,9 @@ passes their device pointers and the current CUDA stream to the function of
 the same name in ``libfattn.so`` and raises ``FattnError`` on a non-OK status.
 All computation happens in the library's kernels; there is no fallback.
 
-The library is called through ctypes; cross attention and rotary positions go
-through the compiled module ``_calls`` (csrc/py_calls.cpp), which makes the
-same checks on the tensors in C++: a decode step's kernels take less time than
+The library is called through ctypes; cross attention, sliding windows, rotary
+positions, norms and the cache's pages go through the compiled module ``_calls``
+(csrc/py_calls.cpp), which makes the same checks on the tensors in C++: a decode step's kernels take less time than
 these checks in Python.  The module is loaded by the first of those calls; the
 others need the library alone.
 """
@@ -39,7 +39,11 @@ EXPORTED = ("fa_fwd", "fa_fwd_ex", "fa_fwd_workspace_bytes", "fa_fwd_partial", "
             "fa_decode_splitkv_ex", "fa_decode_splitkv_noalloc", "fa_decode_paged_workspace_bytes",
             "fa_decode_paged", "fa_decode_paged_ex", "fa_combine", "fa_combine_ex",
             "fa_cross_workspace_bytes", "fa_cross_fwd", "fa_cross_bwd_workspace_bytes", "fa_cross_bwd",
-            "fa_rope_axes_plan", "fa_rope_axes", "fa_rope_axes_paged", "fa_get_status",
+            "fa_rope_axes_plan", "fa_rope_axes", "fa_rope_axes_paged",
+            "fa_window_fwd", "fa_window_bwd_workspace_bytes", "fa_window_bwd",
+            "fa_window_decode_paged_workspace_bytes", "fa_window_decode_paged", "fa_norm_rope_axes",
+            "fa_norm_rope_axes_bwd_workspace_bytes", "fa_norm_rope_axes_bwd", "fa_norm_rope_axes_paged",
+            "fa_pages_extend", "fa_get_status",
             "fa_status_string", "fa_last_error")
 FA_NOALLOC_SCRATCH_BYTES = 8 << 20
 FA_ROPE_MAX_AXES = 4
@@ -65,6 +69,10 @@ class FaBwdOpts(ctypes.Structure):
 
 
 class FaCrossOpts(ctypes.Structure):
+    _fields_ = [("o_fp32", ctypes.c_int), ("wait_budget_cycles", ctypes.c_ulonglong)]
+
+
+class FaWindowOpts(ctypes.Structure):
     _fields_ = [("o_fp32", ctypes.c_int), ("wait_budget_cycles", ctypes.c_ulonglong)]
 
 
@@ -123,6 +131,19 @@ def lib() -> ctypes.CDLL:
         L.fa_rope_axes_plan.argtypes = [plan, i, i, ctypes.POINTER(i), ctypes.c_double, i, i, i]
         L.fa_rope_axes.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, plan, i, vp]
         L.fa_rope_axes_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, plan, vp]
+        L.fa_window_fwd.argtypes = [vp] * 5 + [i] * 6 + [f, i, i, vp, ctypes.POINTER(FaWindowOpts)]
+        L.fa_window_bwd_workspace_bytes.argtypes = [i] * 8
+        L.fa_window_bwd_workspace_bytes.restype = sz
+        L.fa_window_bwd.argtypes = [vp] * 9 + [i] * 6 + [f, i, i, i, vp, sz, vp, ctypes.POINTER(FaBwdOpts)]
+        L.fa_window_decode_paged_workspace_bytes.argtypes = [i] * 9
+        L.fa_window_decode_paged_workspace_bytes.restype = sz
+        L.fa_window_decode_paged.argtypes = [vp] * 7 + [i] * 8 + [f, i, i, vp, sz, vp, ctypes.POINTER(FaDecodeOpts)]
+        L.fa_norm_rope_axes.argtypes = [vp] * 4 + [i] + [vp] * 3 + [i] * 4 + [f, plan, vp]
+        L.fa_norm_rope_axes_bwd_workspace_bytes.argtypes = [i] * 5
+        L.fa_norm_rope_axes_bwd_workspace_bytes.restype = sz
+        L.fa_norm_rope_axes_bwd.argtypes = [vp] * 4 + [i] + [vp] * 7 + [i] * 4 + [f, plan, vp, sz, vp]
+        L.fa_norm_rope_axes_paged.argtypes = [vp] * 5 + [i] + [vp] * 6 + [i] * 6 + [f, plan, vp]
+        L.fa_pages_extend.argtypes = [vp] * 7 + [i] * 5 + [vp]
         L.fa_get_status.argtypes = [vp]
         L.fa_status_string.argtypes = [i]
         L.fa_status_string.restype = ctypes.c_char_p
@@ -132,7 +153,9 @@ def lib() -> ctypes.CDLL:
                      "fa_bwd", "fa_bwd_ex",
                      "fa_decode_splitkv", "fa_decode_splitkv_ex", "fa_decode_splitkv_noalloc", "fa_decode_paged",
                      "fa_decode_paged_ex", "fa_combine", "fa_combine_ex", "fa_cross_fwd", "fa_cross_bwd",
-                     "fa_rope_axes_plan", "fa_rope_axes", "fa_rope_axes_paged", "fa_get_status"):
+                     "fa_rope_axes_plan", "fa_rope_axes", "fa_rope_axes_paged", "fa_window_fwd", "fa_window_bwd",
+                     "fa_window_decode_paged", "fa_norm_rope_axes", "fa_norm_rope_axes_bwd", "fa_norm_rope_axes_paged",
+                     "fa_pages_extend", "fa_get_status"):
             getattr(L, name).restype = i
         _lib = L
     return _lib
@@ -153,7 +176,9 @@ def _load_calls():
                                               "build it with exact_attention_06_gb300.build")
     calls.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
         "fa_cross_fwd", "fa_cross_workspace_bytes", "fa_cross_bwd", "fa_cross_bwd_workspace_bytes",
-        "fa_rope_axes", "fa_rope_axes_paged")))
+        "fa_rope_axes", "fa_rope_axes_paged", "fa_window_fwd", "fa_window_bwd", "fa_window_bwd_workspace_bytes",
+        "fa_window_decode_paged", "fa_window_decode_paged_workspace_bytes", "fa_norm_rope_axes", "fa_norm_rope_axes_bwd",
+        "fa_norm_rope_axes_bwd_workspace_bytes", "fa_norm_rope_axes_paged", "fa_pages_extend")))
     _calls = calls
 
 
@@ -192,6 +217,7 @@ _F32 = (torch.float32,)
 _OUT = (torch.bfloat16, torch.float32)
 _U8 = (torch.uint8,)
 _I32 = (torch.int32,)
+_I64 = (torch.int64,)
 
 
 def _need(func: str, name: str, t, dtypes, shape=None):
@@ -614,6 +640,216 @@ def fa_rope_axes_paged(q, k, v, pos, plan, q_out, k_pages, v_pages, block_table,
             _refuse_paged("fa_rope_axes_paged", q, k, v, pos, plan, q_out, k_pages, v_pages, block_table, seq_lens,
                           new_lens)
         _check(st, "fa_rope_axes_paged")
+
+
+def _window_sizes(func: str, q, k, rest, workspace=None):
+    """Check a windowed call's tensors (``rest``: those of q's, k's and lse's shapes); the call's sizes."""
+    return _cross_sizes(func, q, k, rest, None, workspace)
+
+
+def _window_bwd_sizes(q, k, v, o, dout, lse, dq, dk, dv, workspace):
+    grad = (dq.dtype,) if isinstance(dq, torch.Tensor) and dq.dtype in _OUT else _OUT
+    return _window_sizes("fa_window_bwd", q, k, (
+        ("v", v, _BF16, "k"), ("o", o, _BF16, "q"), ("dout", dout, _BF16, "q"), ("lse", lse, _F32, "lse"),
+        ("dq", dq, grad, "q"), ("dk", dk, grad, "k"), ("dv", dv, grad, "k")), workspace)
+
+
+def fa_window_fwd(q, k, v, o, lse, scale: float, window: int, sinks: int = 0, stream=None, wait_budget_cycles: int = 0):
+    """Causal attention with a sliding window and sinks: q [B, Hq, N, d] are the last N tokens of the Nk that k, v
+    [B, Hkv, Nk, d] hold (query head h reads key head h // (Hq // Hkv)); each sees the ``window`` keys up to its own and
+    the first ``sinks``.  o like q, bf16 or fp32 (from its dtype); lse [B, Hq, N] fp32."""
+    if _calls is None:
+        _load_calls()
+    st = _calls.window_fwd(q, k, v, o, lse, scale, window, sinks, _handle(stream), wait_budget_cycles)
+    if st:
+        if st < 0:
+            _window_sizes("fa_window_fwd", q, k, (("v", v, _BF16, "k"), ("o", o, _OUT, "q"), ("lse", lse, _F32, "lse")))
+            _refused("fa_window_fwd")
+        _check(st, "fa_window_fwd")
+
+
+def fa_window_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, N: int, Nk: int, d: int, window: int, sinks: int = 0) -> int:
+    return int(lib().fa_window_bwd_workspace_bytes(B, Hq, Hkv, N, Nk, d, window, sinks))
+
+
+def fa_window_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale: float, window: int, sinks: int = 0, workspace=None,
+                  stream=None, wait_budget_cycles: int = 0):
+    """Gradients of fa_window_fwd (which produced the bf16 o, and lse, with the same scale, window and sinks): dq like
+    q, dk and dv like k, bf16 or fp32 (from dq's dtype).  ``workspace``: a 1-dimensional uint8 CUDA tensor of
+    fa_window_bwd_workspace_bytes() bytes; allocated here when None."""
+    if _calls is None:
+        _load_calls()
+    handle = _handle(stream)
+    if stream is not None and workspace is None:
+        sizes = _window_bwd_sizes(q, k, v, o, dout, lse, dq, dk, dv, workspace)
+        nbytes = fa_window_bwd_workspace_bytes(*sizes, window, sinks)
+        workspace = _workspace_on(stream, nbytes, q.device) if nbytes else None
+    st = _calls.window_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale, window, sinks, workspace, handle, wait_budget_cycles)
+    if st:
+        if st < 0:
+            _window_bwd_sizes(q, k, v, o, dout, lse, dq, dk, dv, workspace)
+            _refused("fa_window_bwd")
+        _check(st, "fa_window_bwd")
+
+
+def fa_window_decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, d: int, page_size: int, max_pages: int,
+                                           max_seq_len: int, window: int, sinks: int = 0) -> int:
+    return int(lib().fa_window_decode_paged_workspace_bytes(B, Hq, Hkv, d, page_size, max_pages, max_seq_len, window, sinks))
+
+
+def _window_decode_sizes(q, k_pages, v_pages, block_table, seq_lens, o, lse, workspace):
+    func = "fa_window_decode_paged"
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise FattnError(FA_ERR_INVALID_ARG, func, "q must be a 3-dimensional torch.Tensor")
+    B, Hq, d = q.shape
+    P, Hkv, page_size, _ = _shape4(func, "k_pages", k_pages)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise FattnError(FA_ERR_INVALID_ARG, func, "block_table must be a 2-dimensional torch.Tensor")
+    pool = (P, Hkv, page_size, d)
+    _need_here(func, ("q", q, _BF16, (B, Hq, d)), ("k_pages", k_pages, _BF16, pool), ("v_pages", v_pages, _BF16, pool),
+               ("block_table", block_table, _I32, (B, block_table.shape[1])), ("seq_lens", seq_lens, _I32, (B,)),
+               ("o", o, _OUT, (B, Hq, d)), ("lse", lse, _F32, (B, Hq)))
+    if workspace is not None:
+        _need_here(func, ("workspace", workspace, _U8, None))
+    return B, Hq, Hkv, d, page_size, block_table.shape[1]
+
+
+def fa_window_decode_paged(q, k_pages, v_pages, block_table, seq_lens, o, lse, scale: float, max_seq_len: int, window: int,
+                           sinks: int = 0, workspace=None, stream=None, wait_budget_cycles: int = 0):
+    """One token of each sequence over a paged cache, seeing the last ``window`` keys and the first ``sinks``: q
+    [B, Hq, d]; k_pages/v_pages [P, Hkv, page_size, d] (shared heads as fa_window_fwd); block_table [B, max_pages] and
+    seq_lens [B] int32; o [B, Hq, d] bf16 or fp32 (from its dtype); lse [B, Hq] fp32.  ``workspace``: a 1-dimensional
+    uint8 CUDA tensor of fa_window_decode_paged_workspace_bytes() bytes; allocated here when None."""
+    if _calls is None:
+        _load_calls()
+    handle = _handle(stream)
+    if stream is not None and workspace is None:
+        sizes = _window_decode_sizes(q, k_pages, v_pages, block_table, seq_lens, o, lse, workspace)
+        nbytes = fa_window_decode_paged_workspace_bytes(*sizes, max_seq_len, window, sinks)
+        workspace = _workspace_on(stream, nbytes, q.device) if nbytes else None
+    st = _calls.window_decode_paged(q, k_pages, v_pages, block_table, seq_lens, o, lse, scale, max_seq_len, window, sinks,
+                                    workspace, handle, wait_budget_cycles)
+    if st:
+        if st < 0:
+            _window_decode_sizes(q, k_pages, v_pages, block_table, seq_lens, o, lse, workspace)
+            _refused("fa_window_decode_paged")
+        _check(st, "fa_window_decode_paged")
+
+
+def _refuse_norm(func: str, q, k, q_weight, k_weight, pos, plan, of_q=(), of_k=(), of_d=(), more=()):
+    """Find what a norm's call was refused for: ``of_q``, ``of_k``: (name, tensor) like q and k, ``of_d``: fp32 [d] or
+    None; ``more``: other entries of _need_here."""
+    B, Hq, N, d = qs = _shape4(func, "q", q)
+    _need_here(func, ("q", q, _BF16, qs), *((name, t, _BF16, qs) for name, t in of_q))
+    if k is not None:
+        ks = (B, _shape4(func, "k", k)[1], N, d)
+        _need_here(func, ("k", k, _BF16, ks), *((name, t, _BF16, ks) for name, t in of_k))
+    elif any(t is not None for _, t in of_k):
+        raise FattnError(FA_ERR_INVALID_ARG, func, "gradients or outputs of k without k")
+    _need_plan(func, plan, d)
+    _need_here(func, ("pos", pos, _I32, (plan.n_axes, B, N)))
+    weights = [(name, w) for name, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None]
+    for name, w in weights:
+        dtype = weights[0][1].dtype if isinstance(weights[0][1], torch.Tensor) else None
+        _need_here(func, (name, w, (dtype,) if dtype in _OUT else _OUT, (d,)))
+    for name, t in of_d:
+        if t is not None:
+            _need_here(func, (name, t, _F32, (d,)))
+    _need_here(func, *more)
+
+
+def fa_norm_rope_axes(q, k, q_weight, k_weight, pos, plan, q_out=None, k_out=None, eps: float = 1e-6, stream=None):
+    """RMS norm of each head's q [B, Hq, N, d] and k [B, Hk, N, d] (or None) with weights [d] (both bf16 or both fp32; None:
+    ones), then the rotation of fa_rope_axes, in one pass; in place where an output is None or its input."""
+    if _calls is None:
+        _load_calls()
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    st = _calls.norm_rope_axes(q, k, q_weight, k_weight, pos, plan, q_out, k_out, eps, _handle(stream))
+    if st:
+        if st < 0:
+            _refuse_norm("fa_norm_rope_axes", q, k, q_weight, k_weight, pos, plan, [("q_out", q_out)], [("k_out", k_out)])
+            _refused("fa_norm_rope_axes")
+        _check(st, "fa_norm_rope_axes")
+
+
+def fa_norm_rope_axes_bwd_workspace_bytes(B: int, Hq: int, Hk: int, N: int, d: int) -> int:
+    return int(lib().fa_norm_rope_axes_bwd_workspace_bytes(B, Hq, Hk, N, d))
+
+
+def fa_norm_rope_axes_bwd(q, k, q_weight, k_weight, pos, plan, dq_out, dk_out, dq=None, dk=None, dq_weight=None,
+                          dk_weight=None, eps: float = 1e-6, workspace=None, stream=None):
+    """Gradients of fa_norm_rope_axes from q, k (its inputs) and the gradients dq_out, dk_out of its outputs: dq and dk
+    (in dq_out's and dk_out's place where None), dq_weight and dk_weight [d] fp32 (None: not computed).  ``workspace``: a
+    1-dimensional uint8 CUDA tensor of fa_norm_rope_axes_bwd_workspace_bytes() bytes; allocated here when None."""
+    if _calls is None:
+        _load_calls()
+    dq = dq_out if dq is None else dq
+    dk = dk_out if dk is None else dk
+    handle = _handle(stream)
+
+    def check():
+        more = [] if workspace is None else [("workspace", workspace, _U8, None)]
+        _refuse_norm("fa_norm_rope_axes_bwd", q, k, q_weight, k_weight, pos, plan, [("dq_out", dq_out), ("dq", dq)],
+                     [("dk_out", dk_out), ("dk", dk)], [("dq_weight", dq_weight), ("dk_weight", dk_weight)], more)
+
+    if stream is not None and workspace is None and (dq_weight is not None or dk_weight is not None):
+        check()
+        B, Hq, N, d = q.shape
+        nbytes = fa_norm_rope_axes_bwd_workspace_bytes(B, Hq, 0 if k is None else k.shape[1], N, d)
+        workspace = _workspace_on(stream, nbytes, q.device) if nbytes else None
+    st = _calls.norm_rope_axes_bwd(q, k, q_weight, k_weight, pos, plan, dq_out, dk_out, dq, dk, dq_weight, dk_weight, eps,
+                                   workspace, handle)
+    if st:
+        if st < 0:
+            check()
+            _refused("fa_norm_rope_axes_bwd")
+        _check(st, "fa_norm_rope_axes_bwd")
+
+
+def fa_norm_rope_axes_paged(q, k, v, q_weight, k_weight, pos, plan, q_out, k_pages, v_pages, slots, new_lens=None,
+                            eps: float = 1e-6, stream=None):
+    """New tokens of a decode step or prompt chunk: q [B, Hq, N, d] normed and turned into q_out, k [B, Hk, N, d] (the
+    same) and v (copied) into the pools k_pages, v_pages [P, Hk, page_size, d] at fa_pages_extend's slots [B, N] int64
+    (-1: nowhere); tokens from new_lens[b] (int32 [B]) on are padding."""
+    if _calls is None:
+        _load_calls()
+    st = _calls.norm_rope_axes_paged(q, k, v, q_weight, k_weight, pos, plan, q_out, k_pages, v_pages, slots, new_lens, eps,
+                                     _handle(stream))
+    if st:
+        if st < 0:
+            func = "fa_norm_rope_axes_paged"
+            B, _, N, d = _shape4(func, "q", q)
+            Hk = _shape4(func, "k", k)[1]
+            P, _, page_size, _ = _shape4(func, "k_pages", k_pages)
+            pool = (P, Hk, page_size, d)
+            _refuse_norm(func, q, k, q_weight, k_weight, pos, plan, [("q_out", q_out)], [("v", v)], more=(
+                ("k_pages", k_pages, _BF16, pool), ("v_pages", v_pages, _BF16, pool), ("slots", slots, _I64, (B, N)),
+                *([] if new_lens is None else [("new_lens", new_lens, _I32, (B,))])))
+            _refused(func)
+        _check(st, "fa_norm_rope_axes_paged")
+
+
+def fa_pages_extend(block_table, seq_lens, new_lens, free_pages, n_free, granted, slots, page_size: int, stream=None):
+    """Pages of the paged cache: sequence b grows by new_lens[b] tokens (shrinks where negative).  int32 CUDA tensors
+    block_table [B, max_pages], seq_lens [B], free_pages [P] (a stack of page ids) and n_free [1] are updated, granted
+    [B] gets each sequence's change, slots [B, N] int64 (or None) the rows of the new tokens in the pools."""
+    if _calls is None:
+        _load_calls()
+    st = _calls.pages_extend(block_table, seq_lens, new_lens, free_pages, n_free, granted, slots, page_size, _handle(stream))
+    if st:
+        func = "fa_pages_extend"
+        if st < 0:
+            for name, t, dims in (("block_table", block_table, 2), ("free_pages", free_pages, 1), ("slots", slots, 2)):
+                if not (t is None and name == "slots") and (not isinstance(t, torch.Tensor) or t.dim() != dims):
+                    raise FattnError(FA_ERR_INVALID_ARG, func, f"{name} must be a {dims}-dimensional torch.Tensor")
+            B = block_table.shape[0]
+            _need_here(func, ("block_table", block_table, _I32, None), ("seq_lens", seq_lens, _I32, (B,)),
+                       ("new_lens", new_lens, _I32, (B,)), ("free_pages", free_pages, _I32, None),
+                       ("n_free", n_free, _I32, (1,)), ("granted", granted, _I32, (B,)),
+                       *([] if slots is None else [("slots", slots, _I64, (B, slots.shape[1]))]))
+            _refused(func)
+        _check(st, func)
 
 
 def fa_get_status(stream=None) -> int:

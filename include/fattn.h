@@ -512,6 +512,143 @@ fa_status_t fa_rope_axes_paged(const void* q, const void* k, const void* v, cons
                                int num_pages, const fa_rope_axes_plan_t* plan, void* stream);
 
 /*
+ * Causal attention with a sliding window and sinks (the first tokens, which stay visible).  The N queries of a sequence
+ * are its last ones: query i stands at position p = Nk - N + i and sees key j when
+ *     j <= p   and   (j > p - window  or  j < sinks).
+ * Query heads may share key heads: query head h reads key head h / (Hq / Hkv).  N = Nk is a whole prompt or a
+ * training step, N < Nk a chunk of a prompt behind earlier keys.  (One token over a paged cache:
+ * fa_window_decode_paged.)
+ *
+ *   q         [B, Hq, N, d] bf16, 16-byte aligned.
+ *   k, v      [B, Hkv, Nk, d] bf16, 16-byte aligned.  Hq a multiple of Hkv, N <= Nk.  Keys that no query sees
+ *             (before the first query's window, but for the sinks) may hold anything, infinities and NaN
+ *             included, and have no influence; they get gradients of 0.
+ *   window    >= 1 (1: its own key alone; >= Nk: plain causal attention).
+ *   sinks     0 .. 128 (FA_ERR_UNSUPPORTED beyond).
+ *   o         [B, Hq, N, d] bf16, or fp32 with opts->o_fp32 (written), 16-byte aligned.
+ *   lse       [B, Hq, N] fp32 (written), natural log of the scaled scores, as for fa_fwd.
+ *   d in {64, 128}; scale finite and > 0; every size >= 1.
+ */
+typedef struct {
+  int o_fp32;                            /* 0: O is bf16 (round to nearest even); 1: O is fp32 */
+  unsigned long long wait_budget_cycles; /* per-wait budget in SM cycles, as in fa_fwd_opts (0 = default) */
+} fa_window_opts;
+
+/* fa_window_fwd -- opts may be NULL.  One kernel, no workspace. */
+fa_status_t fa_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int N,
+                          int Nk, int d, float scale, int window, int sinks, void* stream, const fa_window_opts* opts);
+
+/* Scratch bytes of fa_window_bwd on the current device: rowsum(O * dO) per query row, and fp32 partial gradients of
+ * the key tile with the sinks, which every query reaches, and of all keys where there are few key tiles under many
+ * queries.  0 for invalid sizes or without a device. */
+size_t fa_window_bwd_workspace_bytes(int B, int Hq, int Hkv, int N, int Nk, int d, int window, int sinks);
+
+/* fa_window_bwd -- the gradients, by the formulas of fa_bwd: dq like q, dk and dv like k and v (bf16, or fp32 when
+ * grad_fp32 = 1).  dk and dv sum over the query heads that share the key head.  o (bf16) and lse are
+ * fa_window_fwd's for the same q, k, v, scale, window and sinks.  No atomics: the gradients are bitwise
+ * repeatable.  A workspace serves one call at a time.  opts may be NULL. */
+fa_status_t fa_window_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                          void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int N, int Nk, int d, float scale,
+                          int window, int sinks, int grad_fp32, void* workspace, size_t ws_bytes, void* stream,
+                          const fa_bwd_opts* opts);
+
+/*
+ * fa_window_decode_paged -- one token of each sequence, at its last position, over the paged cache of fa_decode_paged
+ * with shared heads: it sees the last `window` keys of its sequence and the first `sinks`.
+ *
+ *   q            [B, Hq, d] bf16, 16-byte aligned.  Hq / Hkv at most 32 (FA_ERR_UNSUPPORTED beyond).
+ *   k_pages,     [num_pages, Hkv, page_size, d] bf16 pools, block_table [B, max_pages] and seq_lens [B] int32,
+ *   v_pages      page_size and max_seq_len as for fa_decode_paged.  Only the table's entries of pages that hold a visible
+ *                key are read, and only those pages: pages between the sinks and the window may be given
+ *                back.  A sequence of length 0 gets O = 0 and lse = -inf.
+ *   window       >= 1 (>= max_seq_len: every key);   sinks 0 .. 128.
+ *   o [B, Hq, d] bf16 (fp32 with opts->o_fp32), 16-byte aligned; lse [B, Hq] fp32 (written).
+ *   workspace    caller-owned scratch of fa_window_decode_paged_workspace_bytes() bytes (0 where none is needed),
+ *                256-byte aligned (FA_ERR_WORKSPACE if smaller), or NULL: one kernel without partials.  O and lse are
+ *                the same function of the inputs either way, up to rounding order.
+ * What a page holds in rows that are not visible has no influence.  opts may be NULL.
+ */
+size_t fa_window_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d, int page_size, int max_pages, int max_seq_len,
+                                              int window, int sinks);
+fa_status_t fa_window_decode_paged(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                                   const int* seq_lens, void* o, float* lse, int B, int Hq, int Hkv, int d, int page_size,
+                                   int max_pages, int num_pages, int max_seq_len, float scale, int window, int sinks,
+                                   void* workspace, size_t ws_bytes, void* stream, const fa_decode_opts* opts);
+
+/*
+ * RMS norm of each head's q and k, then the rotation of fa_rope_axes, in one pass:
+ *     y = R (w * x / sqrt(mean(x^2) + eps))     over the d elements of a head's row.
+ *
+ *   q, k      as for fa_rope_axes (Hk = 0: q alone); pos, plan likewise.
+ *   q_weight, [d] bf16, or fp32 with weight_fp32 = 1; NULL: all ones.
+ *   k_weight
+ *   eps       finite and > 0.
+ * Norm, cos, sin and products in fp32, one rounding to bf16 (nearest even).
+ */
+
+/* fa_norm_rope_axes -- q into q_out and k into k_out, in one kernel.  An output may be its own input; otherwise
+ * they do not overlap. */
+fa_status_t fa_norm_rope_axes(const void* q, const void* k, const void* q_weight, const void* k_weight, int weight_fp32,
+                              const int* pos, void* q_out, void* k_out, int B, int Hq, int Hk, int N, float eps,
+                              const fa_rope_axes_plan_t* plan, void* stream);
+
+/* Scratch bytes of fa_norm_rope_axes_bwd's partial sums on the current device; 0 for invalid sizes or without one. */
+size_t fa_norm_rope_axes_bwd_workspace_bytes(int B, int Hq, int Hk, int N, int d);
+
+/* fa_norm_rope_axes_bwd -- from q, k (the inputs of fa_norm_rope_axes) and the gradients dq_out, dk_out of its outputs:
+ *   dq, dk      [B, H, N, d] bf16 (written): the gradients of q and k.  One may be its dq_out (dk_out), or its q (k),
+ *               in place; otherwise they do not overlap.
+ *   dq_weight,  [d] fp32 (written), or NULL: the gradients of the weights, summed over sequences, heads and tokens.
+ *   dk_weight
+ *   workspace   >= fa_norm_rope_axes_bwd_workspace_bytes() bytes, 256-byte aligned; needed where a weight's gradient is
+ *               wanted (FA_ERR_WORKSPACE).
+ * No atomics: the gradients are bitwise repeatable. */
+fa_status_t fa_norm_rope_axes_bwd(const void* q, const void* k, const void* q_weight, const void* k_weight, int weight_fp32,
+                                  const int* pos, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                  float* dq_weight, float* dk_weight, int B, int Hq, int Hk, int N, float eps,
+                                  const fa_rope_axes_plan_t* plan, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * fa_norm_rope_axes_paged -- the serving form: the N new tokens of each sequence.  q is normed and turned into q_out, k
+ * (the same) and v [B, Hk, N, d] (copied) go into the pools [num_pages, Hk, page_size, d] at the slots that
+ * fa_pages_extend gives.
+ *   slots      [B, N] int64, 8-byte aligned: token n of sequence b goes to row slot % page_size of page
+ *              slot / page_size.  A slot outside [0, num_pages * page_size) is no place: that token's k and v are not
+ *              written.  Two tokens of one call must not share a slot.
+ *   new_lens   [B] int32 or NULL: tokens from new_lens[b] on are padding, for which nothing is written (not to
+ *              q_out either), as for fa_rope_axes_paged.
+ */
+fa_status_t fa_norm_rope_axes_paged(const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
+                                    int weight_fp32, const int* pos, void* q_out, void* k_pages, void* v_pages,
+                                    const long long* slots, const int* new_lens, int B, int Hq, int Hk, int N, int page_size,
+                                    int num_pages, float eps, const fa_rope_axes_plan_t* plan, void* stream);
+
+/*
+ * fa_pages_extend -- the pages of a paged cache, on the GPU: sequence b grows by new_lens[b] tokens, or shrinks by
+ * -new_lens[b] (a finished request by its whole length, rejected draft tokens by their number).
+ *
+ *   block_table  [B, max_pages] int32, read and written: entries of new pages get their ids, those of pages given back
+ *                become -1; no other entry is touched.
+ *   seq_lens     [B] int32, read and written: lengths (clamped to [0, max_pages * page_size]), which grow by what is
+ *                granted.
+ *   new_lens     [B] int32: the change of each sequence; no sequence shrinks below 0.
+ *   free_pages   [num_pages] int32, read and written: a stack of free page ids, of which the first n_free[0] count.
+ *   n_free       [1] int32, read and written.
+ *   granted      [B] int32 (written): the change made: new_lens[b], or 0 where a sequence would outgrow its table or
+ *                the stack runs out.  Pages are handed out in the order of the sequences, each sequence's from the top
+ *                of the stack down, and from the first that the stack cannot serve on, none is; a sequence whose tokens
+ *                fit its last page is always served.  Fit to be the new_lens of the calls that write the tokens.
+ *   slots        [B, N] int64 (written), or NULL: token n of those granted to sequence b is row slot % page_size of page
+ *                slot / page_size; -1 for n >= granted[b].  N: tokens a sequence that the caller has slots for.
+ * Pages given back go onto the stack once the call's own pages are taken, so that they come off again in their old
+ * order: giving back what the call before granted leaves the stack as it was.  Entries given back must be
+ * pages that the stack handed out: they are put on it as they are.  seq_lens, new_lens and granted are arrays of their own.
+ * page_size is a positive multiple of 64.  The result does not depend on timing.
+ */
+fa_status_t fa_pages_extend(int* block_table, int* seq_lens, const int* new_lens, int* free_pages, int* n_free, int* granted,
+                            long long* slots, int B, int N, int page_size, int max_pages, int num_pages, void* stream);
+
+/*
  * fa_get_status -- synchronise `stream`, then read and clear the current
  * device's kernel status words (by a small kernel and a copy on `stream`, and
  * a second synchronisation).  Returns FA_ERR_TIMEOUT if any kernel of this
