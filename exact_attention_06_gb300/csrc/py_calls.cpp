@@ -15,7 +15,6 @@
 
 #include <cstdint>
 #include <initializer_list>
-#include <type_traits>
 
 #include "fattn.h"
 
@@ -582,37 +581,35 @@ PyObject* pages_extend(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// Addresses of the library's entry points, in the order of Api.
-PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t n) {
-  constexpr int kCount = 16;
-  void* p[kCount];
-  if (n != kCount) {
-    PyErr_Format(PyExc_TypeError, "bind takes %d addresses", kCount);
+// Reads addresses into the entry points, in their order.
+template <typename... Fn>
+PyObject* set_all(PyObject* const* argv, Py_ssize_t n, Fn&... fn) {
+  if (n != static_cast<Py_ssize_t>(sizeof...(fn))) {
+    PyErr_Format(PyExc_TypeError, "%d addresses expected", static_cast<int>(sizeof...(fn)));
     return nullptr;
   }
-  for (int i = 0; i < kCount; ++i) {
+  void* p[sizeof...(fn)];
+  for (Py_ssize_t i = 0; i < n; ++i) {
     p[i] = PyLong_AsVoidPtr(argv[i]);
     if (PyErr_Occurred()) return nullptr;
   }
   int i = 0;
-  auto set = [&](auto& f) { f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(p[i++]); };
-  set(api.cross_fwd);
-  set(api.cross_bytes);
-  set(api.cross_bwd);
-  set(api.cross_bwd_bytes);
-  set(api.rope);
-  set(api.rope_paged);
-  set(api.window_fwd);
-  set(api.window_bwd);
-  set(api.window_bwd_bytes);
-  set(api.window_decode);
-  set(api.window_decode_bytes);
-  set(api.norm_rope);
-  set(api.norm_rope_bwd);
-  set(api.norm_rope_bwd_bytes);
-  set(api.norm_rope_paged);
-  set(api.pages_extend);
+  ((fn = reinterpret_cast<Fn>(p[i++])), ...);
   Py_RETURN_NONE;
+}
+
+// Addresses of fa_cross_fwd, fa_cross_workspace_bytes, fa_cross_bwd, fa_cross_bwd_workspace_bytes, fa_rope_axes,
+// fa_rope_axes_paged in the loaded library.
+PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return set_all(argv, n, api.cross_fwd, api.cross_bytes, api.cross_bwd, api.cross_bwd_bytes, api.rope, api.rope_paged);
+}
+
+// Those of fa_window_fwd, fa_window_bwd, fa_window_bwd_workspace_bytes, fa_window_decode_paged,
+// fa_window_decode_paged_workspace_bytes, fa_norm_rope_axes, fa_norm_rope_axes_bwd,
+// fa_norm_rope_axes_bwd_workspace_bytes, fa_norm_rope_axes_paged, fa_pages_extend.
+PyObject* bind_layer(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return set_all(argv, n, api.window_fwd, api.window_bwd, api.window_bwd_bytes, api.window_decode, api.window_decode_bytes,
+                 api.norm_rope, api.norm_rope_bwd, api.norm_rope_bwd_bytes, api.norm_rope_paged, api.pages_extend);
 }
 
 template <typename F>
@@ -621,6 +618,7 @@ PyCFunction fast(F f) {
 }
 
 PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
+                         {"bind_layer", fast(bind_layer), METH_FASTCALL, nullptr},
                          {"cross_fwd", fast(cross_fwd), METH_FASTCALL, nullptr},
                          {"cross_bwd", fast(cross_bwd), METH_FASTCALL, nullptr},
                          {"rope_axes", fast(rope_axes), METH_FASTCALL, nullptr},

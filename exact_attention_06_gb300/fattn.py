@@ -174,10 +174,14 @@ def _load_calls():
     if built_for != calls_abi():
         raise FattnError(FA_ERR_CUDA, "load", f"{_HERE}/_calls.so was built for {built_for}, this is {calls_abi()}; "
                                               "build it with exact_attention_06_gb300.build")
-    calls.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
-        "fa_cross_fwd", "fa_cross_workspace_bytes", "fa_cross_bwd", "fa_cross_bwd_workspace_bytes",
-        "fa_rope_axes", "fa_rope_axes_paged", "fa_window_fwd", "fa_window_bwd", "fa_window_bwd_workspace_bytes",
-        "fa_window_decode_paged", "fa_window_decode_paged_workspace_bytes", "fa_norm_rope_axes", "fa_norm_rope_axes_bwd",
+    def address(name):
+        return ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+
+    calls.bind(*map(address, ("fa_cross_fwd", "fa_cross_workspace_bytes", "fa_cross_bwd", "fa_cross_bwd_workspace_bytes",
+                              "fa_rope_axes", "fa_rope_axes_paged")))
+    calls.bind_layer(*map(address, (
+        "fa_window_fwd", "fa_window_bwd", "fa_window_bwd_workspace_bytes", "fa_window_decode_paged",
+        "fa_window_decode_paged_workspace_bytes", "fa_norm_rope_axes", "fa_norm_rope_axes_bwd",
         "fa_norm_rope_axes_bwd_workspace_bytes", "fa_norm_rope_axes_paged", "fa_pages_extend")))
     _calls = calls
 
