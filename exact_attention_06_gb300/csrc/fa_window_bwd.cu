@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
     }
   } else if (warp >= C::MMA) {
     // ------------------------------------------------------------ MMA issuers: the products, dV, dK
-    if (lane == 0) {
+    if (elect_one()) {
       const int role = warp - C::MMA;
       bool ok = true;
       if (role == 0) {
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
     }
   } else if (warp >= C::MMA) {
     // ------------------------------------------------------------ MMA issuers: S, dP, dQ
-    if (lane == 0) {
+    if (elect_one()) {
       const int role = warp - C::MMA;
       bool ok = true;
       int H = 0, jc = 0;  // halves so far, stages of the tiles before

@@ -1472,10 +1472,9 @@ fa_status_t fa_window_fwd(const void* q, const void* k, const void* v, void* o, 
     if ((st = make_map(&l.tks, k, d, Nk, kv_heads, 128, 2, shown)) != FA_OK) return st;
     if ((st = make_map(&l.tvs, v, d, Nk, kv_heads, 128, 2, shown)) != FA_OK) return st;
   }
-  if (!o_fp32 && (st = make_map(&l.to, o, d, N, heads, 128)) != FA_OK) return st;
+  if (!o_fp32 && d == 64 && (st = make_map(&l.to, o, d, N, heads, 128)) != FA_OK) return st;
   l.args = {o, lse, N, Nk, Hq / Hkv, std::min(window, Nk), shown, o_fp32, scale * 1.4426950408889634f,
-            opts && opts->wait_budget_cycles ? opts->wait_budget_cycles : kDefaultBudget, 0};
-  l.BH = heads;
+            opts && opts->wait_budget_cycles ? opts->wait_budget_cycles : kDefaultBudget, heads, 0, 0};
   l.d = d;
   cudaGetLastError();
   const cudaError_t e = fattn::launch_window_fwd(l, static_cast<cudaStream_t>(stream));

@@ -253,14 +253,15 @@ struct WindowFwdArgs {
   int N, Nk, group, window, sinks, o_fp32;
   float sl2;  // scale * log2(e)
   unsigned long long budget;
-  int ng;  // head groups; set by launch_window_fwd
+  int BH;           // B * Hq
+  int n_items, ng;  // items of 256 rows, head groups; set by launch_window_fwd
 };
 struct WindowFwdLaunch {
   CUtensorMap tq, tk, tv;  // 128-row boxes
   CUtensorMap tks, tvs;    // k and v up to their first `sinks` rows
-  CUtensorMap to;          // bf16 O only
+  CUtensorMap to;          // bf16 O at d = 64 only
   WindowFwdArgs args;
-  int BH, d, sms;          // BH: B * Hq
+  int d, sms;
 };
 cudaError_t launch_window_fwd(const WindowFwdLaunch& l, cudaStream_t stream);
 cudaError_t window_fwd_status_word(unsigned int** p);
