@@ -16,6 +16,20 @@ namespace fattn {
 namespace {
 
 constexpr int kElems = 2 * kPairs;  // elements per thread and row
+// Measured (GB300, us): heads whose loads are in flight together, blocks an SM (by registers), heads a thread:
+//   forward, 1 x (32 + 8) x 16381, d = 128    4, 5, 4: 74.4   2, 5, 4: 68.1   2, 8, 4: 64.0   2, 8, 16: 57.9   2, 7, 16: 56.7
+//   forward and backward, 2 x (16 + 4) x 8192  backward 2, 4, 4: 97.1   4, 3, 4: 91.1   4, 3, 8: 86.7   4, 3, 16: 83
+// (6.0 TB/s forward).  Into pages, 4 x (16 + 2 x 16) x 517, d = 64: 4, 5, 4: 8.2   2, 8, 4: 10.3   2, 5, 4: 7.2.
+constexpr int kFwdHeads = 2, kFwdBlocks = 7, kPagedBlocks = 1;
+constexpr int kBwdHeads = 4, kBwdBlocks = 3, kBwdPerSm = 2 * kBwdBlocks;
+constexpr int kMostHeads = 16, kMostPagedHeads = 4;
+
+// Heads a thread takes: as many, and alike.
+int heads_per_thread(int heads, int most) {
+  const int groups = (heads + most - 1) / most;
+  return (heads + groups - 1) / groups;
+}
+
 
 template <int D>
 __device__ __forceinline__ void load_weights(const NormRopeLaunch& a, float (*w)[D]) {
@@ -83,7 +97,7 @@ __device__ __forceinline__ void positions(const RopeLaunch& a, long long rows, l
 
 // Heads 0 .. Hq - 1 are q's, the next Hk k's; PAGED: k's go to the pools, as do v's, the last Hk, as they are.
 template <int D, bool INTER, bool PAGED>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeLaunch n) {
+__global__ void __launch_bounds__(kThreads, PAGED ? kPagedBlocks : kFwdBlocks) norm_rope_kernel(const NormRopeLaunch n) {
   using C = RopeCfg<D>;
   const RopeLaunch& a = n.r;
   __shared__ unsigned long long turns[D / 2];
@@ -115,11 +129,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeLaunc
   const int heads = a.Hq + a.Hk * (PAGED ? 2 : 1);
   const int h0 = static_cast<int>(blockIdx.y) * a.heads, h1 = min(h0 + a.heads, heads);
   const int e0 = first_vec<D, INTER>(t), e1 = e0 + second_vec<D, INTER>();
-  for (int h = h0; h < h1; h += kUnroll) {
-    uint4 x0[kUnroll], x1[kUnroll];
-    __nv_bfloat16* dst[kUnroll];
+  for (int h = h0; h < h1; h += kFwdHeads) {
+    uint4 x0[kFwdHeads], x1[kFwdHeads];
+    __nv_bfloat16* dst[kFwdHeads];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
+    for (int i = 0; i < kFwdHeads; ++i) {
       const int hh = min(h + i, h1 - 1);
       const __nv_bfloat16* src;
       if (hh < a.Hq) {
@@ -144,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeLaunc
       }
     }
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i)
+    for (int i = 0; i < kFwdHeads; ++i)
       if (dst[i]) {  // (the same for all threads of the row)
         if (!PAGED || h + i < a.Hq + a.Hk) {
           float f[kElems], wf[kElems], ss = 0.f;
@@ -173,23 +187,22 @@ struct BwdGrid {
 BwdGrid bwd_grid(int B, int Hq, int Hk, int N, int d, int sms) {
   BwdGrid g;
   const long long groups = (static_cast<long long>(B) * N + kThreads / (d / kElems) - 1) / (kThreads / (d / kElems));
-  g.heads = 4;
+  g.heads = heads_per_thread(Hq > Hk ? Hq : Hk, kMostHeads);
   auto ys = [&] {
     g.yq = (Hq + g.heads - 1) / g.heads;
     g.yk = (Hk + g.heads - 1) / g.heads;
     return g.yq + g.yk;
   };
-  while (ys() && g.heads > 1 && groups * ys() < 4LL * sms) g.heads /= 2;
-  long long gx = 8LL * sms / ys();
+  while (ys() && g.heads > 1 && groups * ys() < 4LL * sms) g.heads = (g.heads + 1) / 2;
+  long long gx = static_cast<long long>(kBwdPerSm) * sms / ys();
   if (gx < 1) gx = 1;
   g.gx = static_cast<int>(gx < groups ? gx : groups);
   return g;
 }
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeLaunch n, const BwdGrid g) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const NormRopeLaunch n, const BwdGrid g) {
   using C = RopeCfg<D>;
-  constexpr int kTwo = 2;  // heads whose loads are in flight together
   const RopeLaunch& a = n.r;
   __shared__ unsigned long long turns[D / 2];
   __shared__ unsigned char axis[D / 2];
@@ -220,10 +233,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeL
     positions(a, rows, r, p);
     float c[kPairs], s[kPairs];
     angles(turns, axis, t, p, -1.f, c, s);
-    for (int h = h0; h < h1; h += kTwo) {
-      uint4 x0[kTwo], x1[kTwo], y0[kTwo], y1[kTwo];
+    for (int h = h0; h < h1; h += kBwdHeads) {
+      uint4 x0[kBwdHeads], x1[kBwdHeads], y0[kBwdHeads], y1[kBwdHeads];
 #pragma unroll
-      for (int i = 0; i < kTwo; ++i) {
+      for (int i = 0; i < kBwdHeads; ++i) {
         const long long at = off + static_cast<long long>(min(h + i, h1 - 1)) * a.N * D;
         x0[i] = *reinterpret_cast<const uint4*>(x + at + e0);
         x1[i] = *reinterpret_cast<const uint4*>(x + at + e1);
@@ -231,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeL
         y1[i] = *reinterpret_cast<const uint4*>(dy + at + e1);
       }
 #pragma unroll
-      for (int i = 0; i < kTwo; ++i)
+      for (int i = 0; i < kBwdHeads; ++i)
         if (h + i < h1) {
           float f[kElems], gr[kElems], ss = 0.f, hn = 0.f;
           unpack(x0[i], x1[i], f);
@@ -275,11 +288,13 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeL
   }
 }
 
-// dw of q (blockIdx.y = 0) and k (1): 8 columns a block, 32 threads a column, which add every 32nd partial sum each and are
-// joined in their order.
+// dw of q (blockIdx.y = 0) and k (1): 8 columns a block, 128 threads a column, which add every 128th partial sum each and
+// are joined in their order.
+constexpr int kSumThreads = 1024, kSumLanes = kSumThreads / 8;
+
 template <int D>
-__global__ void __launch_bounds__(256) norm_rope_weights_kernel(const NormRopeLaunch n, const BwdGrid g) {
-  __shared__ float sum[32][9];
+__global__ void __launch_bounds__(kSumThreads) norm_rope_weights_kernel(const NormRopeLaunch n, const BwdGrid g) {
+  __shared__ float sum[kSumLanes][9];
   grid_dep_wait();  // launched programmatically after the kernel that leaves the partial sums
   float* const out = blockIdx.y ? n.dk_weight : n.dq_weight;
   const int first = blockIdx.y ? g.yq * g.gx : 0, count = (blockIdx.y ? g.yk : g.yq) * g.gx;
@@ -287,13 +302,17 @@ __global__ void __launch_bounds__(256) norm_rope_weights_kernel(const NormRopeLa
   const float* p = n.part + static_cast<size_t>(first) * D + blockIdx.x * 8 + col;
   float v = 0.f;
 #pragma unroll 8
-  for (int i = lane; i < count; i += 32) v += p[static_cast<size_t>(i) * D];
+  for (int i = lane; i < count; i += kSumLanes) v += p[static_cast<size_t>(i) * D];
   sum[lane][col] = v;
   __syncthreads();
-  if (lane || !out) return;
+  const int c = threadIdx.x / 32, l = threadIdx.x % 32;  // a warp a column
+  if (c >= 8) return;
   double total = 0.0;
-  for (int i = 0; i < 32; ++i) total += sum[i][col];
-  out[blockIdx.x * 8 + col] = static_cast<float>(total);
+#pragma unroll
+  for (int i = 0; i < kSumLanes / 32; ++i) total += sum[l + 32 * i][c];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (l == 0 && out) out[blockIdx.x * 8 + c] = static_cast<float>(total);
 }
 
 template <typename Kern, typename... Args>
@@ -315,8 +334,8 @@ cudaError_t launch_t(NormRopeLaunch n, cudaStream_t stream) {
   RopeLaunch& a = n.r;
   const long long bx = (static_cast<long long>(a.B) * a.N + RopeCfg<D>::ROWS - 1) / RopeCfg<D>::ROWS;
   const int heads = a.Hq + a.Hk * (n.slots ? 2 : 1);
-  a.heads = kUnroll;
-  while (a.heads > 1 && bx * ((heads + a.heads - 1) / a.heads) < 4LL * a.sms) a.heads /= 2;
+  a.heads = heads_per_thread(heads, n.slots ? kMostPagedHeads : kMostHeads);
+  while (a.heads > 1 && bx * ((heads + a.heads - 1) / a.heads) < 4LL * a.sms) a.heads = (a.heads + 1) / 2;
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>((heads + a.heads - 1) / a.heads));
   return n.slots ? launch_kernel(norm_rope_kernel<D, INTER, true>, grid, kThreads, stream, n)
                  : launch_kernel(norm_rope_kernel<D, INTER, false>, grid, kThreads, stream, n);
@@ -329,7 +348,7 @@ cudaError_t launch_bwd_t(const NormRopeLaunch& n, cudaStream_t stream) {
   cudaError_t e = launch_kernel(norm_rope_bwd_kernel<D, INTER>,
                                 dim3(static_cast<unsigned>(g.gx), static_cast<unsigned>(g.yq + g.yk)), kThreads, stream, n, g);
   if (e != cudaSuccess || !n.part) return e;
-  return launch_kernel(norm_rope_weights_kernel<D>, dim3(D / 8, a.Hk > 0 ? 2 : 1), 256, stream, n, g);
+  return launch_kernel(norm_rope_weights_kernel<D>, dim3(D / 8, a.Hk > 0 ? 2 : 1), kSumThreads, stream, n, g);
 }
 
 }  // namespace

@@ -1,12 +1,13 @@
 // Causal attention with a sliding window and sinks for sm_103a: query i of N stands at position p = Nk - N + i and
 // sees the `window` keys up to its own and the first `sinks` keys.
 //
-// One CTA per SM walks a list of items: two 128-row query tiles of one query head against the keys that their rows see,
-// by the steps of fa_fwd.cu's schedules.  Those keys are at most two ranges: the sinks before the window of the item's
-// first row, one step, and the keys from that window's first, lo, up to its last row's own.  Tiles are counted from
-// lo, not from a multiple of 128, so that an item scans ceil((window + 255) / 128) of them, and keys before lo
-// are never read (whatever they hold has no influence).  The second query tile starts a step later, since
-// its windows start 128 keys later, and the first ends a step sooner.
+// One CTA per SM walks a list of items: two 128-row query tiles against the keys that their rows see, by the steps of
+// fa_fwd.cu's schedules.  A tile's rows are the query heads that share a key head side by side, 128 / G positions of G
+// heads, so that they see few keys more than one position's window (one TMA box of a 4-D map brings them in
+// that order); or 128 positions of one head.  The keys are at most two ranges: the sinks before the window of the item's
+// first position, one step, and the keys from that window's first, lo, up to its last position's own.  Tiles are counted from
+// lo, not from a multiple of 128, and keys before lo are never read (whatever they hold has no influence).  With one
+// head the second query tile starts a step later, since its windows start 128 keys later.
 //
 // Persistent, because an item of a narrow window is short (a window of 256: four steps): TMEM, barriers and the K/V ring
 // stay between items, the next item's Q and keys are on their way and its first S is computed under the epilogue of the
@@ -26,28 +27,29 @@
 namespace fattn {
 namespace {
 
-// The w-th item of the list: rows row0 .. row0 + 255 of query head bh.  Steps: `ws` of the sinks (0 or 1), then key tiles
-// from lo.  Tile t takes the steps before end(t), but tile 1 not the first of lo where that holds nothing it sees.
+// The w-th item of the list: two tiles of a.tile positions each from n0 on, of unit u.  Steps: `ws` of the sinks (0 or 1),
+// then key tiles from lo.  Tile t takes the steps before end(t), but tile 1 not the first of lo where that holds nothing it
+// sees.
 struct Item {
-  int bh, row0, lo, n_sink, ws, end0, end1, n;
+  int u, n0, lo, n_sink, ws, end0, end1, n;
   bool skip;
   __device__ __forceinline__ Item(const WindowFwdArgs& a, int w) {
-    // heads in groups (the first BH % ng one larger); within a group the last rows of every head first
-    const int n_pairs = (a.N + kRowsPerCta - 1) / kRowsPerCta;
-    const int q = a.BH / a.ng, r = a.BH % a.ng, big = r * (q + 1) * n_pairs;
+    // units in groups (the first units % ng one larger); within a group the last positions of every unit first
+    const int pairs = (a.N + 2 * a.tile - 1) / (2 * a.tile);
+    const int q = a.units / a.ng, r = a.units % a.ng, big = r * (q + 1) * pairs;
     const int size = w < big ? q + 1 : q, in = w < big ? w : w - big;
-    const int g = in / (size * n_pairs), i = in - g * size * n_pairs;
-    bh = (w < big ? 0 : r * (q + 1)) + g * size + i % size;
-    row0 = (n_pairs - 1 - i / size) * kRowsPerCta;
+    const int g = in / (size * pairs), i = in - g * size * pairs;
+    u = (w < big ? 0 : r * (q + 1)) + g * size + i % size;
+    n0 = (pairs - 1 - i / size) * 2 * a.tile;
     const int off = a.Nk - a.N;
-    lo = max(0, off + row0 - a.window + 1);
+    lo = max(0, off + n0 - a.window + 1);
     n_sink = min(a.sinks, lo);
     ws = n_sink > 0 ? 1 : 0;
-    auto end_of = [&](int first) { return first < a.N ? ws + (off + min(first + kBr, a.N) - lo + kBc - 1) / kBc : 0; };
-    end0 = end_of(row0);
-    end1 = end_of(row0 + kBr);
+    auto end_of = [&](int first) { return first < a.N ? ws + (off + min(first + a.tile, a.N) - lo + kBc - 1) / kBc : 0; };
+    end0 = end_of(n0);
+    end1 = end_of(n0 + a.tile);
     n = max(end0, end1);
-    skip = end1 > 0 && off + row0 - a.window + 1 >= 0 && lo >= a.sinks;
+    skip = end1 > 0 && a.tile == kBr && off + n0 - a.window + 1 >= 0 && lo >= a.sinks;
   }
   __device__ __forceinline__ bool has(int t, int j) const { return j < (t ? end1 : end0) && !(t == 1 && skip && j == ws); }
   __device__ __forceinline__ int steps(int t) const { return t ? end1 - (skip ? 1 : 0) : end0; }  // of tile t
@@ -82,6 +84,28 @@ __device__ __forceinline__ void issue_values(uint32_t d_o, uint32_t a_p, uint64_
     for (int kk = 1; kk < kBc / 16; ++kk)
       mma_ts_c<1>(d_o, a_p + 8u * kk, sdesc_add(dv, static_cast<uint32_t>(kk) * 2048u), idesc);
   }
+}
+
+// Row r of tile t: its position among the N, and where its output goes.
+struct Row {
+  int n;
+  bool in;
+  size_t at;
+  __device__ __forceinline__ Row(const Item& I, const WindowFwdArgs& a, int t, int r) {
+    const int i = r / a.pack;
+    n = I.n0 + t * a.tile + i;
+    in = i < a.tile && n < a.N;
+    at = (static_cast<size_t>(I.u) * a.pack + (r - i * a.pack)) * a.N + n;
+  }
+};
+
+// Q's rows behind the packed ones, which no copy writes: zeros.
+template <int NH>
+__device__ __forceinline__ void clear_unused_rows(uint32_t sQ, uint32_t tile_bytes, int rows) {
+  for (int i = threadIdx.x; i < (kBr - rows) * 8; i += blockDim.x)
+    for (int b = 0; b < 2 * NH; ++b)
+      sts128(sQ + (b / NH) * tile_bytes + (b % NH) * kBox + static_cast<uint32_t>(rows) * 128u + i * 16u, 0, 0, 0, 0);
+  fence_proxy_async_smem();
 }
 
 // What a row sees of step j: keys key0 .. , up to `upto`, by the window and the first `sinks`; the sinks' step shows its
@@ -150,6 +174,7 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
   const unsigned long long budget = a.budget;
   const int w0 = static_cast<int>(blockIdx.x), w_step = static_cast<int>(gridDim.x);
   grid_dep_launch();  // a dependent kernel may launch once every CTA has started
+  clear_unused_rows<C::NH>(sQ, C::QB, a.pack * a.tile);
   if (threadIdx.x == 0) {
     mbar_init(BAR(C::B_Q), 1);
     mbar_init(BAR(C::B_QE), 2);  // by both tiles, as the rings' stages are released
@@ -191,7 +216,7 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
       bool ok = true;
       for (int w = w0, it = 0; ok && w < a.n_items; w += w_step, ++it) {
         const Item I(a, w);
-        const int kh = I.bh / a.group;  // key head
+        const int kh = I.u / a.share;  // key head
         auto load = [&](int j, bool is_v, uint32_t dst, uint32_t bar) {
           const bool sink = j < I.ws;
           mbar_arrive_expect_tx(bar, C::KVB);
@@ -201,10 +226,10 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
         auto load_q = [&] {
           // the last item's Q is free once both tiles' last S MMAs have completed
           if (it > 0 && !wait(BAR(C::B_QE), (it - 1) & 1)) return false;
-          mbar_arrive_expect_tx(BAR(C::B_Q), 2 * C::QB);
+          mbar_arrive_expect_tx(BAR(C::B_Q), 2 * C::NH * static_cast<uint32_t>(a.pack * a.tile) * 128u);
           for (int t = 0; t < 2; ++t)
             for (int h = 0; h < C::NH; ++h)
-              tma_load_3d(sQ + t * C::QB + h * kBox, &tq, BAR(C::B_Q), h * 64, I.row0 + t * kBr, I.bh);
+              tma_load_4d(sQ + t * C::QB + h * kBox, &tq, BAR(C::B_Q), h * 64, 0, I.n0 + t * a.tile, I.u);
           q_issued = it + 1;
           return true;
         };
@@ -321,7 +346,7 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
     bool ok = true;
     for (int w = w0; ok && w < a.n_items; w += w_step) {
       const Item I(a, w);
-      const int n = I.steps(t), row = I.row0 + t * kBr + r, p = a.Nk - a.N + row;
+      const int n = I.steps(t), p = a.Nk - a.N + Row(I, a, t, r).n;
       if (n <= 0) continue;  // the tile is past N
       float m2 = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i) {
@@ -383,8 +408,9 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
       tmem_ld_x64(t_o + 64, u[1]);
       tc_fence_before();
       mbar_arrive(BAR(C::B_SC + t));  // U_t is in registers
-      if (row < a.N) {
-        const size_t at = static_cast<size_t>(I.bh) * a.N + row;
+      const Row row(I, a, t, r);
+      if (row.in) {
+        const size_t at = row.at;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         if (a.o_fp32) {
 #pragma unroll
@@ -454,6 +480,7 @@ __global__ void __launch_bounds__(Cfg64::THREADS, 1)
   const unsigned long long budget = a.budget;
   const int w0 = static_cast<int>(blockIdx.x), w_step = static_cast<int>(gridDim.x);
   grid_dep_launch();
+  clear_unused_rows<C::NH>(sQ, C::QB, a.pack * a.tile);
   if (threadIdx.x == 0) {
     mbar_init(BAR(C::B_Q), 1);
     mbar_init(BAR(C::B_QE), 2);
@@ -499,10 +526,10 @@ __global__ void __launch_bounds__(Cfg64::THREADS, 1)
       bool ok = true;
       for (int w = w0, it = 0; ok && w < a.n_items; w += w_step, ++it) {
         const Item I(a, w);
-        const int kh = I.bh / a.group;
+        const int kh = I.u / a.share;
         if (it > 0 && !wait(BAR(C::B_QE), (it - 1) & 1)) break;
-        mbar_arrive_expect_tx(BAR(C::B_Q), 2 * C::QB);
-        for (int t = 0; t < 2; ++t) tma_load_3d(sQ + t * C::QB, &tq, BAR(C::B_Q), 0, I.row0 + t * kBr, I.bh);
+        mbar_arrive_expect_tx(BAR(C::B_Q), 2 * static_cast<uint32_t>(a.pack * a.tile) * 128u);
+        for (int t = 0; t < 2; ++t) tma_load_4d(sQ + t * C::QB, &tq, BAR(C::B_Q), 0, 0, I.n0 + t * a.tile, I.u);
         q_issued = it + 1;
         for (int j = 0; j < I.n; ++j) {
           const int g = kc + j, ks = g % C::KST, vs = g % C::VST;
@@ -606,7 +633,9 @@ __global__ void __launch_bounds__(Cfg64::THREADS, 1)
     bool ok = true;
     for (int w = w0; ok && w < a.n_items; w += w_step) {
       const Item I(a, w);
-      const int n = I.steps(t), row = I.row0 + t * kBr + r, p = a.Nk - a.N + row;
+      const int n = I.steps(t);
+      const Row row(I, a, t, r);
+      const int p = a.Nk - a.N + row.n;
       if (n <= 0) continue;  // the tile is past N
       if (o_issuer && !a.o_fp32) {  // the staging is free once the last store has read it (long done by now)
         bulk_wait_read_all();
@@ -686,19 +715,18 @@ __global__ void __launch_bounds__(Cfg64::THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       const float l_row = l + __shfl_xor_sync(0xffffffffu, l, 16);
-      const size_t at = static_cast<size_t>(I.bh) * a.N + row;
       if (a.o_fp32) {
-        store_half_row<D>(a.o, a.lse, at, h, row < a.N, true, t_o, l_row, m2, 1.f);
+        store_half_row<D>(a.o, a.lse, row.at, h, row.in, true, t_o, l_row, m2, 1.f);
       } else {
         ok = wait_all(BAR(C::B_OSF + t), gi & 1, abort_flag, budget);
         if (!ok) break;
-        store_lse(a.lse, at, h, row < a.N, l_row, m2);
+        store_lse(a.lse, row.at, h, row.in, l_row, m2);
         stage_half_row_bf16<D>(o_stage, o_stage, r, h, t_o, (l_row > 0.f) ? 1.f / l_row : 0.f);
         mbar_arrive(BAR(C::B_OW + t));
         if (o_issuer) {
           ok = wait(BAR(C::B_OW + t), gi & 1);
           if (ok) {
-            tma_store_3d(&to, o_stage, 0, I.row0 + t * kBr, I.bh);
+            tma_store_4d(&to, o_stage, 0, 0, I.n0 + t * a.tile, I.u);
             bulk_commit();
           }
         }
@@ -739,14 +767,15 @@ cudaError_t launch_kernel(Kern kern, int grid, int threads, uint32_t smem, cudaS
 
 cudaError_t launch_window_fwd(const WindowFwdLaunch& l, cudaStream_t stream) {
   WindowFwdArgs a = l.args;
-  const long long items = static_cast<long long>(a.BH) * ((a.N + kRowsPerCta - 1) / kRowsPerCta);
+  const long long items = static_cast<long long>(a.units) * ((a.N + 2 * a.tile - 1) / (2 * a.tile));
   if (items > INT_MAX) return cudaErrorInvalidValue;
   a.n_items = static_cast<int>(items);
-  // Items run in the order of their rows, last first, over all heads of a group: a group is as many heads as have their
-  // windows' K and V in half of L2 together.
+  // Items run in the order of their positions, last first, over all units of a group: a group is as many as have their
+  // windows' K and V in half of L2 together.  (Measured with 1 / 2 / 4 / 10 / 32 groups of 32 heads x 16381, window 4096: 918
+  // / 934 / 927 / 962 / 991 us of an earlier kernel.)
   const long long window_bytes = (static_cast<long long>(a.window) + kRowsPerCta) * l.d * 4;
-  const long long group = std::max<long long>(1, (64ll << 20) / window_bytes) * a.group;
-  a.ng = static_cast<int>((a.BH + group - 1) / group);
+  const long long group = std::max<long long>(1, (64ll << 20) / window_bytes) * a.share;
+  a.ng = static_cast<int>((a.units + group - 1) / group);
   const int grid = static_cast<int>(std::min<long long>(items, l.sms));
   if (l.d == 64)
     return launch_kernel(window_fwd64_kernel, grid, Cfg64::THREADS, Cfg64::SMEM, stream, l.tq, l.tk, l.tv, l.tks, l.tvs, l.to, a);

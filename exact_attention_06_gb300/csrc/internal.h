@@ -246,20 +246,23 @@ struct RopeLaunch {
 cudaError_t launch_rope(const RopeLaunch& a, cudaStream_t stream);
 
 // Causal attention with a sliding window and sinks: N queries of each of the query heads, `group` of which share a key
-// head, against its Nk >= N keys.
+// head, against its Nk >= N keys.  A tile's 128 rows are `tile` positions of `pack` query heads side by side (all that
+// share the key head, or 1), a position's heads one after another; units = B * Hq / pack.
 struct WindowFwdArgs {
   void* o;
   float* lse;
-  int N, Nk, group, window, sinks, o_fp32;
+  int N, Nk, window, sinks, o_fp32;
   float sl2;  // scale * log2(e)
   unsigned long long budget;
-  int BH;           // B * Hq
-  int n_items, ng;  // items of 256 rows, head groups; set by launch_window_fwd
+  int units, share;  // units that share a key head: group / pack
+  int pack, tile;
+  int n_items, ng;   // items of two tiles, groups of units; set by launch_window_fwd
 };
 struct WindowFwdLaunch {
-  CUtensorMap tq, tk, tv;  // 128-row boxes
-  CUtensorMap tks, tvs;    // k and v up to their first `sinks` rows
-  CUtensorMap to;          // bf16 O at d = 64 only
+  CUtensorMap tq;        // {d, pack, N, units}, boxes of 64 x pack x tile
+  CUtensorMap tk, tv;    // 128-row boxes
+  CUtensorMap tks, tvs;  // k and v up to their first `sinks` rows
+  CUtensorMap to;        // as tq: bf16 O at d = 64 only
   WindowFwdArgs args;
   int d, sms;
 };

@@ -121,6 +121,17 @@ def test_more_blocks_than_multiprocessors(B, Hq, Hkv, N, Nk, W, S, d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [2, 3, 5, 7, 8, 12, 16, 31, 32, 40, 64, 100, 128, 130])
+def test_heads_that_share_a_key_head(G, d):
+    """The heads of a tile's rows, rows that no head takes, tiles of one position."""
+    for B, Hkv, N, Nk, W, S in ((1, 2, 97, 140, 45, 3), (2, 1, 3, 200, 130, 70), (1, 1, 200, 200, 3, 0)):
+        _check_bwd(*_inputs(B, Hkv * G, Hkv, N, Nk, d, W, S), W, S, types=(torch.bfloat16,))
+    q, k, v, _ = _inputs(1, G, 1, 133, 300, d, 129, 17)
+    o, lse = _fwd(q, k, v, 0.1, 129, 17, True)
+    _check_fwd(o, lse, q, k, v, 0.1, 129, 17)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_a_window_of_everything_is_causal_attention(d):
     B, H, N = 2, 3, 700
     q, k, v, do = _inputs(B, H, H, N, N, d)
