@@ -34,13 +34,10 @@ struct Item {
   int u, n0, lo, n_sink, ws, end0, end1, n;
   bool skip;
   __device__ __forceinline__ Item(const WindowFwdArgs& a, int w) {
-    // units in groups (the first units % ng one larger); within a group the last positions of every unit first
     const int pairs = (a.N + 2 * a.tile - 1) / (2 * a.tile);
-    const int q = a.units / a.ng, r = a.units % a.ng, big = r * (q + 1) * pairs;
-    const int size = w < big ? q + 1 : q, in = w < big ? w : w - big;
-    const int g = in / (size * pairs), i = in - g * size * pairs;
-    u = (w < big ? 0 : r * (q + 1)) + g * size + i % size;
-    n0 = (pairs - 1 - i / size) * 2 * a.tile;
+    int rank;
+    grouped_item(w, a.units, pairs, a.ng, u, rank);
+    n0 = (pairs - 1 - rank) * 2 * a.tile;  // the last positions first
     const int off = a.Nk - a.N;
     lo = max(0, off + n0 - a.window + 1);
     n_sink = min(a.sinks, lo);

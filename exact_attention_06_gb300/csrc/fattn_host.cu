@@ -566,7 +566,8 @@ fa_status_t check_window_args(int B, int Hq, int Hkv, int N, int Nk, int d, int 
   if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dimension d=%d is not supported (64 or 128)", d);
   if (static_cast<long long>(B) * Hq > INT_MAX)
     return fail(FA_ERR_UNSUPPORTED, "B*Hq=%lld exceeds the grid limit", static_cast<long long>(B) * Hq);
-  if ((Nk + 127LL) / 128 > 60000) return fail(FA_ERR_UNSUPPORTED, "Nk=%d exceeds the 60000 key-tile grid limit", Nk);
+  if (static_cast<long long>(B) * Hq * ((Nk + 127LL) / 128 + 128) > INT_MAX)
+    return fail(FA_ERR_UNSUPPORTED, "B*Hq=%lld heads of Nk=%d keys exceed the grid limit", static_cast<long long>(B) * Hq, Nk);
   return check_window(window, sinks);
 }
 
@@ -585,42 +586,59 @@ int window_pack(int B, int Hq, int Hkv, int N, int window) {
 }
 
 struct WindowBwdPlan {
-  int splits0 = 1, stages0 = 0, splits = 1, stages = 0, own_tiles = 1;
-  size_t delta_bytes = 0, part0_bytes = 0, part_bytes = 0;
-  size_t total() const { return std::max<size_t>(delta_bytes + part0_bytes + part_bytes, 256); }
+  int splits = 1, stages = 0, sink_items = 0, sink_stages = 1, sink_rows = 0, per_head = 0, own_items = 1, own_tiles = 1;
+  size_t rows_bytes = 0, part_bytes = 0, part0_bytes = 0, sink_bytes = 0;
+  size_t total() const { return std::max<size_t>(rows_bytes + part_bytes + part0_bytes + sink_bytes, 256); }
 };
 
 WindowBwdPlan plan_window_bwd(int B, int Hq, int Hkv, int N, int Nk, int d, int window, int sinks, int sms) {
   WindowBwdPlan p;
-  const int W = std::min(window, Nk), G = Hq / Hkv;
+  const int W = std::min(window, Nk), G = Hq / Hkv, off = Nk - N;
   const long long bh = static_cast<long long>(B) * Hkv;
   const int kt = (Nk + 127) / 128, qt = (N + 127) / 128;
-  // The dK/dV kernel's stages (128 query rows): of a key tile inside, for its query heads one after another.
-  const long long per_head = std::min<long long>(qt, (127LL + W + 127) / 128);
-  const long long inner = per_head * G;
-  const double kv = 2.0 * bh * Nk * d * sizeof(float);
-  p.splits = cut_scan(bh * kt, static_cast<int>(std::min<long long>(inner, INT_MAX)), sms, kv);
+  // The dK/dV kernel's stages (128 query rows) of a key tile inside, for its query heads one after another.
+  // (They start at an even row.)
+  const long long inner = std::min<long long>(qt, (127LL + W + (off & 1) + 127) / 128) * G;
+  p.splits = cut_scan(bh * kt, static_cast<int>(std::min<long long>(inner, INT_MAX)), sms, 2.0 * bh * Nk * d * sizeof(float));
   p.stages = static_cast<int>((inner + p.splits - 1) / p.splits);
-  // Key tile 0 with sinks is seen by all queries: ranges as long as the other tiles' blocks, at least 8 stages, and
-  // at most 128 of them.
-  const long long all = sinks > 0 ? static_cast<long long>(qt) * G : inner;
-  long long each = std::max<long long>(p.stages, 8);
-  each = std::max(each, (all + 127) / 128);
-  p.splits0 = static_cast<int>((all + each - 1) / each);
-  p.stages0 = static_cast<int>(each);
-  if (sinks == 0) {
-    p.splits0 = p.splits;
-    p.stages0 = p.stages;
+  if (sinks > 0) {
+    // Queries behind tile 0's window, in ranges as long as the others, at most 128 of them.
+    const int seen = std::max(0, std::min(N, 127 + W - off));  // rows in the window of tile 0
+    const long long rest = static_cast<long long>(qt - (seen + 127) / 128) * G;
+    if (rest > 0) {
+      const long long each = std::max<long long>(p.stages, (rest + 127) / 128);
+      p.sink_stages = static_cast<int>(each);
+      p.sink_items = static_cast<int>((rest + each - 1) / each);
+      p.sink_rows = std::min((sinks + 15) / 16 * 16, Nk);
+    }
   }
-  p.delta_bytes = round256(static_cast<size_t>(B) * Hq * N * sizeof(float));
-  if (p.splits0 > 1) p.part0_bytes = round256(2ull * p.splits0 * bh * 128 * d * sizeof(float));
+  p.per_head = kt * p.splits + p.sink_items;
+  p.rows_bytes = round256(fattn::window_bwd_rows_bytes(B * Hq, N));
   if (p.splits > 1) p.part_bytes = round256(2ull * p.splits * bh * Nk * d * sizeof(float));
-  // Query tiles that a block of the dQ kernel takes: each saves most of a block's set-up and end, but longer blocks
-  // end less evenly.
-  const long long steps = (127LL + W + 127) / 128 + (sinks > 0 ? 1 : 0);
-  while (p.own_tiles < 8 && static_cast<long long>(B) * Hq * ((qt + 2 * p.own_tiles - 1) / (2 * p.own_tiles)) >= 3LL * sms &&
-         2 * p.own_tiles * steps <= 24)
-    p.own_tiles *= 2;
+  else if (p.sink_items > 0) p.part0_bytes = round256(2ull * bh * 128 * d * sizeof(float));
+  if (p.sink_items > 0) p.sink_bytes = round256(2ull * p.sink_items * bh * p.sink_rows * d * sizeof(float));
+  // Items (query tiles) that a block takes: each saves most of a block's set-up and end, but longer blocks fill the SMs less
+  // evenly.  By the rounds that the grid takes, with these times in us: a stage of 128 rows (64 keys) of the dK/dV (dQ)
+  // kernel, an item's part of its own, a block's fixed part.  Measured (GB300, the training step, us), items 1 / 2 / 3 / 4: 4
+  // x 16 heads x 2048, d = 64, window 256: 154 / 138 / 134 / 131; 2 x 16/4 x 8192, d = 128, window 1024: 599 / 597 / 605 / 596.
+  // Query tiles 1 / 2 / 3 / 4 / 6 / 8: 143 / 134 / 136 / 131 / 135 / 129; 611 / 605 / 604 / 605 / 618 / 602.
+  auto own = [&](long long heads, int per_head, double item) {
+    constexpr double kFixed = 3.0;
+    int best = 1;
+    double best_t = 0;
+    for (int n = 1; n <= per_head && n <= 16; ++n) {
+      const double rounds = std::ceil(static_cast<double>(heads * ((per_head + n - 1) / n)) / sms);
+      const double t = rounds * (n * item + kFixed);
+      if (n == 1 || t < 0.98 * best_t) {
+        best_t = t;
+        best = n;
+      }
+    }
+    return best;
+  };
+  const int halves = (W + 127 + 63) / 64 + (sinks + 63) / 64;
+  p.own_items = own(bh, p.per_head, p.stages * (d == 64 ? 1.16 : 1.8) + 2.0);
+  p.own_tiles = own(static_cast<long long>(B) * Hq, qt, halves * (d == 64 ? 0.44 : 0.67) + (d == 64 ? 0.9 : 2.5));
   return p;
 }
 
@@ -1561,19 +1579,20 @@ fa_status_t fa_window_bwd(const void* q, const void* k, const void* v, const voi
   }
   uint8_t* w = static_cast<uint8_t*>(workspace);
   fattn::WindowBwdArgs& a = l.args;
+  l.q = q;
+  l.k = k;
+  l.v = v;
   l.o = o;
   l.dout = dout;
-  l.delta = reinterpret_cast<float*>(w);
+  l.lse = lse;
+  l.rows = reinterpret_cast<float*>(w);
   l.d = d;
-  a.lse = lse;
-  a.delta = l.delta;
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  a.part0 = reinterpret_cast<float*>(w + plan.delta_bytes);
-  a.part = reinterpret_cast<float*>(w + plan.delta_bytes + plan.part0_bytes);
-  a.stride0 = static_cast<long long>(kv_heads) * 128 * d;
-  a.stride = static_cast<long long>(kv_heads) * Nk * d;
+  a.part = reinterpret_cast<float*>(w + plan.rows_bytes);
+  a.part0 = reinterpret_cast<float*>(w + plan.rows_bytes + plan.part_bytes);
+  a.sink_part = reinterpret_cast<float*>(w + plan.rows_bytes + plan.part_bytes + plan.part0_bytes);
   a.N = N;
   a.Nk = Nk;
   a.group = Hq / Hkv;
@@ -1581,10 +1600,13 @@ fa_status_t fa_window_bwd(const void* q, const void* k, const void* v, const voi
   a.sinks = shown;
   a.grad_fp32 = grad_fp32;
   a.kv_heads = kv_heads;
-  a.splits0 = plan.splits0;
-  a.stages0 = plan.stages0;
   a.splits = plan.splits;
   a.stages = plan.stages;
+  a.sink_items = plan.sink_items;
+  a.sink_stages = plan.sink_stages;
+  a.sink_rows = plan.sink_items > 0 ? plan.sink_rows : 0;
+  a.per_head = plan.per_head;
+  a.own_items = plan.own_items;
   a.own_tiles = plan.own_tiles;
   a.sl2 = scale * 1.4426950408889634f;
   a.scale = scale;

@@ -269,35 +269,44 @@ struct WindowFwdLaunch {
 cudaError_t launch_window_fwd(const WindowFwdLaunch& l, cudaStream_t stream);
 cudaError_t window_fwd_status_word(unsigned int** p);
 
-// Its backward.  Key tile 0's list of query stages (128 rows each) is cut into splits0 ranges of stages0, the other key
-// tiles' into `splits` of `stages`; where there are more than one, each leaves fp32 partial sums in part0 [2 (dK, dV)]
-// [splits0][kv_heads * 128, d] or part [2][splits][kv_heads * Nk, d], which a last kernel adds up.
+// Its backward.  The dK/dV kernel's items, per key head: every key tile's window of queries (a list of 128-row stages) in
+// `splits` ranges of `stages`, then the queries behind tile 0's window, which see its sinks, in sink_items ranges of
+// sink_stages.  fp32 partial sums [2 (dK, dV)][range][kv_heads][rows, d]: of the ranges (part, Nk rows) where there are more
+// than one, of tile 0 (part0, 128 rows) where there are not but sinks, of the sinks' ranges (sink_part, sink_rows rows: the
+// sinks).  A last kernel adds them up.
 struct WindowBwdArgs {
-  const float* lse;
-  const float* delta;
+  const float* rows;  // lse and rowsum(O dO) of the query rows, a head's row_stride apart; set by launch_window_bwd
+  int row_stride;
   void* dq;
   void* dk;
   void* dv;
-  float* part0;
   float* part;
-  long long stride0, stride;  // floats from one partial sum to the next
+  float* part0;
+  float* sink_part;
   int N, Nk, group, window, sinks, grad_fp32;
   int kv_heads;               // B * Hkv
-  int splits0, stages0, splits, stages;
-  int own_tiles;              // query tiles that a block of the dQ kernel takes one after another
+  int splits, stages;
+  int sink_items, sink_stages, sink_rows;
+  int per_head;               // items of a key head
+  int own_items, own_tiles;   // items, query tiles that a block takes one after another
+  int ng, ng_q;               // groups of key heads, of query heads; set by launch_window_bwd
   float sl2, scale;
   unsigned long long budget;
-  int ng, ng_q;               // head groups; set by launch_window_bwd
 };
 struct WindowBwdLaunch {
   CUtensorMap tq, tk, tv, tks, tvs, tdo;  // as WindowFwdLaunch
   CUtensorMap tdq, tdk, tdv;              // bf16 gradients only
   WindowBwdArgs args;
+  const void* q;
+  const void* k;
+  const void* v;
   const void* o;
   const void* dout;
-  float* delta;
+  const float* lse;
+  float* rows;  // window_bwd_rows_bytes() of scratch, 256-byte aligned
   int d, sms;
 };
+size_t window_bwd_rows_bytes(int heads, int N);
 cudaError_t launch_window_bwd(const WindowBwdLaunch& l, cudaStream_t stream);
 cudaError_t window_bwd_status_word(unsigned int** p);
 

@@ -20,6 +20,16 @@ __device__ __forceinline__ uint32_t visible_queries(int pos0, int key, int windo
   return ~low_bits(key - pos0) & (key < sinks ? 0xffffffffu : low_bits(key + window - pos0));
 }
 
+// The w-th work item of `heads` heads with `ranks` items each, in the order of grouped_block: heads in ng groups (the first
+// heads % ng one larger), and within a group rank 0 of every head first, then rank 1, and so on.
+__device__ __forceinline__ void grouped_item(int w, int heads, int ranks, int ng, int& head, int& rank) {
+  const int q = heads / ng, r = heads % ng, big = r * (q + 1) * ranks;
+  const int size = w < big ? q + 1 : q, in = w < big ? w : w - big;
+  const int g = in / (size * ranks), i = in - g * size * ranks;
+  rank = i / size;
+  head = (w < big ? 0 : r * (q + 1)) + g * size + (i - rank * size);
+}
+
 // Scores of hidden keys become -inf.
 __device__ __forceinline__ void hide(uint32_t* s, uint32_t visible) {
 #pragma unroll

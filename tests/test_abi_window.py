@@ -55,7 +55,7 @@ def test_window_refusals(fattn):
     for bad in SQUARE:
         assert _fwd(fattn, **bad) == fattn.FA_ERR_INVALID_ARG, bad
         assert _bwd(fattn, **bad) == fattn.FA_ERR_INVALID_ARG, bad
-    for bad in TOO_BIG + [dict(N=BIG, Nk=BIG)]:
+    for bad in TOO_BIG + [dict(N=BIG, Nk=BIG, B=128)]:
         assert _fwd(fattn, **bad) == fattn.FA_ERR_UNSUPPORTED, bad
         assert _bwd(fattn, **bad) == fattn.FA_ERR_UNSUPPORTED, bad
     assert _bwd(fattn, fp32=2) == fattn.FA_ERR_INVALID_ARG and _bwd(fattn, ws=128) == fattn.FA_ERR_INVALID_ARG

@@ -73,8 +73,10 @@ def _check_bwd(q, k, v, do, W, S, types=(torch.float32, torch.bfloat16)):
     bounds = _bounds(q, k, v, scale, W, S)
     _check_fwd(o, lse, q, k, v, scale, W, S, bounds=bounds)
     ref, _, otol, _, eps = bounds
+    # (rows of at most 32 keys have rowsum(O dO) from P and dP: the rounding of O is not in it)
+    few = min(W + S, k.shape[2]) <= 32
     want, bound = ow.window_backward(q, k, v, do, scale, W, S, rel=U + 4 * eps + 2.0 ** -10,
-                                     o_err=otol + U * (np.abs(ref) + otol))
+                                     o_err=None if few else otol + U * (np.abs(ref) + otol))
     for t in types:
         got = {n: torch.full(x.shape, float("nan"), dtype=t, device=DEV) for n, x in (("dq", q), ("dk", k), ("dv", v))}
         fattn.fa_window_bwd(q, k, v, o, do, lse, *got.values(), scale, W, S)
@@ -94,6 +96,8 @@ CASES = [  # B, Hq, Hkv, N, Nk, window, sinks
     (1, 1, 1, 2000, 2000, 600, 64), (1, 2, 2, 640, 640, 639, 2), (1, 2, 2, 640, 640, 640, 2), (1, 2, 2, 640, 640, 641, 2),
     (1, 2, 1, 400, 450, 2 ** 31 - 1, 128), (3, 1, 1, 130, 131, 2, 1), (1, 2, 2, 600, 600, 3, 63), (1, 3, 1, 70, 4000, 900, 50),
     (1, 2, 1, 260, 388, 129, 128), (1, 1, 1, 900, 900, 255, 128), (1, 2, 1, 512, 513, 256, 0),
+    (2, 4, 2, 333, 333, 7, 9), (1, 2, 1, 700, 720, 16, 16), (1, 3, 3, 31, 31, 40, 0), (2, 2, 1, 500, 900, 8, 24),
+    (1, 2, 1, 3000, 3000, 40, 9),
 ]
 
 
