@@ -568,6 +568,7 @@ fa_status_t check_window_args(int B, int Hq, int Hkv, int N, int Nk, int d, int 
     return fail(FA_ERR_UNSUPPORTED, "B*Hq=%lld exceeds the grid limit", static_cast<long long>(B) * Hq);
   if (static_cast<long long>(B) * Hq * ((Nk + 127LL) / 128 + 128) > INT_MAX)
     return fail(FA_ERR_UNSUPPORTED, "B*Hq=%lld heads of Nk=%d keys exceed the grid limit", static_cast<long long>(B) * Hq, Nk);
+  if (Nk > 1 << 30) return fail(FA_ERR_UNSUPPORTED, "Nk=%d exceeds 2^30", Nk);  // (positions and windows add up to an int)
   return check_window(window, sinks);
 }
 
@@ -1509,6 +1510,7 @@ fa_status_t fa_window_fwd(const void* q, const void* k, const void* v, void* o, 
   if (!std::isfinite(scale) || !(scale > 0.f)) return fail(FA_ERR_INVALID_ARG, "scale must be finite and > 0");
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16))
     return fail(FA_ERR_INVALID_ARG, "q, k, v and o must be 16-byte aligned");
+  if (o == q || o == k || o == v) return fail(FA_ERR_INVALID_ARG, "o must be a tensor of its own");
   if (!aligned(lse, 4)) return fail(FA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   fa_status_t st = check_window_args(B, Hq, Hkv, N, Nk, d, window, sinks);
   if (st != FA_OK) return st;
@@ -1556,6 +1558,11 @@ fa_status_t fa_window_bwd(const void* q, const void* k, const void* v, const voi
   if (!aligned(lse, 4)) return fail(FA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   fa_status_t st = check_window_args(B, Hq, Hkv, N, Nk, d, window, sinks);
   if (st != FA_OK) return st;
+  // (the kernels overlap: a gradient is written while other blocks still read the inputs)
+  for (const void* g : {dq, dk, dv})
+    if (g == q || g == k || g == v || g == o || g == dout)
+      return fail(FA_ERR_INVALID_ARG, "dq, dk and dv must be tensors of their own");
+  if (dq == dk || dq == dv || dk == dv) return fail(FA_ERR_INVALID_ARG, "dq, dk and dv must be tensors of their own");
   if (!workspace) return fail(FA_ERR_WORKSPACE, "fa_window_bwd needs a workspace (fa_window_bwd_workspace_bytes)");
   if (!aligned(workspace, 256)) return fail(FA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   fattn::WindowBwdLaunch l{};
@@ -1809,7 +1816,8 @@ fa_status_t fa_pages_extend(int* block_table, int* seq_lens, const int* new_lens
   if (static_cast<long long>(max_pages) * page_size > INT_MAX)
     return fail(FA_ERR_UNSUPPORTED, "max_pages*page_size=%lld exceeds the length range",
                 static_cast<long long>(max_pages) * page_size);
-  if (static_cast<long long>(B) * max_pages > INT_MAX || (slots && static_cast<long long>(B) * ((N + 1023LL) / 1024) > INT_MAX))
+  if (static_cast<long long>(B) * max_pages > INT_MAX ||
+      (slots && (N > 1 << 30 || static_cast<long long>(B) * ((N + 1023LL) / 1024) > INT_MAX)))
     return fail(FA_ERR_UNSUPPORTED, "B=%d with max_pages=%d, N=%d exceeds the grid limit", B, max_pages, N);
   fa_status_t st = check_device(nullptr);
   if (st != FA_OK) return st;

@@ -2,8 +2,9 @@
  * libfattn -- exact fused attention for GB300 (sm_103a): the fused forward
  * (bf16, or E4M3 inputs with block scales), its backward, a split-KV decode
  * (contiguous or paged KV cache), the log-sum-exp combine of partials and a
- * forward over one key shard.  C ABI: plain pointers, sizes and a stream
- * handle.
+ * forward over one key shard; cross attention, sliding windows with sinks,
+ * rotary positions with or without the heads' norms, and the pages of a paged
+ * cache.  C ABI: plain pointers, sizes and a stream handle.
  *
  * What is computed (per batch b and head h, scores scaled by `scale`):
  *     S = scale * Q K^T,   P = softmax(S) row-wise,   O = P V,
@@ -523,11 +524,14 @@ fa_status_t fa_rope_axes_paged(const void* q, const void* k, const void* v, cons
  *   k, v      [B, Hkv, Nk, d] bf16, 16-byte aligned.  Hq a multiple of Hkv, N <= Nk.  Keys that no query sees
  *             (before the first query's window, but for the sinks) may hold anything, infinities and NaN
  *             included, and have no influence; they get gradients of 0.
+ *             (Of keys that some query sees, one that is not finite may make other queries near it NaN too, as a product with
+ *             a probability of 0 does.)
  *   window    >= 1 (1: its own key alone; >= Nk: plain causal attention).
  *   sinks     0 .. 128 (FA_ERR_UNSUPPORTED beyond).
  *   o         [B, Hq, N, d] bf16, or fp32 with opts->o_fp32 (written), 16-byte aligned.
  *   lse       [B, Hq, N] fp32 (written), natural log of the scaled scores, as for fa_fwd.
- *   d in {64, 128}; scale finite and > 0; every size >= 1.
+ *   d in {64, 128}; scale finite and > 0; every size >= 1, Nk at most 2^30.  Outputs and gradients overlap no input
+ *   and not one another.
  */
 typedef struct {
   int o_fp32;                            /* 0: O is bf16 (round to nearest even); 1: O is fp32 */

@@ -20,20 +20,24 @@ def fattn():
     return fattn
 
 
+def _ptrs(n):
+    return tuple(1024 * (j + 1) for j in range(n))
+
+
 def _at(n, i, value):
-    return tuple(value if j == i else 16 for j in range(n))
+    return tuple(value if j == i else x for j, x in enumerate(_ptrs(n)))
 
 
-def _fwd(f, p=(16,) * 5, B=1, Hq=2, Hkv=1, N=4, Nk=8, d=64, scale=0.125, W=3, S=1, opts=None):
+def _fwd(f, p=_ptrs(5), B=1, Hq=2, Hkv=1, N=4, Nk=8, d=64, scale=0.125, W=3, S=1, opts=None):
     return f.lib().fa_window_fwd(*map(vp, p), B, Hq, Hkv, N, Nk, d, cf(scale), W, S, vp(0),
                                  ctypes.byref(opts) if opts else None)
 
 
-def _bwd(f, p=(16,) * 9, B=1, Hq=2, Hkv=1, N=4, Nk=8, d=64, scale=0.125, W=3, S=1, fp32=0, ws=256, wsb=1 << 30):
+def _bwd(f, p=_ptrs(9), B=1, Hq=2, Hkv=1, N=4, Nk=8, d=64, scale=0.125, W=3, S=1, fp32=0, ws=256, wsb=1 << 30):
     return f.lib().fa_window_bwd(*map(vp, p), B, Hq, Hkv, N, Nk, d, cf(scale), W, S, fp32, vp(ws), wsb, vp(0), None)
 
 
-def _decode(f, p=(16,) * 7, B=1, Hq=2, Hkv=1, d=64, ps=64, mp=4, npg=8, L=200, scale=0.125, W=3, S=1, ws=0, wsb=0, opts=None):
+def _decode(f, p=_ptrs(7), B=1, Hq=2, Hkv=1, d=64, ps=64, mp=4, npg=8, L=200, scale=0.125, W=3, S=1, ws=0, wsb=0, opts=None):
     return f.lib().fa_window_decode_paged(*map(vp, p), B, Hq, Hkv, d, ps, mp, npg, L, cf(scale), W, S, vp(ws), wsb, vp(0),
                                           ctypes.byref(opts) if opts else None)
 
@@ -55,7 +59,12 @@ def test_window_refusals(fattn):
     for bad in SQUARE:
         assert _fwd(fattn, **bad) == fattn.FA_ERR_INVALID_ARG, bad
         assert _bwd(fattn, **bad) == fattn.FA_ERR_INVALID_ARG, bad
-    for bad in TOO_BIG + [dict(N=BIG, Nk=BIG, B=128)]:
+    for out in (6, 7, 8):  # outputs are tensors of their own
+        for other in set(range(9)) - {5, out}:
+            assert _bwd(fattn, _at(9, out, _ptrs(9)[other])) == fattn.FA_ERR_INVALID_ARG
+    for other in range(3):
+        assert _fwd(fattn, _at(5, 3, _ptrs(5)[other])) == fattn.FA_ERR_INVALID_ARG
+    for bad in TOO_BIG + [dict(N=BIG, Nk=BIG, B=128), dict(Nk=2 ** 30 + 1)]:
         assert _fwd(fattn, **bad) == fattn.FA_ERR_UNSUPPORTED, bad
         assert _bwd(fattn, **bad) == fattn.FA_ERR_UNSUPPORTED, bad
     assert _bwd(fattn, fp32=2) == fattn.FA_ERR_INVALID_ARG and _bwd(fattn, ws=128) == fattn.FA_ERR_INVALID_ARG
@@ -83,7 +92,7 @@ def _plan(f, d=64):
     return f.fa_rope_axes_plan(d, (d // 2,))
 
 
-def _norm(f, p=(16,) * 7, B=1, Hq=2, Hk=1, N=4, eps=1e-6, w32=1, plan=0):
+def _norm(f, p=_ptrs(7), B=1, Hq=2, Hk=1, N=4, eps=1e-6, w32=1, plan=0):
     q, k, qw, kw, pos, qo, ko = p
     pl = _plan(f) if plan == 0 else plan
     return f.lib().fa_norm_rope_axes(vp(q), vp(k), vp(qw), vp(kw), w32, vp(pos), vp(qo), vp(ko), B, Hq, Hk, N, cf(eps),
@@ -144,7 +153,7 @@ def test_pages_refusals(fattn):
         assert _pages(fattn, p) == fattn.FA_ERR_INVALID_ARG
     for bad in (dict(slots=20), dict(B=0), dict(mp=0), dict(npg=0), dict(slots=16, N=0)):
         assert _pages(fattn, **bad) == fattn.FA_ERR_INVALID_ARG, bad
-    for bad in (dict(ps=0), dict(ps=96), dict(mp=1 << 25), dict(B=1 << 20, mp=1 << 12), dict(slots=16, B=1 << 20, N=1 << 22)):
+    for bad in (dict(ps=0), dict(ps=96), dict(mp=1 << 25), dict(B=1 << 20, mp=1 << 12), dict(slots=16, B=1 << 20, N=1 << 22), dict(slots=16, N=BIG)):
         assert _pages(fattn, **bad) == fattn.FA_ERR_UNSUPPORTED, bad
     if not torch.cuda.is_available():
         assert _pages(fattn, N=0) == fattn.FA_ERR_ARCH and _pages(fattn, slots=16) == fattn.FA_ERR_ARCH
