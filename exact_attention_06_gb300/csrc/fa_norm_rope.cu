@@ -18,8 +18,9 @@ namespace {
 constexpr int kElems = 2 * kPairs;  // elements per thread and row
 // Measured (GB300, us): heads whose loads are in flight together, blocks an SM (by registers), heads a thread:
 //   forward, 1 x (32 + 8) x 16381, d = 128    4, 5, 4: 74.4   2, 5, 4: 68.1   2, 8, 4: 64.0   2, 8, 16: 57.9   2, 7, 16: 56.7
-//   forward and backward, 2 x (16 + 4) x 8192  backward 2, 4, 4: 97.1   4, 3, 4: 91.1   4, 3, 8: 86.7   4, 3, 16: 83
-// (6.0 TB/s forward).  Into pages, 4 x (16 + 2 x 16) x 517, d = 64: 4, 5, 4: 8.2   2, 8, 4: 10.3   2, 5, 4: 7.2.
+//   forward and backward, 2 x (16 + 4) x 8192  backward 2, 4, 4: 97.1   4, 3, 4: 91.1   4, 3, 8: 86.7   4, 3, 16: 83.5
+// (6.0 TB/s forward; the second with two products an instruction, as here: 82.5, and with the next heads' loads before this
+// one's work: 82.7).  Into pages, 4 x (16 + 2 x 16) x 517, d = 64: 4, 5, 4: 8.2   2, 8, 4: 10.3   2, 5, 4: 7.2.
 constexpr int kFwdHeads = 2, kFwdBlocks = 7, kPagedBlocks = 1;
 constexpr int kBwdHeads = 4, kBwdBlocks = 3, kBwdPerSm = 2 * kBwdBlocks;
 constexpr int kMostHeads = 16, kMostPagedHeads = 4;
@@ -29,7 +30,6 @@ int heads_per_thread(int heads, int most) {
   const int groups = (heads + most - 1) / most;
   return (heads + groups - 1) / groups;
 }
-
 
 template <int D>
 __device__ __forceinline__ void load_weights(const NormRopeLaunch& a, float (*w)[D]) {
@@ -56,38 +56,80 @@ __device__ __forceinline__ unsigned int row_mask() {
   return ((1u << TPR) - 1u) << (threadIdx.x & 31 & ~(TPR - 1));
 }
 
-__device__ __forceinline__ void unpack(const uint4& a, const uint4& b, float (&f)[kElems]) {
-  const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// A thread's part of a row as 8 pairs (a, b) to turn, two pairs to a 64-bit register each: the products are for two at once.
+struct Pairs {
+  uint64_t a[kPairs / 2], b[kPairs / 2];
+};
+
+// From two 16-byte vectors: the pairs side by side (INTER), or the a's in the first and the b's in the second.
+template <bool INTER>
+__device__ __forceinline__ Pairs unpack(const uint4& v0, const uint4& v1) {
+  const uint32_t x[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  Pairs p;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[2 * i] = bf16lo(x[i]);
-    f[2 * i + 1] = bf16hi(x[i]);
+  for (int i = 0; i < kPairs / 2; ++i) {
+    const uint32_t u = INTER ? x[2 * i] : x[i], w = INTER ? x[2 * i + 1] : x[i + 4];
+    p.a[i] = INTER ? f2_pack(bf16lo(u), bf16lo(w)) : f2_pack(bf16lo(u), bf16hi(u));
+    p.b[i] = INTER ? f2_pack(bf16hi(u), bf16hi(w)) : f2_pack(bf16lo(w), bf16hi(w));
   }
+  return p;
 }
-__device__ __forceinline__ void pack(const float (&f)[kElems], uint4& a, uint4& b) {
-  a = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-  b = make_uint4(pack_bf16(f[8], f[9]), pack_bf16(f[10], f[11]), pack_bf16(f[12], f[13]), pack_bf16(f[14], f[15]));
+template <bool INTER>
+__device__ __forceinline__ void pack(const Pairs& p, uint4& v0, uint4& v1) {
+  uint32_t x[8];
+#pragma unroll
+  for (int i = 0; i < kPairs / 2; ++i) {
+    float a0, a1, b0, b1;
+    f2_unpack(p.a[i], a0, a1);
+    f2_unpack(p.b[i], b0, b1);
+    x[INTER ? 2 * i : i] = INTER ? pack_bf16(a0, b0) : pack_bf16(a0, a1);
+    x[INTER ? 2 * i + 1 : i + 4] = INTER ? pack_bf16(a1, b1) : pack_bf16(b0, b1);
+  }
+  v0 = make_uint4(x[0], x[1], x[2], x[3]);
+  v1 = make_uint4(x[4], x[5], x[6], x[7]);
 }
 
-// Turn the thread's 8 pairs: elements (2i, 2i + 1), or (i, i + 8).
-template <bool INTER>
-__device__ __forceinline__ void turn(float (&f)[kElems], const float (&c)[kPairs], const float (&s)[kPairs]) {
+// The cos, sin and -sin of the thread's pairs.
+struct Turn {
+  uint64_t c[kPairs / 2], s[kPairs / 2], ns[kPairs / 2];
+  __device__ __forceinline__ Turn(const unsigned long long* turns, const unsigned char* axis, int t,
+                                  const int (&p)[FA_ROPE_MAX_AXES], float sign) {
+    float cf[kPairs], sf[kPairs];
+    angles(turns, axis, t, p, sign, cf, sf);
 #pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    float &a = f[INTER ? 2 * i : i], &b = f[INTER ? 2 * i + 1 : i + kPairs];
-    const float x = a, y = b;
-    a = fmaf(x, c[i], -y * s[i]);
-    b = fmaf(x, s[i], y * c[i]);
+    for (int i = 0; i < kPairs / 2; ++i) {
+      c[i] = f2_pack(cf[2 * i], cf[2 * i + 1]);
+      s[i] = f2_pack(sf[2 * i], sf[2 * i + 1]);
+      ns[i] = f2_pack(-sf[2 * i], -sf[2 * i + 1]);
+    }
   }
+  __device__ __forceinline__ void operator()(Pairs& p) const {
+#pragma unroll
+    for (int i = 0; i < kPairs / 2; ++i) {
+      const uint64_t a = p.a[i], b = p.b[i];
+      p.a[i] = f2_fma(a, c[i], f2_mul(b, ns[i]));
+      p.b[i] = f2_fma(a, s[i], f2_mul(b, c[i]));
+    }
+  }
+};
+
+__device__ __forceinline__ float sum_of(uint64_t x) {
+  float lo, hi;
+  f2_unpack(x, lo, hi);
+  return lo + hi;
 }
 
 // The thread's 16 weights (w: a row of D in shared memory).
-__device__ __forceinline__ void weights_of(const float* w, int e0, int e1, float (&f)[kElems]) {
+template <bool INTER>
+__device__ __forceinline__ Pairs weights_of(const float* w, int e0, int e1) {
+  Pairs p;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    reinterpret_cast<float4*>(f)[i] = reinterpret_cast<const float4*>(w + e0)[i];
-    reinterpret_cast<float4*>(f)[2 + i] = reinterpret_cast<const float4*>(w + e1)[i];
+  for (int i = 0; i < kPairs / 2; ++i) {
+    const float* const u = w + (INTER ? (i < 2 ? e0 + 4 * i : e1 + 4 * (i - 2)) : e0 + 2 * i);
+    p.a[i] = INTER ? f2_pack(u[0], u[2]) : f2_pack(u[0], u[1]);
+    p.b[i] = INTER ? f2_pack(u[1], u[3]) : f2_pack(u[e1 - e0], u[e1 - e0 + 1]);
   }
+  return p;
 }
 
 __device__ __forceinline__ void positions(const RopeLaunch& a, long long rows, long long r, int (&p)[FA_ROPE_MAX_AXES]) {
@@ -124,8 +166,7 @@ __global__ void __launch_bounds__(kThreads, PAGED ? kPagedBlocks : kFwdBlocks) n
   }
   int p[FA_ROPE_MAX_AXES];
   positions(a, rows, r, p);
-  float c[kPairs], s[kPairs];
-  angles(turns, axis, t, p, 1.f, c, s);
+  const Turn turn(turns, axis, t, p, 1.f);
   const int heads = a.Hq + a.Hk * (PAGED ? 2 : 1);
   const int h0 = static_cast<int>(blockIdx.y) * a.heads, h1 = min(h0 + a.heads, heads);
   const int e0 = first_vec<D, INTER>(t), e1 = e0 + second_vec<D, INTER>();
@@ -161,16 +202,23 @@ __global__ void __launch_bounds__(kThreads, PAGED ? kPagedBlocks : kFwdBlocks) n
     for (int i = 0; i < kFwdHeads; ++i)
       if (dst[i]) {  // (the same for all threads of the row)
         if (!PAGED || h + i < a.Hq + a.Hk) {
-          float f[kElems], wf[kElems], ss = 0.f;
-          unpack(x0[i], x1[i], f);
+          Pairs f = unpack<INTER>(x0[i], x1[i]);
+          uint64_t sa = 0, sb = 0;
 #pragma unroll
-          for (int e = 0; e < kElems; ++e) ss = fmaf(f[e], f[e], ss);
-          const float rs = rsqrtf(fmaf(row_sum<C::TPR>(ss, mask), 1.f / D, n.eps));
-          weights_of(w[h + i < a.Hq ? 0 : 1], e0, e1, wf);
+          for (int e = 0; e < kPairs / 2; ++e) {
+            sa = f2_fma(f.a[e], f.a[e], sa);
+            sb = f2_fma(f.b[e], f.b[e], sb);
+          }
+          const float rs = rsqrtf(fmaf(row_sum<C::TPR>(sum_of(sa) + sum_of(sb), mask), 1.f / D, n.eps));
+          const uint64_t r2 = f2_pack(rs, rs);
+          const Pairs wf = weights_of<INTER>(w[h + i < a.Hq ? 0 : 1], e0, e1);
 #pragma unroll
-          for (int e = 0; e < kElems; ++e) f[e] = f[e] * rs * wf[e];
-          turn<INTER>(f, c, s);
-          pack(f, x0[i], x1[i]);
+          for (int e = 0; e < kPairs / 2; ++e) {
+            f.a[e] = f2_mul(f2_mul(f.a[e], r2), wf.a[e]);
+            f.b[e] = f2_mul(f2_mul(f.b[e], r2), wf.b[e]);
+          }
+          turn(f);
+          pack<INTER>(f, x0[i], x1[i]);
         }
         *reinterpret_cast<uint4*>(dst[i] + e0) = x0[i];
         *reinterpret_cast<uint4*>(dst[i] + e1) = x1[i];
@@ -220,10 +268,8 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
   __nv_bfloat16* const dx = is_q ? n.dq : n.dk;
   const unsigned int mask = row_mask<C::TPR>();
   const int e0 = first_vec<D, INTER>(t), e1 = e0 + second_vec<D, INTER>();
-  float wf[kElems], acc[kElems];
-  weights_of(w[is_q ? 0 : 1], e0, e1, wf);
-#pragma unroll
-  for (int e = 0; e < kElems; ++e) acc[e] = 0.f;
+  const Pairs wf = weights_of<INTER>(w[is_q ? 0 : 1], e0, e1);
+  Pairs acc = {};
   const long long rows = static_cast<long long>(a.B) * a.N;
   for (long long r = static_cast<long long>(blockIdx.x) * C::ROWS + threadIdx.x / C::TPR; r < rows;
        r += static_cast<long long>(g.gx) * C::ROWS) {
@@ -231,8 +277,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     const long long off = (b * H * a.N + tok) * D;
     int p[FA_ROPE_MAX_AXES];
     positions(a, rows, r, p);
-    float c[kPairs], s[kPairs];
-    angles(turns, axis, t, p, -1.f, c, s);
+    const Turn turn(turns, axis, t, p, -1.f);
     for (int h = h0; h < h1; h += kBwdHeads) {
       uint4 x0[kBwdHeads], x1[kBwdHeads], y0[kBwdHeads], y1[kBwdHeads];
 #pragma unroll
@@ -246,26 +291,30 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
 #pragma unroll
       for (int i = 0; i < kBwdHeads; ++i)
         if (h + i < h1) {
-          float f[kElems], gr[kElems], ss = 0.f, hn = 0.f;
-          unpack(x0[i], x1[i], f);
-          unpack(y0[i], y1[i], gr);
-          turn<INTER>(gr, c, s);  // g
+          Pairs f = unpack<INTER>(x0[i], x1[i]), g = unpack<INTER>(y0[i], y1[i]);
+          turn(g);
+          uint64_t sa = 0, sb = 0, ha = 0, hb = 0;
 #pragma unroll
-          for (int e = 0; e < kElems; ++e) {
-            ss = fmaf(f[e], f[e], ss);
-            hn = fmaf(gr[e] * wf[e], f[e], hn);
+          for (int e = 0; e < kPairs / 2; ++e) {
+            sa = f2_fma(f.a[e], f.a[e], sa);
+            sb = f2_fma(f.b[e], f.b[e], sb);
+            ha = f2_fma(f2_mul(g.a[e], wf.a[e]), f.a[e], ha);
+            hb = f2_fma(f2_mul(g.b[e], wf.b[e]), f.b[e], hb);
           }
-          ss = row_sum<C::TPR>(ss, mask);
-          hn = row_sum<C::TPR>(hn, mask);
+          const float ss = row_sum<C::TPR>(sum_of(sa) + sum_of(sb), mask);
+          const float hx = row_sum<C::TPR>(sum_of(ha) + sum_of(hb), mask);
           const float rs = rsqrtf(fmaf(ss, 1.f / D, n.eps));
-          const float m = hn * rs * (1.f / D);  // mean(h n)
+          const float m = -hx * rs * (1.f / D);  // -mean(h n)
+          const uint64_t r2 = f2_pack(rs, rs), m2 = f2_pack(m, m);
 #pragma unroll
-          for (int e = 0; e < kElems; ++e) {
-            const float nn = f[e] * rs;
-            acc[e] = fmaf(gr[e], nn, acc[e]);
-            f[e] = rs * fmaf(gr[e], wf[e], -nn * m);
+          for (int e = 0; e < kPairs / 2; ++e) {
+            const uint64_t na = f2_mul(f.a[e], r2), nb = f2_mul(f.b[e], r2);
+            acc.a[e] = f2_fma(g.a[e], na, acc.a[e]);
+            acc.b[e] = f2_fma(g.b[e], nb, acc.b[e]);
+            f.a[e] = f2_mul(r2, f2_fma(g.a[e], wf.a[e], f2_mul(na, m2)));
+            f.b[e] = f2_mul(r2, f2_fma(g.b[e], wf.b[e], f2_mul(nb, m2)));
           }
-          pack(f, x0[i], x1[i]);
+          pack<INTER>(f, x0[i], x1[i]);
           __nv_bfloat16* const to = dx + off + static_cast<long long>(h + i) * a.N * D;
           *reinterpret_cast<uint4*>(to + e0) = x0[i];
           *reinterpret_cast<uint4*>(to + e1) = x1[i];
@@ -275,9 +324,10 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
   if (!n.part) return;
   float* const mine = sum[threadIdx.x / C::TPR];
 #pragma unroll
-  for (int e = 0; e < kElems / 2; ++e) {
-    mine[e0 + e] = acc[e];
-    mine[e1 + e] = acc[kElems / 2 + e];
+  for (int i = 0; i < kPairs / 2; ++i) {
+    float* const u = mine + (INTER ? (i < 2 ? e0 + 4 * i : e1 + 4 * (i - 2)) : e0 + 2 * i);
+    f2_unpack(acc.a[i], u[0], u[INTER ? 2 : 1]);
+    f2_unpack(acc.b[i], u[INTER ? 1 : e1 - e0], u[INTER ? 3 : e1 - e0 + 1]);
   }
   __syncthreads();
   if (threadIdx.x < D) {

@@ -1,12 +1,16 @@
 // Backward of causal attention with a sliding window and sinks (fa_window_fwd.cu) for sm_103a: dK, dV (a CTA takes a few key
-// tiles one after another) and dQ (a few query tiles), by the formulas of fa_bwd.cu, P recomputed from the forward's lse.  The scanned side is taken in halves of 64 rows, two or three in flight, as
-// in fa_cross_bwd.cu.
+// tiles one after another) and dQ (a few query tiles), by the formulas of fa_bwd.cu, P recomputed from the forward's lse.  The
+// scanned side is taken in halves of 64 rows, two or three in flight, as in fa_cross_bwd.cu.  Bound by the products whose
+// operands both come from shared memory (N = 64) at d = 128, by the halves' chains at d = 64.  Measured (GB300, us, the
+// kernels one at a time): 2 x 16/4 x 8192, d = 128, window 1024: D 23, dK/dV 260, dQ 213, sums 5; 4 x 16 x 2048, d = 64,
+// window 256: 9, 58, 35, 5.
 //
 // dK, dV.  The queries that see a key tile are, in every query head that shares the key head, the tile's window, W + 127 of
 // them: one list of 128-row stages.  Key tile 0 holds the sinks (at most 128), which every later query sees: those
 // queries are a list of their own, as long as many windows, cut into ranges of about a window's length whose fp32 partial
 // sums (of the sinks' rows alone) a last kernel adds in their order.  So are the lists of all tiles where there are
-// too few of them to fill the SMs.
+// too few of them to fill the SMs.  What the sinks cost (the whole backward, none / 4 / 16): 427 / 461 / 461 and 78.5 / 99.5 /
+// 99 us at the sizes above.
 //
 // dQ.  A query tile scans the sinks before its first row's window (through tensor maps that end behind the sinks), then
 // the keys from that window's first, lo, up to its last row's own.

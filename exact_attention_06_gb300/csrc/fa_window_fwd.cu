@@ -17,6 +17,11 @@
 // three comparisons (window.cuh).  The sinks' step reads K and V through tensor maps that end after `sinks` rows, so that
 // the rows behind them arrive as zeros, whatever the cache holds there; its products take no more than the sinks' groups of
 // 16 keys, and its softmax 32 columns where they suffice.
+//
+// Bound by the tensor cores and the softmax's chains in a long window, by an item's begin and end in a narrow one.  Measured
+// (GB300): 32/8 heads x 16381, d = 128, window 4096: 666 us (1443 TFLOP/s of the visible pairs, 0.75 of the library's largest
+// product); 2 x 16/4 x 8192, window 1024: 124 us; 4 x 16 x 2048, d = 64, window 256: 26 us (the tiles' keys are 1.5 times
+// the window's); 4 x 16/4 x 517 behind 1500 keys, window 333: 10.2 us.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
