@@ -66,21 +66,21 @@ def _peaks():
 # DRAM bytes per launch (dram__bytes_read.sum + dram__bytes_write.sum) from ncu captures summarised
 # under profiles/, keyed by kernel and workload, valid only while the kernels' code is unchanged: each source
 # with the digest (_code_digest) of it and all it includes.
-_FWD = "612b84ef8eaac17181b353fc5ae66ca3f857330e5dd29481c052a4b7bdb531a0"
-_BWD = "c6ff0b37c37d4af6feb5634dc39ff5ff3fe9ac504066ecc866c9a1f50ee6e413"
-_DEC = "f5eb7a7cf97578a63327f8468739b0ae62d5bf689a64dc9f5193ba35663904f1"
+_FWD = "651a43dfda36af233d0fb8f61fbf90619bd81d1714c4955fab2017278a1c0cb4"
+_BWD = "d032e86e6b82332953e16bd93213d1bd3344fe63fc09530d287b5a12767bb6d5"
+_DEC = "530a392fe46150c5de6023c83a486505df4266addb7fff62725c81811673774d"
 NCU_TRAFFIC = {
-    ("fwd_kernel", "ragged"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 559.038e6},
-    ("fwd_kernel", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 263.172e6},
-    ("fwd_kernel_fp8", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 136.563e6},
-    ("fwd_persist_kernel", "prefill"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 50.603e6},
+    ("fwd_kernel", "ragged"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 559.537e6},
+    ("fwd_kernel", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 264.576e6},
+    ("fwd_kernel_fp8", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 136.400e6},
+    ("fwd_persist_kernel", "prefill"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 50.645e6},
     # backward: the dominant kernel (dK/dV) on the causal workload
-    ("bwd_dkdv_kernel", "causal"): {"sources": {"fa_bwd.cu": _BWD}, "bytes": 372.816e6},
+    ("bwd_dkdv_kernel", "causal"): {"sources": {"fa_bwd.cu": _BWD}, "bytes": 372.525e6},
     # the four-shard step: four forward launches over the key shards and the combine, summed
-    ("causal_sharded4", "causal"): {"sources": {"fa_fwd.cu": _FWD, "fa_decode.cu": _DEC}, "bytes": 1108.964e6},
+    ("causal_sharded4", "causal"): {"sources": {"fa_fwd.cu": _FWD, "fa_decode.cu": _DEC}, "bytes": 1110.309e6},
     # decode: captured on the B4 slice (decode_small) and scaled by 16 to B64 (K/V streamed once)
-    ("decode_split_kernel", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.947e6},
-    ("decode_split_kernel_paged", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.934e6},
+    ("decode_split_kernel", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.950e6},
+    ("decode_split_kernel_paged", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.946e6},
 }
 SOURCE_DIRS = (os.path.join(ROOT, "exact_attention_06_gb300", "csrc"), os.path.join(ROOT, "include"))
 

@@ -615,7 +615,7 @@ fa_status_t fa_norm_rope_axes_bwd(const void* q, const void* k, const void* q_we
 /*
  * fa_norm_rope_axes_paged -- the serving form: the N new tokens of each sequence.  q is normed and turned into q_out, k
  * (the same) and v [B, Hk, N, d] (copied) go into the pools [num_pages, Hk, page_size, d] at the slots that
- * fa_pages_extend gives.
+ * fa_pages_extend gives.  q_out may be q.
  *   slots      [B, N] int64, 8-byte aligned: token n of sequence b goes to row slot % page_size of page
  *              slot / page_size.  A slot outside [0, num_pages * page_size) is no place: that token's k and v are not
  *              written.  Two tokens of one call must not share a slot.

@@ -3,6 +3,8 @@ tokens, their q and k normed and turned into the cache, one token's attention ov
 of both.  Every stage is compared with the fp64 definition on the values that reached it (the bounds are those of
 the stages' own tests), and captured steps with the calls one by one."""
 
+import os
+import re
 import threading
 
 import numpy as np
@@ -299,3 +301,18 @@ def test_calls_from_two_threads():
     for t in threads:
         t.join()
     assert not wrong and fattn.fa_get_status() == fattn.FA_OK
+
+
+def test_the_examples_of_the_readme():
+    """They run, and the serving step's outputs are those of one key (the token's own)."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    with open(path) as f:
+        blocks = re.findall(r"```python\n(.*?)```", f.read(), re.S)
+    names = {}
+    for block in blocks:
+        exec(block, names)
+    torch.cuda.synchronize()
+    assert fattn.fa_get_status() == fattn.FA_OK
+    assert names["lens"].tolist() == [1] * 8 and names["granted"].tolist() == [1] * 8 and int(names["n_free"]) == 1016
+    own = names["v"][:, :, 0].repeat_interleave(4, 1)
+    assert torch.equal(names["o"], own)  # (a softmax over one key)
