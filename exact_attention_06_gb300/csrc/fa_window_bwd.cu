@@ -3,14 +3,14 @@
 // scanned side is taken in halves of 64 rows, two or three in flight, as in fa_cross_bwd.cu.  Bound by the products whose
 // operands both come from shared memory (N = 64) at d = 128, by the halves' chains at d = 64.  Measured (GB300, us, the
 // kernels one at a time): 2 x 16/4 x 8192, d = 128, window 1024: D 23, dK/dV 260, dQ 213, sums 5; 4 x 16 x 2048, d = 64,
-// window 256: 9, 58, 35, 5.
+// window 256: 10, 53, 33, 6.
 //
 // dK, dV.  The queries that see a key tile are, in every query head that shares the key head, the tile's window, W + 127 of
 // them: one list of 128-row stages.  Key tile 0 holds the sinks (at most 128), which every later query sees: those
 // queries are a list of their own, as long as many windows, cut into ranges of about a window's length whose fp32 partial
 // sums (of the sinks' rows alone) a last kernel adds in their order.  So are the lists of all tiles where there are
-// too few of them to fill the SMs.  What the sinks cost (the whole backward, none / 4 / 16): 427 / 461 / 461 and 78.5 / 99.5 /
-// 99 us at the sizes above.
+// too few of them to fill the SMs.  What the sinks cost (the whole backward, none / 4 / 16): 427 / 462 / 463 and 73.7 / 92 /
+// 91.6 us at the sizes above.
 //
 // dQ.  A query tile scans the sinks before its first row's window (through tensor maps that end behind the sinks), then
 // the keys from that window's first, lo, up to its last row's own.
@@ -222,6 +222,29 @@ __device__ __forceinline__ void ew_window_dq(const uint32_t (&sv)[32], const uin
   }
 }
 
+// The items of a block: n of the list of all heads' items, from rank `rank` of `head` on.  FLAT (one row of blocks): every `own` of
+// the list, over the heads' ends; else `own` of one head, heads and ranks in the order of grouped_block, the last ranks first if
+// `reversed`.
+struct BlockItems {
+  int head, rank, n, per_head;
+  __device__ __forceinline__ BlockItems(bool flat, int heads, int per, int own, int ng, bool reversed) : per_head(per) {
+    if (flat) {
+      const int at = static_cast<int>(blockIdx.x) * own;  // (the host keeps the list within an int)
+      head = at / per_head;
+      rank = at - head * per_head;
+      n = min(own, heads * per_head - at);
+    } else {
+      grouped_block(ng, head, rank);
+      rank = (reversed ? static_cast<int>(gridDim.y) - 1 - rank : rank) * own;
+      n = min(own, per_head - rank);
+    }
+  }
+  __device__ __forceinline__ void place(int t, int& h, int& r) const {
+    h = head;
+    for (r = rank + t; r >= per_head; r -= per_head) ++h;
+  }
+};
+
 // Layout of the dK/dV kernel: CrossCfg's, with room for two tiles' K and V at d = 64.
 template <int D>
 struct DkdvCfg : CrossCfg<D, 2 * D> {
@@ -269,7 +292,7 @@ struct KeyItem {
   __device__ __forceinline__ int rows(const WindowBwdArgs& a) const { return sink ? a.sink_rows : min(kTile, a.Nk - kt * kTile); }
 };
 
-// One CTA per a.own_items items of a key head, one after another, the next one's K and V (d = 64) and first stages on their way meanwhile.
+// One CTA per a.own_items items, one after another, the next one's K and V (d = 64) and first stages on their way meanwhile.
 // Halves and stages are counted over all its items, so that their phases go on.  P^T and dS^T are packed into their
 // S^T and dP^T.
 template <int D>
@@ -290,11 +313,13 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
 #define BAR(i) (sBar + 8u * static_cast<uint32_t>(i))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, N = a.N;
   const unsigned long long budget = a.budget;
-  int bh, rank0;  // (the last key tiles have the fewest queries: they end the grid)
-  grouped_block(a.ng, bh, rank0);
-  rank0 *= a.own_items;
-  const int nt = min(a.own_items, a.per_head - rank0);
-  auto item = [&](int t) { return KeyItem(a, bh, rank0 + t); };
+  const BlockItems mine(a.flat, a.kv_heads, a.per_head, a.own_items, a.ng, false);  // (the last key tiles have the fewest queries)
+  const int nt = mine.n;
+  auto item = [&](int t) {
+    int head, rank;
+    mine.place(t, head, rank);
+    return KeyItem(a, head, rank);
+  };
   if (threadIdx.x == 0) {
     mbar_init(BAR(C::B_OWN), 1);
     mbar_init(BAR(C::B_OWN + 1), 1);
@@ -559,7 +584,7 @@ struct DqTile {
   __device__ __forceinline__ bool ends_stage(int hh) const { return hh + 1 == hs || hh + 1 == n_h || (hh >= hs && half(hh)); }
 };
 
-// One CTA per a.own_tiles query tiles of a query head, scanned one after another, the next one's Q, dO and first keys
+// One CTA per a.own_tiles query tiles, scanned one after another, the next one's Q, dO and first keys
 // on their way meanwhile.  Halves and stages are counted over all its tiles, so that their phases go on.  dS is
 // packed into its dP.
 template <int D>
@@ -578,12 +603,19 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, N = a.N;
   const unsigned long long budget = a.budget;
-  int bh, qb;
-  grouped_block(a.ng_q, bh, qb);
-  qb = static_cast<int>(gridDim.y) - 1 - qb;  // the rows with whole windows first
-  const int t0 = qb * a.own_tiles, nt = min(a.own_tiles, (N + kTile - 1) / kTile - t0), kh = bh / a.group;
+  const int per_head = (N + kTile - 1) / kTile;
+  const BlockItems mine(a.flat, a.kv_heads * a.group, per_head, a.own_tiles, a.ng_q, true);  // the rows with whole windows first
+  const int nt = mine.n;
   const bool producer = threadIdx.x == C::TMA * 32;
-  auto keys_of = [&](int t) { return DqTile(a, (t0 + t) * kTile); };
+  struct Place {
+    int bh, row;
+  };
+  auto place_of = [&](int t) {  // tile t's query head and first row
+    int bh, tile;
+    mine.place(t, bh, tile);
+    return Place{bh, tile * kTile};
+  };
+  auto keys_of = [&](int t) { return DqTile(a, place_of(t).row); };
   if (producer) {
     for (int b = 0; b < C::NB; ++b) {
       mbar_init(BAR(C::B_OWN + b), 1);
@@ -603,7 +635,7 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  auto load = [&](int jj, const DqTile& k, int j) {  // stage j of a tile as the block's stage jj
+  auto load = [&](int jj, const DqTile& k, int kh, int j) {  // stage j of a tile, of key head kh, as the block's stage jj
     const int s = jj % C::ST;
     const bool sink = k.hs > 0 && j == 0;
     const int key = sink ? 0 : k.lo + (j - (k.hs > 0 ? 1 : 0)) * kTile;
@@ -616,17 +648,18 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
   };
   auto load_own = [&](int t) {  // Q, dO of the block's tile t
     const uint32_t full = BAR(C::B_OWN + t % C::NB), own = sOwn + t % C::NB * (2 * C::TB);
+    const Place p = place_of(t);
     mbar_arrive_expect_tx(full, 2 * C::TB);
     for (int h = 0; h < C::NH; ++h) {
-      tma_load_3d(own + h * kBox, &tq, full, h * 64, (t0 + t) * kTile, bh);
-      tma_load_3d(own + C::OFF_B + h * kBox, &tdo, full, h * 64, (t0 + t) * kTile, bh);
+      tma_load_3d(own + h * kBox, &tq, full, h * 64, p.row, p.bh);
+      tma_load_3d(own + C::OFF_B + h * kBox, &tdo, full, h * 64, p.row, p.bh);
     }
   };
   const int first = min(C::ST, keys_of(0).n_j);  // stages asked for at once
   if (producer) {
     const DqTile k = keys_of(0);
     load_own(0);
-    for (int j = 0; j < first; ++j) load(j, k, j);
+    for (int j = 0; j < first; ++j) load(j, k, place_of(0).bh / a.group, j);
     if (C::NB > 1 && nt > 1) load_own(1);
   }
   if (warp == C::MMA) {
@@ -645,20 +678,22 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
       auto finish = [&](int t) {  // tile t's dQ: stored from Q's place, which is then free, as dO's
         ok = bwait(BAR(C::B_OW + t % C::NB), (t / C::NB) & 1, abort_flag, budget);
         if (!ok || a.grad_fp32) return;
+        const Place p = place_of(t);
         for (int h = 0; h < C::NH; ++h)
-          tma_store_3d(&tdq, sOwn + t % C::NB * (2 * C::TB) + h * kBox, h * 64, (t0 + t) * kTile, bh);
+          tma_store_3d(&tdq, sOwn + t % C::NB * (2 * C::TB) + h * kBox, h * 64, p.row, p.bh);
         bulk_commit();
         bulk_wait_read_all();
       };
       int done = 0;  // tiles finished
       for (int t = 0; ok && t < nt; ++t) {
         const DqTile k = keys_of(t);
+        const int kh = place_of(t).bh / a.group;
         auto take = [&](int end) {  // the tile's stages before `end`
           for (; ok && issued < before + end; ++issued) {
             const int s = issued % C::ST;
             if (issued >= C::ST) ok = bwait(BAR(C::B_EMPTY + s), ((issued / C::ST) - 1) & 1, abort_flag, budget);
             if (!ok) return;
-            load(issued, k, issued - before);
+            load(issued, k, kh, issued - before);
           }
         };
         take(min(C::ST, k.n_j));
@@ -738,24 +773,26 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
     bool ok = true;
     int out = 0;  // tiles whose dQ is out (the first four warps take them out of TMEM)
     auto put_out = [&](int t) {
-      const int b = t % C::NB, row = (t0 + t) * kTile + r;
+      const Place p = place_of(t);
+      const int b = t % C::NB, row = p.row + r;
       ok = bwait_all(BAR(C::B_GF + b), (t / C::NB) & 1, abort_flag, budget);
       if (!ok) return;
       tc_fence_after();
       const uint32_t acc = lanes + C::COL_ACC + b * D, place = sOwn + b * (2 * C::TB);
-      if (a.grad_fp32) store_grad_row<D>(a.dq, static_cast<size_t>(bh) * N + row, row < N, acc, a.scale);
+      if (a.grad_fp32) store_grad_row<D>(a.dq, static_cast<size_t>(p.bh) * N + row, row < N, acc, a.scale);
       else stage_row_bf16<D>(place, place + kBox, r, acc, a.scale);  // (its Q is no longer read)
       tc_fence_before();
       mbar_arrive(BAR(C::B_OW + b));
     };
     auto row_of = [&](int t) {  // {-lse2, -D}
-      const int row = (t0 + t) * kTile + r;  // (within the array: row < N + 127)
-      const float* v = a.rows + (static_cast<size_t>(bh) * a.row_stride + (row & ~1)) * 2 + (row & 1);
+      const Place p = place_of(t);
+      const int row = p.row + r;  // (within the array: row < N + 127)
+      const float* v = a.rows + (static_cast<size_t>(p.bh) * a.row_stride + (row & ~1)) * 2 + (row & 1);
       return make_float2(v[0], v[2]);
     };
     DqTile k = keys_of(0);
     float2 next = row_of(0);  // of tile t + 1, read a tile ahead
-    int t = -1, hh = g, i = 0;
+    int t = -1, hh = g, i = 0, pos = 0;  // pos: the row's position
     uint64_t nl2 = 0, nd2 = 0;
     for (int tile = 0; ok; hh += C::FLIGHT, ++i) {
       while (tile < nt && hh >= k.n_h) {
@@ -768,6 +805,7 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
       if (tile != t) {
         const float2 x = tile == t + 1 ? next : row_of(tile);
         t = tile;
+        pos = a.Nk - N + place_of(t).row + r;
         nl2 = f2_pack(x.x, x.x);
         nd2 = f2_pack(x.y, x.y);
         if (t + 1 < nt) next = row_of(t + 1);
@@ -778,7 +816,7 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
       // the half's keys and what the row sees of them; the sinks' halves show their n_sink keys to every row
       const bool sink = hh < k.hs;
       const int key0 = sink ? hh * kHalf : k.lo + (hh - k.hs) * kHalf;
-      const int upto = sink ? k.n_sink - 1 : a.Nk - N + (t0 + t) * kTile + r, sinks = sink ? kTile : a.sinks;
+      const int upto = sink ? k.n_sink - 1 : pos, sinks = sink ? kTile : a.sinks;
       const bool all = key0 + kHalf - 1 <= upto && (key0 > upto - a.window || key0 + kHalf <= sinks);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -872,7 +910,7 @@ cudaError_t launch_t(const WindowBwdLaunch& l, cudaStream_t stream) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   auto grid = [&](long long n, int each, int threads, size_t smem) {
-    cfg.gridDim = dim3(static_cast<unsigned>((n + each - 1) / each));
+    cfg.gridDim = dim3(static_cast<unsigned>((n + each - 1) / each));  // (y = 1)
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
   };
@@ -887,13 +925,13 @@ cudaError_t launch_t(const WindowBwdLaunch& l, cudaStream_t stream) {
   const bool all_few = few == (a.N + 15) / 16;
   if (few > 0 && (e = delta(window_delta_kernel<D, true>, 0, all_few ? groups : few, true)) != cudaSuccess) return e;
   if (!all_few && (e = delta(window_delta_kernel<D, false>, few, groups, few == 0)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.kv_heads), static_cast<unsigned>((a.per_head + a.own_items - 1) / a.own_items));
-  cfg.blockDim = dim3(KV::THREADS);
-  cfg.dynamicSmemBytes = KV::SMEM;
+  auto items = [&](int heads, int per_head, int own, int threads, size_t smem) {
+    grid(a.flat ? static_cast<long long>(heads) * per_head : own * static_cast<long long>(heads), own, threads, smem);
+    if (!a.flat) cfg.gridDim.y = static_cast<unsigned>((per_head + own - 1) / own);
+  };
+  items(a.kv_heads, a.per_head, a.own_items, KV::THREADS, KV::SMEM);
   if ((e = cudaLaunchKernelEx(&cfg, k1, l.tq, l.tk, l.tv, l.tdo, l.tdk, l.tdv, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(q_heads), static_cast<unsigned>(q_blocks));
-  cfg.blockDim = dim3(Q::THREADS);
-  cfg.dynamicSmemBytes = Q::SMEM;
+  items(q_heads, (a.N + kTile - 1) / kTile, a.own_tiles, Q::THREADS, Q::SMEM);
   if ((e = cudaLaunchKernelEx(&cfg, k2, l.tq, l.tk, l.tv, l.tks, l.tvs, l.tdo, l.tdq, a)) != cudaSuccess) return e;
   if (a.splits < 2 && a.sink_items == 0) return cudaSuccess;
   const int rows = a.splits > 1 || a.Nk < kTile ? a.Nk : kTile;

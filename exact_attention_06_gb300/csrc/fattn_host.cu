@@ -588,6 +588,7 @@ int window_pack(int B, int Hq, int Hkv, int N, int window) {
 
 struct WindowBwdPlan {
   int splits = 1, stages = 0, sink_items = 0, sink_stages = 1, sink_rows = 0, per_head = 0, own_items = 1, own_tiles = 1;
+  bool flat = false;
   size_t rows_bytes = 0, part_bytes = 0, part0_bytes = 0, sink_bytes = 0;
   size_t total() const { return std::max<size_t>(rows_bytes + part_bytes + part0_bytes + sink_bytes, 256); }
 };
@@ -623,23 +624,32 @@ WindowBwdPlan plan_window_bwd(int B, int Hq, int Hkv, int N, int Nk, int d, int 
   // kernel, an item's part of its own, a block's fixed part.  Measured (GB300, the training step, us), items 1 / 2 / 3 / 4: 4
   // x 16 heads x 2048, d = 64, window 256: 154 / 138 / 134 / 131; 2 x 16/4 x 8192, d = 128, window 1024: 599 / 597 / 605 / 596.
   // Query tiles 1 / 2 / 3 / 4 / 6 / 8: 143 / 134 / 136 / 131 / 135 / 129; 611 / 605 / 604 / 605 / 618 / 602.
-  auto own = [&](long long heads, int per_head, double item) {
+  struct Own {
+    int n = 1;
+    double t = 0;
+  };
+  auto own = [&](long long heads, long long per_head, double item) {
     constexpr double kFixed = 3.0;
-    int best = 1;
-    double best_t = 0;
+    Own best;
     for (int n = 1; n <= per_head && n <= 16; ++n) {
       const double rounds = std::ceil(static_cast<double>(heads * ((per_head + n - 1) / n)) / sms);
       const double t = rounds * (n * item + kFixed);
-      if (n == 1 || t < 0.98 * best_t) {
-        best_t = t;
-        best = n;
-      }
+      if (n == 1 || t < 0.98 * best.t) best = {n, t};
     }
     return best;
   };
   const int halves = (W + 127 + 63) / 64 + (sinks + 63) / 64;
-  p.own_items = own(bh, p.per_head, p.stages * (d == 64 ? 1.16 : 1.8) + 2.0);
-  p.own_tiles = own(static_cast<long long>(B) * Hq, qt, halves * (d == 64 ? 0.44 : 0.67) + (d == 64 ? 0.9 : 2.5));
+  const double item = p.stages * (d == 64 ? 1.16 : 1.8) + 2.0, tile = halves * (d == 64 ? 0.44 : 0.67) + (d == 64 ? 0.9 : 2.5);
+  const long long bh_q = static_cast<long long>(B) * Hq;
+  // Of one head; or of the list of all heads' items, where that fills the SMs evenly and one head's do not.  The dQ kernel's go with
+  // them: behind a dK/dV kernel whose blocks end together its own have to be even, behind another they fill its last
+  // round.  Measured (GB300, the backward alone, us), one head's / the list: 4 x 16 x 2048, window 256, d = 64 99.3 / 91.1, d = 128
+  // 172 / 163; 16 x 16 x 512, d = 64, window 128 95 / 85; 32 x 4096, d = 128, window 512 206 / 196; and where the rule keeps one
+  // head's: 2 x 16/4 x 8192, d = 128, window 1024 461 / 490; 2 x 32/8 x 2048, d = 64, window 512 101.3 / 103.6.
+  const Own one = own(bh, p.per_head, item), all = own(1, bh * p.per_head, item);
+  p.flat = all.t < 0.93 * one.t;
+  p.own_items = (p.flat ? all : one).n;
+  p.own_tiles = (p.flat ? own(1, bh_q * qt, tile) : own(bh_q, qt, tile)).n;
   return p;
 }
 
@@ -1615,6 +1625,7 @@ fa_status_t fa_window_bwd(const void* q, const void* k, const void* v, const voi
   a.per_head = plan.per_head;
   a.own_items = plan.own_items;
   a.own_tiles = plan.own_tiles;
+  a.flat = plan.flat;
   a.sl2 = scale * 1.4426950408889634f;
   a.scale = scale;
   a.budget = opts && opts->wait_budget_cycles ? opts->wait_budget_cycles : kDefaultBudget;

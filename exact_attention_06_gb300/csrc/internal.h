@@ -289,6 +289,7 @@ struct WindowBwdArgs {
   int sink_items, sink_stages, sink_rows;
   int per_head;               // items of a key head
   int own_items, own_tiles;   // items, query tiles that a block takes one after another
+  bool flat;                  // of the list of all heads', not of one head's
   int ng, ng_q;               // groups of key heads, of query heads; set by launch_window_bwd
   float sl2, scale;
   unsigned long long budget;

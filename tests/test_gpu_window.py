@@ -125,6 +125,14 @@ def test_more_blocks_than_multiprocessors(B, Hq, Hkv, N, Nk, W, S, d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,N,Nk,W,S", [(2, 32, 32, 300, 300, 30, 17), (2, 32, 16, 300, 300, 65, 0),
+                                               (2, 40, 40, 200, 277, 65, 17), (2, 96, 48, 200, 277, 30, 3)])
+def test_blocks_of_several_items(B, Hq, Hkv, N, Nk, W, S, d):
+    """Of one head (the first two), or of all heads' list, so that a block's items are of two heads (the others)."""
+    _check_bwd(*_inputs(B, Hq, Hkv, N, Nk, d, W, S), W, S)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G", [2, 3, 5, 7, 8, 12, 16, 31, 32, 40, 64, 100, 128, 130])
 def test_heads_that_share_a_key_head(G, d):
     """The heads of a tile's rows, rows that no head takes, tiles of one position."""
