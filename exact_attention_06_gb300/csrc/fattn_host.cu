@@ -647,7 +647,7 @@ WindowBwdPlan plan_window_bwd(int B, int Hq, int Hkv, int N, int Nk, int d, int 
   // 172 / 163; 16 x 16 x 512, d = 64, window 128 95 / 85; 32 x 4096, d = 128, window 512 206 / 196; and where the rule keeps one
   // head's: 2 x 16/4 x 8192, d = 128, window 1024 461 / 490; 2 x 32/8 x 2048, d = 64, window 512 101.3 / 103.6.
   const Own one = own(bh, p.per_head, item), all = own(1, bh * p.per_head, item);
-  p.flat = all.t < 0.93 * one.t;
+  p.flat = all.t < 0.93 * one.t || std::max(p.per_head, qt) > 65535;  // (or more than a grid's second dimension holds)
   p.own_items = (p.flat ? all : one).n;
   p.own_tiles = (p.flat ? own(1, bh_q * qt, tile) : own(bh_q, qt, tile)).n;
   return p;

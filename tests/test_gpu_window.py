@@ -278,3 +278,28 @@ def test_offsets_past_32_bits():
     got, want = step(q, k, v, do), step(*last)
     # the same ranges of queries for the sinks' tile (their length is the window's), so the same sums
     assert all(torch.equal(x[:, -1:], y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_tiles_than_a_grid_has_rows(d):
+    """65600 tiles of one head; its ends against the definition on the tokens that reach them."""
+    N, W, T = 65600 * 128 + 77, 100, 500
+    q, k, v, do = (inputs.normal_bf16((1, 1, N, d), s, DEV) for s in range(4))
+    scale = d ** -0.5
+    o, lse = _fwd(q, k, v, scale, W, 0)
+    got = [torch.full_like(x, float("nan")) for x in (q, k, v)]
+    fattn.fa_window_bwd(q, k, v, o, do, lse, *got, scale, W, 0)
+    assert fattn.fa_get_status() == fattn.FA_OK
+    for rows, keys, dk_from, dk_to in ((slice(N - T, N), slice(N - T - W, N), W, T + W), (slice(0, T), slice(0, T), 0, T - W)):
+        qs, dos = q[:, :, rows], do[:, :, rows]
+        ks, vs = k[:, :, keys], v[:, :, keys]
+        bounds = _bounds(qs, ks, vs, scale, W, 0)
+        _check_fwd(o[:, :, rows], lse[:, :, rows], qs, ks, vs, scale, W, 0, bounds=bounds)
+        ref, _, otol, _, eps = bounds
+        want, bound = ow.window_backward(qs, ks, vs, dos, scale, W, 0, rel=U + 4 * eps + 2.0 ** -10,
+                                         o_err=otol + U * (np.abs(ref) + otol))
+        for n, g in zip(("dq", "dk", "dv"), got):
+            part = slice(0, T) if n == "dq" else slice(dk_from, dk_to)  # (the keys all of whose queries are here)
+            tol = bound[n] * (1 + 2.0 ** -6) + 1e-30
+            tol = tol + U * (np.abs(want[n]) + tol)
+            _inside(g[:, :, rows if n == "dq" else keys][:, :, part], want[n][:, :, part], tol[:, :, part], n)
