@@ -2,14 +2,14 @@
 // tiles one after another) and dQ (a few query tiles), by the formulas of fa_bwd.cu, P recomputed from the forward's lse.  The
 // scanned side is taken in halves of 64 rows, two or three in flight, as in fa_cross_bwd.cu.  Bound by the products whose
 // operands both come from shared memory (N = 64) at d = 128, by the halves' chains at d = 64.  Measured (GB300, us, the
-// kernels one at a time): 2 x 16/4 x 8192, d = 128, window 1024: D 23, dK/dV 260, dQ 213, sums 5; 4 x 16 x 2048, d = 64,
+// kernels one at a time): 2 x 16/4 x 8192, d = 128, window 1024: D 23, dK/dV 257, dQ 206, sums 5; 4 x 16 x 2048, d = 64,
 // window 256: 10, 53, 33, 6.
 //
 // dK, dV.  The queries that see a key tile are, in every query head that shares the key head, the tile's window, W + 127 of
 // them: one list of 128-row stages.  Key tile 0 holds the sinks (at most 128), which every later query sees: those
 // queries are a list of their own, as long as many windows, cut into ranges of about a window's length whose fp32 partial
 // sums (of the sinks' rows alone) a last kernel adds in their order.  So are the lists of all tiles where there are
-// too few of them to fill the SMs.  What the sinks cost (the whole backward, none / 4 / 16): 427 / 462 / 463 and 73.7 / 92 /
+// too few of them to fill the SMs.  What the sinks cost (the whole backward, none / 4 / 16): 420 / 453 / 454 and 73.4 / 92 /
 // 91.6 us at the sizes above.
 //
 // dQ.  A query tile scans the sinks before its first row's window (through tensor maps that end behind the sinks), then
@@ -222,6 +222,26 @@ __device__ __forceinline__ void ew_window_dq(const uint32_t (&sv)[32], const uin
   }
 }
 
+// A row of a gradient from TMEM to memory, rounded to bf16.
+template <int D>
+__device__ __forceinline__ void store_row_bf16(__nv_bfloat16* out, size_t row, bool valid, uint32_t taddr, float scale) {
+#pragma unroll
+  for (int q = 0; q < D / 32; ++q) {
+    uint32_t u[32];
+    tmem_ld_x32(taddr + 32u * q, u);
+    if (!valid) continue;
+    uint4* const dst = reinterpret_cast<uint4*>(out + row * D + 32 * q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = pack_bf16(__uint_as_float(u[8 * i + 2 * j]) * scale, __uint_as_float(u[8 * i + 2 * j + 1]) * scale);
+      dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 // The items of a block: n of the list of all heads' items, from rank `rank` of `head` on.  FLAT (one row of blocks): every `own` of
 // the list, over the heads' ends; else `own` of one head, heads and ranks in the order of grouped_block, the last ranks first if
 // `reversed`.
@@ -292,7 +312,9 @@ struct KeyItem {
   __device__ __forceinline__ int rows(const WindowBwdArgs& a) const { return sink ? a.sink_rows : min(kTile, a.Nk - kt * kTile); }
 };
 
-// One CTA per a.own_items items, one after another, the next one's K and V (d = 64) and first stages on their way meanwhile.
+// One CTA per a.own_items items, one after another, the next one's K, V and first stages on their way meanwhile: into a place of their
+// own (d = 64), or into the last one's once its last products with them are complete (d = 128; its gradients then go straight to
+// memory, not through K's and V's place).
 // Halves and stages are counted over all its items, so that their phases go on.  P^T and dS^T are packed into their
 // S^T and dP^T.
 template <int D>
@@ -302,6 +324,7 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
                        const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv,
                        const WindowBwdArgs a) {
   using C = DkdvCfg<D>;
+  constexpr int kOwnRead = C::B_OW + 1;  // (free with one place)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -333,10 +356,10 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
     }
     for (int c = 0; c < 2 * C::FLIGHT; ++c) mbar_init(BAR(C::B_PF + c), 128);
     mbar_init(BAR(C::B_GF), 2);    // an item's gradients are complete
-    // and out of TMEM (bf16: in K's and V's place).  A barrier for each place, so that it is never two phases ahead of a
+    // and out of TMEM (two places, bf16: in K's and V's).  A barrier for each place, so that it is never two phases ahead of a
     // waiting thread: an item that takes the place again starts with the copies that follow this one's store.
     mbar_init(BAR(C::B_OW), 256);
-    mbar_init(BAR(C::B_OW + 1), 256);
+    mbar_init(BAR(C::B_OW + 1), C::NB > 1 ? 256 : 1);  // (one place: the item's products with K and V are complete)
     for (int i = 0; i < kIssuers; ++i) mbar_init(BAR(C::B_DRAIN + i), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -408,16 +431,20 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
           }
         };
         take(min(C::ST, I.n_i));
-        if (t > 0 && ok) {
+        if (C::NB > 1 && t > 0 && ok) {
           ok = finish(done++);
           if (ok && owned < nt) load_own(owned++);
         }
         take(I.n_i);
+        if (C::NB == 1 && ok && owned < nt) {
+          ok = bwait(BAR(kOwnRead), t & 1, abort_flag, budget);
+          if (ok) load_own(owned++);
+        }
       }
       // every copy lands before the shared memory is released
       for (int t = max(0, owned - C::NB); t < owned; ++t) bdrain(BAR(C::B_OWN + t % C::NB), (t / C::NB) & 1, budget);
       for (int i = max(0, issued - C::ST); i < issued; ++i) bdrain(BAR(C::B_FULL + i % C::ST), (i / C::ST) & 1, budget);
-      while (ok && done < nt) ok = finish(done++);
+      while (C::NB > 1 && ok && done < nt) ok = finish(done++);
       bulk_wait_all();  // the stores complete before the CTA exits
     }
   } else if (warp >= C::MMA) {
@@ -444,6 +471,7 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
             issue_half_product<D>(d + 64, dV, sdesc_add(dR, st + C::TB), hh & 1);  // dP^T = V dO^T
             tc_commit(BAR(C::B_SF + g));
           }
+          if (C::NB == 1 && ok) tc_commit(BAR(kOwnRead));
         }
       } else {
         // dV += P^T dO (role 1), dK += dS^T Q (role 2)
@@ -487,21 +515,27 @@ __global__ void __launch_bounds__(CrossCfg<D, 2 * D>::THREADS, 1)
       ok = bwait_all(BAR(C::B_GF), t & 1, abort_flag, budget);
       if (!ok) return;
       tc_fence_after();
-      // an item without queries: its copies have landed (nothing else here has waited for them)
-      if (I.n_i == 0) ok = bwait_all(BAR(C::B_OWN + t % C::NB), (t / C::NB) & 1, abort_flag, budget);
+      // an item without queries: its copies have landed (nothing else here has waited for them) before zeros take their place
+      if (C::NB > 1 && I.n_i == 0) ok = bwait_all(BAR(C::B_OWN + t % C::NB), (t / C::NB) & 1, abort_flag, budget);
       if (!ok) return;
       const uint32_t acc = lanes + (g == 0 ? kV : kK);
       const float scale = g == 0 ? 1.f : a.scale;
       const uint32_t place = base + t % C::NB * (2 * C::TB) + (g == 0 ? C::TB : 0u);
       const bool part = I.part(a), in = r < I.rows(a);
+      const size_t row0 = static_cast<size_t>(I.bh) * a.Nk + I.kt * kTile;
+      void* const grad = g == 0 ? a.dv : a.dk;
+      auto no_query = [&](void* row, int bytes) {  // no query sees the tile
+        if (in)
+          for (int i = 0; i < bytes / 16; ++i) static_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
+      };
       if (part || a.grad_fp32) {
-        float* const dst = part ? I.part_at(a, g == 0 ? 1 : 0, D)
-                                : static_cast<float*>(g == 0 ? a.dv : a.dk) + (static_cast<size_t>(I.bh) * a.Nk + I.kt * kTile) * D;
-        if (I.n_i > 0) {
-          store_grad_row<D>(dst, r, in, acc, scale);
-        } else if (in) {  // no query sees the tile
-          for (int i = 0; i < D / 4; ++i) reinterpret_cast<float4*>(dst + static_cast<size_t>(r) * D)[i] = make_float4(0, 0, 0, 0);
-        }
+        float* const dst = part ? I.part_at(a, g == 0 ? 1 : 0, D) : static_cast<float*>(grad) + row0 * D;
+        if (I.n_i > 0) store_grad_row<D>(dst, r, in, acc, scale);
+        else no_query(dst + static_cast<size_t>(r) * D, D * 4);
+      } else if constexpr (C::NB == 1) {
+        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(grad) + row0 * D;
+        if (I.n_i > 0) store_row_bf16<D>(dst, r, in, acc, scale);
+        else no_query(dst + static_cast<size_t>(r) * D, D * 2);
       } else if (I.n_i > 0) {  // through shared memory: the V and K tiles have their shape and are no longer read
         stage_row_bf16<D>(place, place + kBox, r, acc, scale);
       } else {
@@ -585,8 +619,10 @@ struct DqTile {
 };
 
 // One CTA per a.own_tiles query tiles, scanned one after another, the next one's Q, dO and first keys
-// on their way meanwhile.  Halves and stages are counted over all its tiles, so that their phases go on.  dS is
-// packed into its dP.
+// on their way meanwhile: into places of their own (d = 64), or into the last one's once its last products with them are
+// complete (d = 128; dQ then goes straight to memory, not through Q's place; with the dK/dV kernel's items likewise, the
+// backward of 2 x 16/4 x 8192, window 1024: 462 -> 453 us, of 2 x 16/2 x 4096, window 256: 138 -> 132).  Halves and
+// stages are counted over all its tiles, so that their phases go on.  dS is packed into its dP.
 template <int D>
 __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -603,6 +639,7 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, N = a.N;
   const unsigned long long budget = a.budget;
+  constexpr int kQRead = C::B_OW + 1;  // (free with one place)
   const int per_head = (N + kTile - 1) / kTile;
   const BlockItems mine(a.flat, a.kv_heads * a.group, per_head, a.own_tiles, a.ng_q, true);  // the rows with whole windows first
   const int nt = mine.n;
@@ -620,8 +657,9 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
     for (int b = 0; b < C::NB; ++b) {
       mbar_init(BAR(C::B_OWN + b), 1);
       mbar_init(BAR(C::B_GF + b), 1);    // the tile's dQ is complete
-      mbar_init(BAR(C::B_OW + b), 128);  // and out of TMEM (bf16: in Q's place)
+      mbar_init(BAR(C::B_OW + b), 128);  // and out of TMEM (two places, bf16: in Q's)
     }
+    if (C::NB == 1) mbar_init(BAR(kQRead), 2);  // the tile's products with Q and dO are complete
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(BAR(C::B_FULL + s), 1);
       mbar_init(BAR(C::B_EMPTY + s), 1);
@@ -697,17 +735,21 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
           }
         };
         take(min(C::ST, k.n_j));
-        if (ok && t > 0) {
+        if (C::NB > 1 && ok && t > 0) {
           finish(done++);
           if (ok && owned < nt) load_own(owned++);
         }
         take(k.n_j);
+        if (C::NB == 1 && ok && owned < nt) {
+          ok = bwait(BAR(kQRead), t & 1, abort_flag, budget);
+          if (ok) load_own(owned++);
+        }
         before += k.n_j;
       }
       // every copy lands before the shared memory is released
       for (int t = max(0, owned - C::NB); t < owned; ++t) bdrain(BAR(C::B_OWN + t % C::NB), (t / C::NB) & 1, budget);
       for (int j = max(0, issued - C::ST); j < issued; ++j) bdrain(BAR(C::B_FULL + j % C::ST), (j / C::ST) & 1, budget);
-      while (ok && done < nt) finish(done++);
+      while (C::NB > 1 && ok && done < nt) finish(done++);
       bulk_wait_all();  // the stores complete before the CTA exits
     }
   } else if (warp >= C::MMA) {
@@ -733,6 +775,7 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
                                   sdesc_add(dR, s * C::STAGE), k.half(hh));
             tc_commit(BAR(C::B_SF + g));
           }
+          if (C::NB == 1 && ok) tc_commit(BAR(kQRead));
           jc += k.n_j;
         }
       } else {  // dQ += dS K
@@ -780,7 +823,8 @@ __global__ void __launch_bounds__(CrossCfg<D, D>::THREADS, 1)
       tc_fence_after();
       const uint32_t acc = lanes + C::COL_ACC + b * D, place = sOwn + b * (2 * C::TB);
       if (a.grad_fp32) store_grad_row<D>(a.dq, static_cast<size_t>(p.bh) * N + row, row < N, acc, a.scale);
-      else stage_row_bf16<D>(place, place + kBox, r, acc, a.scale);  // (its Q is no longer read)
+      else if (C::NB > 1) stage_row_bf16<D>(place, place + kBox, r, acc, a.scale);  // (its Q is no longer read)
+      else store_row_bf16<D>(static_cast<__nv_bfloat16*>(a.dq), static_cast<size_t>(p.bh) * N + row, row < N, acc, a.scale);
       tc_fence_before();
       mbar_arrive(BAR(C::B_OW + b));
     };
