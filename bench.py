@@ -66,21 +66,21 @@ def _peaks():
 # DRAM bytes per launch (dram__bytes_read.sum + dram__bytes_write.sum) from ncu captures summarised
 # under profiles/, keyed by kernel and workload, valid only while the kernels' code is unchanged: each source
 # with the digest (_code_digest) of it and all it includes.
-_FWD = "651a43dfda36af233d0fb8f61fbf90619bd81d1714c4955fab2017278a1c0cb4"
-_BWD = "d032e86e6b82332953e16bd93213d1bd3344fe63fc09530d287b5a12767bb6d5"
-_DEC = "530a392fe46150c5de6023c83a486505df4266addb7fff62725c81811673774d"
+_FWD = "6acd36ec28b8baed9aa0b4f829d4a259dba69bc12cf038b9f30d0d0d85f3fe9e"
+_BWD = "aa1f8da96f45ab86fe9b4fc5d18ebc061949c890fc3accc37cc5cef7f7c6f844"
+_DEC = "267f9dfbaeb9e85a32589f6d3ea491a98eede1078cfaf32e1f70eac084c48bab"
 NCU_TRAFFIC = {
-    ("fwd_kernel", "ragged"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 559.537e6},
-    ("fwd_kernel", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 264.576e6},
-    ("fwd_kernel_fp8", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 136.400e6},
-    ("fwd_persist_kernel", "prefill"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 50.645e6},
+    ("fwd_kernel", "ragged"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 561.071e6},
+    ("fwd_kernel", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 263.962e6},
+    ("fwd_kernel_fp8", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 136.472e6},
+    ("fwd_persist_kernel", "prefill"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 50.500e6},
     # backward: the dominant kernel (dK/dV) on the causal workload
-    ("bwd_dkdv_kernel", "causal"): {"sources": {"fa_bwd.cu": _BWD}, "bytes": 372.525e6},
+    ("bwd_dkdv_kernel", "causal"): {"sources": {"fa_bwd.cu": _BWD}, "bytes": 372.937e6},
     # the four-shard step: four forward launches over the key shards and the combine, summed
-    ("causal_sharded4", "causal"): {"sources": {"fa_fwd.cu": _FWD, "fa_decode.cu": _DEC}, "bytes": 1110.309e6},
+    ("causal_sharded4", "causal"): {"sources": {"fa_fwd.cu": _FWD, "fa_decode.cu": _DEC}, "bytes": 1110.280e6},
     # decode: captured on the B4 slice (decode_small) and scaled by 16 to B64 (K/V streamed once)
-    ("decode_split_kernel", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.950e6},
-    ("decode_split_kernel_paged", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.946e6},
+    ("decode_split_kernel", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2151.049e6},
+    ("decode_split_kernel_paged", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.918e6},
 }
 SOURCE_DIRS = (os.path.join(ROOT, "exact_attention_06_gb300", "csrc"), os.path.join(ROOT, "include"))
 
