@@ -9,8 +9,8 @@
 // them: one list of 128-row stages.  Key tile 0 holds the sinks (at most 128), which every later query sees: those
 // queries are a list of their own, as long as many windows, cut into ranges of about a window's length whose fp32 partial
 // sums (of the sinks' rows alone) a last kernel adds in their order.  So are the lists of all tiles where there are
-// too few of them to fill the SMs.  What the sinks cost (the whole backward, none / 4 / 16): 420 / 453 / 454 and 73.4 / 92 /
-// 91.6 us at the sizes above.
+// too few of them to fill the SMs.  What the sinks cost (the whole backward, none / 4 / 16): 420 / 454 / 454 and 72.2 / 91 /
+// 90.8 us at the sizes above.
 //
 // dQ.  A query tile scans the sinks before its first row's window (through tensor maps that end behind the sinks), then
 // the keys from that window's first, lo, up to its last row's own.
@@ -33,7 +33,8 @@ namespace {
 // dP_ij - D_i is small beside it: measured over rows of 2 / 4 / 12 / 64 keys (d = 128, norms of dQ's error
 // over dQ) 0.0038 / 0.0030 / 0.0026 / 0.0024, of which rounding dQ itself is 0.0017; in the second form 0.0024 throughout.  So
 // rows of at most kFewKeys keys (all of a narrow window's, the first of any sequence) take the second form, with warp-level
-// products of their 16 rows and the keys that they see, bound by their loads' latency.  The first form is
+// products of their 16 rows and the keys that they see, bound by their loads' latency (rows of up to 32 / 48 / 64 keys: dQ's error
+// 0.00250 / 0.00246 / 0.00237 at most; 2 x 16 x 8192, d = 128, window 64: 180 / 180 / 228 us of backward).  The first form is
 // bound by memory, and a kernel of its own, whose few registers leave room for the warps that keep loads in flight (one kernel
 // of both: 25 instead of 20 us for 262144 rows at d = 128, 6.7 TB/s).
 //
@@ -41,7 +42,7 @@ namespace {
 // dK/dV kernel has those of a stage by one bulk copy; a head's rows are row_stride(N) apart, those from N on
 // {-inf, 0}: their P is 0.
 __host__ __device__ constexpr int row_stride(int N) { return (N + kTile) & ~1; }
-constexpr int kFewKeys = 64;
+constexpr int kFewKeys = 48;
 constexpr int kDeltaThreads = 128;
 
 // Leading groups of 16 rows whose first row, which sees the fewest keys, sees at most kFewKeys.
