@@ -33,8 +33,10 @@ namespace {
 // dP_ij - D_i is small beside it: measured over rows of 2 / 4 / 12 / 64 keys (d = 128, norms of dQ's error
 // over dQ) 0.0038 / 0.0030 / 0.0026 / 0.0024, of which rounding dQ itself is 0.0017; in the second form 0.0024 throughout.  So
 // rows of at most kFewKeys keys (all of a narrow window's, the first of any sequence) take the second form, with warp-level
-// products of their 16 rows and the keys that they see, bound by their loads' latency (rows of up to 32 / 48 / 64 keys: dQ's error
-// 0.00250 / 0.00246 / 0.00237 at most; 2 x 16 x 8192, d = 128, window 64: 180 / 180 / 228 us of backward).  The first form is
+// products of their 16 rows and the keys that they see, bound by their loads' latency.  (Rows of up to 32 / 48 / 64 keys:
+// dQ's error 0.00250 / 0.00246 / 0.00237 at most; us of backward: 64 x 8 x 128, d = 128, window 64 47 / 49 / 58, 4 x 16 x 2048,
+// d = 64, window 256 90 / 91 / 92; 2 x 16 x 8192, d = 128, window 64, whose rows are all the second form's with 64 only: 180
+// instead of 228.)  The first form is
 // bound by memory, and a kernel of its own, whose few registers leave room for the warps that keep loads in flight (one kernel
 // of both: 25 instead of 20 us for 262144 rows at d = 128, 6.7 TB/s).
 //
