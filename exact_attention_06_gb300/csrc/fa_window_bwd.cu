@@ -225,22 +225,23 @@ __device__ __forceinline__ void ew_window_dq(const uint32_t (&sv)[32], const uin
   }
 }
 
-// A row of a gradient from TMEM to memory, rounded to bf16.
+// A row of a gradient from TMEM to memory, rounded to bf16; whole sectors where `out` is 32-byte aligned.
 template <int D>
 __device__ __forceinline__ void store_row_bf16(__nv_bfloat16* out, size_t row, bool valid, uint32_t taddr, float scale) {
+  const bool whole = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
 #pragma unroll
   for (int q = 0; q < D / 32; ++q) {
     uint32_t u[32];
     tmem_ld_x32(taddr + 32u * q, u);
     if (!valid) continue;
-    uint4* const dst = reinterpret_cast<uint4*>(out + row * D + 32 * q);
+    __nv_bfloat16* const dst = out + row * D + 32 * q;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w[4];
+    for (int i = 0; i < 2; ++i) {
+      uint32_t w[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = pack_bf16(__uint_as_float(u[8 * i + 2 * j]) * scale, __uint_as_float(u[8 * i + 2 * j + 1]) * scale);
-      dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int j = 0; j < 8; ++j)
+        w[j] = pack_bf16(__uint_as_float(u[16 * i + 2 * j]) * scale, __uint_as_float(u[16 * i + 2 * j + 1]) * scale);
+      store_bf16x16(dst + 16 * i, w, whole);
     }
   }
 }

@@ -337,6 +337,17 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+// 16 bf16 values to memory, 16-byte aligned, or (`whole`) a 32-byte sector at once.
+__device__ __forceinline__ void store_bf16x16(void* p, const uint32_t (&x)[8], bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }

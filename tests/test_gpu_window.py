@@ -260,6 +260,27 @@ def test_a_wait_that_runs_out_is_reported(d):
         assert e.value.status == fattn.FA_ERR_TIMEOUT and fattn.fa_get_status() == fattn.FA_OK
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S", [0, 3])
+def test_outputs_aligned_to_16_bytes_only(S, d):
+    """The same values as in outputs of torch's own alignment, and nothing before or behind them."""
+    q, k, v, do = _inputs(2, 6, 2, 333, 333, d, 70, S)
+
+    def step(shift):
+        def out(x):
+            buf = torch.full((x.numel() + 64,), 7.0, dtype=torch.bfloat16, device=DEV)
+            return buf, buf[shift:shift + x.numel()].view(x.shape)
+        bufs, outs = zip(*(out(x) for x in (q, q, k, v)))
+        lse = torch.empty(q.shape[:3], device=DEV)
+        fattn.fa_window_fwd(q, k, v, outs[0], lse, 0.1, 70, S)
+        fattn.fa_window_bwd(q, k, v, outs[0], do, lse, *outs[1:], 0.1, 70, S)
+        assert fattn.fa_get_status() == fattn.FA_OK
+        for b, o in zip(bufs, outs):
+            assert (b[:shift] == 7).all() and (b[shift + o.numel():] == 7).all()
+        return outs
+    assert all(torch.equal(x, y) for x, y in zip(step(0), step(8)))
+
+
 def test_offsets_past_32_bits():
     """The last head lies behind 2^31 elements: what a call of its own gives."""
     B, Hq, Hkv, N, d, W, S = 1, 66, 66, 2 ** 18, 128, 130, 3
