@@ -19,8 +19,8 @@
 // 16 keys, and its softmax 32 columns where they suffice.
 //
 // Bound by the tensor cores and the softmax's chains in a long window, by an item's begin and end in a narrow one.  Measured
-// (GB300): 32/8 heads x 16381, d = 128, window 4096: 666 us (1443 TFLOP/s of the visible pairs, 0.75 of the library's largest
-// product); 2 x 16/4 x 8192, window 1024: 124 us; 4 x 16 x 2048, d = 64, window 256: 26 us (the tiles' keys are 1.5 times
+// (GB300): 32/8 heads x 16381, d = 128, window 4096: 650 us (1478 TFLOP/s of the visible pairs, 0.78 of the library's largest
+// product); 2 x 16/4 x 8192, window 1024: 118 us; 4 x 16 x 2048, d = 64, window 256: 26 us (the tiles' keys are 1.5 times
 // the window's); 4 x 16/4 x 517 behind 1500 keys, window 333: 10.2 us.
 #include <algorithm>
 #include <climits>
@@ -152,7 +152,7 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
 // item only after its threads have U in registers (SC), so the barrier is never two phases ahead of them.  O goes
 // straight from registers to memory: the shared memory is full, and Q's place is the next item's.
 struct Cfg128 : FwdCfg<128> {
-  static constexpr int B_Q = 0, B_QE = 1, B_KF = 2, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST, B_SF = B_VE + VST,
+  static constexpr int B_Q = 0, B_QE = 2, B_KF = 4, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST, B_SF = B_VE + VST,
                        B_PF = B_SF + 2, B_SC = B_PF + 2, B_DRAIN = B_SC + 2, NBAR = B_DRAIN + 1;
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR;
   static constexpr uint32_t SMEM = OFF_MISC + 16u + 1024u;
@@ -178,8 +178,6 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
   grid_dep_launch();  // a dependent kernel may launch once every CTA has started
   clear_unused_rows<C::NH>(sQ, C::QB, a.pack * a.tile);
   if (threadIdx.x == 0) {
-    mbar_init(BAR(C::B_Q), 1);
-    mbar_init(BAR(C::B_QE), 2);  // by both tiles, as the rings' stages are released
     for (int s = 0; s < C::KST; ++s) {
       mbar_init(BAR(C::B_KF + s), 1);
       mbar_init(BAR(C::B_KE + s), 1);
@@ -189,6 +187,8 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
       mbar_init(BAR(C::B_VE + s), 1);
     }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(BAR(C::B_Q + t), 1);
+      mbar_init(BAR(C::B_QE + t), 1);
       mbar_init(BAR(C::B_SF + t), 1);
       mbar_init(BAR(C::B_PF + t), C::SMW * 32);
       mbar_init(BAR(C::B_SC + t), C::SMW * 32);
@@ -226,13 +226,15 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
             tma_load_3d(dst + h * kBox, is_v ? (sink ? &tvs : &tv) : (sink ? &tks : &tk), bar, h * 64, I.key(j), kh);
         };
         auto load_q = [&] {
-          // the last item's Q is free once both tiles' last S MMAs have completed
-          if (it > 0 && !wait(BAR(C::B_QE), (it - 1) & 1)) return false;
-          mbar_arrive_expect_tx(BAR(C::B_Q), 2 * C::NH * static_cast<uint32_t>(a.pack * a.tile) * 128u);
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2; ++t) {
+            // The last item's Q is free once the tile's last S MMA has completed (when both tiles' have, 2 x 16 heads x 8192 at
+            // windows of 64 / 256 / 1024: 62.8 / 71.7 / 122.6 instead of 57.9 / 67.0 / 120.4 us).
+            if (it > 0 && !wait(BAR(C::B_QE + t), (it - 1) & 1)) return false;
+            mbar_arrive_expect_tx(BAR(C::B_Q + t), C::NH * static_cast<uint32_t>(a.pack * a.tile) * 128u);
             for (int h = 0; h < C::NH; ++h)
-              tma_load_4d(sQ + t * C::QB + h * kBox, &tq, BAR(C::B_Q), h * 64, 0, I.n0 + t * a.tile, I.u);
-          q_issued = it + 1;
+              tma_load_4d(sQ + t * C::QB + h * kBox, &tq, BAR(C::B_Q + t), h * 64, 0, I.n0 + t * a.tile, I.u);
+            ++q_issued;
+          }
           return true;
         };
         for (int j = 0; ok && j < I.n; ++j) {
@@ -250,7 +252,10 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
         kc += I.n;
       }
       // Every copy this CTA started must land before its shared memory is released.
-      if (q_issued > 0) drain_wait(BAR(C::B_Q), (q_issued - 1) & 1, budget);
+      for (int t = 0; t < 2; ++t) {
+        const int n = (q_issued + 1 - t) / 2;
+        if (n > 0) drain_wait(BAR(C::B_Q + t), (n - 1) & 1, budget);
+      }
       for (int g = max(0, k_issued - C::KST); g < k_issued; ++g)
         drain_wait(BAR(C::B_KF + g % C::KST), (g / C::KST) & 1, budget);
       for (int g = max(0, v_issued - C::VST); g < v_issued; ++g)
@@ -281,7 +286,6 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
           const uint64_t dk = sdesc_add(dk0, ks * C::KVB), dv = sdesc_add(dv0, vs * C::KVB);
           if (has_v && !wait(BAR(C::B_VF + vs), vp)) return false;
           if (has_k && !wait(BAR(C::B_KF + ks), kp)) return false;
-          if (!MID && j == 0 && !wait(BAR(C::B_Q), it & 1)) return false;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const uint32_t d_s = tmem + static_cast<uint32_t>(t * kBc), d_o = tmem + kColO + t * D;
@@ -300,6 +304,7 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
               if (!pv && !sc) continue;
               if (pv && !wait(BAR(C::B_PF + t), g & 1)) return false;
               if (sc && j == begin && e > 0 && !wait(BAR(C::B_SC + t), (e - 1) & 1)) return false;  // its last U is out
+              if (sc && j == begin && !wait(BAR(C::B_Q + t), it & 1)) return false;
               tc_fence_after();
               if (pv) {
                 if (j > I.ws) issue_values<D, false>(d_o, d_s, dv, 8, j - 1 == begin);
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
               // S_t ready and the PV before it done: U_t may be rescaled (not between the sinks and a skipped step); or
               // U final.
               if (sc || last) tc_commit(BAR(C::B_SF + t));
-              if (sc && j + 1 == end) tc_commit(BAR(C::B_QE));
+              if (sc && j + 1 == end) tc_commit(BAR(C::B_QE + t));
               if (last) ++e;
             }
           }
@@ -332,7 +337,10 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
         for (; ok && j < min(mid0, I.n + 1); ++j) ok = iterate(std::false_type{}, j);
         for (; ok && j < mid1; ++j) ok = iterate(std::true_type{}, j);
         for (; ok && j <= I.n; ++j) ok = iterate(std::false_type{}, j);
-        if (I.end1 == 0) mbar_arrive(BAR(C::B_QE));  // no second tile
+        if (ok && I.end1 == 0) {  // no second tile
+          ok = wait(BAR(C::B_Q + 1), it & 1);
+          mbar_arrive(BAR(C::B_QE + 1));
+        }
       }
       tc_commit(BAR(C::B_DRAIN));  // all MMAs complete before TMEM is released
       drain_wait(BAR(C::B_DRAIN), 0, budget);
