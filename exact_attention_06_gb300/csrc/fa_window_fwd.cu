@@ -19,8 +19,8 @@
 // 16 keys, and its softmax 32 columns where they suffice.
 //
 // Bound by the tensor cores and the softmax's chains in a long window, by an item's begin and end in a narrow one.  Measured
-// (GB300): 32/8 heads x 16381, d = 128, window 4096: 650 us (1478 TFLOP/s of the visible pairs, 0.78 of the library's largest
-// product); 2 x 16/4 x 8192, window 1024: 118 us; 4 x 16 x 2048, d = 64, window 256: 26 us (the tiles' keys are 1.5 times
+// (GB300): 32/8 heads x 16381, d = 128, window 4096: 645 us (1490 TFLOP/s of the visible pairs, 0.78 of the library's largest
+// product); 2 x 16/4 x 8192, window 1024: 114 us; 4 x 16 x 2048, d = 64, window 256: 26 us (the tiles' keys are 1.5 times
 // the window's); 4 x 16/4 x 517 behind 1500 keys, window 333: 10.2 us.
 #include <algorithm>
 #include <climits>
@@ -150,19 +150,30 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
 // d = 128: P~ aliases S (fa_fwd.cu's schedule for d = 128), one issuing thread.  Per tile the SF barrier completes once a
 // step (S ready, and the PV before it done) and once more at an item's end (U final); the issuer starts the tile's next
 // item only after its threads have U in registers (SC), so the barrier is never two phases ahead of them.  O goes
-// straight from registers to memory: the shared memory is full, and Q's place is the next item's.
+// straight from registers to memory, as far as it has no room of its own: Q's place is the next item's.
+// STAGED, for tiles of several heads: two K stages, and in place of the third half of each tile's O on its way to memory.
+// Straight to memory a warp's rows are a line each, which keeps the load-store unit busy for 11 of 118 us at 2 x 16/4 x 8192,
+// window 1024 (by whole sectors; 15 of 122 by halves of them; put together by shuffles it takes 138).  Where both tiles of an
+// item end together, half of the columns go through shared memory: 118 -> 114 us, at window 256 66 -> 59; tiles of one
+// head, a step apart: 55 -> 58 (2 x 16 x 8192, window 64).
+template <bool STAGED>
 struct Cfg128 : FwdCfg<128> {
+  static constexpr int KST = STAGED ? 2 : 3;
+  static constexpr uint32_t OFF_V = OFF_K + KST * KVB, OFF_O = OFF_V + VST * KVB, OFF_BAR = OFF_O + (STAGED ? 2 * kBox : 0);
   static constexpr int B_Q = 0, B_QE = 2, B_KF = 4, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST, B_SF = B_VE + VST,
-                       B_PF = B_SF + 2, B_SC = B_PF + 2, B_DRAIN = B_SC + 2, NBAR = B_DRAIN + 1;
+                       B_PF = B_SF + 2, B_SC = B_PF + 2, B_OSF = B_SC + 2, B_OW = B_OSF + 2, B_DRAIN = B_OW + 2,
+                       NBAR = B_DRAIN + 1;
   static constexpr uint32_t OFF_MISC = OFF_BAR + 8u * NBAR;
   static constexpr uint32_t SMEM = OFF_MISC + 16u + 1024u;
 };
 
-__global__ void __launch_bounds__(Cfg128::THREADS, 1)
+template <bool STAGED>
+__global__ void __launch_bounds__(Cfg128<STAGED>::THREADS, 1)
     window_fwd128_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tks,
-                         const __grid_constant__ CUtensorMap tvs, const WindowFwdArgs a) {
-  using C = Cfg128;
+                         const __grid_constant__ CUtensorMap tvs, const __grid_constant__ CUtensorMap to,
+                         const WindowFwdArgs a) {
+  using C = Cfg128<STAGED>;
   constexpr int D = 128;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -192,6 +203,8 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
       mbar_init(BAR(C::B_SF + t), 1);
       mbar_init(BAR(C::B_PF + t), C::SMW * 32);
       mbar_init(BAR(C::B_SC + t), C::SMW * 32);
+      mbar_init(BAR(C::B_OSF + t), 1);            // the last item's staged O has been read
+      mbar_init(BAR(C::B_OW + t), C::SMW * 32);   // this one's is there
     }
     mbar_init(BAR(C::B_DRAIN), 1);
     *abort_flag = 0;
@@ -352,7 +365,9 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
     const uint32_t t_s = tmem + lane_addr + static_cast<uint32_t>(t * kBc);
     const uint32_t t_o = tmem + lane_addr + kColO + static_cast<uint32_t>(t * D);
     const uint64_t c2 = f2_pack(a.sl2, a.sl2);
-    int ph = 0;  // phases of SF so far
+    const bool o_issuer = warp % C::SMW == 0 && lane == 0;
+    const uint32_t o_stage = base + C::OFF_O + static_cast<uint32_t>(t) * kBox;
+    int ph = 0, gi = 0;  // phases of SF so far, O tiles staged
     bool ok = true;
     for (int w = w0; ok && w < a.n_items; w += w_step) {
       const Item I(a, w);
@@ -419,36 +434,68 @@ __global__ void __launch_bounds__(Cfg128::THREADS, 1)
       tc_fence_before();
       mbar_arrive(BAR(C::B_SC + t));  // U_t is in registers
       const Row row(I, a, t, r);
-      if (row.in) {
-        const size_t at = row.at;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        if (a.o_fp32) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      if (row.in) a.lse[row.at] = l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
+      if (a.o_fp32) {
+        if (row.in) {
+          float* const dst = static_cast<float*>(a.o) + row.at * D;
 #pragma unroll
-          for (int i = 0; i < D; ++i) u[i / 64][i % 64] = __float_as_uint(__uint_as_float(u[i / 64][i % 64]) * inv);
-          float* dst = static_cast<float*>(a.o) + at * D;
-#pragma unroll
-          for (int i = 0; i < D / 4; ++i)
-            *reinterpret_cast<uint4*>(dst + 4 * i) = *reinterpret_cast<const uint4*>(&u[i / 16][4 * (i % 16)]);
-        } else {
-          __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(a.o) + at * D;
-          // Rows are a line each for their thread: sectors at once halve the stores (124 -> 118 us at 2 x 16/4 x 8192, window
-          // 1024, of which 11 are the stores; lines put together by shuffles: 138).
-          const bool whole = (reinterpret_cast<uintptr_t>(a.o) & 31) == 0;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int e = 16 * i + 2 * j;
-              w[j] = pack_bf16(__uint_as_float(u[e / 64][e % 64]) * inv, __uint_as_float(u[e / 64][e % 64 + 1]) * inv);
-            }
-            store_bf16x16(dst + 16 * i, w, whole);
+          for (int i = 0; i < D / 4; ++i) {
+            const uint32_t* x = &u[i / 16][4 * (i % 16)];
+            reinterpret_cast<float4*>(dst)[i] = make_float4(__uint_as_float(x[0]) * inv, __uint_as_float(x[1]) * inv,
+                                                            __uint_as_float(x[2]) * inv, __uint_as_float(x[3]) * inv);
           }
         }
-        a.lse[at] = l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
+        __syncwarp();
+        continue;
       }
+      auto pieces = [&](int i, uint32_t (&w)[8]) {  // columns 16 i ..
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          w[e] = pack_bf16(__uint_as_float(u[i / 4][16 * (i % 4) + 2 * e]) * inv,
+                           __uint_as_float(u[i / 4][16 * (i % 4) + 2 * e + 1]) * inv);
+      };
+      if constexpr (STAGED) {
+        if (gi > 0) {
+          if (o_issuer) {
+            bulk_wait_read_all();
+            mbar_arrive(BAR(C::B_OSF + t));
+          }
+          ok = wait_all(BAR(C::B_OSF + t), (gi - 1) & 1, abort_flag, budget);
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[8];
+          pieces(i, w);
+          const uint32_t at = o_stage + static_cast<uint32_t>(r) * 128u, x = static_cast<uint32_t>(r & 7);
+          sts128(at + (((2u * i) ^ x) << 4), w[0], w[1], w[2], w[3]);
+          sts128(at + (((2u * i + 1u) ^ x) << 4), w[4], w[5], w[6], w[7]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(BAR(C::B_OW + t));
+      }
+      if (row.in) {
+        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(a.o) + row.at * D;
+        const bool whole = (reinterpret_cast<uintptr_t>(a.o) & 31) == 0;
+#pragma unroll
+        for (int i = STAGED ? 4 : 0; i < 8; ++i) {
+          uint32_t w[8];
+          pieces(i, w);
+          store_bf16x16(dst + 16 * i, w, whole);
+        }
+      }
+      if (STAGED && o_issuer) {
+        ok = wait(BAR(C::B_OW + t), gi & 1);
+        if (ok) {
+          tma_store_4d(&to, o_stage, 0, 0, I.n0 + t * a.tile, I.u);
+          bulk_commit();
+        }
+      }
+      ++gi;
       __syncwarp();
     }
+    if (o_issuer) bulk_wait_all();  // the stores complete before the CTA exits
     tmem_wait_st();
   }
 #undef BAR
@@ -474,7 +521,8 @@ struct Cfg64 : FwdCfg<64> {
   static constexpr uint32_t OFF_O = (OFF_MISC + 16u + 1023u) & ~1023u;
   static constexpr uint32_t SMEM = OFF_O + 2u * kBr * 128u + 1024u;
 };
-static_assert(Cfg128::SMEM <= 232448 && Cfg64::SMEM <= 232448, "shared memory of the window kernels exceeds 227 KB");
+static_assert(Cfg128<true>::SMEM <= 232448 && Cfg128<false>::SMEM <= 232448 && Cfg64::SMEM <= 232448,
+              "shared memory of the window kernels exceeds 227 KB");
 
 __global__ void __launch_bounds__(Cfg64::THREADS, 1)
     window_fwd64_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -794,7 +842,11 @@ cudaError_t launch_window_fwd(const WindowFwdLaunch& l, cudaStream_t stream) {
   const int grid = static_cast<int>(std::min<long long>(items, l.sms));
   if (l.d == 64)
     return launch_kernel(window_fwd64_kernel, grid, Cfg64::THREADS, Cfg64::SMEM, stream, l.tq, l.tk, l.tv, l.tks, l.tvs, l.to, a);
-  return launch_kernel(window_fwd128_kernel, grid, Cfg128::THREADS, Cfg128::SMEM, stream, l.tq, l.tk, l.tv, l.tks, l.tvs, a);
+  auto launch128 = [&](auto kern, int threads, uint32_t smem) {
+    return launch_kernel(kern, grid, threads, smem, stream, l.tq, l.tk, l.tv, l.tks, l.tvs, l.to, a);
+  };
+  return a.pack > 1 ? launch128(window_fwd128_kernel<true>, Cfg128<true>::THREADS, Cfg128<true>::SMEM)
+                    : launch128(window_fwd128_kernel<false>, Cfg128<false>::THREADS, Cfg128<false>::SMEM);
 }
 
 cudaError_t window_fwd_status_word(unsigned int** p) {

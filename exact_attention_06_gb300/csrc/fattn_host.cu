@@ -575,7 +575,8 @@ fa_status_t check_window_args(int B, int Hq, int Hkv, int N, int Nk, int d, int 
 // Query heads that share a tile of the forward: all of the key head's G, so that a tile's 128 rows are 128 / G positions,
 // whose windows together span fewer keys; or one, where a G that does not divide 128 would leave too many rows unused.
 // By the steps of 128 keys that all items of two tiles take.  Measured (GB300, us), one head a tile / G = 4: d = 64, 4 x
-// 16/4 heads, 517 behind 1500 keys, window 333: 14.6 / 10.2; d = 128, 32/8 heads x 16381, window 4096: 673 / 666.
+// 16/4 heads, 517 behind 1500 keys, window 333: 14.7 / 10.1; d = 128, 2 x
+// 16/4 x 8192, windows of 64 / 1024: 52.6 / 36.2, 122.9 / 118.5; 32/8 heads x 16381, window 4096: 622 / 614.
 int window_pack(int B, int Hq, int Hkv, int N, int window) {
   const int G = Hq / Hkv;
   auto steps = [&](int pack) {
@@ -1535,7 +1536,7 @@ fa_status_t fa_window_fwd(const void* q, const void* k, const void* v, void* o, 
     if ((st = make_map(&l.tks, k, d, Nk, kv_heads, 128, 2, shown)) != FA_OK) return st;
     if ((st = make_map(&l.tvs, v, d, Nk, kv_heads, 128, 2, shown)) != FA_OK) return st;
   }
-  if (!o_fp32 && d == 64 && (st = make_packed_map(&l.to, o, d, pack, N, units, tile)) != FA_OK) return st;
+  if (!o_fp32 && (st = make_packed_map(&l.to, o, d, pack, N, units, tile)) != FA_OK) return st;
   l.args = {o, lse, N, Nk, std::min(window, Nk), shown, o_fp32, scale * 1.4426950408889634f,
             opts && opts->wait_budget_cycles ? opts->wait_budget_cycles : kDefaultBudget, units, Hq / Hkv / pack, pack, tile,
             0, 0};
