@@ -492,8 +492,8 @@ __global__ void __launch_bounds__(Cfg128<STAGED>::THREADS, 1)
           bulk_commit();
         }
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);  // (the lanes leave together: the next item's waits are the whole warp's)
       ++gi;
-      __syncwarp();
     }
     if (o_issuer) bulk_wait_all();  // the stores complete before the CTA exits
     tmem_wait_st();
@@ -793,6 +793,7 @@ __global__ void __launch_bounds__(Cfg64::THREADS, 1)
             bulk_commit();
           }
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);  // (the lanes leave together: the next item's waits are the whole warp's)
         ++gi;
       }
       // The U_t loads above complete (tcgen05.wait::ld) before this thread's first P~-ready arrival of the next item,

@@ -1,0 +1,56 @@
+"""Waits that run out in the persistent forward kernels while their blocks have several items to go: the call ends, reports
+FA_ERR_TIMEOUT (or has finished within the budget, with the right outputs), and the next call's outputs are what they were.
+
+Budgets from one cycle (nothing arrives) to about the length of a call, so that waits run out at a block's first item, between
+its items and at its last, and in only some of a tile's warps."""
+
+import pytest
+import torch
+
+from _util import ensure_built
+from exact_attention_06_gb300 import fattn, inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BUDGETS = (1, 300, 1000, 2000, 4000, 8000, 16000, 50000)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+def _outputs(q, o_fp32):
+    return (torch.full(q.shape, float("nan"), dtype=torch.float32 if o_fp32 else torch.bfloat16, device=DEV),
+            torch.full(q.shape[:3], float("nan"), device=DEV))
+
+
+def _check(call, q, o_fp32, items):
+    assert items > 2 * torch.cuda.get_device_properties(0).multi_processor_count  # (blocks of several items)
+    want = _outputs(q, o_fp32)
+    call(*want, 0)
+    assert fattn.fa_get_status() == fattn.FA_OK
+    for budget in BUDGETS:
+        for _ in range(3):
+            got = _outputs(q, o_fp32)
+            call(*got, budget)
+            try:
+                fattn.fa_get_status()
+                assert budget > 1 and all(torch.equal(a, b) for a, b in zip(got, want)), f"budget {budget}"
+            except fattn.FattnError as e:
+                assert e.status == fattn.FA_ERR_TIMEOUT, f"budget {budget}"
+        got = _outputs(q, o_fp32)
+        call(*got, 0)
+        assert fattn.fa_get_status() == fattn.FA_OK
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), f"after a budget of {budget}"
+
+
+@pytest.mark.parametrize("o_fp32", [False, True])
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 16, 16), (64, 16, 4), (128, 16, 16), (128, 16, 4)])
+def test_window(d, Hq, Hkv, o_fp32):
+    """Tiles of one head and of the heads that share a key head (d = 128: with half of O staged)."""
+    B, N, W, S = 4, 2100, 256, 4
+    q = inputs.normal_bf16((B, Hq, N, d), 1, DEV)
+    k, v = inputs.normal_bf16((B, Hkv, N, d), 2, DEV), inputs.normal_bf16((B, Hkv, N, d), 3, DEV)
+    _check(lambda o, lse, budget: fattn.fa_window_fwd(q, k, v, o, lse, 0.1, W, S, wait_budget_cycles=budget), q, o_fp32,
+           B * Hq * N // 256)
