@@ -1027,6 +1027,7 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
             bulk_commit();
           }
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);  // (the lanes leave together: the next item's waits are the whole warp's)
         ++gi;
       }
       // The U_t loads above complete (tcgen05.wait::ld) before this thread's first P~-ready

@@ -54,3 +54,23 @@ def test_window(d, Hq, Hkv, o_fp32):
     k, v = inputs.normal_bf16((B, Hkv, N, d), 2, DEV), inputs.normal_bf16((B, Hkv, N, d), 3, DEV)
     _check(lambda o, lse, budget: fattn.fa_window_fwd(q, k, v, o, lse, 0.1, W, S, wait_budget_cycles=budget), q, o_fp32,
            B * Hq * N // 256)
+
+
+@pytest.mark.parametrize("o_fp32", [False, True])
+def test_prefill(o_fp32):
+    B, H, N, d = 4, 16, 2100, 64
+    q, k, v = (inputs.normal_bf16((B, H, N, d), s, DEV) for s in (1, 2, 3))
+    _check(lambda o, lse, budget: fattn.fa_fwd_ex(q, k, v, o, lse, 0.1, False, wait_budget_cycles=budget), q, o_fp32,
+           B * H * N // 256)
+
+
+@pytest.mark.parametrize("o_fp32", [False, True])
+def test_cross(o_fp32):
+    """Sequences of their own lengths, one of them empty, whose last key tiles are cleared behind them."""
+    B, Hq, Hkv, Nq, Nk, d = 4, 16, 8, 2100, 700, 64
+    q = inputs.normal_bf16((B, Hq, Nq, d), 1, DEV)
+    k, v = inputs.normal_bf16((B, Hkv, Nk, d), 2, DEV), inputs.normal_bf16((B, Hkv, Nk, d), 3, DEV)
+    v[1, :, 333:] = float("nan")
+    kv_lens = torch.tensor([Nk, 333, 0, 650], dtype=torch.int32, device=DEV)
+    _check(lambda o, lse, budget: fattn.fa_cross_fwd(q, k, v, o, lse, 0.1, kv_lens, wait_budget_cycles=budget), q, o_fp32,
+           B * Hq * Nq // 256)
