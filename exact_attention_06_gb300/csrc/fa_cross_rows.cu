@@ -21,8 +21,9 @@
 // fragments, so that 0 times what the padding holds never reaches U.
 //
 // Paged.  A stage is 64 keys of one page (page sizes are multiples of 64).  A sequence's stages are those of the sinks
-// before its window and those from the window's first key on; nothing between them is read, neither table nor
-// pages.  The producer's lanes look up the pages of 32 stages at once, a batch ahead.
+// before its window and those from the window's first key on; no page between them is read.  The producer's lanes look up
+// the pages of 32 stages at once, a batch ahead; of a short table they hold the sequence's whole row, read before its length is
+// known, of whose entries those without a visible key are not used.
 #include <cuda_bf16.h>
 
 #include <type_traits>

@@ -562,9 +562,10 @@ fa_status_t fa_window_bwd(const void* q, const void* k, const void* v, const voi
  *
  *   q            [B, Hq, d] bf16, 16-byte aligned.  Hq / Hkv at most 32 (FA_ERR_UNSUPPORTED beyond).
  *   k_pages,     [num_pages, Hkv, page_size, d] bf16 pools, block_table [B, max_pages] and seq_lens [B] int32,
- *   v_pages      page_size and max_seq_len as for fa_decode_paged.  Only the table's entries of pages that hold a visible
- *                key are read, and only those pages: pages between the sinks and the window may be given
- *                back.  A sequence of length 0 gets O = 0 and lse = -inf.
+ *   v_pages      page_size and max_seq_len as for fa_decode_paged.  Only pages that hold a visible key are read: pages
+ *                between the sinks and the window may be given back.  Any entry of the table may be read and must be readable
+ *                (up to 128 pages a sequence, its whole row is); what entries without a visible key hold has no influence.  A
+ *                sequence of length 0 gets O = 0 and lse = -inf.
  *   window       >= 1 (>= max_seq_len: every key);   sinks 0 .. 128.
  *   o [B, Hq, d] bf16 (fp32 with opts->o_fp32), 16-byte aligned; lse [B, Hq] fp32 (written).
  *   workspace    caller-owned scratch of fa_window_decode_paged_workspace_bytes() bytes (0 where none is needed),
