@@ -262,7 +262,7 @@ struct WindowFwdLaunch {
   CUtensorMap tq;        // {d, pack, N, units}, boxes of 64 x pack x tile
   CUtensorMap tk, tv;    // 128-row boxes
   CUtensorMap tks, tvs;  // k and v up to their first `sinks` rows
-  CUtensorMap to;        // as tq: bf16 O at d = 64 only
+  CUtensorMap to;        // as tq, of a bf16 O (unset for fp32): at d = 64, and at d = 128 where pack > 1 for columns 0 .. 63
   WindowFwdArgs args;
   int d, sms;
 };
