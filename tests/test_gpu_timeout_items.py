@@ -74,3 +74,30 @@ def test_cross(o_fp32):
     kv_lens = torch.tensor([Nk, 333, 0, 650], dtype=torch.int32, device=DEV)
     _check(lambda o, lse, budget: fattn.fa_cross_fwd(q, k, v, o, lse, 0.1, kv_lens, wait_budget_cycles=budget), q, o_fp32,
            B * Hq * Nq // 256)
+
+
+@pytest.mark.parametrize("grads", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,B,H,N,W,S", [(64, 4, 16, 2100, 256, 4), (128, 2, 32, 4100, 128, 17), (64, 2, 96, 200, 30, 3)])
+def test_window_backward(d, B, H, N, W, S, grads):
+    """Blocks of several key tiles and several query tiles, of one head and of all heads' list."""
+    q, k, v, do = (inputs.normal_bf16((B, H, N, d), s, DEV) for s in (1, 2, 3, 4))
+    o, lse = torch.empty_like(q), torch.empty(B, H, N, device=DEV)
+    fattn.fa_window_fwd(q, k, v, o, lse, 0.1, W, S)
+
+    def step(budget):
+        g = [torch.full(q.shape, float("nan"), dtype=grads, device=DEV) for _ in range(3)]
+        fattn.fa_window_bwd(q, k, v, o, do, lse, *g, 0.1, W, S, wait_budget_cycles=budget)
+        return g
+    want = step(0)
+    assert fattn.fa_get_status() == fattn.FA_OK
+    for budget in BUDGETS:
+        for _ in range(2):
+            got = step(budget)
+            try:
+                fattn.fa_get_status()
+                assert budget > 1 and all(torch.equal(a, b) for a, b in zip(got, want)), f"budget {budget}"
+            except fattn.FattnError as e:
+                assert e.status == fattn.FA_ERR_TIMEOUT, f"budget {budget}"
+        got = step(0)
+        assert fattn.fa_get_status() == fattn.FA_OK
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), f"after a budget of {budget}"
