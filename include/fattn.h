@@ -588,7 +588,8 @@ fa_status_t fa_window_decode_paged(const void* q, const void* k_pages, const voi
  *   q_weight, [d] bf16, or fp32 with weight_fp32 = 1; NULL: all ones.
  *   k_weight
  *   eps       finite and > 0.
- * Norm, cos, sin and products in fp32, one rounding to bf16 (nearest even).
+ * Norm, cos, sin and products in fp32, one rounding to bf16 (nearest even); elements below 2^60 in magnitude (the squares'
+ * sum has to stay in fp32).
  */
 
 /* fa_norm_rope_axes -- q into q_out and k into k_out, in one kernel.  An output may be its own input; otherwise
