@@ -1020,14 +1020,11 @@ __global__ void __launch_bounds__(PersistCfg::THREADS, 1)
         store_lse(lse, static_cast<size_t>(frow), h, row < N, l_row, m2);
         stage_half_row_bf16<D>(o_stage, o_stage, r, h, t_o, (l_row > 0.f) ? 1.f / l_row : 0.f);
         mbar_arrive(BAR(C::B_OW + t));
-        if (o_issuer) {
-          ok = mbar_wait(BAR(C::B_OW + t), gi & 1, abort_flag, budget, &g_fwd_status);
-          if (ok) {
-            tma_store_3d(&to, o_stage, 0, E.pair * kRowsPerCta + t * kBr, E.bh);
-            bulk_commit();
-          }
+        // (One lane's wait does not end the loop: the next item's waits are the whole warp's, and see that it ran out.)
+        if (o_issuer && mbar_wait(BAR(C::B_OW + t), gi & 1, abort_flag, budget, &g_fwd_status)) {
+          tma_store_3d(&to, o_stage, 0, E.pair * kRowsPerCta + t * kBr, E.bh);
+          bulk_commit();
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);  // (the lanes leave together: the next item's waits are the whole warp's)
         ++gi;
       }
       // The U_t loads above complete (tcgen05.wait::ld) before this thread's first P~-ready

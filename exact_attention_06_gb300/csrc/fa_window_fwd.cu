@@ -485,15 +485,13 @@ __global__ void __launch_bounds__(Cfg128<STAGED>::THREADS, 1)
           store_bf16x16(dst + 16 * i, w, whole);
         }
       }
-      if (STAGED && o_issuer) {
-        ok = wait(BAR(C::B_OW + t), gi & 1);
-        if (ok) {
-          tma_store_4d(&to, o_stage, 0, 0, I.n0 + t * a.tile, I.u);
-          bulk_commit();
-        }
+      // (One lane's wait does not end the loop: the next item's waits are the whole warp's, and see that it ran out.)
+      if (STAGED && o_issuer && wait(BAR(C::B_OW + t), gi & 1)) {
+        tma_store_4d(&to, o_stage, 0, 0, I.n0 + t * a.tile, I.u);
+        bulk_commit();
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);  // (the lanes leave together: the next item's waits are the whole warp's)
       ++gi;
+      __syncwarp();
     }
     if (o_issuer) bulk_wait_all();  // the stores complete before the CTA exits
     tmem_wait_st();
@@ -786,14 +784,11 @@ __global__ void __launch_bounds__(Cfg64::THREADS, 1)
         store_lse(a.lse, row.at, h, row.in, l_row, m2);
         stage_half_row_bf16<D>(o_stage, o_stage, r, h, t_o, (l_row > 0.f) ? 1.f / l_row : 0.f);
         mbar_arrive(BAR(C::B_OW + t));
-        if (o_issuer) {
-          ok = wait(BAR(C::B_OW + t), gi & 1);
-          if (ok) {
-            tma_store_4d(&to, o_stage, 0, 0, I.n0 + t * a.tile, I.u);
-            bulk_commit();
-          }
+        // (One lane's wait does not end the loop: the next item's waits are the whole warp's, and see that it ran out.)
+        if (o_issuer && wait(BAR(C::B_OW + t), gi & 1)) {
+          tma_store_4d(&to, o_stage, 0, 0, I.n0 + t * a.tile, I.u);
+          bulk_commit();
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);  // (the lanes leave together: the next item's waits are the whole warp's)
         ++gi;
       }
       // The U_t loads above complete (tcgen05.wait::ld) before this thread's first P~-ready arrival of the next item,
