@@ -66,21 +66,21 @@ def _peaks():
 # DRAM bytes per launch (dram__bytes_read.sum + dram__bytes_write.sum) from ncu captures summarised
 # under profiles/, keyed by kernel and workload, valid only while the kernels' code is unchanged: each source
 # with the digest (_code_digest) of it and all it includes.
-_FWD = "da14f37ef543d94c9a33c279df4531b22ad70fb2068bc610d93db4ec96be6e25"
+_FWD = "05efdd7fdcb913c85dfb2444a85691201c38a0aacfa4961a990637324d4112c8"
 _BWD = "f5d8fd8f69e89b3dd4f472669cb7b99dda188c015addd1e675cd66d19d09e77e"
 _DEC = "51794bc0b77b1d1b33e6b01d76e3b6bb8d8b889cbeba18e7031641239bd90252"
 NCU_TRAFFIC = {
-    ("fwd_kernel", "ragged"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 559.948e6},
-    ("fwd_kernel", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 264.462e6},
-    ("fwd_kernel_fp8", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 136.318e6},
-    ("fwd_persist_kernel", "prefill"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 50.658e6},
+    ("fwd_kernel", "ragged"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 557.123e6},
+    ("fwd_kernel", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 264.517e6},
+    ("fwd_kernel_fp8", "causal"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 136.280e6},
+    ("fwd_persist_kernel", "prefill"): {"sources": {"fa_fwd.cu": _FWD}, "bytes": 50.477e6},
     # backward: the dominant kernel (dK/dV) on the causal workload
-    ("bwd_dkdv_kernel", "causal"): {"sources": {"fa_bwd.cu": _BWD}, "bytes": 372.696e6},
+    ("bwd_dkdv_kernel", "causal"): {"sources": {"fa_bwd.cu": _BWD}, "bytes": 372.424e6},
     # the four-shard step: four forward launches over the key shards and the combine, summed
-    ("causal_sharded4", "causal"): {"sources": {"fa_fwd.cu": _FWD, "fa_decode.cu": _DEC}, "bytes": 1109.814e6},
+    ("causal_sharded4", "causal"): {"sources": {"fa_fwd.cu": _FWD, "fa_decode.cu": _DEC}, "bytes": 1109.327e6},
     # decode: captured on the B4 slice (decode_small) and scaled by 16 to B64 (K/V streamed once)
-    ("decode_split_kernel", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2151.005e6},
-    ("decode_split_kernel_paged", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.879e6},
+    ("decode_split_kernel", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.946e6},
+    ("decode_split_kernel_paged", "decode"): {"sources": {"fa_decode.cu": _DEC}, "bytes": 16 * 2150.872e6},
 }
 SOURCE_DIRS = (os.path.join(ROOT, "exact_attention_06_gb300", "csrc"), os.path.join(ROOT, "include"))
 
