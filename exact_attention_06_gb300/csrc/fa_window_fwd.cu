@@ -19,9 +19,10 @@
 // 16 keys, and its softmax 32 columns where they suffice.
 //
 // Bound by the tensor cores and the softmax's chains in a long window, by an item's begin and end in a narrow one.  Measured
-// (GB300): 32/8 heads x 16381, d = 128, window 4096: 645 us (1490 TFLOP/s of the visible pairs, 0.78 of the library's largest
-// product); 2 x 16/4 x 8192, window 1024: 114 us; 4 x 16 x 2048, d = 64, window 256: 26 us (the tiles' keys are 1.5 times
-// the window's); 4 x 16/4 x 517 behind 1500 keys, window 333: 10.2 us.
+// (GB300): 32/8 heads x 16381, d = 128, window 4096: 598 us in a short burst (2070 MHz; 1610 TFLOP/s of the visible pairs, 0.85 of
+// the library's largest product), 645 in a long run (1935 MHz under the power cap; 0.88 of that product there); 2 x 16/4 x 8192,
+// window 1024: 114 us; 4 x 16 x 2048, d = 64, window 256: 26 us (the tiles' keys are 1.5 times the window's); 4 x 16/4 x 517
+// behind 1500 keys, window 333: 10.2 us.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
